@@ -66,6 +66,7 @@ enum {
 #define MT_DEV_TREE_TOO_BIG 0x08  /* a request with more than MT_MAX_TREE draft nodes */
 #define MT_DEV_TIMEOUT      0x10  /* a bounded wait inside a kernel gave up */
 #define MT_DEV_MISMATCH     0x20  /* validate mode: the two kernels disagree beyond the tolerance */
+#define MT_DEV_BAD_POSITION 0x40  /* rope position outside the angle table */
 
 #define MT_D_QK 576
 #define MT_D_V 512
@@ -377,6 +378,112 @@ int mla_tree_verify_noalloc(const mt_bf16* q, const mt_bf16* kv_buf, int64_t num
                             int batch, int total_q, int heads, float sm_scale,
                             mt_bf16* out, float* lse, int max_splits, int path,
                             int32_t* dev_status, mt_stream_t stream);
+
+/*
+ * Paged latent cache. The pool of the verify calls, cut into pages of
+ * page_size rows: cache row (page p, row r) is 576 bf16 (512 latent dims then
+ * 64 rope dims) at cache + p * page_stride + r * 576. Request b's position j
+ * lives in page block_table[b * table_stride + j / page_size], row
+ * j % page_size, for j < kv_lens[b] <= max_pages * page_size. With
+ * page_stride == page_size * 576 the cache is a [num_slots, 576] pool whose
+ * slot page * page_size + row the verify calls read through kv_indices; a
+ * larger page_stride leaves room for the pages of other layers in between.
+ * The pages describe the verify call and have no counterpart for these
+ * entry points: they are the steps around it, writing the rows that it reads
+ * (prompts, accepted tokens, drafts) and plain one-token decoding.
+ *
+ * Shared rules: block_table, kv_lens and qo_indptr are int32. cache, the
+ * data pointers and their strides are 16-byte aligned (strides are counted
+ * in elements and are multiples of 8), else MT_EINVAL. A page number outside
+ * [0, num_pages) sets MT_DEV_BAD_SLOT; a kv_lens entry below 0 or beyond
+ * max_pages * page_size (at most 2^31 - 1, else MT_EINVAL) sets
+ * MT_DEV_BAD_INDPTR. Table entries behind a
+ * request's last position are never read.
+ */
+
+/* Pairs that the rotation turns (rope_style). */
+#define MT_ROPE_PAIRS 0   /* dims (2i, 2i + 1) */
+#define MT_ROPE_HALVES 1  /* dims (i, i + 32) */
+
+#define MT_MAX_PAGED_HEADS 4096   /* query heads of the paged calls (more: MT_EUNSUPPORTED) */
+
+/*
+ * Append new tokens' rows to the paged cache, with the position rotation
+ * (and, where norm_weight is given, the latent's RMS norm) on the way, and
+ * rotate the queries' rope part next to it. Request b owns the new tokens
+ * t = qo_indptr[b] + i, i < n_b = qo_indptr[b+1] - qo_indptr[b]; kv_lens[b] is
+ * its length with them, so token t is position j = kv_lens[b] - n_b + i, and
+ * its angle position is r = positions[t], or j where positions is NULL (the
+ * nodes of a draft tree are consecutive rows, but turn by their depth).
+ *     latent' = latent[t]                                    norm_weight NULL
+ *             = latent[t] * rsqrt(mean(latent[t]^2) + norm_eps) * norm_weight
+ *     rot(x)_a = x_a cos_i - x_b sin_i,  rot(x)_b = x_b cos_i + x_a sin_i
+ *     cache row of position j  = bf16_rne(latent' ++ rot(k_rope[t]))
+ *     q_out[t, h, 0:64]        = bf16_rne(rot(q_rope[t, h, 0:64]))   h < heads
+ * with (a, b) the i-th pair of rope_style, cos_i = rope_table[r, i] and
+ * sin_i = rope_table[r, 32 + i]. All arithmetic is fp32, rounded once.
+ *   latent: bf16 [total_q, 512], k_rope: bf16 [total_q, 64], row strides given
+ *   q_rope, q_out: bf16, element (t, h, 0) at t * token_stride + h *
+ *            head_stride; both NULL with heads 0 leaves the queries out.
+ *            q_out may be q_rope with the same strides (in place), but may
+ *            not overlap it in any other way.
+ *   rope_table: fp32 [max_positions, 64], 16-byte aligned
+ *   positions: int32 [total_q] or NULL; norm_weight: bf16 [512] or NULL
+ *   qo_indptr: int32 [batch+1], non-decreasing from 0; tokens t >=
+ *            qo_indptr[batch] belong to no request and are left out, and
+ *            what they would write stays as it was.
+ * Two tokens must not share a cache row (its content is unspecified then).
+ * n_b > kv_lens[b], or a qo_indptr that decreases or passes total_q, sets
+ * MT_DEV_BAD_INDPTR and leaves out that request; an angle position outside
+ * [0, max_positions) sets MT_DEV_BAD_POSITION and leaves out that token, its
+ * query included; a bad page leaves out that token's cache row.
+ */
+int mla_paged_append(const mt_bf16* latent, int64_t latent_stride, const mt_bf16* k_rope,
+                     int64_t k_rope_stride, const mt_bf16* norm_weight, float norm_eps,
+                     const mt_bf16* q_rope, int64_t q_token_stride, int64_t q_head_stride,
+                     mt_bf16* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                     int heads, const float* rope_table, int64_t max_positions, int rope_style,
+                     const int32_t* positions, const int32_t* qo_indptr, const int32_t* kv_lens,
+                     int batch, int total_q, const int32_t* block_table, int64_t table_stride,
+                     int max_pages, mt_bf16* cache, int64_t page_stride, int64_t num_pages,
+                     int page_size, int32_t* dev_status, mt_stream_t stream);
+
+/*
+ * Bytes of workspace mla_paged_decode needs on the current device for this
+ * batch and head count (0 for arguments it would reject). It holds the
+ * partial results of split requests; nothing in it has to be cleared and no
+ * call depends on what an earlier one left there. Calls that may overlap on
+ * the GPU need workspaces of their own.
+ */
+size_t mla_paged_decode_workspace_bytes(int batch, int heads);
+
+/*
+ * Attention of one new token per request over the paged cache:
+ *     s_j = sm_scale * <q[b, h, 0:576], row of position j>,   j < kv_lens[b]
+ *     lse[b, h] = ln sum_j exp(s_j)
+ *     out[b, h, :] = bf16_rne( sum_j exp(s_j - lse[b, h]) * (row of position j)[0:512] )
+ * A request of length 0 gets out = 0 and lse = -inf. Positions in a bad page
+ * are left out of both sums; the rows of a request with a bad length are
+ * left unwritten. What cache rows behind a request's last position hold
+ * (NaN included) does not matter.
+ * Scores are fp32 sums of bf16 products, the softmax and its sums are fp32,
+ * the weights are rounded to bf16 for the product with the values (page
+ * sizes that are powers of two from 8 on; they stay fp32 for others), and
+ * partial results of a split are fp32. A request's result does not depend on
+ * the rest of the batch beyond fp32 rounding of where the splits fall, and
+ * is the same in every run.
+ *   q:   bf16, element (b, h, 0) at b * q_token_stride + h * q_head_stride
+ *        (both at least 576)
+ *   out: bf16 [batch, heads, 512], 16-byte aligned; lse: fp32 [batch, heads]
+ *   workspace: 256-byte aligned
+ * Any page size works; powers of two from 8 on take the tensor-core kernel.
+ */
+int mla_paged_decode(const mt_bf16* q, int64_t q_token_stride, int64_t q_head_stride,
+                     const mt_bf16* cache, int64_t page_stride, int64_t num_pages, int page_size,
+                     const int32_t* block_table, int64_t table_stride, int max_pages,
+                     const int32_t* kv_lens, int batch, int heads, float sm_scale,
+                     mt_bf16* out, float* lse, void* workspace, size_t workspace_bytes,
+                     int32_t* dev_status, mt_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -14,14 +14,15 @@ LIB_PATH = os.path.join(_HERE, "lib", "libmla_tree.so")
 
 MT_OK, MT_EINVAL, MT_EUNSUPPORTED, MT_EWORKSPACE, MT_ECUDA = 0, -1, -2, -3, -4
 DEV_BAD_SLOT, DEV_BAD_PARENT, DEV_BAD_INDPTR, DEV_TREE_TOO_BIG, DEV_TIMEOUT = 1, 2, 4, 8, 16
-DEV_MISMATCH = 32
+DEV_MISMATCH, DEV_BAD_POSITION = 32, 64
 PATH_AUTO, PATH_SIMT, PATH_TC = 0, 1, 2
 
 EXPORTS = ["mla_tree_abi_version", "mla_tree_status_string", "mla_tree_draft_kv_scatter",
            "mla_tree_kv_indices_build", "tree_mask_pack", "tree_mask_pack_bits", "mla_tree_prepare",
            "mla_tree_verify_workspace_bytes", "mla_tree_verify_launch_count", "mla_tree_verify",
            "mla_tree_verify_bits", "mla_tree_verify_masked", "mla_tree_verify_validate_workspace_bytes",
-           "mla_tree_verify_validate", "mla_tree_verify_noalloc", "mla_tree_test_wait_limits"]
+           "mla_tree_verify_validate", "mla_tree_verify_noalloc", "mla_tree_test_wait_limits",
+           "mla_paged_append", "mla_paged_decode_workspace_bytes", "mla_paged_decode"]
 MT_ESCRATCH = -5
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -79,6 +80,14 @@ def load():
     lib.mla_tree_verify_noalloc.restype = I32
     lib.mla_tree_verify_noalloc.argtypes = [P, P, I64, P, I64, P, P, P, I64, P, I32, I32, I32, F32,
                                             P, P, I32, I32, P, P]
+    lib.mla_paged_append.restype = I32
+    lib.mla_paged_append.argtypes = [P, I64, P, I64, P, F32, P, I64, I64, P, I64, I64, I32, P, I64, I32,
+                                     P, P, P, I32, I32, P, I64, I32, P, I64, I64, I32, P, P]
+    lib.mla_paged_decode_workspace_bytes.restype = SZ
+    lib.mla_paged_decode_workspace_bytes.argtypes = [I32, I32]
+    lib.mla_paged_decode.restype = I32
+    lib.mla_paged_decode.argtypes = [P, I64, I64, P, I64, I64, I32, P, I64, I32, P, I32, I32, F32,
+                                     P, P, P, SZ, P, P]
     _lib = lib
     return lib
 
@@ -309,3 +318,127 @@ def mla_tree_verify_noalloc(q, kv_buf, kv_indices, kv_indptr, qo_indptr, packed_
         _ptr(out, torch.bfloat16, "out"), _ptr(lse, torch.float32, "lse"), max_splits, path,
         _ptr(status, torch.int32, "status"), _stream(stream))
     _check(rc, "mla_tree_verify_noalloc")
+
+
+ROPE_PAIRS, ROPE_HALVES = 0, 1
+
+
+def _strided(t, dtype, dim, name, device):
+    """A CUDA tensor of that type, rank and device with unit stride in its last dim."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise MlaTreeError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype or t.dim() != dim:
+        raise MlaTreeError("%s must be %d-dimensional %s, got %s of %s" % (name, dim, dtype, tuple(t.shape), t.dtype))
+    if t.device != device:
+        raise MlaTreeError("%s is on %s, the cache on %s" % (name, t.device, device))
+    if dim and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise MlaTreeError("%s must have unit stride in its last dimension" % name)
+    return t
+
+
+def _whole(t, dtype, shape, name, device):
+    """A contiguous CUDA tensor of that type, shape and device."""
+    _strided(t, dtype, len(shape), name, device)
+    if tuple(t.shape) != tuple(shape):
+        raise MlaTreeError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if not t.is_contiguous():
+        raise MlaTreeError("%s must be contiguous" % name)
+    return t
+
+
+def _paged(cache, block_table, kv_lens):
+    """(arguments of the cache, of its table) as the library takes them, checked."""
+    if not isinstance(cache, torch.Tensor) or not cache.is_cuda:
+        raise MlaTreeError("cache must be a CUDA tensor")
+    dev = cache.device
+    _strided(cache, torch.bfloat16, 3, "cache", dev)
+    pages, size, width = cache.shape
+    if width != 576 or size < 1 or (size > 1 and cache.stride(1) != 576):
+        raise MlaTreeError("cache must be [num_pages, page_size, 576] with rows of 576 elements one after another")
+    _strided(block_table, torch.int32, 2, "block_table", dev)
+    batch, max_pages = block_table.shape
+    _whole(kv_lens, torch.int32, (batch,), "kv_lens", dev)
+    page_stride = cache.stride(0) if pages > 1 else size * 576
+    table_stride = block_table.stride(0) if batch > 1 else max_pages
+    return ((cache.data_ptr(), page_stride, pages, size),
+            (block_table.data_ptr(), table_stride, max_pages), batch, dev)
+
+
+def _call(dev, stream, fn, args):
+    """fn(*args, stream) with dev current: the stream given, or dev's current one."""
+    if dev.index == torch.cuda.current_device():
+        return fn(*args, _stream(stream))
+    with torch.cuda.device(dev):
+        return fn(*args, _stream(stream))
+
+
+def mla_paged_append(latent, k_rope, qo_indptr, kv_lens, block_table, cache, rope_table, q_rope=None,
+                     q_out=None, positions=None, norm_weight=None, norm_eps=1e-6,
+                     rope_style=ROPE_PAIRS, status=None, stream=None):
+    """Append new tokens to a paged latent cache [num_pages, page_size, 576]:
+    latent [T, 512] (RMS-normalised where norm_weight is given) and k_rope
+    [T, 64] rotated to its position, at position kv_lens[b] - n_b + i of
+    request b's pages block_table[b]; and q_out = q_rope [T, H, 64] rotated
+    alike (q_out may be q_rope). rope_table: fp32 [positions, 64], cos | sin."""
+    c, table, batch, dev = _paged(cache, block_table, kv_lens)
+    bf16 = torch.bfloat16
+    _strided(latent, bf16, 2, "latent", dev)
+    _strided(k_rope, bf16, 2, "k_rope", dev)
+    t = latent.shape[0]
+    if latent.shape[1] != 512 or tuple(k_rope.shape) != (t, 64):
+        raise MlaTreeError("latent must be [T, 512] and k_rope [T, 64]")
+    _whole(qo_indptr, torch.int32, (batch + 1,), "qo_indptr", dev)
+    _whole(rope_table, torch.float32, (rope_table.shape[0], 64), "rope_table", dev)
+    heads, q = 0, (None, 0, 0, None, 0, 0)
+    if (q_rope is None) != (q_out is None):
+        raise MlaTreeError("q_rope and q_out go together")
+    if q_rope is not None:
+        _strided(q_rope, bf16, 3, "q_rope", dev)
+        _strided(q_out, bf16, 3, "q_out", dev)
+        heads = q_rope.shape[1]
+        if tuple(q_rope.shape) != (t, heads, 64) or q_out.shape != q_rope.shape:
+            raise MlaTreeError("q_rope and q_out must be [T, heads, 64]")
+        if heads:
+            q = (q_rope.data_ptr(), q_rope.stride(0), q_rope.stride(1),
+                 q_out.data_ptr(), q_out.stride(0), q_out.stride(1))
+    if positions is not None:
+        _whole(positions, torch.int32, (t,), "positions", dev)
+    if norm_weight is not None:
+        _whole(norm_weight, bf16, (512,), "norm_weight", dev)
+    if status is not None:
+        _strided(status, torch.int32, status.dim(), "status", dev)
+    rc = _call(dev, stream, load().mla_paged_append, (
+        latent.data_ptr(), latent.stride(0) if t > 1 else 512, k_rope.data_ptr(),
+        k_rope.stride(0) if t > 1 else 64,
+        None if norm_weight is None else norm_weight.data_ptr(), norm_eps, *q, heads,
+        rope_table.data_ptr(), rope_table.shape[0], rope_style,
+        None if positions is None else positions.data_ptr(), qo_indptr.data_ptr(), kv_lens.data_ptr(),
+        batch, t, *table, *c, None if status is None else status.data_ptr()))
+    _check(rc, "mla_paged_append")
+
+
+def mla_paged_decode_workspace_bytes(batch, heads):
+    return int(load().mla_paged_decode_workspace_bytes(batch, heads))
+
+
+def mla_paged_decode(q, cache, block_table, kv_lens, sm_scale, out, lse, workspace, status=None,
+                     stream=None):
+    """Attention of one new token per request over a paged latent cache: q
+    [B, H, 576] over the first kv_lens[b] positions of request b's pages;
+    out [B, H, 512] bf16 and lse [B, H] fp32. workspace: uint8, at least
+    mla_paged_decode_workspace_bytes(B, H)."""
+    c, table, batch, dev = _paged(cache, block_table, kv_lens)
+    _strided(q, torch.bfloat16, 3, "q", dev)
+    heads = q.shape[1]
+    if tuple(q.shape) != (batch, heads, 576):
+        raise MlaTreeError("q must be [batch, heads, 576]")
+    _whole(out, torch.bfloat16, (batch, heads, 512), "out", dev)
+    _whole(lse, torch.float32, (batch, heads), "lse", dev)
+    _whole(workspace, torch.uint8, (workspace.numel(),), "workspace", dev)
+    if status is not None:
+        _strided(status, torch.int32, status.dim(), "status", dev)
+    rc = _call(dev, stream, load().mla_paged_decode, (
+        q.data_ptr(), q.stride(0) if batch > 1 else heads * 576, q.stride(1) if heads > 1 else 576, *c, *table,
+        kv_lens.data_ptr(), batch, heads, sm_scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), None if status is None else status.data_ptr()))
+    _check(rc, "mla_paged_decode")

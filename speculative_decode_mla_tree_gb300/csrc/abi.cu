@@ -58,6 +58,16 @@ WorkspaceLayout workspace_layout(int batch, int total_q, int heads, int max_spli
 
 using namespace mt;
 
+// Geometry of a paged cache: what the host can check of it.
+static bool paged_cache_ok(const void* cache, int64_t page_stride, int64_t num_pages, int page_size,
+                           int64_t table_stride, int max_pages) {
+  if (page_size <= 0 || num_pages < 0 || max_pages < 0 || table_stride < max_pages) return false;
+  if ((uintptr_t)cache % 16 || page_stride % 8 || page_stride < (int64_t)page_size * MT_D_QK) return false;
+  // positions and page numbers are 32-bit, element offsets 64-bit
+  return (int64_t)max_pages * page_size <= INT32_MAX && num_pages <= INT32_MAX &&
+         (num_pages == 0 || page_stride <= INT64_MAX / 2 / num_pages);
+}
+
 static int cuda_status(cudaError_t e) { return e == cudaSuccess ? MT_OK : MT_ECUDA; }
 
 extern "C" {
@@ -308,6 +318,116 @@ int mla_tree_verify_masked(const mt_bf16* q, const mt_bf16* kv_buf, int64_t num_
                        bits ? nullptr : (const uint8_t*)mask, bits ? (const uint32_t*)mask : nullptr,
                        mask_len, mask_indptr, batch, total_q, heads, sm_scale, out, lse, workspace,
                        workspace_bytes, max_splits, path, dev_status, stream);
+}
+
+int mla_paged_append(const mt_bf16* latent, int64_t latent_stride, const mt_bf16* k_rope,
+                     int64_t k_rope_stride, const mt_bf16* norm_weight, float norm_eps,
+                     const mt_bf16* q_rope, int64_t q_token_stride, int64_t q_head_stride,
+                     mt_bf16* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                     int heads, const float* rope_table, int64_t max_positions, int rope_style,
+                     const int32_t* positions, const int32_t* qo_indptr, const int32_t* kv_lens,
+                     int batch, int total_q, const int32_t* block_table, int64_t table_stride,
+                     int max_pages, mt_bf16* cache, int64_t page_stride, int64_t num_pages,
+                     int page_size, int32_t* dev_status, mt_stream_t stream) {
+  if (batch < 0 || total_q < 0 || heads < 0 || max_positions < 0 || norm_eps < 0.f ||
+      !isfinite(norm_eps) || (rope_style != MT_ROPE_PAIRS && rope_style != MT_ROPE_HALVES) ||
+      !paged_cache_ok(cache, page_stride, num_pages, page_size, table_stride, max_pages) ||
+      latent_stride < MT_D_V || latent_stride % 8 || k_rope_stride < MT_D_QK - MT_D_V ||
+      k_rope_stride % 8)
+    return MT_EINVAL;
+  if (batch == 0 || total_q == 0) return MT_OK;
+  if (!latent || !k_rope || !rope_table || !qo_indptr || !kv_lens || !block_table || !cache)
+    return MT_EINVAL;
+  if ((uintptr_t)latent % 16 || (uintptr_t)k_rope % 16 || (uintptr_t)norm_weight % 16 ||
+      (uintptr_t)rope_table % 16)
+    return MT_EINVAL;
+  if (heads > 0) {
+    if (!q_rope || !q_out || (uintptr_t)q_rope % 16 || (uintptr_t)q_out % 16 ||
+        q_token_stride < 0 || q_head_stride < 0 || q_token_stride % 8 || q_head_stride % 8 ||
+        q_out_token_stride % 8 || q_out_head_stride % 8)
+      return MT_EINVAL;
+    if (q_out == q_rope &&
+        (q_out_token_stride != q_token_stride || q_out_head_stride != q_head_stride))
+      return MT_EINVAL;
+    // no two outputs may share elements: the wider stride has to step over
+    // everything the narrower one spans (either may be the head's)
+    const int64_t lo = q_out_token_stride < q_out_head_stride ? q_out_token_stride : q_out_head_stride;
+    const int64_t hi = q_out_token_stride < q_out_head_stride ? q_out_head_stride : q_out_token_stride;
+    const int64_t nlo = q_out_token_stride < q_out_head_stride ? total_q : heads;
+    if (total_q > 1 && heads > 1) {
+      if (lo < 64 || hi / lo < nlo - 1 || hi < lo * (nlo - 1) + 64) return MT_EINVAL;
+    } else if ((total_q > 1 && q_out_token_stride < 64) || (heads > 1 && q_out_head_stride < 64)) {
+      return MT_EINVAL;
+    }
+  } else if (q_rope || q_out) {
+    return MT_EINVAL;
+  }
+  if (heads > MT_MAX_PAGED_HEADS) return MT_EUNSUPPORTED;
+  AppendArgs a;
+  a.latent = latent;
+  a.latent_stride = latent_stride;
+  a.k_rope = k_rope;
+  a.k_rope_stride = k_rope_stride;
+  a.norm_weight = norm_weight;
+  a.norm_eps = norm_eps;
+  a.q_rope = q_rope;
+  a.q_tok = q_token_stride;
+  a.q_head = q_head_stride;
+  a.q_out = q_out;
+  a.qo_tok = q_out_token_stride;
+  a.qo_head = q_out_head_stride;
+  a.heads = heads;
+  a.table = rope_table;
+  a.max_positions = max_positions;
+  a.positions = positions;
+  a.qo_indptr = qo_indptr;
+  a.batch = batch;
+  a.total_q = total_q;
+  a.kv = {cache, page_stride, num_pages, page_size, block_table, table_stride, max_pages, kv_lens};
+  a.status = dev_status;
+  return cuda_status(launch_paged_append(a, rope_style, (cudaStream_t)stream));
+}
+
+size_t mla_paged_decode_workspace_bytes(int batch, int heads) {
+  if (batch < 0 || heads <= 0 || heads > MT_MAX_PAGED_HEADS) return 0;
+  return decode_layout(heads, sm_count()).total;
+}
+
+int mla_paged_decode(const mt_bf16* q, int64_t q_token_stride, int64_t q_head_stride,
+                     const mt_bf16* cache, int64_t page_stride, int64_t num_pages, int page_size,
+                     const int32_t* block_table, int64_t table_stride, int max_pages,
+                     const int32_t* kv_lens, int batch, int heads, float sm_scale,
+                     mt_bf16* out, float* lse, void* workspace, size_t workspace_bytes,
+                     int32_t* dev_status, mt_stream_t stream) {
+  if (batch < 0 || heads <= 0 || !isfinite(sm_scale) || q_token_stride < MT_D_QK ||
+      q_token_stride % 8 || q_head_stride < MT_D_QK || q_head_stride % 8 ||
+      !paged_cache_ok(cache, page_stride, num_pages, page_size, table_stride, max_pages))
+    return MT_EINVAL;
+  if (batch == 0) return MT_OK;
+  if (!q || !kv_lens || !out || !lse || (max_pages > 0 && !block_table) || (num_pages > 0 && !cache))
+    return MT_EINVAL;
+  if ((uintptr_t)q % 16 || (uintptr_t)out % 16 || (uintptr_t)lse % 4) return MT_EINVAL;
+  if (batch > 65535 || heads > MT_MAX_PAGED_HEADS) return MT_EUNSUPPORTED;
+  const int nsm = sm_count();
+  const DecodeLayout wl = decode_layout(heads, nsm);
+  if (!workspace || (uintptr_t)workspace % 256 || workspace_bytes < wl.total) return MT_EWORKSPACE;
+  DecodeArgs a;
+  a.q = q;
+  a.q_tok = q_token_stride;
+  a.q_head = q_head_stride;
+  a.kv = {const_cast<mt_bf16*>(cache), page_stride, num_pages, page_size, block_table, table_stride,
+          max_pages, kv_lens};
+  a.batch = batch;
+  a.heads = heads;
+  a.sm_scale = sm_scale;
+  a.out = out;
+  a.lse = lse;
+  a.status = dev_status;
+  char* ws = (char*)workspace;
+  a.ws_entry = (MergeEntry*)ws;
+  a.ws_lse = (float*)(ws + wl.lse_off);
+  a.ws_o = (float*)(ws + wl.o_off);
+  return cuda_status(launch_paged_decode_simt(a, nsm, (cudaStream_t)stream));
 }
 
 }  // extern "C"

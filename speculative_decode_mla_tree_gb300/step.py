@@ -1,8 +1,10 @@
 """Device buffers for one batch shape and the four library calls of one
 verify step: draft-KV scatter, KV index marshaling, tree-mask packing and
-tree-verify attention. Buffers are allocated once, so a step can be
-replayed or captured into a CUDA graph; refilling the input buffers in place
-(``load``) gives a new step of the same shape."""
+tree-verify attention (``VerifyStep``); and those of one plain decoding step
+over a paged cache: append with rotation and single-token attention
+(``DecodeStep``). Buffers are allocated once, so a step can be replayed or
+captured into a CUDA graph; refilling the input buffers in place (``load``)
+gives a new step of the same shape."""
 from __future__ import annotations
 
 import torch
@@ -140,3 +142,48 @@ class VerifyStep:
         abi.mla_tree_verify(self.q, self.pool, self.kv_indices, self.kv_indptr, self.qo_indptr,
                             self.mask, self.mask_indptr, self.sm_scale, self.out, self.lse,
                             self.workspace, self.max_splits, self.path, self.status, stream)
+
+
+class DecodeStep:
+    """One new token per request over a paged latent cache: its row is
+    appended (latent normalised where norm_weight is given, rope parts rotated
+    to the position) and its heads attend over the request's positions, the
+    new one included.
+
+    A program fills ``latent`` [B, 512], ``k_rope`` [B, 64] and ``q`` [B, H,
+    576] (absorbed latent query, then the rope part as projected: the step
+    rotates it in place), keeps ``block_table`` and ``kv_lens`` (lengths with
+    the new token), and reads ``out``
+    and ``lse``. ``q`` holds rotated rope parts after ``run``: refill it
+    before the next step."""
+
+    def __init__(self, cache, batch, heads, max_pages, rope_table, sm_scale, norm_weight=None,
+                 norm_eps=1e-6, rope_style=abi.ROPE_PAIRS):
+        dev = cache.device
+        self.cache, self.rope_table, self.norm_weight = cache, rope_table, norm_weight
+        self.sm_scale, self.norm_eps, self.rope_style = sm_scale, norm_eps, rope_style
+        self.latent = torch.zeros(batch, 512, dtype=torch.bfloat16, device=dev)
+        self.k_rope = torch.zeros(batch, 64, dtype=torch.bfloat16, device=dev)
+        self.q = torch.zeros(batch, heads, 576, dtype=torch.bfloat16, device=dev)
+        self.block_table = torch.zeros(batch, max_pages, dtype=torch.int32, device=dev)
+        self.kv_lens = torch.zeros(batch, dtype=torch.int32, device=dev)
+        self.qo_indptr = torch.arange(batch + 1, dtype=torch.int32, device=dev)
+        self.out = torch.zeros(batch, heads, 512, dtype=torch.bfloat16, device=dev)
+        self.lse = torch.zeros(batch, heads, dtype=torch.float32, device=dev)
+        n = abi.mla_paged_decode_workspace_bytes(batch, heads)
+        self.workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def append(self, stream=None):
+        q_rope = self.q[:, :, 512:]
+        abi.mla_paged_append(self.latent, self.k_rope, self.qo_indptr, self.kv_lens, self.block_table,
+                             self.cache, self.rope_table, q_rope, q_rope, None, self.norm_weight,
+                             self.norm_eps, self.rope_style, self.status, stream)
+
+    def attend(self, stream=None):
+        abi.mla_paged_decode(self.q, self.cache, self.block_table, self.kv_lens, self.sm_scale, self.out,
+                             self.lse, self.workspace, self.status, stream)
+
+    def run(self, stream=None):
+        self.append(stream)
+        self.attend(stream)
