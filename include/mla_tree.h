@@ -217,8 +217,10 @@ int mla_tree_verify_launch_count(int batch, int total_q, int heads, int64_t kv_i
  *                  from its work item drop_item on (items number the
  *                  (128-row tile, key split) pairs of a call from 0), so
  *                  the waits on those keys run out.
- * Process-wide: applies to every tensor-core verify call enqueued after it
- * until it is called again with (-1, 0). Returns MT_EINVAL for
+ * The tensor-core kernel of mla_paged_decode obeys the same two settings; its
+ * work items are the equal shares that it cuts a batch into.
+ * Process-wide: applies to every tensor-core call enqueued after it until it
+ * is called again with (-1, 0). Returns MT_EINVAL for
  * drop_item < -1 or a negative limit. Not for production use.
  */
 int mla_tree_test_wait_limits(int drop_item, int64_t wait_limit_ns);

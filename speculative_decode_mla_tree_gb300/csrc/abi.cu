@@ -179,6 +179,7 @@ size_t mla_tree_verify_workspace_bytes(int batch, int total_q, int heads, int ma
 int mla_tree_test_wait_limits(int drop_item, int64_t wait_limit_ns) {
   if (drop_item < -1 || wait_limit_ns < 0) return MT_EINVAL;
   set_tc_test_hooks(drop_item, (unsigned long long)wait_limit_ns);
+  set_paged_test_hooks(drop_item, (unsigned long long)wait_limit_ns);
   return MT_OK;
 }
 
@@ -427,6 +428,8 @@ int mla_paged_decode(const mt_bf16* q, int64_t q_token_stride, int64_t q_head_st
   a.ws_entry = (MergeEntry*)ws;
   a.ws_lse = (float*)(ws + wl.lse_off);
   a.ws_o = (float*)(ws + wl.o_off);
+  const cudaError_t e = launch_paged_decode_tc(a, nsm, (cudaStream_t)stream);
+  if (e != cudaErrorNotSupported) return cuda_status(e);
   return cuda_status(launch_paged_decode_simt(a, nsm, (cudaStream_t)stream));
 }
 

@@ -141,6 +141,10 @@ struct DecodeLayout {
   size_t lse_off, o_off, total;
 };
 DecodeLayout decode_layout(int heads, int num_sms);
+// Tensor-core kernel; returns cudaErrorNotSupported when it cannot serve `a`.
+cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_t stream);
+// The same test hooks for that kernel (drop_item counts its teams' shares).
+void set_paged_test_hooks(int drop_item, unsigned long long limit_ns);
 cudaError_t launch_paged_decode_simt(const DecodeArgs& a, int num_sms, cudaStream_t stream);
 // Joins the partials of `entries` merge entries; step: distance of the slots
 // after the first.

@@ -1,0 +1,748 @@
+// Single-token attention over a paged latent cache on the tensor cores
+// (tcgen05 / TMEM / TMA), for page sizes that are powers of two from 8 on.
+//
+// With one query token per request a tile has only the heads as rows, so both
+// products are taken transposed, keys and value dims in the MMA's M and the
+// heads in its N, and no MMA row is padding however few heads there are:
+//     S^T [64 keys x N heads]   = K [64 x 576] Q^T          (M = 64)
+//     O^T [512 dims x N heads] += V^T [512 x 64] P^T        (4 x M = 128)
+// K and V^T are the same shared-memory tile, read K-major and MN-major. A CTA
+// serves N = 16, 32 or 64 heads (more heads are groups of 64 in CTAs of their
+// own, side by side) and walks a contiguous range of 64-key tiles that may
+// span several requests.
+//
+// Softmax over keys is over TMEM lanes here. Its maximum would cross lanes and
+// warps for every tile; instead the reference of each head (the number its
+// weights are relative to) moves only when a score exceeds it by more than
+// 2^8, which is asked with one block-wide OR per tile. Only then are the
+// maxima exchanged and O^T rescaled; after a request's first tile that is
+// rare. Weights stay below 2^8 and the sums fp32, so nothing is lost.
+//
+// Work split: the batch is a line of 64-key tiles (a request adds kOverhead
+// tiles for its query load and epilogue), cut into equal shares, one per team
+// (the CTAs of all head groups). Every CTA finds its share from kv_lens by
+// itself. A request inside one share is finished in place; others leave fp32
+// partials, at most two per CTA, for the merge kernel.
+//
+// Roles (192 threads): four softmax warps (one per TMEM lane quarter), a TMA
+// producer warp, an MMA warp that owns TMEM. Every wait is time-bounded: a
+// timeout sets MT_DEV_TIMEOUT, nothing more is issued, what is in flight is
+// drained and TMEM released.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <float.h>
+#include <math.h>
+
+#include <mutex>
+
+#include "mt_common.cuh"
+#include "mt_internal.h"
+#include "sm100_ptx.cuh"
+
+namespace mt {
+namespace ptc {
+
+using namespace sm100;
+
+constexpr int kTile = 64;                     // keys per tile
+constexpr int kThreads = 192;
+constexpr int kSoft = 128;                    // softmax threads: warps 0-3
+constexpr int kProducerWarp = 4, kMmaWarp = 5;
+constexpr int kChunk = kTile * 128;           // 64 keys x 64 dims, 128-byte rows, 128B swizzle
+constexpr int kStage = 9 * kChunk;            // a tile: 8 latent chunks, the rope chunk
+constexpr int kStages = 2;
+// Loads and releases go by groups of a stage: latent chunk pairs 0-3 (the 128
+// value dims of one P.V MMA row block) and the rope chunk 4.
+constexpr int kGroups = 5;
+constexpr float kRescale = 8.f;               // log2 of how far a weight may exceed 1
+constexpr int kOverhead = 2;                  // a request's fixed cost, in tiles
+constexpr int kMinShare = 4;                  // smallest share of a team, in tiles
+constexpr uint64_t kDrainNs = 100000000ull;
+constexpr unsigned kFull = 0xffffffffu;
+
+enum {
+  B_Q_FULL, B_Q_EMPTY, B_P_FULL, B_P_EMPTY, B_O_EMPTY, B_DRAIN,
+  B_S_FULL,                                   // x 2
+  B_S_EMPTY = B_S_FULL + 2,                   // x 2
+  B_KV_FULL = B_S_EMPTY + 2,                  // x kStages x kGroups
+  B_KV_EMPTY = B_KV_FULL + kStages * kGroups,
+  kNumBars = B_KV_EMPTY + kStages * kGroups
+};
+
+// Shared memory from a 1024-byte aligned base, TMEM columns.
+template <int N>
+struct Lay {
+  static constexpr int kQ = 0;                          // [9][N][128 B] 128B swizzle
+  static constexpr int kKV = kQ + N * 9 * 128;
+  static constexpr int kP = kKV + kStages * kStage;     // [N heads][64 keys] bf16, 128B swizzle
+  static constexpr int kBars = kP + N * 128;
+  static constexpr int kMask = kBars + kNumBars * 8;    // per stage: the tile's visible keys
+  static constexpr int kPlan = kMask + kStages * 8;     // 8 x int64
+  static constexpr int kMisc = kPlan + 8 * 8;           // tmem base, abort flag
+  static constexpr int kRed = kMisc + 16;               // [4][N] fp32
+  static constexpr int kVec = kRed + 4 * N * 4;         // [N] fp32
+  static constexpr int kUsed = kVec + N * 4;
+  static constexpr int kBytes = kUsed + 1024;           // slack for aligning the base
+  static_assert(kBytes <= 232448, "shared memory budget");
+  static_assert(kKV % 1024 == 0 && kP % 1024 == 0 && kRed % 16 == 0 && kVec % 16 == 0, "alignment");
+  static constexpr uint32_t kO = 0;                     // four blocks of N columns: dims 128 m + lane
+  static constexpr uint32_t kS = 4 * N;                 // two score buffers of N columns
+  static constexpr uint32_t kCols = N == 64 ? 512 : N == 32 ? 256 : 128;
+};
+
+struct Params {
+  DecodeArgs a;
+  int page_shift;
+  int groups;                   // head groups = CTAs per team
+  int nteams;
+  int drop_team;                // test hook: this team's and later producers issue nothing (-1: off)
+  unsigned long long limit_ns;  // bound of every wait
+};
+
+// ---------------------------------------------------------------- PTX forms
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// 16 TMEM lanes x 8 K columns: thread t gets, for every 8 columns i, rows t / 4
+// (r[4i], r[4i+1]) and t / 4 + 8 (r[4i+2], r[4i+3]), columns 8 i + 2 (t % 4) + {0, 1}.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+        "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Four 8x8 blocks of 16-bit elements, each stored transposed: lane 8 i + j
+// gives the address of block i's column j, which becomes 16 bytes there.
+__device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a),
+               "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ bool bar_any(int id, int nthreads, bool v) {
+  int r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n"
+      " selp.s32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((int)v), "r"(id), "r"(nthreads)
+      : "memory");
+  return r != 0;
+}
+
+// --------------------------------------------------------------------- plan
+
+__device__ __forceinline__ bool length_ok(const DecodeArgs& a, int len) {
+  return len >= 0 && len <= (int64_t)a.kv.max_pages * a.kv.page_size;
+}
+__device__ __forceinline__ int tiles_of(const DecodeArgs& a, int len) {
+  return length_ok(a, len) ? (int)(((int64_t)len + kTile - 1) / kTile) : 0;
+}
+
+// A team's walk over its share [s, e) of the line of tiles. Each role keeps
+// one of its own.
+struct Walk {
+  int64_t s, e, o;  // o: where request b starts on the line
+  int b;
+};
+struct Piece {
+  int b, len, tiles, t0, t1;
+  int64_t o;
+  bool ok;
+};
+
+__device__ __forceinline__ bool next_piece(const DecodeArgs& a, Walk& w, Piece& p) {
+  while (w.b < a.batch && w.o < w.e) {
+    p.b = w.b;
+    p.o = w.o;
+    p.len = __ldg(a.kv.lens + w.b);
+    p.ok = length_ok(a, p.len);
+    p.tiles = tiles_of(a, p.len);
+    const int64_t first = w.o + kOverhead;  // the request's tiles start here
+    const int64_t t0 = w.s - first, t1 = w.e - first;
+    p.t0 = (int)(t0 > 0 ? (t0 < p.tiles ? t0 : p.tiles) : 0);
+    p.t1 = (int)(t1 < p.tiles ? (t1 > 0 ? t1 : 0) : p.tiles);
+    w.o = first + p.tiles;
+    ++w.b;
+    if (p.t1 > p.t0 || (p.tiles == 0 && p.o >= w.s)) return true;
+  }
+  return false;
+}
+
+__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+// The share size and where this team's share starts, by all threads.
+__device__ Walk make_plan(const Params& p, int team, int64_t* sh, int64_t* share_out) {
+  const DecodeArgs& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kW = kThreads / 32;
+  int64_t mine = 0;
+  for (int b = tid; b < a.batch; b += kThreads) mine += kOverhead + tiles_of(a, __ldg(a.kv.lens + b));
+  mine = warp_sum64(mine);
+  if (lane == 0) sh[warp] = mine;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kW; ++w) total += sh[w];
+  int64_t share = (total + p.nteams - 1) / p.nteams;
+  if (share < kMinShare + kOverhead) share = kMinShare + kOverhead;
+  *share_out = share;
+  Walk r;
+  r.s = team * share;
+  r.e = r.s + share;
+  r.b = a.batch;
+  r.o = total;
+  if (r.s >= total) return r;  // the same for all threads
+  int64_t run = 0;
+  for (int base = 0; run <= r.s; base += kThreads) {
+    __syncthreads();
+    const int b = base + tid;
+    const int64_t u = b < a.batch ? kOverhead + tiles_of(a, __ldg(a.kv.lens + b)) : 0;
+    int64_t inc = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(kFull, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) sh[warp] = inc;
+    __syncthreads();
+    int64_t off = run;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      if (w < warp) off += sh[w];
+      run += sh[w];
+    }
+    const int64_t at = off + inc - u;
+    if (u > 0 && at <= r.s && r.s < at + u) {
+      sh[6] = b;
+      sh[7] = at;
+    }
+  }
+  __syncthreads();
+  r.b = (int)sh[6];
+  r.o = sh[7];
+  return r;
+}
+
+// ------------------------------------------------------------------- kernel
+
+template <int N>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_decode_tc_kernel(const Params p, const __grid_constant__ CUtensorMap tq,
+                           const __grid_constant__ CUtensorMap tpair, const __grid_constant__ CUtensorMap tone) {
+  using L = Lay<N>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBars);
+  uint64_t* vmask = reinterpret_cast<uint64_t*>(sm + L::kMask);
+  int64_t* plan = reinterpret_cast<int64_t*>(sm + L::kPlan);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kMisc);
+  volatile int* abort = reinterpret_cast<volatile int*>(sm + L::kMisc + 4);
+  float* red = reinterpret_cast<float*>(sm + L::kRed);
+  float* vec = reinterpret_cast<float*>(sm + L::kVec);
+
+  const DecodeArgs& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int team = blockIdx.x / p.groups, grp = blockIdx.x % p.groups;
+  const uint64_t limit = p.limit_ns;
+
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, L::kCols);
+    tmem_relinquish();
+  } else if (tid == 0) {
+    *abort = 0;
+    for (int i = 0; i < kNumBars; ++i) mbar_init(&bars[i], 1);
+    mbar_init(&bars[B_P_FULL], 4);
+    mbar_init(&bars[B_O_EMPTY], 4);
+    mbar_init(&bars[B_S_EMPTY], 4);
+    mbar_init(&bars[B_S_EMPTY + 1], 4);
+    fence_mbar_init_cluster();
+  } else if (tid == kProducerWarp * 32) {
+    prefetch_tmap(&tq);
+    prefetch_tmap(&tpair);
+    prefetch_tmap(&tone);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int64_t share;
+  Walk walk = make_plan(p, team, plan, &share);
+  Piece pc;
+
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------ producer
+    const int P = 1 << p.page_shift;
+    const int rp = P < kTile ? P : kTile;       // rows a page gives to a tile
+    const int npg = kTile / rp;                 // pages a tile touches
+    const uint32_t kv0 = smem_u32(sm + L::kKV);
+    const bool drop = p.drop_team >= 0 && team >= p.drop_team;
+    uint32_t it = 0, pieces = 0, cnt[kGroups] = {0, 0, 0, 0, 0}, cntq = 0;
+    bool dead = drop;
+    while (!dead && next_piece(a, walk, pc)) {
+      if (pc.t1 <= pc.t0) continue;
+      dead = __any_sync(kFull, !mbar_wait<false>(&bars[B_Q_EMPTY], (pieces & 1) ^ 1, abort, limit));
+      if (dead) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars[B_Q_FULL], N * 9 * 128);
+        tma_load_4d(smem_u32(sm + L::kQ), &tq, 0, grp * N, 0, pc.b, &bars[B_Q_FULL]);
+      }
+      ++cntq;
+      ++pieces;
+      const int32_t* table = a.kv.table + pc.b * a.kv.table_stride;
+      auto entry = [&](int t) {  // page of this lane's part of tile t, -1: none
+        const int64_t row = (int64_t)t * kTile + lane * rp;
+        return lane < npg && row < pc.len ? __ldg(table + (row >> p.page_shift)) : -1;
+      };
+      int page_next = entry(pc.t0);
+      bool asked_next = lane < npg && (int64_t)pc.t0 * kTile + lane * rp < pc.len;
+      for (int t = pc.t0; t < pc.t1 && !dead; ++t, ++it) {
+        const int st = it & 1, ph = (it >> 1) & 1;
+        const int page = page_next;
+        const bool asked = asked_next;
+        if (t + 1 < pc.t1) {
+          page_next = entry(t + 1);
+          asked_next = lane < npg && (int64_t)(t + 1) * kTile + lane * rp < pc.len;
+        }
+        const bool ok = asked && page >= 0 && page < a.kv.num_pages;
+        if (asked && !ok && grp == 0) flag(a.status, MT_DEV_BAD_SLOT);
+        const unsigned okm = __ballot_sync(kFull, ok);
+        // visible keys: pages that are there, positions below the length
+        uint64_t vis = 0;
+        if (ok) vis = (rp == 64 ? ~0ull : (1ull << rp) - 1) << (lane * rp & 63);
+        uint32_t lo = __reduce_or_sync(kFull, (uint32_t)vis), hi = __reduce_or_sync(kFull, (uint32_t)(vis >> 32));
+        vis = (uint64_t)hi << 32 | lo;
+        const int64_t left = (int64_t)pc.len - (int64_t)t * kTile;
+        if (left < kTile) vis &= (1ull << left) - 1;
+        const uint32_t chunk_bytes = (uint32_t)__popc(okm) * rp * 128;
+        const int row = (int)(((int64_t)t * kTile) & (P - 1));
+#pragma unroll
+        for (int gi = 0; gi < kGroups; ++gi) {
+          const int g = gi == 0 ? 4 : gi - 1;  // rope first: its slot is the first that a tile frees
+          if (!dead)
+            dead = __any_sync(kFull, !mbar_wait<false>(&bars[B_KV_EMPTY + st * kGroups + g], ph ^ 1, abort, limit));
+          if (dead) continue;
+          uint64_t* full = &bars[B_KV_FULL + st * kGroups + g];
+          if (lane == 0) {
+            // the last pair's release says that the softmax is done with the old mask
+            if (g == 3) vmask[st] = vis;
+            if (chunk_bytes) mbar_arrive_expect_tx(full, g == 4 ? chunk_bytes : 2 * chunk_bytes);
+            else mbar_arrive(full);
+          }
+          __syncwarp();
+          ++cnt[g];
+          const uint32_t dst = kv0 + st * kStage + 2 * g * kChunk;
+          if (P >= kTile) {
+            if (lane == 0 && ok) tma_load_4d(dst, g == 4 ? &tone : &tpair, 0, row, 2 * g, page, full);
+          } else {
+            const int pg = lane & (npg - 1), ch = lane / npg;
+            const int id = __shfl_sync(kFull, page, pg);
+            if (ch < (g == 4 ? 1 : 2) && (okm >> pg & 1))
+              tma_load_4d(dst + ch * kChunk + pg * rp * 128, &tone, 0, 0, 2 * g + ch, id, full);
+          }
+        }
+      }
+    }
+    if (*abort) {  // let the copies in flight land
+      if (cntq) mbar_drain(&bars[B_Q_FULL], (cntq - 1) & 1, kDrainNs);
+      for (int g = 0; g < kGroups; ++g)
+        for (uint32_t st = 0; st < kStages; ++st)
+          if (cnt[g] > st) mbar_drain(&bars[B_KV_FULL + st * kGroups + g], ((cnt[g] - 1 - st) >> 1) & 1, kDrainNs);
+    }
+  } else if (warp == kMmaWarp) {
+    // ----------------------------------------------------------------- MMA
+    if (lane == 0) {
+      constexpr uint32_t id_qk = idesc_bf16(kTile, N, 0, 0), id_pv = idesc_bf16(128, N, 1, 0);
+      const uint64_t dk = smem_desc(smem_u32(sm + L::kKV), 16, 1024, kSwizzle128B);
+      const uint64_t dv = smem_desc(smem_u32(sm + L::kKV), kChunk, 1024, kSwizzle128B);
+      const uint64_t dq = smem_desc(smem_u32(sm + L::kQ), 16, 1024, kSwizzle128B);
+      const uint64_t dp = smem_desc(smem_u32(sm + L::kP), 16, 1024, kSwizzle128B);
+      uint32_t it = 0, pieces = 0;
+      bool dead = false;
+      auto qk = [&](uint32_t i, bool last) {
+        const uint32_t st = i & 1, ph = (i >> 1) & 1;
+        const uint32_t d = tmem + L::kS + st * N;
+        dead = !mbar_wait<false>(&bars[B_S_EMPTY + st], ph ^ 1, abort, limit);
+#pragma unroll
+        for (int gi = 0; gi < kGroups; ++gi) {
+          const int g = gi == 0 ? 4 : gi - 1;
+          if (!dead) dead = !mbar_wait<false>(&bars[B_KV_FULL + st * kGroups + g], ph, abort, limit);
+          if (dead) return;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < (g == 4 ? 4 : 8); ++k) {
+            const int c = 2 * g + (k >> 2);
+            mma_bf16_ss(d, dk + ((st * kStage + c * kChunk + 32 * (k & 3)) >> 4),
+                        dq + ((c * N * 128 + 32 * (k & 3)) >> 4), id_qk, gi > 0 || k > 0);
+          }
+        }
+        mma_commit(&bars[B_S_FULL + st]);
+        mma_commit(&bars[B_KV_EMPTY + st * kGroups + 4]);
+        if (last) mma_commit(&bars[B_Q_EMPTY]);
+      };
+      while (!dead && next_piece(a, walk, pc)) {
+        const int n = pc.t1 - pc.t0;
+        if (n <= 0) continue;
+        dead = !mbar_wait<false>(&bars[B_Q_FULL], pieces & 1, abort, limit);
+        if (dead) break;
+        qk(it, n == 1);
+        for (int j = 0; j < n && !dead; ++j, ++it) {
+          if (j + 1 < n) qk(it + 1, j + 2 == n);
+          if (dead) break;
+          if (j == 0) dead = !mbar_wait<false>(&bars[B_O_EMPTY], (pieces & 1) ^ 1, abort, limit);
+          if (!dead) dead = !mbar_wait<false>(&bars[B_P_FULL], it & 1, abort, limit);
+          if (dead) break;
+          tc_fence_after();
+          const uint32_t st = it & 1;
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              mma_bf16_ss(tmem + L::kO + m * N, dv + ((st * kStage + m * 2 * kChunk + k * 2048) >> 4),
+                          dp + ((32 * k) >> 4), id_pv, j > 0 || k > 0);
+            mma_commit(&bars[B_KV_EMPTY + st * kGroups + m]);
+          }
+          mma_commit(&bars[B_P_EMPTY]);
+        }
+        ++pieces;
+      }
+      if (dead) {
+        mma_commit(&bars[B_DRAIN]);
+        mbar_drain(&bars[B_DRAIN], 0, kDrainNs);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------ softmax, epilogue
+    constexpr int kC = N / 4;                   // columns (heads) of a thread: 8 i + 2 (lane % 4) + e
+    const float scale = a.sm_scale * kLog2e;
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    const int r0 = warp * 16 + (lane >> 2);     // this thread's keys of a tile: r0 and r0 + 8
+    const uint32_t pbase = smem_u32(sm + L::kP);
+    // stmatrix: lanes 0-7 / 8-15 address keys 0-7 / 8-15 of the warp for heads 0-7, lanes 16-31 for heads 8-15
+    const int sh = (lane & 7) + ((lane >> 4) << 3);
+    const uint32_t paddr = pbase + sh * 128 + (((2 * warp + ((lane >> 3) & 1)) ^ (sh & 7)) << 4);
+    MergeEntry entry = {0, 0, 0, 0};
+    uint32_t it = 0;
+    bool dead = false;
+    while (next_piece(a, walk, pc)) {
+      const int64_t orow = (int64_t)pc.b * a.heads + grp * N;
+      const int nh = min(N, a.heads - grp * N);
+      if (pc.t1 <= pc.t0) {  // no keys
+        if (!pc.ok) {
+          if (tid == 0 && grp == 0) flag(a.status, MT_DEV_BAD_INDPTR);
+          continue;
+        }
+        uint4* dst = reinterpret_cast<uint4*>(a.out + orow * kDv);
+        for (int i = tid; i < nh * (kDv / 8); i += kSoft) dst[i] = make_uint4(0, 0, 0, 0);
+        if (tid < nh) a.lse[orow + tid] = -INFINITY;
+        continue;
+      }
+      float ref[kC], l[kC];
+#pragma unroll
+      for (int j = 0; j < kC; ++j) {
+        ref[j] = -FLT_MAX;
+        l[j] = 0.f;
+      }
+      for (int t = pc.t0; t < pc.t1; ++t, ++it) {
+        const int st = it & 1, ph = (it >> 1) & 1;
+        if (!dead) dead = !mbar_wait<false>(&bars[B_S_FULL + st], ph, abort, limit);
+        if (!dead) dead = !mbar_wait<false>(&bars[B_KV_FULL + st * kGroups + 3], ph, abort, limit);
+        tc_fence_after();
+        uint32_t s[4 * (N / 8)];
+        tmem_ld_frag(tmem + lane_base + L::kS + st * N, s);
+        const uint64_t vis = vmask[st];
+        tmem_ld_wait();
+        tmem_regs_ready(s);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_S_EMPTY + st]);
+        const bool v0 = vis >> r0 & 1, v1 = vis >> (r0 + 8) & 1;
+        float x[4 * (N / 8)], top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < N / 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float y0 = v0 ? __uint_as_float(s[4 * i + e]) * scale : -INFINITY;
+            const float y1 = v1 ? __uint_as_float(s[4 * i + 2 + e]) * scale : -INFINITY;
+            x[4 * i + e] = y0;
+            x[4 * i + 2 + e] = y1;
+            top = fmaxf(top, fmaxf(y0, y1) - ref[2 * i + e]);
+          }
+        if (bar_any(1, kSoft, top > kRescale)) {
+          // new references: every head's maximum over the tile's 64 keys
+          float f[kC];
+#pragma unroll
+          for (int j = 0; j < kC; ++j) {
+            float m = fmaxf(x[4 * (j >> 1) + (j & 1)], x[4 * (j >> 1) + 2 + (j & 1)]);
+            m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
+            if (lane < 4) red[warp * N + 8 * (j >> 1) + 2 * lane + (j & 1)] = m;
+          }
+          named_bar_sync(2, kSoft);
+#pragma unroll
+          for (int j = 0; j < kC; ++j) {
+            const int c = 8 * (j >> 1) + 2 * (lane & 3) + (j & 1);
+            const float m = fmaxf(fmaxf(red[c], red[N + c]), fmaxf(red[2 * N + c], red[3 * N + c]));
+            const float nr = fmaxf(ref[j], m);
+            f[j] = ex2_approx(ref[j] - nr);
+            ref[j] = nr;
+            l[j] *= f[j];
+            if (warp == 0 && lane < 4) vec[c] = f[j];
+          }
+          if (t > pc.t0) {  // the first tile's P.V overwrites O
+            named_bar_sync(2, kSoft);
+            if (!dead) dead = !mbar_wait<false>(&bars[B_P_EMPTY], (it & 1) ^ 1, abort, limit);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 4 * N; c += 16) {
+              uint32_t o[16];
+              tmem_ld16_nw(tmem + lane_base + L::kO + c, o);
+              tmem_ld_wait();
+              tmem_regs_ready(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * vec[(c & (N - 1)) + e]);
+              tmem_st16(tmem + lane_base + L::kO + c, o);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+          }
+        }
+        uint32_t pk[N / 4];  // key r0 at 2 i, key r0 + 8 at 2 i + 1; two heads each
+#pragma unroll
+        for (int i = 0; i < N / 8; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float p0 = ex2_approx(x[4 * i + 2 * k] - ref[2 * i]);
+            const float p1 = ex2_approx(x[4 * i + 2 * k + 1] - ref[2 * i + 1]);
+            l[2 * i] += p0;
+            l[2 * i + 1] += p1;
+            const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+            pk[2 * i + k] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        if (!dead) dead = !mbar_wait<false>(&bars[B_P_EMPTY], (it & 1) ^ 1, abort, limit);
+#pragma unroll
+        for (int i = 0; i < N / 8; i += 2)
+          stmatrix4_trans(paddr + i * 8 * 128, pk[2 * i], pk[2 * i + 1], pk[2 * i + 2], pk[2 * i + 3]);
+        if (~vis != 0) {
+          // rows that are no keys of this request count with weight 0, but
+          // 0 x NaN is NaN: their values are made 0
+          for (int r = tid >> 6; r < kTile; r += kSoft / 64)
+            if (!(vis >> r & 1))
+              *reinterpret_cast<uint4*>(sm + L::kKV + st * kStage + ((tid & 63) >> 3) * kChunk + r * 128 +
+                                        (tid & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_P_FULL]);
+      }
+
+      // epilogue: sums over the keys' lanes and warps, then O^T / l
+#pragma unroll
+      for (int j = 0; j < kC; ++j) {
+        float v = l[j];
+        v += __shfl_xor_sync(kFull, v, 4);
+        v += __shfl_xor_sync(kFull, v, 8);
+        v += __shfl_xor_sync(kFull, v, 16);
+        const int c = 8 * (j >> 1) + 2 * (lane & 3) + (j & 1);
+        if (lane < 4) {
+          red[warp * N + c] = v;
+          if (warp == 0) vec[c] = ref[j];
+        }
+      }
+      named_bar_sync(2, kSoft);
+      const bool starts = pc.t0 == 0, whole = starts && pc.t1 == pc.tiles;
+      const int64_t wrow = ((int64_t)(2 * team + (starts ? 1 : 0)) * p.groups + grp) * N;
+      if (tid < N) {
+        const float sum = (red[tid] + red[N + tid]) + (red[2 * N + tid] + red[3 * N + tid]);
+        const float lse = sum != 0.f ? (vec[tid] + log2f(sum)) * kLn2 : -INFINITY;
+        if (tid < nh && !*abort) (whole ? a.lse[orow + tid] : a.ws_lse[wrow + tid]) = lse;
+        red[tid] = sum != 0.f ? 1.f / sum : 0.f;
+      }
+      named_bar_sync(2, kSoft);
+      if (!dead) dead = !mbar_wait<false>(&bars[B_P_EMPTY], (it - 1) & 1, abort, limit);
+      tc_fence_after();
+      const bool give_up = __any_sync(kFull, dead || *abort);  // nothing to write
+#pragma unroll 1
+      for (int c = 0; c < 4 * N && !give_up; c += 16) {
+        uint32_t o[16];
+        tmem_ld16_nw(tmem + lane_base + L::kO + c, o);
+        tmem_ld_wait();
+        tmem_regs_ready(o);
+        const int h0 = c & (N - 1), dim = c / N * 128 + warp * 32 + lane;
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (h0 + e < nh)
+              a.out[(orow + h0 + e) * kDv + dim] =
+                  __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(o[e]) * red[h0 + e]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (h0 + e < nh) a.ws_o[(wrow + h0 + e) * kDv + dim] = __uint_as_float(o[e]) * red[h0 + e];
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[B_O_EMPTY]);
+      if (starts && !whole) {
+        const int64_t first = pc.o + kOverhead;
+        entry.b = pc.b;
+        entry.n = (int)((first + pc.tiles - 1) / share - team + 1);
+        entry.first = 2 * team + 1;
+        entry.next = 2 * (team + 1);
+      }
+    }
+    if (tid == 0 && grp == 0) {
+      if (*abort) entry.n = 0;
+      *reinterpret_cast<int4*>(a.ws_entry + team) = make_int4(entry.b, entry.n, entry.first, entry.next);
+    }
+  }
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *abort) flag(a.status, MT_DEV_TIMEOUT);
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kCols);
+  }
+}
+
+// --------------------------------------------------------------------- host
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+int g_test_drop_team = -1;
+unsigned long long g_test_limit_ns = 0;
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  std::call_once(g_encode_once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  return g_encode;
+}
+
+// 576-wide bf16 rows as [chunk of 64 dims] [row] [chunk] [outer]: a box lays
+// `chunks` chunks of `rows` 128-byte swizzled rows one after another.
+bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t row_stride, int64_t outer,
+              int64_t outer_stride, int box_rows, int box_chunks) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {64, (cuuint64_t)rows, 9, (cuuint64_t)outer};
+  cuuint64_t strides[3] = {(cuuint64_t)row_stride * 2, 128, (cuuint64_t)outer_stride * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_chunks, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int N>
+cudaError_t launch(const Params& p, const CUtensorMap& tq, const CUtensorMap& tpair, const CUtensorMap& tone,
+                   cudaStream_t stream) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static std::mutex mu;
+  static bool set[64] = {};
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 0 || dev >= 64 || !set[dev]) {
+      e = cudaFuncSetAttribute(paged_decode_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               Lay<N>::kBytes);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < 64) set[dev] = true;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.nteams * p.groups));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Lay<N>::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_decode_tc_kernel<N>, p, tq, tpair, tone);
+}
+
+}  // namespace ptc
+
+void set_paged_test_hooks(int drop_item, unsigned long long limit_ns) {
+  ptc::g_test_drop_team = drop_item;
+  ptc::g_test_limit_ns = limit_ns;
+}
+
+cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_t stream) {
+  using namespace ptc;
+  const int P = a.kv.page_size;
+  if (P < 8 || (P & (P - 1)) || a.kv.num_pages <= 0) return cudaErrorNotSupported;
+  const int N = a.heads <= 16 ? 16 : a.heads <= 32 ? 32 : 64;
+  const int nsm = num_sms > 0 ? num_sms : 152;
+  Params p;
+  p.a = a;
+  p.page_shift = 0;
+  while ((1 << p.page_shift) < P) ++p.page_shift;
+  p.groups = (a.heads + N - 1) / N;
+  p.nteams = nsm / p.groups > 0 ? nsm / p.groups : 1;
+  p.drop_team = g_test_drop_team;
+  p.limit_ns = g_test_limit_ns > 0 ? g_test_limit_ns : sm100::kWaitLimitNs;
+  const int rows = P < kTile ? P : kTile;
+  CUtensorMap tq, tpair, tone;
+  if (!make_map(&tq, a.q, a.heads, a.q_head, a.batch, a.q_tok, N, 9) ||
+      !make_map(&tpair, a.kv.rows, P, kDqk, a.kv.num_pages, a.kv.page_stride, rows, 2) ||
+      !make_map(&tone, a.kv.rows, P, kDqk, a.kv.num_pages, a.kv.page_stride, rows, 1))
+    return cudaErrorNotSupported;
+  const cudaError_t e = N == 16   ? launch<16>(p, tq, tpair, tone, stream)
+                        : N == 32 ? launch<32>(p, tq, tpair, tone, stream)
+                                  : launch<64>(p, tq, tpair, tone, stream);
+  if (e != cudaSuccess || p.nteams == 1) return e;
+  return launch_paged_merge(a, p.nteams, 2, p.groups * N, nsm, stream);
+}
+
+}  // namespace mt
