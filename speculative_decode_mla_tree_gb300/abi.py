@@ -322,54 +322,66 @@ def mla_tree_verify_noalloc(q, kv_buf, kv_indices, kv_indptr, qo_indptr, packed_
 
 ROPE_PAIRS, ROPE_HALVES = 0, 1
 
+# The paged calls run once per layer and token, where their own time shows:
+# each argument is checked with a handful of attribute reads.
 
-def _strided(t, dtype, dim, name, device):
-    """A CUDA tensor of that type, rank and device with unit stride in its last dim."""
+
+def _refuse(t, dtype, dev, shape, name, more):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise MlaTreeError("%s must be a CUDA tensor" % name)
-    if t.dtype != dtype or t.dim() != dim:
-        raise MlaTreeError("%s must be %d-dimensional %s, got %s of %s" % (name, dim, dtype, tuple(t.shape), t.dtype))
-    if t.device != device:
-        raise MlaTreeError("%s is on %s, the cache on %s" % (name, t.device, device))
-    if dim and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise MlaTreeError("%s must have unit stride in its last dimension" % name)
-    return t
+    if t.get_device() != dev:
+        raise MlaTreeError("%s is on %s, the cache on cuda:%d" % (name, t.device, dev))
+    raise MlaTreeError("%s must be %s %s, %s; got %s %s with strides %s"
+                       % (name, dtype, tuple(shape), more, t.dtype, tuple(t.shape), t.stride()))
 
 
-def _whole(t, dtype, shape, name, device):
-    """A contiguous CUDA tensor of that type, shape and device."""
-    _strided(t, dtype, len(shape), name, device)
-    if tuple(t.shape) != tuple(shape):
-        raise MlaTreeError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if not t.is_contiguous():
-        raise MlaTreeError("%s must be contiguous" % name)
-    return t
+def _strided(t, dtype, dev, shape, name):
+    """Strides of a CUDA tensor of that type, device and shape, the last one 1."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _refuse(t, dtype, dev, shape, name, "with unit stride in the last dimension")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        _refuse(t, dtype, dev, shape, name, "with unit stride in the last dimension")
+    return st
+
+
+def _whole(t, dtype, dev, shape, name):
+    """Address of a contiguous CUDA tensor of that type, device and shape."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or t.shape != shape
+            or not t.is_contiguous()):
+        _refuse(t, dtype, dev, shape, name, "contiguous")
+    return t.data_ptr()
 
 
 def _paged(cache, block_table, kv_lens):
-    """(arguments of the cache, of its table) as the library takes them, checked."""
+    """((cache arguments), (table arguments), kv_lens, batch, device index), checked."""
     if not isinstance(cache, torch.Tensor) or not cache.is_cuda:
         raise MlaTreeError("cache must be a CUDA tensor")
-    dev = cache.device
-    _strided(cache, torch.bfloat16, 3, "cache", dev)
-    pages, size, width = cache.shape
-    if width != 576 or size < 1 or (size > 1 and cache.stride(1) != 576):
-        raise MlaTreeError("cache must be [num_pages, page_size, 576] with rows of 576 elements one after another")
-    _strided(block_table, torch.int32, 2, "block_table", dev)
-    batch, max_pages = block_table.shape
-    _whole(kv_lens, torch.int32, (batch,), "kv_lens", dev)
-    page_stride = cache.stride(0) if pages > 1 else size * 576
-    table_stride = block_table.stride(0) if batch > 1 else max_pages
-    return ((cache.data_ptr(), page_stride, pages, size),
-            (block_table.data_ptr(), table_stride, max_pages), batch, dev)
+    if not isinstance(block_table, torch.Tensor) or cache.dim() != 3 or block_table.dim() != 2:
+        raise MlaTreeError("cache must be [num_pages, page_size, 576] and block_table [batch, max_pages]")
+    dev = cache.get_device()
+    pages, size, _ = cache.shape
+    st = _strided(cache, torch.bfloat16, dev, (pages, size, 576), "cache")
+    if size > 1 and st[1] != 576:
+        raise MlaTreeError("cache must hold a page's rows of 576 elements one after another")
+    batch, max_pages = shape = block_table.shape
+    tst = _strided(block_table, torch.int32, dev, shape, "block_table")
+    lens = _whole(kv_lens, torch.int32, dev, (batch,), "kv_lens")
+    return ((cache.data_ptr(), st[0] if pages > 1 else size * 576, pages, size),
+            (block_table.data_ptr(), tst[0] if batch > 1 else max_pages, max_pages), lens, batch, dev)
 
 
-def _call(dev, stream, fn, args):
+def _status(status, dev):
+    return None if status is None else _whole(status, torch.int32, dev, status.shape, "status")
+
+
+def _call(dev, stream, fn, *args):
     """fn(*args, stream) with dev current: the stream given, or dev's current one."""
-    if dev.index == torch.cuda.current_device():
-        return fn(*args, _stream(stream))
-    with torch.cuda.device(dev):
-        return fn(*args, _stream(stream))
+    now = torch._C._cuda_getDevice()
+    if now != dev:
+        with torch.cuda.device(dev):
+            return _call(dev, stream, fn, *args)
+    return fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
 
 
 def mla_paged_append(latent, k_rope, qo_indptr, kv_lens, block_table, cache, rope_table, q_rope=None,
@@ -380,41 +392,31 @@ def mla_paged_append(latent, k_rope, qo_indptr, kv_lens, block_table, cache, rop
     [T, 64] rotated to its position, at position kv_lens[b] - n_b + i of
     request b's pages block_table[b]; and q_out = q_rope [T, H, 64] rotated
     alike (q_out may be q_rope). rope_table: fp32 [positions, 64], cos | sin."""
-    c, table, batch, dev = _paged(cache, block_table, kv_lens)
-    bf16 = torch.bfloat16
-    _strided(latent, bf16, 2, "latent", dev)
-    _strided(k_rope, bf16, 2, "k_rope", dev)
-    t = latent.shape[0]
-    if latent.shape[1] != 512 or tuple(k_rope.shape) != (t, 64):
-        raise MlaTreeError("latent must be [T, 512] and k_rope [T, 64]")
-    _whole(qo_indptr, torch.int32, (batch + 1,), "qo_indptr", dev)
-    _whole(rope_table, torch.float32, (rope_table.shape[0], 64), "rope_table", dev)
-    heads, q = 0, (None, 0, 0, None, 0, 0)
+    c, table, lens, batch, dev = _paged(cache, block_table, kv_lens)
+    bf16, i32 = torch.bfloat16, torch.int32
+    t = latent.shape[0] if isinstance(latent, torch.Tensor) and latent.dim() else 0
+    ls = _strided(latent, bf16, dev, (t, 512), "latent")
+    ks = _strided(k_rope, bf16, dev, (t, 64), "k_rope")
+    indptr = _whole(qo_indptr, i32, dev, (batch + 1,), "qo_indptr")
+    angles = rope_table.shape[0] if isinstance(rope_table, torch.Tensor) and rope_table.dim() else 0
+    rope = _whole(rope_table, torch.float32, dev, (angles, 64), "rope_table")
+    heads, q, qs, o, os_ = 0, None, (0, 0), None, (0, 0)
     if (q_rope is None) != (q_out is None):
         raise MlaTreeError("q_rope and q_out go together")
     if q_rope is not None:
-        _strided(q_rope, bf16, 3, "q_rope", dev)
-        _strided(q_out, bf16, 3, "q_out", dev)
-        heads = q_rope.shape[1]
-        if tuple(q_rope.shape) != (t, heads, 64) or q_out.shape != q_rope.shape:
-            raise MlaTreeError("q_rope and q_out must be [T, heads, 64]")
+        heads = q_rope.shape[1] if isinstance(q_rope, torch.Tensor) and q_rope.dim() > 1 else 0
+        qs = _strided(q_rope, bf16, dev, (t, heads, 64), "q_rope")
+        os_ = _strided(q_out, bf16, dev, (t, heads, 64), "q_out")
         if heads:
-            q = (q_rope.data_ptr(), q_rope.stride(0), q_rope.stride(1),
-                 q_out.data_ptr(), q_out.stride(0), q_out.stride(1))
-    if positions is not None:
-        _whole(positions, torch.int32, (t,), "positions", dev)
-    if norm_weight is not None:
-        _whole(norm_weight, bf16, (512,), "norm_weight", dev)
-    if status is not None:
-        _strided(status, torch.int32, status.dim(), "status", dev)
-    rc = _call(dev, stream, load().mla_paged_append, (
-        latent.data_ptr(), latent.stride(0) if t > 1 else 512, k_rope.data_ptr(),
-        k_rope.stride(0) if t > 1 else 64,
-        None if norm_weight is None else norm_weight.data_ptr(), norm_eps, *q, heads,
-        rope_table.data_ptr(), rope_table.shape[0], rope_style,
-        None if positions is None else positions.data_ptr(), qo_indptr.data_ptr(), kv_lens.data_ptr(),
-        batch, t, *table, *c, None if status is None else status.data_ptr()))
-    _check(rc, "mla_paged_append")
+            q, o = q_rope.data_ptr(), q_out.data_ptr()
+    rc = _call(dev, stream, (_lib or load()).mla_paged_append,
+               latent.data_ptr(), ls[0] if t > 1 else 512, k_rope.data_ptr(), ks[0] if t > 1 else 64,
+               None if norm_weight is None else _whole(norm_weight, bf16, dev, (512,), "norm_weight"), norm_eps,
+               q, qs[0], qs[1], o, os_[0], os_[1], heads, rope, angles, rope_style,
+               None if positions is None else _whole(positions, i32, dev, (t,), "positions"), indptr, lens,
+               batch, t, *table, *c, _status(status, dev))
+    if rc != MT_OK:
+        _check(rc, "mla_paged_append")
 
 
 def mla_paged_decode_workspace_bytes(batch, heads):
@@ -427,18 +429,14 @@ def mla_paged_decode(q, cache, block_table, kv_lens, sm_scale, out, lse, workspa
     [B, H, 576] over the first kv_lens[b] positions of request b's pages;
     out [B, H, 512] bf16 and lse [B, H] fp32. workspace: uint8, at least
     mla_paged_decode_workspace_bytes(B, H)."""
-    c, table, batch, dev = _paged(cache, block_table, kv_lens)
-    _strided(q, torch.bfloat16, 3, "q", dev)
-    heads = q.shape[1]
-    if tuple(q.shape) != (batch, heads, 576):
-        raise MlaTreeError("q must be [batch, heads, 576]")
-    _whole(out, torch.bfloat16, (batch, heads, 512), "out", dev)
-    _whole(lse, torch.float32, (batch, heads), "lse", dev)
-    _whole(workspace, torch.uint8, (workspace.numel(),), "workspace", dev)
-    if status is not None:
-        _strided(status, torch.int32, status.dim(), "status", dev)
-    rc = _call(dev, stream, load().mla_paged_decode, (
-        q.data_ptr(), q.stride(0) if batch > 1 else heads * 576, q.stride(1) if heads > 1 else 576, *c, *table,
-        kv_lens.data_ptr(), batch, heads, sm_scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), None if status is None else status.data_ptr()))
-    _check(rc, "mla_paged_decode")
+    c, table, lens, batch, dev = _paged(cache, block_table, kv_lens)
+    heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() > 1 else 0
+    qs = _strided(q, torch.bfloat16, dev, (batch, heads, 576), "q")
+    nbytes = workspace.numel() if isinstance(workspace, torch.Tensor) else 0
+    rc = _call(dev, stream, (_lib or load()).mla_paged_decode,
+               q.data_ptr(), qs[0] if batch > 1 else heads * 576, qs[1] if heads > 1 else 576, *c, *table, lens,
+               batch, heads, sm_scale, _whole(out, torch.bfloat16, dev, (batch, heads, 512), "out"),
+               _whole(lse, torch.float32, dev, (batch, heads), "lse"),
+               _whole(workspace, torch.uint8, dev, (nbytes,), "workspace"), nbytes, _status(status, dev))
+    if rc != MT_OK:
+        _check(rc, "mla_paged_decode")

@@ -24,8 +24,9 @@
 // itself. A request inside one share is finished in place; others leave fp32
 // partials, at most two per CTA, for the merge kernel.
 //
-// Roles (192 threads): four softmax warps (one per TMEM lane quarter), a TMA
-// producer warp, an MMA warp that owns TMEM. Every wait is time-bounded: a
+// Roles (224 threads): four softmax warps (one per TMEM lane quarter), a TMA
+// producer warp, a warp for each of the two products (the first owns TMEM).
+// Every wait is time-bounded: a
 // timeout sets MT_DEV_TIMEOUT, nothing more is issued, what is in flight is
 // drained and TMEM released.
 #include <cuda.h>
@@ -45,9 +46,9 @@ namespace ptc {
 using namespace sm100;
 
 constexpr int kTile = 64;                     // keys per tile
-constexpr int kThreads = 192;
+constexpr int kThreads = 224;
 constexpr int kSoft = 128;                    // softmax threads: warps 0-3
-constexpr int kProducerWarp = 4, kMmaWarp = 5;
+constexpr int kProducerWarp = 4, kQkWarp = 5, kPvWarp = 6;
 constexpr int kChunk = kTile * 128;           // 64 keys x 64 dims, 128-byte rows, 128B swizzle
 constexpr int kStage = 9 * kChunk;            // a tile: 8 latent chunks, the rope chunk
 constexpr int kStages = 2;
@@ -61,8 +62,9 @@ constexpr uint64_t kDrainNs = 100000000ull;
 constexpr unsigned kFull = 0xffffffffu;
 
 enum {
-  B_Q_FULL, B_Q_EMPTY, B_P_FULL, B_P_EMPTY, B_O_EMPTY, B_DRAIN,
-  B_S_FULL,                                   // x 2
+  B_Q_FULL, B_Q_EMPTY, B_P_FULL, B_P_EMPTY, B_O_EMPTY,
+  B_DRAIN,                                    // x 2: one per MMA warp
+  B_S_FULL = B_DRAIN + 2,                     // x 2
   B_S_EMPTY = B_S_FULL + 2,                   // x 2
   B_KV_FULL = B_S_EMPTY + 2,                  // x kStages x kGroups
   B_KV_EMPTY = B_KV_FULL + kStages * kGroups,
@@ -77,9 +79,9 @@ struct Lay {
   static constexpr int kP = kKV + kStages * kStage;     // [N heads][64 keys] bf16, 128B swizzle
   static constexpr int kBars = kP + N * 128;
   static constexpr int kMask = kBars + kNumBars * 8;    // per stage: the tile's visible keys
-  static constexpr int kPlan = kMask + kStages * 8;     // 8 x int64
-  static constexpr int kMisc = kPlan + 8 * 8;           // tmem base, abort flag
-  static constexpr int kRed = kMisc + 16;               // [4][N] fp32
+  static constexpr int kPlan = kMask + kStages * 8;     // 10 x int64
+  static constexpr int kMisc = kPlan + 10 * 8;          // tmem base, abort flag
+  static constexpr int kRed = (kMisc + 8 + 15) / 16 * 16;  // [4][N] fp32
   static constexpr int kVec = kRed + 4 * N * 4;         // [N] fp32
   static constexpr int kUsed = kVec + N * 4;
   static constexpr int kBytes = kUsed + 1024;           // slack for aligning the base
@@ -147,6 +149,24 @@ __device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t a, uint3
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a),
                "r"(b), "r"(c), "r"(d)
                : "memory");
+}
+
+// The MMA and commit of the shared helpers for a converged warp: the lane
+// that elect.sync picks issues them (the same lane every time, so a commit
+// covers the MMAs before it).
+__device__ __forceinline__ void mma_bf16_ss_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                  uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
+      : "memory");
 }
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -250,13 +270,13 @@ __device__ Walk make_plan(const Params& p, int team, int64_t* sh, int64_t* share
     }
     const int64_t at = off + inc - u;
     if (u > 0 && at <= r.s && r.s < at + u) {
-      sh[6] = b;
-      sh[7] = at;
+      sh[kW] = b;
+      sh[kW + 1] = at;
     }
   }
   __syncthreads();
-  r.b = (int)sh[6];
-  r.o = sh[7];
+  r.b = (int)sh[kW];
+  r.o = sh[kW + 1];
   return r;
 }
 
@@ -282,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int team = blockIdx.x / p.groups, grp = blockIdx.x % p.groups;
   const uint64_t limit = p.limit_ns;
 
-  if (warp == kMmaWarp) {
+  if (warp == kQkWarp) {
     tmem_alloc(tmem_slot, L::kCols);
     tmem_relinquish();
   } else if (tid == 0) {
@@ -386,69 +406,91 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t st = 0; st < kStages; ++st)
           if (cnt[g] > st) mbar_drain(&bars[B_KV_FULL + st * kGroups + g], ((cnt[g] - 1 - st) >> 1) & 1, kDrainNs);
     }
-  } else if (warp == kMmaWarp) {
-    // ----------------------------------------------------------------- MMA
-    if (lane == 0) {
-      constexpr uint32_t id_qk = idesc_bf16(kTile, N, 0, 0), id_pv = idesc_bf16(128, N, 1, 0);
-      const uint64_t dk = smem_desc(smem_u32(sm + L::kKV), 16, 1024, kSwizzle128B);
-      const uint64_t dv = smem_desc(smem_u32(sm + L::kKV), kChunk, 1024, kSwizzle128B);
-      const uint64_t dq = smem_desc(smem_u32(sm + L::kQ), 16, 1024, kSwizzle128B);
-      const uint64_t dp = smem_desc(smem_u32(sm + L::kP), 16, 1024, kSwizzle128B);
-      uint32_t it = 0, pieces = 0;
-      bool dead = false;
-      auto qk = [&](uint32_t i, bool last) {
-        const uint32_t st = i & 1, ph = (i >> 1) & 1;
+  } else if (warp == kQkWarp) {
+    // --------------------------------------------------------------- S = QK
+    // The MMA warps run converged and elect a lane per instruction: issued
+    // from a one-lane branch an MMA takes 48 cycles and more, from uniform
+    // code the tensor core's own time (25 to 35 cycles at M = 64, N = 16 to 64).
+    constexpr uint32_t idesc = idesc_bf16(kTile, N, 0, 0);
+    const uint64_t dk = smem_desc(smem_u32(sm + L::kKV), 16, 1024, kSwizzle128B);
+    const uint64_t dq = smem_desc(smem_u32(sm + L::kQ), 16, 1024, kSwizzle128B);
+    uint32_t it = 0, pieces = 0;
+    bool dead = false;
+    auto wait = [&](int bar, uint32_t parity) {
+      if (!dead) dead = __any_sync(kFull, !mbar_wait<false>(&bars[bar], parity, abort, limit));
+    };
+    while (!dead && next_piece(a, walk, pc)) {
+      const int n = __shfl_sync(kFull, pc.t1 - pc.t0, 0);
+      if (n <= 0) continue;
+      wait(B_Q_FULL, pieces & 1);
+      for (int j = 0; j < n && !dead; ++j, ++it) {
+        const uint32_t st = it & 1, ph = (it >> 1) & 1;
+        wait(B_S_EMPTY + st, ph ^ 1);
+        const uint64_t dks = dk + ((st * kStage) >> 4);
         const uint32_t d = tmem + L::kS + st * N;
-        dead = !mbar_wait<false>(&bars[B_S_EMPTY + st], ph ^ 1, abort, limit);
 #pragma unroll
         for (int gi = 0; gi < kGroups; ++gi) {
           const int g = gi == 0 ? 4 : gi - 1;
-          if (!dead) dead = !mbar_wait<false>(&bars[B_KV_FULL + st * kGroups + g], ph, abort, limit);
-          if (dead) return;
+          wait(B_KV_FULL + st * kGroups + g, ph);
+          if (dead) break;
           tc_fence_after();
 #pragma unroll
           for (int k = 0; k < (g == 4 ? 4 : 8); ++k) {
             const int c = 2 * g + (k >> 2);
-            mma_bf16_ss(d, dk + ((st * kStage + c * kChunk + 32 * (k & 3)) >> 4),
-                        dq + ((c * N * 128 + 32 * (k & 3)) >> 4), id_qk, gi > 0 || k > 0);
+            mma_bf16_ss_elect(d, dks + ((c * kChunk + 32 * (k & 3)) >> 4), dq + ((c * N * 128 + 32 * (k & 3)) >> 4),
+                              idesc, gi > 0 || k > 0);
           }
         }
-        mma_commit(&bars[B_S_FULL + st]);
-        mma_commit(&bars[B_KV_EMPTY + st * kGroups + 4]);
-        if (last) mma_commit(&bars[B_Q_EMPTY]);
-      };
-      while (!dead && next_piece(a, walk, pc)) {
-        const int n = pc.t1 - pc.t0;
-        if (n <= 0) continue;
-        dead = !mbar_wait<false>(&bars[B_Q_FULL], pieces & 1, abort, limit);
         if (dead) break;
-        qk(it, n == 1);
-        for (int j = 0; j < n && !dead; ++j, ++it) {
-          if (j + 1 < n) qk(it + 1, j + 2 == n);
-          if (dead) break;
-          if (j == 0) dead = !mbar_wait<false>(&bars[B_O_EMPTY], (pieces & 1) ^ 1, abort, limit);
-          if (!dead) dead = !mbar_wait<false>(&bars[B_P_FULL], it & 1, abort, limit);
-          if (dead) break;
-          tc_fence_after();
-          const uint32_t st = it & 1;
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              mma_bf16_ss(tmem + L::kO + m * N, dv + ((st * kStage + m * 2 * kChunk + k * 2048) >> 4),
-                          dp + ((32 * k) >> 4), id_pv, j > 0 || k > 0);
-            mma_commit(&bars[B_KV_EMPTY + st * kGroups + m]);
-          }
-          mma_commit(&bars[B_P_EMPTY]);
-        }
-        ++pieces;
+        mma_commit_elect(&bars[B_S_FULL + st]);
+        mma_commit_elect(&bars[B_KV_EMPTY + st * kGroups + 4]);
+        if (j + 1 == n) mma_commit_elect(&bars[B_Q_EMPTY]);
       }
-      if (dead) {
-        mma_commit(&bars[B_DRAIN]);
-        mbar_drain(&bars[B_DRAIN], 0, kDrainNs);
-      }
+      ++pieces;
     }
-    __syncwarp();
+    if (dead) {
+      mma_commit_elect(&bars[B_DRAIN]);
+      mbar_drain(&bars[B_DRAIN], 0, kDrainNs);
+    }
+  } else if (warp == kPvWarp) {
+    // ----------------------------------------------------------- O += V^T P
+    // A warp of its own: P.V of a tile must not queue behind QK of the next,
+    // whose keys may still be on their way into the other stage.
+    constexpr uint32_t idesc = idesc_bf16(128, N, 1, 0);
+    const uint64_t dv = smem_desc(smem_u32(sm + L::kKV), kChunk, 1024, kSwizzle128B);
+    const uint64_t dp = smem_desc(smem_u32(sm + L::kP), 16, 1024, kSwizzle128B);
+    uint32_t it = 0, pieces = 0;
+    bool dead = false;
+    auto wait = [&](int bar, uint32_t parity) {
+      if (!dead) dead = __any_sync(kFull, !mbar_wait<false>(&bars[bar], parity, abort, limit));
+    };
+    while (!dead && next_piece(a, walk, pc)) {
+      const int n = __shfl_sync(kFull, pc.t1 - pc.t0, 0);
+      if (n <= 0) continue;
+      wait(B_O_EMPTY, (pieces & 1) ^ 1);
+      for (int j = 0; j < n && !dead; ++j, ++it) {
+        const uint32_t st = it & 1;
+        wait(B_KV_FULL + st * kGroups + 3, (it >> 1) & 1);
+        wait(B_P_FULL, it & 1);
+        if (dead) break;
+        tc_fence_after();
+        const uint64_t dvs = dv + ((st * kStage) >> 4);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            mma_bf16_ss_elect(tmem + L::kO + m * N, dvs + ((m * 2 * kChunk + k * 2048) >> 4), dp + ((32 * k) >> 4),
+                              idesc, j > 0 || k > 0);
+          mma_commit_elect(&bars[B_KV_EMPTY + st * kGroups + m]);
+        }
+        mma_commit_elect(&bars[B_P_EMPTY]);
+      }
+      ++pieces;
+    }
+    if (dead) {
+      mma_commit_elect(&bars[B_DRAIN + 1]);
+      mbar_drain(&bars[B_DRAIN + 1], 0, kDrainNs);
+    }
   } else {
     // ------------------------------------------------------ softmax, epilogue
     constexpr int kC = N / 4;                   // columns (heads) of a thread: 8 i + 2 (lane % 4) + e
@@ -641,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort) flag(a.status, MT_DEV_TIMEOUT);
-  if (warp == kMmaWarp) {
+  if (warp == kQkWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kCols);
   }
