@@ -24,8 +24,8 @@
 // itself. A request inside one share is finished in place; others leave fp32
 // partials, at most two per CTA, for the merge kernel.
 //
-// Roles (224 threads): four softmax warps (one per TMEM lane quarter), a TMA
-// producer warp, a warp for each of the two products (the first owns TMEM).
+// Roles (352 threads): eight softmax warps (a TMEM lane quarter and half of
+// the heads each), a TMA producer warp, a warp for each of the two products (the first owns TMEM).
 // Every wait is time-bounded: a
 // timeout sets MT_DEV_TIMEOUT, nothing more is issued, what is in flight is
 // drained and TMEM released.
@@ -46,15 +46,16 @@ namespace ptc {
 using namespace sm100;
 
 constexpr int kTile = 64;                     // keys per tile
-constexpr int kThreads = 224;
-constexpr int kSoft = 128;                    // softmax threads: warps 0-3
-constexpr int kProducerWarp = 4, kQkWarp = 5, kPvWarp = 6;
-constexpr int kChunk = kTile * 128;           // 64 keys x 64 dims, 128-byte rows, 128B swizzle
-constexpr int kStage = 9 * kChunk;            // a tile: 8 latent chunks, the rope chunk
+constexpr int kSoftWarps = 8;                 // warps 0-7
+constexpr int kProducerWarp = 8, kQkWarp = 9, kPvWarp = 10;
+constexpr int kThreads = 352;
+// A tile is eight groups of eight keys, each [9 chunks of 64 dims][8 keys][128
+// bytes] with 128-byte swizzle: 9216 bytes that are one contiguous piece of a
+// page in memory, so any page size from 8 on loads alike.
+constexpr int kGroup = 9 * 1024;
+constexpr int kStage = 8 * kGroup;
 constexpr int kStages = 2;
-// Loads and releases go by groups of a stage: latent chunk pairs 0-3 (the 128
-// value dims of one P.V MMA row block) and the rope chunk 4.
-constexpr int kGroups = 5;
+constexpr int kQuarters = 4;                  // a stage is released by quarters, two groups = one P.V K step
 constexpr float kRescale = 8.f;               // log2 of how far a weight may exceed 1
 constexpr int kOverhead = 2;                  // a request's fixed cost, in tiles
 constexpr int kMinShare = 4;                  // smallest share of a team, in tiles
@@ -66,9 +67,9 @@ enum {
   B_DRAIN,                                    // x 2: one per MMA warp
   B_S_FULL = B_DRAIN + 2,                     // x 2
   B_S_EMPTY = B_S_FULL + 2,                   // x 2
-  B_KV_FULL = B_S_EMPTY + 2,                  // x kStages x kGroups
-  B_KV_EMPTY = B_KV_FULL + kStages * kGroups,
-  kNumBars = B_KV_EMPTY + kStages * kGroups
+  B_KV_FULL = B_S_EMPTY + 2,                  // x kStages
+  B_KV_EMPTY = B_KV_FULL + kStages,           // x kStages x kQuarters
+  kNumBars = B_KV_EMPTY + kStages * kQuarters
 };
 
 // Shared memory from a 1024-byte aligned base, TMEM columns.
@@ -79,8 +80,8 @@ struct Lay {
   static constexpr int kP = kKV + kStages * kStage;     // [N heads][64 keys] bf16, 128B swizzle
   static constexpr int kBars = kP + N * 128;
   static constexpr int kMask = kBars + kNumBars * 8;    // per stage: the tile's visible keys
-  static constexpr int kPlan = kMask + kStages * 8;     // 10 x int64
-  static constexpr int kMisc = kPlan + 10 * 8;          // tmem base, abort flag
+  static constexpr int kPlan = kMask + kStages * 8;     // 14 x int64
+  static constexpr int kMisc = kPlan + 14 * 8;          // tmem base, abort flag
   static constexpr int kRed = (kMisc + 8 + 15) / 16 * 16;  // [4][N] fp32
   static constexpr int kVec = kRed + 4 * N * 4;         // [N] fp32
   static constexpr int kUsed = kVec + N * 4;
@@ -103,17 +104,41 @@ struct Params {
 
 // ---------------------------------------------------------------- PTX forms
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
-                                            uint64_t* bar) {
+// TMA tile loads and an arrival with its byte count, from one lane of a converged warp.
+__device__ __forceinline__ void tma_load_4d_elect(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                                  uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];\n}\n" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_5d_elect(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                                  int v, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void expect_elect(uint64_t* bar, uint32_t tx) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(smem_u32(bar)),
+      "r"(tx)
       : "memory");
 }
 
 // 16 TMEM lanes x 8 K columns: thread t gets, for every 8 columns i, rows t / 4
 // (r[4i], r[4i+1]) and t / 4 + 8 (r[4i+2], r[4i+3]), columns 8 i + 2 (t % 4) + {0, 1}.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -129,25 +154,17 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) 
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
-        "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
-        "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-
 // Four 8x8 blocks of 16-bit elements, each stored transposed: lane 8 i + j
 // gives the address of block i's column j, which becomes 16 bytes there.
 __device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a),
                "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// Two such blocks; lanes 0-15 give the addresses.
+__device__ __forceinline__ void stmatrix2_trans(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b)
                : "memory");
 }
 
@@ -227,33 +244,30 @@ __device__ __forceinline__ int64_t warp_sum64(int64_t v) {
   return v;
 }
 
-// The share size and where this team's share starts, by all threads.
+// The share size and where this team's share starts, by all threads. A batch
+// of up to kThreads requests takes one round of loads and two barriers.
 __device__ Walk make_plan(const Params& p, int team, int64_t* sh, int64_t* share_out) {
   const DecodeArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kW = kThreads / 32;
-  int64_t mine = 0;
-  for (int b = tid; b < a.batch; b += kThreads) mine += kOverhead + tiles_of(a, __ldg(a.kv.lens + b));
-  mine = warp_sum64(mine);
-  if (lane == 0) sh[warp] = mine;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kW; ++w) total += sh[w];
-  int64_t share = (total + p.nteams - 1) / p.nteams;
-  if (share < kMinShare + kOverhead) share = kMinShare + kOverhead;
-  *share_out = share;
-  Walk r;
-  r.s = team * share;
-  r.e = r.s + share;
-  r.b = a.batch;
-  r.o = total;
-  if (r.s >= total) return r;  // the same for all threads
-  int64_t run = 0;
-  for (int base = 0; run <= r.s; base += kThreads) {
+  auto units = [&](int b) { return b < a.batch ? (int64_t)kOverhead + tiles_of(a, __ldg(a.kv.lens + b)) : 0; };
+  int64_t rest = 0;  // requests behind the first kThreads
+  if (a.batch > kThreads) {
+    for (int b = kThreads + tid; b < a.batch; b += kThreads) rest += units(b);
+    rest = warp_sum64(rest);
+    if (lane == 0) sh[warp] = rest;
     __syncthreads();
-    const int b = base + tid;
-    const int64_t u = b < a.batch ? kOverhead + tiles_of(a, __ldg(a.kv.lens + b)) : 0;
+    rest = 0;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) rest += sh[w];
+    __syncthreads();
+  }
+  Walk r;
+  r.b = a.batch;
+  r.o = r.s = r.e = 0;
+  int64_t run = 0;
+  for (int base = 0; base < a.batch; base += kThreads) {
+    const int64_t u = units(base + tid);
     int64_t inc = u;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -262,19 +276,29 @@ __device__ Walk make_plan(const Params& p, int team, int64_t* sh, int64_t* share
     }
     if (lane == 31) sh[warp] = inc;
     __syncthreads();
-    int64_t off = run;
+    int64_t at = run + inc - u, sum = 0;
 #pragma unroll
     for (int w = 0; w < kW; ++w) {
-      if (w < warp) off += sh[w];
-      run += sh[w];
+      if (w < warp) at += sh[w];
+      sum += sh[w];
     }
-    const int64_t at = off + inc - u;
+    if (base == 0) {
+      const int64_t total = sum + rest;
+      int64_t share = (total + p.nteams - 1) / p.nteams;
+      if (share < kMinShare + kOverhead) share = kMinShare + kOverhead;
+      *share_out = share;
+      r.s = team * share;
+      r.e = r.s + share;
+      if (r.s >= total) return r;  // nothing for this team (the same for all threads)
+    }
+    run += sum;
     if (u > 0 && at <= r.s && r.s < at + u) {
-      sh[kW] = b;
+      sh[kW] = base + tid;
       sh[kW + 1] = at;
     }
+    __syncthreads();
+    if (run > r.s) break;
   }
-  __syncthreads();
   r.b = (int)sh[kW];
   r.o = sh[kW + 1];
   return r;
@@ -285,7 +309,7 @@ __device__ Walk make_plan(const Params& p, int team, int64_t* sh, int64_t* share
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_decode_tc_kernel(const Params p, const __grid_constant__ CUtensorMap tq,
-                           const __grid_constant__ CUtensorMap tpair, const __grid_constant__ CUtensorMap tone) {
+                           const __grid_constant__ CUtensorMap tkv) {
   using L = Lay<N>;
   extern __shared__ uint8_t raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
@@ -308,15 +332,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (tid == 0) {
     *abort = 0;
     for (int i = 0; i < kNumBars; ++i) mbar_init(&bars[i], 1);
-    mbar_init(&bars[B_P_FULL], 4);
-    mbar_init(&bars[B_O_EMPTY], 4);
-    mbar_init(&bars[B_S_EMPTY], 4);
-    mbar_init(&bars[B_S_EMPTY + 1], 4);
+    mbar_init(&bars[B_P_FULL], kSoftWarps);
+    mbar_init(&bars[B_O_EMPTY], kSoftWarps);
+    mbar_init(&bars[B_S_EMPTY], kSoftWarps);
+    mbar_init(&bars[B_S_EMPTY + 1], kSoftWarps);
     fence_mbar_init_cluster();
   } else if (tid == kProducerWarp * 32) {
     prefetch_tmap(&tq);
-    prefetch_tmap(&tpair);
-    prefetch_tmap(&tone);
+    prefetch_tmap(&tkv);
   }
   tc_fence_before();
   __syncthreads();
@@ -330,81 +353,76 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
     const int P = 1 << p.page_shift;
-    const int rp = P < kTile ? P : kTile;       // rows a page gives to a tile
-    const int npg = kTile / rp;                 // pages a tile touches
+    const int per = P >= 16 ? 2 : 1;            // groups of a box
     const uint32_t kv0 = smem_u32(sm + L::kKV);
     const bool drop = p.drop_team >= 0 && team >= p.drop_team;
-    uint32_t it = 0, pieces = 0, cnt[kGroups] = {0, 0, 0, 0, 0}, cntq = 0;
+    uint32_t it = 0, pieces = 0;
     bool dead = drop;
+    auto wait = [&](int bar, uint32_t parity) {
+      if (!dead) dead = __any_sync(kFull, !mbar_wait<false>(&bars[bar], parity, abort, limit));
+    };
     while (!dead && next_piece(a, walk, pc)) {
       if (pc.t1 <= pc.t0) continue;
-      dead = __any_sync(kFull, !mbar_wait<false>(&bars[B_Q_EMPTY], (pieces & 1) ^ 1, abort, limit));
+      wait(B_Q_EMPTY, (pieces & 1) ^ 1);
       if (dead) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bars[B_Q_FULL], N * 9 * 128);
-        tma_load_4d(smem_u32(sm + L::kQ), &tq, 0, grp * N, 0, pc.b, &bars[B_Q_FULL]);
-      }
-      ++cntq;
+      expect_elect(&bars[B_Q_FULL], N * 9 * 128);
+      tma_load_4d_elect(smem_u32(sm + L::kQ), &tq, 0, grp * N, 0, pc.b, &bars[B_Q_FULL]);
       ++pieces;
       const int32_t* table = a.kv.table + pc.b * a.kv.table_stride;
-      auto entry = [&](int t) {  // page of this lane's part of tile t, -1: none
-        const int64_t row = (int64_t)t * kTile + lane * rp;
-        return lane < npg && row < pc.len ? __ldg(table + (row >> p.page_shift)) : -1;
+      // lane l looks after group l of a tile: its page, -1 behind the length
+      auto entry = [&](int t) {
+        const int64_t row = (int64_t)t * kTile + lane * 8;
+        return lane < 8 && row < pc.len ? __ldg(table + (row >> p.page_shift)) : -1;
       };
       int page_next = entry(pc.t0);
-      bool asked_next = lane < npg && (int64_t)pc.t0 * kTile + lane * rp < pc.len;
       for (int t = pc.t0; t < pc.t1 && !dead; ++t, ++it) {
         const int st = it & 1, ph = (it >> 1) & 1;
         const int page = page_next;
-        const bool asked = asked_next;
-        if (t + 1 < pc.t1) {
-          page_next = entry(t + 1);
-          asked_next = lane < npg && (int64_t)(t + 1) * kTile + lane * rp < pc.len;
-        }
+        if (t + 1 < pc.t1) page_next = entry(t + 1);
+        const int64_t row = (int64_t)t * kTile + lane * 8;
+        const bool asked = lane < 8 && row < pc.len;
         const bool ok = asked && page >= 0 && page < a.kv.num_pages;
         if (asked && !ok && grp == 0) flag(a.status, MT_DEV_BAD_SLOT);
         const unsigned okm = __ballot_sync(kFull, ok);
-        // visible keys: pages that are there, positions below the length
+        // visible keys: groups whose page is there, positions below the length
         uint64_t vis = 0;
-        if (ok) vis = (rp == 64 ? ~0ull : (1ull << rp) - 1) << (lane * rp & 63);
-        uint32_t lo = __reduce_or_sync(kFull, (uint32_t)vis), hi = __reduce_or_sync(kFull, (uint32_t)(vis >> 32));
-        vis = (uint64_t)hi << 32 | lo;
+#pragma unroll
+        for (int g = 0; g < 8; ++g)
+          if (okm >> g & 1) vis |= 0xffull << (8 * g);
         const int64_t left = (int64_t)pc.len - (int64_t)t * kTile;
         if (left < kTile) vis &= (1ull << left) - 1;
-        const uint32_t chunk_bytes = (uint32_t)__popc(okm) * rp * 128;
-        const int row = (int)(((int64_t)t * kTile) & (P - 1));
+        uint64_t* full = &bars[B_KV_FULL + st];
+        // a box of two groups lies in one page: they are good or bad together,
+        // but the second may start behind the length
+        uint32_t boxes = 0;
 #pragma unroll
-        for (int gi = 0; gi < kGroups; ++gi) {
-          const int g = gi == 0 ? 4 : gi - 1;  // rope first: its slot is the first that a tile frees
-          if (!dead)
-            dead = __any_sync(kFull, !mbar_wait<false>(&bars[B_KV_EMPTY + st * kGroups + g], ph ^ 1, abort, limit));
-          if (dead) continue;
-          uint64_t* full = &bars[B_KV_FULL + st * kGroups + g];
-          if (lane == 0) {
-            // the last pair's release says that the softmax is done with the old mask
-            if (g == 3) vmask[st] = vis;
-            if (chunk_bytes) mbar_arrive_expect_tx(full, g == 4 ? chunk_bytes : 2 * chunk_bytes);
-            else mbar_arrive(full);
+        for (int g = 0; g < 8; ++g)
+          if ((g & (per - 1)) == 0) boxes += okm >> g & 1;
+#pragma unroll
+        for (int q = 0; q < kQuarters; ++q) {
+          wait(B_KV_EMPTY + st * kQuarters + q, ph ^ 1);
+          if (dead) break;
+          if (q == 0) {  // every release of the stage came after the softmax had read its old mask
+            if (lane == 0) vmask[st] = vis;
+            __syncwarp();
+            expect_elect(full, boxes * per * kGroup);
           }
-          __syncwarp();
-          ++cnt[g];
-          const uint32_t dst = kv0 + st * kStage + 2 * g * kChunk;
-          if (P >= kTile) {
-            if (lane == 0 && ok) tma_load_4d(dst, g == 4 ? &tone : &tpair, 0, row, 2 * g, page, full);
-          } else {
-            const int pg = lane & (npg - 1), ch = lane / npg;
-            const int id = __shfl_sync(kFull, page, pg);
-            if (ch < (g == 4 ? 1 : 2) && (okm >> pg & 1))
-              tma_load_4d(dst + ch * kChunk + pg * rp * 128, &tone, 0, 0, 2 * g + ch, id, full);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int g = 2 * q + h;
+            const int id = __shfl_sync(kFull, page, g);
+            if ((h == 0 || per == 1) && (okm >> g & 1))
+              tma_load_5d_elect(kv0 + st * kStage + g * kGroup, &tkv, 0, 0, 0,
+                                (int)((((int64_t)t * kTile) & (P - 1)) >> 3) + (g & ((P >> 3) - 1)), id, full);
           }
         }
       }
     }
-    if (*abort) {  // let the copies in flight land
-      if (cntq) mbar_drain(&bars[B_Q_FULL], (cntq - 1) & 1, kDrainNs);
-      for (int g = 0; g < kGroups; ++g)
-        for (uint32_t st = 0; st < kStages; ++st)
-          if (cnt[g] > st) mbar_drain(&bars[B_KV_FULL + st * kGroups + g], ((cnt[g] - 1 - st) >> 1) & 1, kDrainNs);
+    if (*abort) {  // let the copies in flight land (a phase that no copy ends runs out here)
+      if (pieces) mbar_drain(&bars[B_Q_FULL], (pieces - 1) & 1, kDrainNs);
+      for (uint32_t back = 0; back < kStages; ++back)
+        if (it > back)  // `it` counts the tile that was broken off
+          mbar_drain(&bars[B_KV_FULL + ((it - 1 - back) & 1)], ((it - 1 - back) >> 1) & 1, kDrainNs);
     }
   } else if (warp == kQkWarp) {
     // --------------------------------------------------------------- S = QK
@@ -412,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // from a one-lane branch an MMA takes 48 cycles and more, from uniform
     // code the tensor core's own time (25 to 35 cycles at M = 64, N = 16 to 64).
     constexpr uint32_t idesc = idesc_bf16(kTile, N, 0, 0);
-    const uint64_t dk = smem_desc(smem_u32(sm + L::kKV), 16, 1024, kSwizzle128B);
+    const uint64_t dk = smem_desc(smem_u32(sm + L::kKV), 16, kGroup, kSwizzle128B);
     const uint64_t dq = smem_desc(smem_u32(sm + L::kQ), 16, 1024, kSwizzle128B);
     uint32_t it = 0, pieces = 0;
     bool dead = false;
@@ -426,24 +444,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < n && !dead; ++j, ++it) {
         const uint32_t st = it & 1, ph = (it >> 1) & 1;
         wait(B_S_EMPTY + st, ph ^ 1);
+        wait(B_KV_FULL + st, ph);
+        if (dead) break;
+        tc_fence_after();
         const uint64_t dks = dk + ((st * kStage) >> 4);
         const uint32_t d = tmem + L::kS + st * N;
 #pragma unroll
-        for (int gi = 0; gi < kGroups; ++gi) {
-          const int g = gi == 0 ? 4 : gi - 1;
-          wait(B_KV_FULL + st * kGroups + g, ph);
-          if (dead) break;
-          tc_fence_after();
+        for (int c = 0; c < 9; ++c)
 #pragma unroll
-          for (int k = 0; k < (g == 4 ? 4 : 8); ++k) {
-            const int c = 2 * g + (k >> 2);
-            mma_bf16_ss_elect(d, dks + ((c * kChunk + 32 * (k & 3)) >> 4), dq + ((c * N * 128 + 32 * (k & 3)) >> 4),
-                              idesc, gi > 0 || k > 0);
-          }
-        }
-        if (dead) break;
+          for (int k = 0; k < 4; ++k)
+            mma_bf16_ss_elect(d, dks + ((c * 1024 + 32 * k) >> 4), dq + ((c * N * 128 + 32 * k) >> 4), idesc,
+                              c > 0 || k > 0);
         mma_commit_elect(&bars[B_S_FULL + st]);
-        mma_commit_elect(&bars[B_KV_EMPTY + st * kGroups + 4]);
         if (j + 1 == n) mma_commit_elect(&bars[B_Q_EMPTY]);
       }
       ++pieces;
@@ -457,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A warp of its own: P.V of a tile must not queue behind QK of the next,
     // whose keys may still be on their way into the other stage.
     constexpr uint32_t idesc = idesc_bf16(128, N, 1, 0);
-    const uint64_t dv = smem_desc(smem_u32(sm + L::kKV), kChunk, 1024, kSwizzle128B);
+    const uint64_t dv = smem_desc(smem_u32(sm + L::kKV), 1024, kGroup, kSwizzle128B);
     const uint64_t dp = smem_desc(smem_u32(sm + L::kP), 16, 1024, kSwizzle128B);
     uint32_t it = 0, pieces = 0;
     bool dead = false;
@@ -470,18 +482,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait(B_O_EMPTY, (pieces & 1) ^ 1);
       for (int j = 0; j < n && !dead; ++j, ++it) {
         const uint32_t st = it & 1;
-        wait(B_KV_FULL + st * kGroups + 3, (it >> 1) & 1);
+        wait(B_KV_FULL + st, (it >> 1) & 1);
         wait(B_P_FULL, it & 1);
         if (dead) break;
         tc_fence_after();
         const uint64_t dvs = dv + ((st * kStage) >> 4);
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
+        for (int k = 0; k < kQuarters; ++k) {
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_bf16_ss_elect(tmem + L::kO + m * N, dvs + ((m * 2 * kChunk + k * 2048) >> 4), dp + ((32 * k) >> 4),
+          for (int m = 0; m < 4; ++m)
+            mma_bf16_ss_elect(tmem + L::kO + m * N, dvs + ((k * 2 * kGroup + m * 2048) >> 4), dp + ((32 * k) >> 4),
                               idesc, j > 0 || k > 0);
-          mma_commit_elect(&bars[B_KV_EMPTY + st * kGroups + m]);
+          mma_commit_elect(&bars[B_KV_EMPTY + st * kQuarters + k]);
         }
         mma_commit_elect(&bars[B_P_EMPTY]);
       }
@@ -493,14 +505,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------ softmax, epilogue
-    constexpr int kC = N / 4;                   // columns (heads) of a thread: 8 i + 2 (lane % 4) + e
+    // Warp w serves TMEM lane quarter w % 4 and one half of the heads, w / 4;
+    // the halves never wait for one another.
+    constexpr int NC = N / 2;                   // columns (heads) of a warp
+    constexpr int kC = NC / 4;                  // of a thread: 8 i + 2 (lane % 4) + e
+    constexpr int kHalf = kSoftWarps / 2 * 32;
+    const int quad = warp & 3, half = warp >> 2, c0 = half * NC, bar_id = 1 + half;
+    const int htid = quad * 32 + lane;
     const float scale = a.sm_scale * kLog2e;
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    const int r0 = warp * 16 + (lane >> 2);     // this thread's keys of a tile: r0 and r0 + 8
-    const uint32_t pbase = smem_u32(sm + L::kP);
+    const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+    const int r0 = quad * 16 + (lane >> 2);     // this thread's keys of a tile: r0 and r0 + 8
     // stmatrix: lanes 0-7 / 8-15 address keys 0-7 / 8-15 of the warp for heads 0-7, lanes 16-31 for heads 8-15
-    const int sh = (lane & 7) + ((lane >> 4) << 3);
-    const uint32_t paddr = pbase + sh * 128 + (((2 * warp + ((lane >> 3) & 1)) ^ (sh & 7)) << 4);
+    const int sh = c0 + (lane & 7) + (NC >= 16 ? (lane >> 4) << 3 : 0);
+    const uint32_t paddr =
+        smem_u32(sm + L::kP) + sh * 128 + (((2 * quad + ((lane >> 3) & 1)) ^ (sh & 7)) << 4);
+    float* redh = red + c0;                     // [4][N], this half's columns
+    float* vech = vec + c0;
     MergeEntry entry = {0, 0, 0, 0};
     uint32_t it = 0;
     bool dead = false;
@@ -513,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         uint4* dst = reinterpret_cast<uint4*>(a.out + orow * kDv);
-        for (int i = tid; i < nh * (kDv / 8); i += kSoft) dst[i] = make_uint4(0, 0, 0, 0);
+        for (int i = tid; i < nh * (kDv / 8); i += 2 * kHalf) dst[i] = make_uint4(0, 0, 0, 0);
         if (tid < nh) a.lse[orow + tid] = -INFINITY;
         continue;
       }
@@ -526,10 +546,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = pc.t0; t < pc.t1; ++t, ++it) {
         const int st = it & 1, ph = (it >> 1) & 1;
         if (!dead) dead = !mbar_wait<false>(&bars[B_S_FULL + st], ph, abort, limit);
-        if (!dead) dead = !mbar_wait<false>(&bars[B_KV_FULL + st * kGroups + 3], ph, abort, limit);
+        if (!dead) dead = !mbar_wait<false>(&bars[B_KV_FULL + st], ph, abort, limit);
         tc_fence_after();
-        uint32_t s[4 * (N / 8)];
-        tmem_ld_frag(tmem + lane_base + L::kS + st * N, s);
+        uint32_t s[NC / 2];
+        tmem_ld_frag(tmem + lane_base + L::kS + st * N + c0, s);
         const uint64_t vis = vmask[st];
         tmem_ld_wait();
         tmem_regs_ready(s);
@@ -537,9 +557,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_S_EMPTY + st]);
         const bool v0 = vis >> r0 & 1, v1 = vis >> (r0 + 8) & 1;
-        float x[4 * (N / 8)], top = -INFINITY;
+        float x[NC / 2], top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < N / 8; ++i)
+        for (int i = 0; i < NC / 8; ++i)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float y0 = v0 ? __uint_as_float(s[4 * i + e]) * scale : -INFINITY;
@@ -548,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             x[4 * i + 2 + e] = y1;
             top = fmaxf(top, fmaxf(y0, y1) - ref[2 * i + e]);
           }
-        if (bar_any(1, kSoft, top > kRescale)) {
+        if (bar_any(bar_id, kHalf, top > kRescale)) {
           // new references: every head's maximum over the tile's 64 keys
           float f[kC];
 #pragma unroll
@@ -557,40 +577,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
-            if (lane < 4) red[warp * N + 8 * (j >> 1) + 2 * lane + (j & 1)] = m;
+            if (lane < 4) redh[quad * N + 8 * (j >> 1) + 2 * lane + (j & 1)] = m;
           }
-          named_bar_sync(2, kSoft);
+          named_bar_sync(bar_id, kHalf);
 #pragma unroll
           for (int j = 0; j < kC; ++j) {
             const int c = 8 * (j >> 1) + 2 * (lane & 3) + (j & 1);
-            const float m = fmaxf(fmaxf(red[c], red[N + c]), fmaxf(red[2 * N + c], red[3 * N + c]));
+            const float m = fmaxf(fmaxf(redh[c], redh[N + c]), fmaxf(redh[2 * N + c], redh[3 * N + c]));
             const float nr = fmaxf(ref[j], m);
             f[j] = ex2_approx(ref[j] - nr);
             ref[j] = nr;
             l[j] *= f[j];
-            if (warp == 0 && lane < 4) vec[c] = f[j];
+            if (quad == 0 && lane < 4) vech[c] = f[j];
           }
           if (t > pc.t0) {  // the first tile's P.V overwrites O
-            named_bar_sync(2, kSoft);
+            named_bar_sync(bar_id, kHalf);
             if (!dead) dead = !mbar_wait<false>(&bars[B_P_EMPTY], (it & 1) ^ 1, abort, limit);
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < 4 * N; c += 16) {
-              uint32_t o[16];
-              tmem_ld16_nw(tmem + lane_base + L::kO + c, o);
-              tmem_ld_wait();
-              tmem_regs_ready(o);
+            for (int m = 0; m < 4; ++m)
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * vec[(c & (N - 1)) + e]);
-              tmem_st16(tmem + lane_base + L::kO + c, o);
-            }
+              for (int c = 0; c < NC; c += 8) {
+                uint32_t o[8];
+                tmem_ld8_nw(tmem + lane_base + L::kO + m * N + c0 + c, o);
+                tmem_ld_wait();
+                tmem_regs_ready(o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * vech[c + e]);
+                tmem_st8(tmem + lane_base + L::kO + m * N + c0 + c, o);
+              }
             tmem_st_wait();
             tc_fence_before();
           }
         }
-        uint32_t pk[N / 4];  // key r0 at 2 i, key r0 + 8 at 2 i + 1; two heads each
+        uint32_t pk[NC / 4];  // key r0 at 2 i, key r0 + 8 at 2 i + 1; two heads each
 #pragma unroll
-        for (int i = 0; i < N / 8; ++i)
+        for (int i = 0; i < NC / 8; ++i)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float p0 = ex2_approx(x[4 * i + 2 * k] - ref[2 * i]);
@@ -601,16 +623,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             pk[2 * i + k] = *reinterpret_cast<const uint32_t*>(&h);
           }
         if (!dead) dead = !mbar_wait<false>(&bars[B_P_EMPTY], (it & 1) ^ 1, abort, limit);
+        if constexpr (NC == 8) {
+          stmatrix2_trans(paddr, pk[0], pk[1]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < N / 8; i += 2)
-          stmatrix4_trans(paddr + i * 8 * 128, pk[2 * i], pk[2 * i + 1], pk[2 * i + 2], pk[2 * i + 3]);
+          for (int i = 0; i < NC / 8; i += 2)
+            stmatrix4_trans(paddr + i * 8 * 128, pk[2 * i], pk[2 * i + 1], pk[2 * i + 2], pk[2 * i + 3]);
+        }
         if (~vis != 0) {
           // rows that are no keys of this request count with weight 0, but
           // 0 x NaN is NaN: their values are made 0
-          for (int r = tid >> 6; r < kTile; r += kSoft / 64)
+          for (int r = tid >> 6; r < kTile; r += 2 * kHalf / 64)
             if (!(vis >> r & 1))
-              *reinterpret_cast<uint4*>(sm + L::kKV + st * kStage + ((tid & 63) >> 3) * kChunk + r * 128 +
-                                        (tid & 7) * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(sm + L::kKV + st * kStage + (r >> 3) * kGroup + ((tid & 63) >> 3) * 1024 +
+                                        (r & 7) * 128 + (tid & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_async_smem();
         __syncwarp();
@@ -626,40 +652,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         v += __shfl_xor_sync(kFull, v, 16);
         const int c = 8 * (j >> 1) + 2 * (lane & 3) + (j & 1);
         if (lane < 4) {
-          red[warp * N + c] = v;
-          if (warp == 0) vec[c] = ref[j];
+          redh[quad * N + c] = v;
+          if (quad == 0) vech[c] = ref[j];
         }
       }
-      named_bar_sync(2, kSoft);
+      named_bar_sync(bar_id, kHalf);
       const bool starts = pc.t0 == 0, whole = starts && pc.t1 == pc.tiles;
       const int64_t wrow = ((int64_t)(2 * team + (starts ? 1 : 0)) * p.groups + grp) * N;
-      if (tid < N) {
-        const float sum = (red[tid] + red[N + tid]) + (red[2 * N + tid] + red[3 * N + tid]);
-        const float lse = sum != 0.f ? (vec[tid] + log2f(sum)) * kLn2 : -INFINITY;
-        if (tid < nh && !*abort) (whole ? a.lse[orow + tid] : a.ws_lse[wrow + tid]) = lse;
-        red[tid] = sum != 0.f ? 1.f / sum : 0.f;
+      if (htid < NC) {
+        const float sum = (redh[htid] + redh[N + htid]) + (redh[2 * N + htid] + redh[3 * N + htid]);
+        const float lse = sum != 0.f ? (vech[htid] + log2f(sum)) * kLn2 : -INFINITY;
+        if (c0 + htid < nh && !*abort) (whole ? a.lse[orow + c0 + htid] : a.ws_lse[wrow + c0 + htid]) = lse;
+        redh[htid] = sum != 0.f ? 1.f / sum : 0.f;
       }
-      named_bar_sync(2, kSoft);
+      named_bar_sync(bar_id, kHalf);
       if (!dead) dead = !mbar_wait<false>(&bars[B_P_EMPTY], (it - 1) & 1, abort, limit);
       tc_fence_after();
       const bool give_up = __any_sync(kFull, dead || *abort);  // nothing to write
 #pragma unroll 1
-      for (int c = 0; c < 4 * N && !give_up; c += 16) {
-        uint32_t o[16];
-        tmem_ld16_nw(tmem + lane_base + L::kO + c, o);
+      for (int m = 0; m < 4 && !give_up; ++m) {
+        uint32_t o[NC];
+#pragma unroll
+        for (int c = 0; c < NC; c += 8) {
+          uint32_t part[8];
+          tmem_ld8_nw(tmem + lane_base + L::kO + m * N + c0 + c, part);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[c + e] = part[e];
+        }
         tmem_ld_wait();
         tmem_regs_ready(o);
-        const int h0 = c & (N - 1), dim = c / N * 128 + warp * 32 + lane;
+        const int dim = m * 128 + quad * 32 + lane;
         if (whole) {
+          uint16_t* dst = a.out + (orow + c0) * kDv + dim;
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (h0 + e < nh)
-              a.out[(orow + h0 + e) * kDv + dim] =
-                  __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(o[e]) * red[h0 + e]));
+          for (int c = 0; c < NC; ++c)
+            if (c0 + c < nh)
+              dst[c * kDv] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(o[c]) * redh[c]));
         } else {
+          float* dst = a.ws_o + (wrow + c0) * kDv + dim;
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (h0 + e < nh) a.ws_o[(wrow + h0 + e) * kDv + dim] = __uint_as_float(o[e]) * red[h0 + e];
+          for (int c = 0; c < NC; ++c)
+            if (c0 + c < nh) dst[c * kDv] = __uint_as_float(o[c]) * redh[c];
         }
       }
       tc_fence_before();
@@ -708,24 +741,37 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return g_encode;
 }
 
-// 576-wide bf16 rows as [chunk of 64 dims] [row] [chunk] [outer]: a box lays
-// `chunks` chunks of `rows` 128-byte swizzled rows one after another.
-bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t row_stride, int64_t outer,
-              int64_t outer_stride, int box_rows, int box_chunks) {
+// 576-wide bf16 rows as boxes of 128-byte swizzled rows, chunk of 64 dims
+// after chunk. Queries: [64 dims][heads][9 chunks][requests], one box is all
+// heads of a CTA.
+bool make_q_map(CUtensorMap* m, const DecodeArgs& a, int n) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[4] = {64, (cuuint64_t)rows, 9, (cuuint64_t)outer};
-  cuuint64_t strides[3] = {(cuuint64_t)row_stride * 2, 128, (cuuint64_t)outer_stride * 2};
-  cuuint32_t box[4] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_chunks, 1};
+  cuuint64_t dims[4] = {64, (cuuint64_t)a.heads, 9, (cuuint64_t)a.batch};
+  cuuint64_t strides[3] = {(cuuint64_t)a.q_head * 2, 128, (cuuint64_t)a.q_tok * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)n, 9, 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(a.q), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Cache: [64 dims][8 rows][9 chunks][groups of 8 rows][pages], one box is one
+// or two groups.
+bool make_kv_map(CUtensorMap* m, const PagedCache& kv) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[5] = {64, 8, 9, (cuuint64_t)kv.page_size / 8, (cuuint64_t)kv.num_pages};
+  cuuint64_t strides[4] = {kDqk * 2, 128, 8 * kDqk * 2, (cuuint64_t)kv.page_stride * 2};
+  cuuint32_t box[5] = {64, 8, 9, (cuuint32_t)(kv.page_size >= 16 ? 2 : 1), 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, kv.rows, dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int N>
-cudaError_t launch(const Params& p, const CUtensorMap& tq, const CUtensorMap& tpair, const CUtensorMap& tone,
-                   cudaStream_t stream) {
+cudaError_t launch(const Params& p, const CUtensorMap& tq, const CUtensorMap& tkv, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -750,7 +796,7 @@ cudaError_t launch(const Params& p, const CUtensorMap& tq, const CUtensorMap& tp
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_decode_tc_kernel<N>, p, tq, tpair, tone);
+  return cudaLaunchKernelEx(&cfg, paged_decode_tc_kernel<N>, p, tq, tkv);
 }
 
 }  // namespace ptc
@@ -774,15 +820,12 @@ cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_
   p.nteams = nsm / p.groups > 0 ? nsm / p.groups : 1;
   p.drop_team = g_test_drop_team;
   p.limit_ns = g_test_limit_ns > 0 ? g_test_limit_ns : sm100::kWaitLimitNs;
-  const int rows = P < kTile ? P : kTile;
-  CUtensorMap tq, tpair, tone;
-  if (!make_map(&tq, a.q, a.heads, a.q_head, a.batch, a.q_tok, N, 9) ||
-      !make_map(&tpair, a.kv.rows, P, kDqk, a.kv.num_pages, a.kv.page_stride, rows, 2) ||
-      !make_map(&tone, a.kv.rows, P, kDqk, a.kv.num_pages, a.kv.page_stride, rows, 1))
+  CUtensorMap tq, tkv;
+  if (!make_q_map(&tq, a, N) || !make_kv_map(&tkv, a.kv))
     return cudaErrorNotSupported;
-  const cudaError_t e = N == 16   ? launch<16>(p, tq, tpair, tone, stream)
-                        : N == 32 ? launch<32>(p, tq, tpair, tone, stream)
-                                  : launch<64>(p, tq, tpair, tone, stream);
+  const cudaError_t e = N == 16   ? launch<16>(p, tq, tkv, stream)
+                        : N == 32 ? launch<32>(p, tq, tkv, stream)
+                                  : launch<64>(p, tq, tkv, stream);
   if (e != cudaSuccess || p.nteams == 1) return e;
   return launch_paged_merge(a, p.nteams, 2, p.groups * N, nsm, stream);
 }
