@@ -145,100 +145,126 @@ __global__ void __launch_bounds__(32 * kWarps) decode_simt_kernel(const DecodeAr
 
 // Joins split requests: with w_i = exp(lse_i - max lse),
 //     out = sum_i w_i o_i / sum_i w_i,  lse = max lse + ln sum_i w_i.
-// An item is one (split request, head, quarter of the value dims): the CTA's
-// warps take the partials in turn, a lane four dims (512 bytes a warp load,
-// several in flight), and add up in shared memory in warp order, so the
-// result is the same in every run. One request over all SMs leaves 152
-// partials of 2 KB a head, which is why a head is spread over four CTAs and
-// eight warps each rather than walked by one.
+// An item is one (split request, head, quarter of the value dims), a lane four
+// dims of it (512 bytes a warp load). Where the items fill the card, as in a
+// batch of which most requests are split in a few, a warp takes an item by
+// itself. One long request over all SMs leaves few items of 152 partials each:
+// there a block's warps take an item's partials in turn and add up in shared
+// memory. Both add in a fixed order, so the result is the same in every run.
+// Bound by latency: entries, then lse, then partials, each from L2.
 constexpr int kMergeThreads = 256;
+constexpr int kMergeWarps = kMergeThreads / 32;
+constexpr int kMergeBlocksPerSm = 6;
 constexpr int kMaxParts = 1024;
 constexpr int kQuarter = kDv / 4;
+
+__device__ __forceinline__ int64_t part_row(const MergeEntry& e, int i, int step, int rows_per_slot) {
+  return (int64_t)(i == 0 ? e.first : e.next + (i - 1) * step) * rows_per_slot;
+}
+
+// Adds up partials i = first, first + stride, ... of one item: sum of
+// weights in tot (equal in all lanes), weighted values in s.
+__device__ __forceinline__ void add_parts(const DecodeArgs& a, const MergeEntry& e, int h, int quarter, int lane,
+                                          int first, int stride, int step, int rows_per_slot, float mx, float& tot,
+                                          float4& s) {
+  for (int base = first; base < e.n; base += 32 * stride) {
+    const int mine = base + lane * stride;
+    float w = 0.f;
+    if (mine < e.n) {
+      const float v = __ldcg(a.ws_lse + part_row(e, mine, step, rows_per_slot) + h);
+      w = v == -INFINITY ? 0.f : exp2f((v - mx) * kLog2e);
+    }
+    const int n = min(32, (e.n - base + stride - 1) / stride);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float wk = __shfl_sync(kFull, w, k);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(
+                                  a.ws_o + (part_row(e, base + k * stride, step, rows_per_slot) + h) * kDv +
+                                  quarter * kQuarter) + lane);
+      tot += wk;
+      s.x = fmaf(wk, v.x, s.x);
+      s.y = fmaf(wk, v.y, s.y);
+      s.z = fmaf(wk, v.z, s.z);
+      s.w = fmaf(wk, v.w, s.w);
+    }
+  }
+}
+
+__device__ __forceinline__ void write_item(const DecodeArgs& a, int b, int h, int quarter, int lane, float mx,
+                                           float tot, const float4& s) {
+  const float inv = tot != 0.f ? 1.f / tot : 0.f;
+  const __nv_bfloat162 x = __floats2bfloat162_rn(s.x * inv, s.y * inv);
+  const __nv_bfloat162 y = __floats2bfloat162_rn(s.z * inv, s.w * inv);
+  const int64_t row = (int64_t)b * a.heads + h;
+  *reinterpret_cast<uint2*>(a.out + row * kDv + quarter * kQuarter + 4 * lane) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  if (quarter == 0 && lane == 0) a.lse[row] = tot != 0.f ? mx + logf(tot) : -INFINITY;
+}
 
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const DecodeArgs a, const int entries,
                                                                     const int step, const int rows_per_slot) {
   __shared__ MergeEntry list[kMaxParts];
-  __shared__ int count;
-  __shared__ float wt[kMaxParts];
-  __shared__ float red[kMergeThreads / 32];
-  __shared__ float4 acc[kMergeThreads / 32][32];
+  __shared__ int counts[kMergeWarps];
+  __shared__ float tots[kMergeWarps];
+  __shared__ float4 acc[kMergeWarps][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kW = kMergeThreads / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (warp == 0) {  // the entries with something to merge, in order
-    int n = 0;
-    for (int base = 0; base < entries; base += 32) {
-      MergeEntry e = {0, 0, 0, 0};
-      if (base + lane < entries) {
-        const int4 u = __ldcg(reinterpret_cast<const int4*>(a.ws_entry + base + lane));
-        e = {u.x, u.y, u.z, u.w};
-      }
-      const unsigned any = __ballot_sync(kFull, e.n > 0);
-      if (e.n > 0) list[n + __popc(any & ((1u << lane) - 1))] = e;
-      n += __popc(any);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int n = 0;  // the entries with something to merge, in order
+  for (int base = 0; base < entries; base += kMergeThreads) {
+    int4 u = make_int4(0, 0, 0, 0);
+    if (base + tid < entries) u = __ldcg(reinterpret_cast<const int4*>(a.ws_entry + base + tid));
+    const unsigned any = __ballot_sync(kFull, u.y > 0);
+    if (lane == 0) counts[warp] = __popc(any);
+    __syncthreads();
+    int at = n + __popc(any & ((1u << lane) - 1));
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
+      if (w < warp) at += counts[w];
+      n += counts[w];
     }
-    if (lane == 0) count = n;
+    if (u.y > 0) list[at] = {u.x, u.y, u.z, u.w};
+    __syncthreads();
   }
-  __syncthreads();
-  const int64_t items = (int64_t)count * a.heads * 4;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+  const int64_t items = (int64_t)n * a.heads * 4;
+  const bool alone = items >= (int64_t)gridDim.x * (kMergeWarps / 2);
+  const int64_t stride = (int64_t)gridDim.x * (alone ? kMergeWarps : 1);
+  for (int64_t it = alone ? (int64_t)blockIdx.x * kMergeWarps + warp : blockIdx.x; it < items; it += stride) {
     const int quarter = (int)(it & 3);
     const int64_t eh = it >> 2;
     const MergeEntry e = list[eh / a.heads];
     const int h = (int)(eh % a.heads);
-    auto row_of = [&](int i) {
-      return (int64_t)(i == 0 ? e.first : e.next + (i - 1) * step) * rows_per_slot + h;
-    };
     float mx = -INFINITY;
-    for (int i = tid; i < e.n; i += kMergeThreads) {
-      const float v = __ldcg(a.ws_lse + row_of(i));
-      wt[i] = v;
+    for (int i = lane; i < e.n; i += 32) {
+      const float v = __ldcg(a.ws_lse + part_row(e, i, step, rows_per_slot) + h);
       mx = fmaxf(mx, v != v ? INFINITY : v);  // a NaN is not lost next to empty partials
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-    if (lane == 0) red[warp] = mx;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kW; ++w) mx = fmaxf(mx, red[w]);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     float tot = 0.f;
-    if (mx != -INFINITY) {
-#pragma unroll 4
-      for (int i = warp; i < e.n; i += kW) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.ws_o + row_of(i) * kDv + quarter * kQuarter) + lane);
-        const float w = wt[i] == -INFINITY ? 0.f : exp2f((wt[i] - mx) * kLog2e);
-        tot += w;
-        s.x = fmaf(w, v.x, s.x);
-        s.y = fmaf(w, v.y, s.y);
-        s.z = fmaf(w, v.z, s.z);
-        s.w = fmaf(w, v.w, s.w);
-      }
+    if (alone) {
+      add_parts(a, e, h, quarter, lane, 0, 1, step, rows_per_slot, mx, tot, s);
+      write_item(a, e.b, h, quarter, lane, mx, tot, s);
+      continue;
     }
+    add_parts(a, e, h, quarter, lane, warp, kMergeWarps, step, rows_per_slot, mx, tot, s);
     acc[warp][lane] = s;
-    __syncthreads();  // also: everyone has read red
-    if (lane == 0) red[warp] = tot;
+    if (lane == 0) tots[warp] = tot;
     __syncthreads();
     if (warp == 0) {
-      tot = red[0];
 #pragma unroll
-      for (int w = 1; w < kW; ++w) {
+      for (int w = 1; w < kMergeWarps; ++w) {
         const float4 v = acc[w][lane];
-        tot += red[w];
+        tot += tots[w];
         s.x += v.x;
         s.y += v.y;
         s.z += v.z;
         s.w += v.w;
       }
-      const float inv = tot != 0.f ? 1.f / tot : 0.f;
-      const __nv_bfloat162 x = __floats2bfloat162_rn(s.x * inv, s.y * inv);
-      const __nv_bfloat162 y = __floats2bfloat162_rn(s.z * inv, s.w * inv);
-      const int64_t row = (int64_t)e.b * a.heads + h;
-      *reinterpret_cast<uint2*>(a.out + row * kDv + quarter * kQuarter + 4 * lane) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-      if (quarter == 0 && lane == 0) a.lse[row] = tot != 0.f ? mx + logf(tot) : -INFINITY;
+      write_item(a, e.b, h, quarter, lane, mx, tot, s);
     }
-    __syncthreads();  // red, wt and acc are free for the next item
+    __syncthreads();  // acc and tots are free for the next item
   }
 }
 
@@ -247,7 +273,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const Decode
 cudaError_t launch_paged_merge(const DecodeArgs& a, int entries, int step, int rows_per_slot,
                                int num_sms, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(4 * (num_sms > 0 ? num_sms : 152)));
+  cfg.gridDim = dim3((unsigned)(kMergeBlocksPerSm * (num_sms > 0 ? num_sms : 152)));
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr;

@@ -188,6 +188,16 @@ __device__ __forceinline__ void mma_commit_elect(uint64_t* bar) {
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// Waits for a phase: a probe in line, the bounded wait out of line, because
+// every copy of the polling loop would have to be fetched by a kernel that for
+// short requests runs most of its code once.
+__device__ __noinline__ bool wait_phase_slow(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit) {
+  return mbar_wait<false>(bar, parity, abort, limit);
+}
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit) {
+  return mbar_test_wait(bar, parity) || wait_phase_slow(bar, parity, abort, limit);
+}
+
 __device__ __forceinline__ bool bar_any(int id, int nthreads, bool v) {
   int r;
   asm volatile(
@@ -359,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0, pieces = 0;
     bool dead = drop;
     auto wait = [&](int bar, uint32_t parity) {
-      if (!dead) dead = __any_sync(kFull, !mbar_wait<false>(&bars[bar], parity, abort, limit));
+      if (!dead) dead = __any_sync(kFull, !wait_phase(&bars[bar], parity, abort, limit));
     };
     while (!dead && next_piece(a, walk, pc)) {
       if (pc.t1 <= pc.t0) continue;
@@ -435,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0, pieces = 0;
     bool dead = false;
     auto wait = [&](int bar, uint32_t parity) {
-      if (!dead) dead = __any_sync(kFull, !mbar_wait<false>(&bars[bar], parity, abort, limit));
+      if (!dead) dead = __any_sync(kFull, !wait_phase(&bars[bar], parity, abort, limit));
     };
     while (!dead && next_piece(a, walk, pc)) {
       const int n = __shfl_sync(kFull, pc.t1 - pc.t0, 0);
@@ -474,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0, pieces = 0;
     bool dead = false;
     auto wait = [&](int bar, uint32_t parity) {
-      if (!dead) dead = __any_sync(kFull, !mbar_wait<false>(&bars[bar], parity, abort, limit));
+      if (!dead) dead = __any_sync(kFull, !wait_phase(&bars[bar], parity, abort, limit));
     };
     while (!dead && next_piece(a, walk, pc)) {
       const int n = __shfl_sync(kFull, pc.t1 - pc.t0, 0);
@@ -545,8 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int t = pc.t0; t < pc.t1; ++t, ++it) {
         const int st = it & 1, ph = (it >> 1) & 1;
-        if (!dead) dead = !mbar_wait<false>(&bars[B_S_FULL + st], ph, abort, limit);
-        if (!dead) dead = !mbar_wait<false>(&bars[B_KV_FULL + st], ph, abort, limit);
+        if (!dead) dead = !wait_phase(&bars[B_S_FULL + st], ph, abort, limit);
+        if (!dead) dead = !wait_phase(&bars[B_KV_FULL + st], ph, abort, limit);
         tc_fence_after();
         uint32_t s[NC / 2];
         tmem_ld_frag(tmem + lane_base + L::kS + st * N + c0, s);
@@ -592,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (t > pc.t0) {  // the first tile's P.V overwrites O
             named_bar_sync(bar_id, kHalf);
-            if (!dead) dead = !mbar_wait<false>(&bars[B_P_EMPTY], (it & 1) ^ 1, abort, limit);
+            if (!dead) dead = !wait_phase(&bars[B_P_EMPTY], (it & 1) ^ 1, abort, limit);
             tc_fence_after();
 #pragma unroll 1
             for (int m = 0; m < 4; ++m)
@@ -622,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
             pk[2 * i + k] = *reinterpret_cast<const uint32_t*>(&h);
           }
-        if (!dead) dead = !mbar_wait<false>(&bars[B_P_EMPTY], (it & 1) ^ 1, abort, limit);
+        if (!dead) dead = !wait_phase(&bars[B_P_EMPTY], (it & 1) ^ 1, abort, limit);
         if constexpr (NC == 8) {
           stmatrix2_trans(paddr, pk[0], pk[1]);
         } else {
@@ -666,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         redh[htid] = sum != 0.f ? 1.f / sum : 0.f;
       }
       named_bar_sync(bar_id, kHalf);
-      if (!dead) dead = !mbar_wait<false>(&bars[B_P_EMPTY], (it - 1) & 1, abort, limit);
+      if (!dead) dead = !wait_phase(&bars[B_P_EMPTY], (it - 1) & 1, abort, limit);
       tc_fence_after();
       const bool give_up = __any_sync(kFull, dead || *abort);  // nothing to write
 #pragma unroll 1
@@ -682,17 +692,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
         tmem_regs_ready(o);
         const int dim = m * 128 + quad * 32 + lane;
+        // all products before the first store: it might change the factors for all the compiler knows
+#pragma unroll
+        for (int c = 0; c < NC; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * redh[c]);
         if (whole) {
           uint16_t* dst = a.out + (orow + c0) * kDv + dim;
 #pragma unroll
           for (int c = 0; c < NC; ++c)
-            if (c0 + c < nh)
-              dst[c * kDv] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(o[c]) * redh[c]));
+            if (c0 + c < nh) dst[c * kDv] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(o[c])));
         } else {
           float* dst = a.ws_o + (wrow + c0) * kDv + dim;
 #pragma unroll
           for (int c = 0; c < NC; ++c)
-            if (c0 + c < nh) dst[c * kDv] = __uint_as_float(o[c]) * redh[c];
+            if (c0 + c < nh) dst[c * kDv] = __uint_as_float(o[c]);
         }
       }
       tc_fence_before();
