@@ -145,68 +145,61 @@ __global__ void __launch_bounds__(32 * kWarps) decode_simt_kernel(const DecodeAr
 
 // Joins split requests: with w_i = exp(lse_i - max lse),
 //     out = sum_i w_i o_i / sum_i w_i,  lse = max lse + ln sum_i w_i.
-// An item is one (split request, head, quarter of the value dims), a lane four
-// dims of it (512 bytes a warp load). Where the items fill the card, as in a
-// batch of which most requests are split in a few, a warp takes an item by
-// itself. One long request over all SMs leaves few items of 152 partials each:
-// there a block's warps take an item's partials in turn and add up in shared
-// memory. Both add in a fixed order, so the result is the same in every run.
-// Bound by latency: entries, then lse, then partials, each from L2.
+// Where most requests of a batch are split in a few, a warp takes one (request,
+// head, quarter of the value dims) at a time, a lane four dims: 512 bytes a
+// warp load. One long request over all SMs leaves 152 partials a head but few
+// heads: there a block takes a (request, head, sixteenth of the dims), a warp
+// load is 128 bytes of each of four partials, and the block's 32 lane groups
+// add up in shared memory. Both add in a fixed order, so the result is the
+// same in every run. Bound by latency: entries, then lse and partials, from L2.
 constexpr int kMergeThreads = 256;
 constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kMergeBlocksPerSm = 6;
 constexpr int kMaxParts = 1024;
 constexpr int kQuarter = kDv / 4;
+constexpr int kSixteenth = kDv / 16;
+constexpr int kLaneGroups = kMergeThreads / 8;
+constexpr int kAhead = 5;   // partials a lane of a block holds while the weights are made: 160 a block
 
 __device__ __forceinline__ int64_t part_row(const MergeEntry& e, int i, int step, int rows_per_slot) {
   return (int64_t)(i == 0 ? e.first : e.next + (i - 1) * step) * rows_per_slot;
 }
 
-// Adds up partials i = first, first + stride, ... of one item: sum of
-// weights in tot (equal in all lanes), weighted values in s.
-__device__ __forceinline__ void add_parts(const DecodeArgs& a, const MergeEntry& e, int h, int quarter, int lane,
-                                          int first, int stride, int step, int rows_per_slot, float mx, float& tot,
-                                          float4& s) {
-  for (int base = first; base < e.n; base += 32 * stride) {
-    const int mine = base + lane * stride;
-    float w = 0.f;
-    if (mine < e.n) {
-      const float v = __ldcg(a.ws_lse + part_row(e, mine, step, rows_per_slot) + h);
-      w = v == -INFINITY ? 0.f : exp2f((v - mx) * kLog2e);
-    }
-    const int n = min(32, (e.n - base + stride - 1) / stride);
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float wk = __shfl_sync(kFull, w, k);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(
-                                  a.ws_o + (part_row(e, base + k * stride, step, rows_per_slot) + h) * kDv +
-                                  quarter * kQuarter) + lane);
-      tot += wk;
-      s.x = fmaf(wk, v.x, s.x);
-      s.y = fmaf(wk, v.y, s.y);
-      s.z = fmaf(wk, v.z, s.z);
-      s.w = fmaf(wk, v.w, s.w);
-    }
-  }
+__device__ __forceinline__ float weight(float lse, float mx) {
+  return lse == -INFINITY ? 0.f : exp2f((lse - mx) * kLog2e);
 }
 
-__device__ __forceinline__ void write_item(const DecodeArgs& a, int b, int h, int quarter, int lane, float mx,
-                                           float tot, const float4& s) {
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+
+__device__ __forceinline__ float not_nan(float v) { return v != v ? INFINITY : v; }  // a NaN is not lost in a maximum
+
+__device__ __forceinline__ void add(float4& s, float w, const float4& v) {
+  s.x = fmaf(w, v.x, s.x);
+  s.y = fmaf(w, v.y, s.y);
+  s.z = fmaf(w, v.z, s.z);
+  s.w = fmaf(w, v.w, s.w);
+}
+
+// Four dims of a result row, from their weighted sum.
+__device__ __forceinline__ void write_dims(const DecodeArgs& a, int64_t row, int dim, float tot, const float4& s) {
   const float inv = tot != 0.f ? 1.f / tot : 0.f;
   const __nv_bfloat162 x = __floats2bfloat162_rn(s.x * inv, s.y * inv);
   const __nv_bfloat162 y = __floats2bfloat162_rn(s.z * inv, s.w * inv);
-  const int64_t row = (int64_t)b * a.heads + h;
-  *reinterpret_cast<uint2*>(a.out + row * kDv + quarter * kQuarter + 4 * lane) =
+  *reinterpret_cast<uint2*>(a.out + row * kDv + dim) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-  if (quarter == 0 && lane == 0) a.lse[row] = tot != 0.f ? mx + logf(tot) : -INFINITY;
 }
 
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const DecodeArgs a, const int entries,
                                                                     const int step, const int rows_per_slot) {
   __shared__ MergeEntry list[kMaxParts];
+  __shared__ float wt[kMaxParts];
+  __shared__ float4 acc[kMergeWarps][8];
+  __shared__ float red[kMergeWarps];
   __shared__ int counts[kMergeWarps];
-  __shared__ float tots[kMergeWarps];
-  __shared__ float4 acc[kMergeWarps][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -226,45 +219,104 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const Decode
     if (u.y > 0) list[at] = {u.x, u.y, u.z, u.w};
     __syncthreads();
   }
-  const int64_t items = (int64_t)n * a.heads * 4;
-  const bool alone = items >= (int64_t)gridDim.x * (kMergeWarps / 2);
-  const int64_t stride = (int64_t)gridDim.x * (alone ? kMergeWarps : 1);
-  for (int64_t it = alone ? (int64_t)blockIdx.x * kMergeWarps + warp : blockIdx.x; it < items; it += stride) {
-    const int quarter = (int)(it & 3);
-    const int64_t eh = it >> 2;
-    const MergeEntry e = list[eh / a.heads];
-    const int h = (int)(eh % a.heads);
-    float mx = -INFINITY;
-    for (int i = lane; i < e.n; i += 32) {
-      const float v = __ldcg(a.ws_lse + part_row(e, i, step, rows_per_slot) + h);
-      mx = fmaxf(mx, v != v ? INFINITY : v);  // a NaN is not lost next to empty partials
+
+  const int64_t heads = (int64_t)n * a.heads;
+  if (heads * 4 >= (int64_t)gridDim.x * (kMergeWarps / 2)) {
+    for (int64_t it = (int64_t)blockIdx.x * kMergeWarps + warp; it < heads * 4; it += (int64_t)gridDim.x * kMergeWarps) {
+      const int dim = (int)(it & 3) * kQuarter + 4 * lane;
+      const MergeEntry e = list[(it >> 2) / a.heads];
+      const int h = (int)((it >> 2) % a.heads);
+      float mx = -INFINITY, tot = 0.f;
+      for (int i = lane; i < e.n; i += 32)
+        mx = fmaxf(mx, not_nan(__ldcg(a.ws_lse + part_row(e, i, step, rows_per_slot) + h)));
+      mx = warp_max(mx);
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int base = 0; base < e.n; base += 32) {
+        const int mine = base + lane;
+        const float w = mine < e.n ? weight(__ldcg(a.ws_lse + part_row(e, mine, step, rows_per_slot) + h), mx) : 0.f;
+        const int m = min(32, e.n - base);
+#pragma unroll 4
+        for (int k = 0; k < m; ++k) {
+          const float wk = __shfl_sync(kFull, w, k);
+          tot += wk;
+          add(s, wk, __ldcg(reinterpret_cast<const float4*>(
+                         a.ws_o + (part_row(e, base + k, step, rows_per_slot) + h) * kDv + dim)));
+        }
+      }
+      const int64_t row = (int64_t)e.b * a.heads + h;
+      write_dims(a, row, dim, tot, s);
+      if (dim == 0) a.lse[row] = tot != 0.f ? mx + logf(tot) : -INFINITY;
     }
+    return;
+  }
+
+  const int grp = tid >> 3, li = tid & 7;
+  for (int64_t it = blockIdx.x; it < heads * 16; it += gridDim.x) {
+    const int dim = (int)(it & 15) * kSixteenth + 4 * li;
+    const MergeEntry e = list[(it >> 4) / a.heads];
+    const int h = (int)((it >> 4) % a.heads);
+    const float* src = a.ws_o + h * kDv + dim;
+    float4 v[kAhead];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = grp + kLaneGroups * k;
+      if (i < e.n)
+        v[k] = __ldcg(reinterpret_cast<const float4*>(src + part_row(e, i, step, rows_per_slot) * kDv));
+    }
+    float mx = -INFINITY;
+    for (int i = tid; i < e.n; i += kMergeThreads) {
+      const float l = __ldcg(a.ws_lse + part_row(e, i, step, rows_per_slot) + h);
+      wt[i] = l;
+      mx = fmaxf(mx, not_nan(l));
+    }
+    mx = warp_max(mx);
+    if (lane == 0) red[warp] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) mx = fmaxf(mx, red[w]);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     float tot = 0.f;
-    if (alone) {
-      add_parts(a, e, h, quarter, lane, 0, 1, step, rows_per_slot, mx, tot, s);
-      write_item(a, e.b, h, quarter, lane, mx, tot, s);
-      continue;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = grp + kLaneGroups * k;
+      if (i < e.n) {
+        const float w = weight(wt[i], mx);
+        tot += w;
+        add(s, w, v[k]);
+      }
     }
-    add_parts(a, e, h, quarter, lane, warp, kMergeWarps, step, rows_per_slot, mx, tot, s);
-    acc[warp][lane] = s;
-    if (lane == 0) tots[warp] = tot;
+    for (int i = grp + kLaneGroups * kAhead; i < e.n; i += kLaneGroups) {
+      const float w = weight(wt[i], mx);
+      tot += w;
+      add(s, w, __ldcg(reinterpret_cast<const float4*>(src + part_row(e, i, step, rows_per_slot) * kDv)));
+    }
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+      tot += __shfl_xor_sync(kFull, tot, o);
+      s.x += __shfl_xor_sync(kFull, s.x, o);
+      s.y += __shfl_xor_sync(kFull, s.y, o);
+      s.z += __shfl_xor_sync(kFull, s.z, o);
+      s.w += __shfl_xor_sync(kFull, s.w, o);
+    }
+    __syncthreads();  // everyone has read red
+    if (lane < 8) acc[warp][lane] = s;
+    if (lane == 0) red[warp] = tot;
     __syncthreads();
-    if (warp == 0) {
+    if (tid < 8) {
 #pragma unroll
       for (int w = 1; w < kMergeWarps; ++w) {
-        const float4 v = acc[w][lane];
-        tot += tots[w];
-        s.x += v.x;
-        s.y += v.y;
-        s.z += v.z;
-        s.w += v.w;
+        const float4 x = acc[w][lane];
+        tot += red[w];
+        s.x += x.x;
+        s.y += x.y;
+        s.z += x.z;
+        s.w += x.w;
       }
-      write_item(a, e.b, h, quarter, lane, mx, tot, s);
+      const int64_t row = (int64_t)e.b * a.heads + h;
+      write_dims(a, row, dim, tot, s);
+      if (dim == 0) a.lse[row] = tot != 0.f ? mx + logf(tot) : -INFINITY;
     }
-    __syncthreads();  // acc and tots are free for the next item
+    __syncthreads();  // wt, red and acc are free for the next item
   }
 }
 

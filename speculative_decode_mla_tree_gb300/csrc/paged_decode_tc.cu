@@ -838,7 +838,9 @@ cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_
   const cudaError_t e = N == 16   ? launch<16>(p, tq, tkv, stream)
                         : N == 32 ? launch<32>(p, tq, tkv, stream)
                                   : launch<64>(p, tq, tkv, stream);
-  if (e != cudaSuccess || p.nteams == 1) return e;
+  // No request of this table can be split when it holds no more tiles than a share.
+  const int64_t most = ((int64_t)a.kv.max_pages * P + kTile - 1) / kTile;
+  if (e != cudaSuccess || p.nteams == 1 || (a.batch == 1 && most <= kMinShare)) return e;
   return launch_paged_merge(a, p.nteams, 2, p.groups * N, nsm, stream);
 }
 
