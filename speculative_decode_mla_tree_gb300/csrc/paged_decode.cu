@@ -145,24 +145,28 @@ __global__ void __launch_bounds__(32 * kWarps) decode_simt_kernel(const DecodeAr
 
 // Joins split requests: with w_i = exp(lse_i - max lse),
 //     out = sum_i w_i o_i / sum_i w_i,  lse = max lse + ln sum_i w_i.
-// Where most requests of a batch are split in a few, a warp takes one (request,
-// head, quarter of the value dims) at a time, a lane four dims: 512 bytes a
-// warp load. One long request over all SMs leaves 152 partials a head but few
-// heads: there a block takes a (request, head, sixteenth of the dims), a warp
-// load is 128 bytes of each of four partials, and the block's 32 lane groups
-// add up in shared memory. Both add in a fixed order, so the result is the
-// same in every run. Bound by latency: entries, then lse and partials, from L2.
+// What bounds it is latency (entries, then lse and partials, from L2), so as
+// many partials as possible are loaded at once and the weights made meanwhile.
+// Requests split in a few: W warps take a (request, head, quarter of the dims),
+// a lane four dims, each warp kAheadWarp partials; W grows with the number of
+// partials and until the items fill the card. One long request over all SMs
+// leaves 152 partials a head: there a block takes a (request, head, eighth of
+// the dims), a warp load is 256 bytes of each of two partials. Sums are in a
+// fixed order, so the result is the same in every run.
 constexpr int kMergeThreads = 256;
 constexpr int kMergeWarps = kMergeThreads / 32;
-constexpr int kMergeBlocksPerSm = 6;
+constexpr int kMergeBlocksPerSm = 3;
 constexpr int kMaxParts = 1024;
 constexpr int kQuarter = kDv / 4;
-constexpr int kSixteenth = kDv / 16;
-constexpr int kLaneGroups = kMergeThreads / 8;
-constexpr int kAhead = 5;   // partials a lane of a block holds while the weights are made: 160 a block
+constexpr int kEighth = kDv / 8;
+constexpr int kAheadWarp = 8;                      // partials in flight of a lane, one warp (divides 32)
+constexpr int kHalfWarps = kMergeThreads / 16;
+constexpr int kAheadBlock = 10;                    // and of a lane, one block: 160 partials
 
+// Rows and items count in 32 bits: the workspace has fewer than 2^31 rows, and
+// a 64-bit division costs more than an item's arithmetic.
 __device__ __forceinline__ int64_t part_row(const MergeEntry& e, int i, int step, int rows_per_slot) {
-  return (int64_t)(i == 0 ? e.first : e.next + (i - 1) * step) * rows_per_slot;
+  return (int)((i == 0 ? e.first : e.next + (i - 1) * step) * rows_per_slot);
 }
 
 __device__ __forceinline__ float weight(float lse, float mx) {
@@ -193,75 +197,120 @@ __device__ __forceinline__ void write_dims(const DecodeArgs& a, int64_t row, int
       make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const DecodeArgs a, const int entries,
+__global__ void __launch_bounds__(kMergeThreads, kMergeBlocksPerSm) paged_merge_kernel(const DecodeArgs a, const int entries,
                                                                     const int step, const int rows_per_slot) {
   __shared__ MergeEntry list[kMaxParts];
   __shared__ float wt[kMaxParts];
-  __shared__ float4 acc[kMergeWarps][8];
-  __shared__ float red[kMergeWarps];
-  __shared__ int counts[kMergeWarps];
+  __shared__ float4 acc[kMergeWarps][32];
+  __shared__ float red[kMergeWarps], tots[kMergeWarps];
+  __shared__ int counts[kMergeWarps], sums[kMergeWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int n = 0;  // the entries with something to merge, in order
+  int n = 0, parts = 0;  // the entries with something to merge, in order; their partials
   for (int base = 0; base < entries; base += kMergeThreads) {
     int4 u = make_int4(0, 0, 0, 0);
     if (base + tid < entries) u = __ldcg(reinterpret_cast<const int4*>(a.ws_entry + base + tid));
     const unsigned any = __ballot_sync(kFull, u.y > 0);
-    if (lane == 0) counts[warp] = __popc(any);
+    const int sum = __reduce_add_sync(kFull, u.y);
+    if (lane == 0) counts[warp] = __popc(any), sums[warp] = sum;
     __syncthreads();
     int at = n + __popc(any & ((1u << lane) - 1));
 #pragma unroll
     for (int w = 0; w < kMergeWarps; ++w) {
       if (w < warp) at += counts[w];
       n += counts[w];
+      parts += sums[w];
     }
     if (u.y > 0) list[at] = {u.x, u.y, u.z, u.w};
     __syncthreads();
   }
 
-  const int64_t heads = (int64_t)n * a.heads;
-  if (heads * 4 >= (int64_t)gridDim.x * (kMergeWarps / 2)) {
-    for (int64_t it = (int64_t)blockIdx.x * kMergeWarps + warp; it < heads * 4; it += (int64_t)gridDim.x * kMergeWarps) {
+  if (n == 0) return;
+  const unsigned heads = (unsigned)n * a.heads, H = a.heads;
+  const int each = (parts + n - 1) / n;
+
+  if (each <= kMergeWarps * kAheadWarp) {
+    const unsigned items = heads * 4;
+    int wl = 0;  // W = 2^wl
+    while ((1 << wl) < kMergeWarps &&
+           (each > (kAheadWarp << wl) || (items << (wl + 1)) <= gridDim.x * (unsigned)kMergeWarps))
+      ++wl;
+    const int W = 1 << wl;
+    const int sub = warp & (W - 1);
+    const unsigned per = kMergeWarps >> wl;
+    for (unsigned base = blockIdx.x * per; base < items; base += gridDim.x * per) {
+      const unsigned it = base + (warp >> wl);
+      const bool mine = it < items;
       const int dim = (int)(it & 3) * kQuarter + 4 * lane;
-      const MergeEntry e = list[(it >> 2) / a.heads];
-      const int h = (int)((it >> 2) % a.heads);
-      float mx = -INFINITY, tot = 0.f;
-      for (int i = lane; i < e.n; i += 32)
-        mx = fmaxf(mx, not_nan(__ldcg(a.ws_lse + part_row(e, i, step, rows_per_slot) + h)));
+      const unsigned entry = (it >> 2) / H;
+      const MergeEntry e = mine ? list[entry] : MergeEntry{0, 0, 0, 0};
+      const int h = (int)((it >> 2) - entry * H);
+      const float* src = a.ws_o + h * kDv + dim;
+      float4 v[kAheadWarp];
+      auto load = [&](int k0) {  // this warp's partials are sub + W k
+#pragma unroll
+        for (int k = 0; k < kAheadWarp; ++k)
+          if (sub + ((k0 + k) << wl) < e.n)
+            v[k] = __ldcg(reinterpret_cast<const float4*>(
+                src + part_row(e, sub + ((k0 + k) << wl), step, rows_per_slot) * kDv));
+      };
+      auto lse_of = [&](int i) {
+        return i < e.n ? __ldcg(a.ws_lse + part_row(e, i, step, rows_per_slot) + h) : -INFINITY;
+      };
+      load(0);
+      // lane l: partial l for the maximum, this warp's l-th partial for its weight
+      const float seen = lse_of(lane), own = wl == 0 ? seen : lse_of(sub + (lane << wl));
+      float mx = not_nan(seen);
+      for (int i = 32 + lane; i < e.n; i += 32) mx = fmaxf(mx, not_nan(lse_of(i)));
       mx = warp_max(mx);
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int base = 0; base < e.n; base += 32) {
-        const int mine = base + lane;
-        const float w = mine < e.n ? weight(__ldcg(a.ws_lse + part_row(e, mine, step, rows_per_slot) + h), mx) : 0.f;
-        const int m = min(32, e.n - base);
-#pragma unroll 4
-        for (int k = 0; k < m; ++k) {
-          const float wk = __shfl_sync(kFull, w, k);
-          tot += wk;
-          add(s, wk, __ldcg(reinterpret_cast<const float4*>(
-                         a.ws_o + (part_row(e, base + k, step, rows_per_slot) + h) * kDv + dim)));
+      float tot = 0.f, w = weight(own, mx);
+      for (int k0 = 0; sub + (k0 << wl) < e.n; k0 += kAheadWarp) {
+        if (k0 > 0) {
+          load(k0);
+          if ((k0 & 31) == 0) w = weight(lse_of(sub + ((k0 + lane) << wl)), mx);
         }
+#pragma unroll
+        for (int k = 0; k < kAheadWarp; ++k)
+          if (sub + ((k0 + k) << wl) < e.n) {
+            const float wk = __shfl_sync(kFull, w, (k0 + k) & 31);
+            tot += wk;
+            add(s, wk, v[k]);
+          }
       }
-      const int64_t row = (int64_t)e.b * a.heads + h;
-      write_dims(a, row, dim, tot, s);
-      if (dim == 0) a.lse[row] = tot != 0.f ? mx + logf(tot) : -INFINITY;
+      if (W > 1) {
+        __syncthreads();  // the item before has been read
+        acc[warp][lane] = s;
+        if (lane == 0) tots[warp] = tot;
+        __syncthreads();
+        if (sub == 0)
+          for (int k = 1; k < W; ++k) {
+            tot += tots[warp + k];
+            add(s, 1.f, acc[warp + k][lane]);
+          }
+      }
+      if (mine && sub == 0) {
+        const int64_t row = (int64_t)e.b * a.heads + h;
+        write_dims(a, row, dim, tot, s);
+        if (dim == 0) a.lse[row] = tot != 0.f ? mx + logf(tot) : -INFINITY;
+      }
     }
     return;
   }
 
-  const int grp = tid >> 3, li = tid & 7;
-  for (int64_t it = blockIdx.x; it < heads * 16; it += gridDim.x) {
-    const int dim = (int)(it & 15) * kSixteenth + 4 * li;
-    const MergeEntry e = list[(it >> 4) / a.heads];
-    const int h = (int)((it >> 4) % a.heads);
+  const int grp = tid >> 4, li = tid & 15;
+  for (unsigned it = blockIdx.x; it < heads * 8; it += gridDim.x) {
+    const int dim = (int)(it & 7) * kEighth + 4 * li;
+    const unsigned entry = (it >> 3) / H;
+    const MergeEntry e = list[entry];
+    const int h = (int)((it >> 3) - entry * H);
     const float* src = a.ws_o + h * kDv + dim;
-    float4 v[kAhead];
+    float4 v[kAheadBlock];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int i = grp + kLaneGroups * k;
-      if (i < e.n)
-        v[k] = __ldcg(reinterpret_cast<const float4*>(src + part_row(e, i, step, rows_per_slot) * kDv));
+    for (int k = 0; k < kAheadBlock; ++k) {
+      const int i = grp + kHalfWarps * k;
+      if (i < e.n) v[k] = __ldcg(reinterpret_cast<const float4*>(src + part_row(e, i, step, rows_per_slot) * kDv));
     }
     float mx = -INFINITY;
     for (int i = tid; i < e.n; i += kMergeThreads) {
@@ -277,46 +326,38 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const Decode
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     float tot = 0.f;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int i = grp + kLaneGroups * k;
+    for (int k = 0; k < kAheadBlock; ++k) {
+      const int i = grp + kHalfWarps * k;
       if (i < e.n) {
         const float w = weight(wt[i], mx);
         tot += w;
         add(s, w, v[k]);
       }
     }
-    for (int i = grp + kLaneGroups * kAhead; i < e.n; i += kLaneGroups) {
+    for (int i = grp + kHalfWarps * kAheadBlock; i < e.n; i += kHalfWarps) {
       const float w = weight(wt[i], mx);
       tot += w;
       add(s, w, __ldcg(reinterpret_cast<const float4*>(src + part_row(e, i, step, rows_per_slot) * kDv)));
     }
-#pragma unroll
-    for (int o = 8; o < 32; o <<= 1) {
-      tot += __shfl_xor_sync(kFull, tot, o);
-      s.x += __shfl_xor_sync(kFull, s.x, o);
-      s.y += __shfl_xor_sync(kFull, s.y, o);
-      s.z += __shfl_xor_sync(kFull, s.z, o);
-      s.w += __shfl_xor_sync(kFull, s.w, o);
-    }
-    __syncthreads();  // everyone has read red
-    if (lane < 8) acc[warp][lane] = s;
-    if (lane == 0) red[warp] = tot;
+    tot += __shfl_xor_sync(kFull, tot, 16);
+    s.x += __shfl_xor_sync(kFull, s.x, 16);
+    s.y += __shfl_xor_sync(kFull, s.y, 16);
+    s.z += __shfl_xor_sync(kFull, s.z, 16);
+    s.w += __shfl_xor_sync(kFull, s.w, 16);
+    if (lane < 16) acc[warp][lane] = s;
+    if (lane == 0) tots[warp] = tot;
     __syncthreads();
-    if (tid < 8) {
+    if (tid < 16) {
 #pragma unroll
       for (int w = 1; w < kMergeWarps; ++w) {
-        const float4 x = acc[w][lane];
-        tot += red[w];
-        s.x += x.x;
-        s.y += x.y;
-        s.z += x.z;
-        s.w += x.w;
+        tot += tots[w];
+        add(s, 1.f, acc[w][lane]);
       }
       const int64_t row = (int64_t)e.b * a.heads + h;
       write_dims(a, row, dim, tot, s);
       if (dim == 0) a.lse[row] = tot != 0.f ? mx + logf(tot) : -INFINITY;
     }
-    __syncthreads();  // wt, red and acc are free for the next item
+    __syncthreads();  // wt, red, acc and tots are free for the next item
   }
 }
 

@@ -58,7 +58,7 @@ constexpr int kStages = 2;
 constexpr int kQuarters = 4;                  // a stage is released by quarters, two groups = one P.V K step
 constexpr float kRescale = 8.f;               // log2 of how far a weight may exceed 1
 constexpr int kOverhead = 2;                  // a request's fixed cost, in tiles
-constexpr int kMinShare = 4;                  // smallest share of a team, in tiles
+constexpr int kMinShare = 1;                  // smallest share of a team, in tiles
 constexpr uint64_t kDrainNs = 100000000ull;
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -294,7 +294,9 @@ __device__ Walk make_plan(const Params& p, int team, int64_t* sh, int64_t* share
     }
     if (base == 0) {
       const int64_t total = sum + rest;
-      int64_t share = (total + p.nteams - 1) / p.nteams;
+      // (a 64-bit division takes longer than the rest of this function)
+      int64_t share = total <= INT32_MAX ? (int64_t)(((uint32_t)total + p.nteams - 1) / (uint32_t)p.nteams)
+                                         : (total + p.nteams - 1) / p.nteams;
       if (share < kMinShare + kOverhead) share = kMinShare + kOverhead;
       *share_out = share;
       r.s = team * share;
@@ -356,6 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the merge may be set up from here on; it waits for this grid's completion
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int64_t share;
   Walk walk = make_plan(p, team, plan, &share);
   Piece pc;
@@ -724,7 +728,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort) flag(a.status, MT_DEV_TIMEOUT);
