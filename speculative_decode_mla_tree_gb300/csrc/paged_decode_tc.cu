@@ -8,7 +8,8 @@
 //     O^T [512 dims x N heads] += V^T [512 x 64] P^T        (4 x M = 128)
 // K and V^T are the same shared-memory tile, read K-major and MN-major. A CTA
 // serves N = 16, 32 or 64 heads (more heads are groups of 64 in CTAs of their
-// own, side by side) and walks a contiguous range of 64-key tiles that may
+// own, side by side; of two groups the CTAs are a cluster, and each loads half
+// of every tile into both by multicast) and walks a contiguous range of 64-key tiles that may
 // span several requests.
 //
 // Softmax over keys is over TMEM lanes here. Its maximum would cross lanes and
@@ -56,10 +57,12 @@ constexpr int kGroup = 9 * 1024;
 constexpr int kStage = 8 * kGroup;
 constexpr int kStages = 2;
 constexpr int kQuarters = 4;                  // a stage is released by quarters, two groups = one P.V K step
+constexpr int kAhead = 1;                     // a tile's loads go out with the L2 prefetch of the tile so far behind it
 constexpr float kRescale = 8.f;               // log2 of how far a weight may exceed 1
 constexpr int kOverhead = 2;                  // a request's fixed cost, in tiles
 constexpr int kMinShare = 1;                  // smallest share of a team, in tiles
 constexpr uint64_t kDrainNs = 100000000ull;
+constexpr uint64_t kSettleNs = 50000ull;
 constexpr unsigned kFull = 0xffffffffu;
 
 enum {
@@ -123,6 +126,25 @@ __device__ __forceinline__ void tma_load_5d_elect(uint32_t dst, const CUtensorMa
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(bar))
       : "memory");
 }
+// Brings a box into L2 only.
+__device__ __forceinline__ void tma_prefetch_5d_elect(const CUtensorMap* map, int x, int y, int z, int w, int v) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %4, %5}];\n}\n" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
+      : "memory");
+}
+// The 5-D load into the same place of both CTAs of a pair, signalling each CTA's own barrier.
+__device__ __forceinline__ void tma_load_5d_both_elect(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                                       int w, int v, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n .reg .b16 m;\n mov.b16 m, 3;\n elect.sync _|q, 0xffffffff;\n"
+      " @q cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], m;\n}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(bar))
+      : "memory");
+}
 __device__ __forceinline__ void expect_elect(uint64_t* bar, uint32_t tx) {
   asm volatile(
       "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
@@ -160,6 +182,16 @@ __device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t a, uint3
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a),
                "r"(b), "r"(c), "r"(d)
                : "memory");
+}
+
+// Arrives on the same barrier of CTA `rank` of the cluster.
+__device__ __forceinline__ void mma_commit_to_elect(uint64_t* bar, int rank) {
+  asm volatile(
+      "{\n .reg .pred q;\n .reg .b16 m;\n cvt.u16.u32 m, %1;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}\n" ::"r"(
+          smem_u32(bar)),
+      "r"(1u << rank)
+      : "memory");
 }
 
 // Two such blocks; lanes 0-15 give the addresses.
@@ -318,7 +350,9 @@ __device__ Walk make_plan(const Params& p, int team, int64_t* sh, int64_t* share
 
 // ------------------------------------------------------------------- kernel
 
-template <int N>
+// kPair: the two head groups of a team are a cluster of two CTAs, and each
+// loads every other quarter of a tile into both.
+template <int N, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_decode_tc_kernel(const Params p, const __grid_constant__ CUtensorMap tq,
                            const __grid_constant__ CUtensorMap tkv) {
@@ -348,12 +382,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars[B_O_EMPTY], kSoftWarps);
     mbar_init(&bars[B_S_EMPTY], kSoftWarps);
     mbar_init(&bars[B_S_EMPTY + 1], kSoftWarps);
+    if (kPair)
+      for (int i = 0; i < kStages * kQuarters; ++i) mbar_init(&bars[B_KV_EMPTY + i], 2);
     fence_mbar_init_cluster();
   } else if (tid == kProducerWarp * 32) {
     prefetch_tmap(&tq);
     prefetch_tmap(&tkv);
   }
   tc_fence_before();
+  if (kPair) cluster_sync();  // the other CTA's barriers are there
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -383,20 +420,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_load_4d_elect(smem_u32(sm + L::kQ), &tq, 0, grp * N, 0, pc.b, &bars[B_Q_FULL]);
       ++pieces;
       const int32_t* table = a.kv.table + pc.b * a.kv.table_stride;
-      // lane l looks after group l of a tile: its page, -1 behind the length
+      // lane l looks after group l of a tile: its page, -1 behind the length or the share
       auto entry = [&](int t) {
         const int64_t row = (int64_t)t * kTile + lane * 8;
-        return lane < 8 && row < pc.len ? __ldg(table + (row >> p.page_shift)) : -1;
+        return lane < 8 && t < pc.t1 && row < pc.len ? __ldg(table + (row >> p.page_shift)) : -1;
       };
-      int page_next = entry(pc.t0);
+      auto good = [&](int page) { return page >= 0 && page < a.kv.num_pages; };
+      int pages[kAhead + 2];  // of tile t, t + 1, ...
+#pragma unroll
+      for (int i = 0; i <= kAhead; ++i) pages[i] = entry(pc.t0 + i);
       for (int t = pc.t0; t < pc.t1 && !dead; ++t, ++it) {
         const int st = it & 1, ph = (it >> 1) & 1;
-        const int page = page_next;
-        if (t + 1 < pc.t1) page_next = entry(t + 1);
+        const int page = pages[0];
+        pages[kAhead + 1] = entry(t + kAhead + 1);
         const int64_t row = (int64_t)t * kTile + lane * 8;
         const bool asked = lane < 8 && row < pc.len;
-        const bool ok = asked && page >= 0 && page < a.kv.num_pages;
+        const bool ok = asked && good(page);
         if (asked && !ok && grp == 0) flag(a.status, MT_DEV_BAD_SLOT);
+        const unsigned next = __ballot_sync(kFull, good(pages[kAhead]));
         const unsigned okm = __ballot_sync(kFull, ok);
         // visible keys: groups whose page is there, positions below the length
         uint64_t vis = 0;
@@ -414,9 +455,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if ((g & (per - 1)) == 0) boxes += okm >> g & 1;
 #pragma unroll
         for (int q = 0; q < kQuarters; ++q) {
+          if (kPair && (q & 1) != grp) continue;  // the other CTA's to load
           wait(B_KV_EMPTY + st * kQuarters + q, ph ^ 1);
           if (dead) break;
-          if (q == 0) {  // every release of the stage came after the softmax had read its old mask
+          if (q == (kPair ? grp : 0)) {  // every release of the stage came after the softmax had read its old mask
             if (lane == 0) vmask[st] = vis;
             __syncwarp();
             expect_elect(full, boxes * per * kGroup);
@@ -425,13 +467,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int h = 0; h < 2; ++h) {
             const int g = 2 * q + h;
             const int id = __shfl_sync(kFull, page, g);
-            if ((h == 0 || per == 1) && (okm >> g & 1))
-              tma_load_5d_elect(kv0 + st * kStage + g * kGroup, &tkv, 0, 0, 0,
-                                (int)((((int64_t)t * kTile) & (P - 1)) >> 3) + (g & ((P >> 3) - 1)), id, full);
+            const int at = (int)((((int64_t)t * kTile) & (P - 1)) >> 3) + (g & ((P >> 3) - 1));
+            if ((h == 0 || per == 1) && (okm >> g & 1)) {
+              if (kPair) tma_load_5d_both_elect(kv0 + st * kStage + g * kGroup, &tkv, 0, 0, 0, at, id, full);
+              else tma_load_5d_elect(kv0 + st * kStage + g * kGroup, &tkv, 0, 0, 0, at, id, full);
+            }
+            const int later = __shfl_sync(kFull, pages[kAhead], g);
+            if ((h == 0 || per == 1) && (next >> g & 1))
+              tma_prefetch_5d_elect(&tkv, 0, 0, 0,
+                                    (int)((((int64_t)(t + kAhead) * kTile) & (P - 1)) >> 3) + (g & ((P >> 3) - 1)),
+                                    later);
           }
         }
+#pragma unroll
+        for (int i = 0; i <= kAhead; ++i) pages[i] = pages[i + 1];
       }
     }
+    if (kPair)  // no arrival of the other CTA may find this one gone
+      for (uint32_t back = 0; back < kStages; ++back)
+        for (int q = grp; q < kQuarters; q += 2)
+          if (it > back) wait(B_KV_EMPTY + ((it - 1 - back) & 1) * kQuarters + q, ((it - 1 - back) >> 1) & 1);
     if (*abort) {  // let the copies in flight land (a phase that no copy ends runs out here)
       if (pieces) mbar_drain(&bars[B_Q_FULL], (pieces - 1) & 1, kDrainNs);
       for (uint32_t back = 0; back < kStages; ++back)
@@ -507,7 +562,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int m = 0; m < 4; ++m)
             mma_bf16_ss_elect(tmem + L::kO + m * N, dvs + ((k * 2 * kGroup + m * 2048) >> 4), dp + ((32 * k) >> 4),
                               idesc, j > 0 || k > 0);
-          mma_commit_elect(&bars[B_KV_EMPTY + st * kQuarters + k]);
+          if (kPair) mma_commit_to_elect(&bars[B_KV_EMPTY + st * kQuarters + k], k & 1);
+          else mma_commit_elect(&bars[B_KV_EMPTY + st * kQuarters + k]);
         }
         mma_commit_elect(&bars[B_P_EMPTY]);
       }
@@ -731,6 +787,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort) flag(a.status, MT_DEV_TIMEOUT);
+  if (kPair) {
+    if (tid == 0 && *abort) {  // what either CTA sent before it gave up lands within microseconds
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < kSettleNs) {
+      }
+    }
+    cluster_sync();
+  }
   if (warp == kQkWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kCols);
@@ -785,33 +849,62 @@ bool make_kv_map(CUtensorMap* m, const PagedCache& kv) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int N>
-cudaError_t launch(const Params& p, const CUtensorMap& tq, const CUtensorMap& tkv, cudaStream_t stream) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  static std::mutex mu;
-  static bool set[64] = {};
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (dev < 0 || dev >= 64 || !set[dev]) {
-      e = cudaFuncSetAttribute(paged_decode_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               Lay<N>::kBytes);
-      if (e != cudaSuccess) return e;
-      if (dev >= 0 && dev < 64) set[dev] = true;
-    }
-  }
+template <int N, bool kPair>
+cudaLaunchConfig_t config(int ctas, cudaLaunchAttribute (&attr)[2], cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.nteams * p.groups));
+  cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Lay<N>::kBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_decode_tc_kernel<N>, p, tq, tkv);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kPair ? 2 : 1;
+  return cfg;
+}
+
+// Makes the kernel ready on the current device, once; returns how many teams
+// fit at once (pairs: what the device's cluster placement allows).
+template <int N, bool kPair>
+cudaError_t prepare(int num_sms, int groups, int* teams) {
+  static std::mutex mu;
+  static int pairs[64] = {};  // per device; 1 where no pairs are counted
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  *teams = num_sms / groups > 0 ? num_sms / groups : 1;
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev < 0 || dev >= 64 || pairs[dev] == 0) {
+    e = cudaFuncSetAttribute(paged_decode_tc_kernel<N, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Lay<N>::kBytes);
+    if (e != cudaSuccess) return e;
+    int n = 1;
+    if (kPair) {
+      cudaLaunchAttribute attr[2];
+      cudaLaunchConfig_t cfg = config<N, kPair>(2 * *teams, attr, nullptr);
+      cfg.attrs = attr + 1;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&n, paged_decode_tc_kernel<N, kPair>, &cfg) != cudaSuccess || n <= 0)
+        return cudaErrorNotSupported;
+    }
+    if (dev >= 0 && dev < 64) pairs[dev] = n;
+    else if (kPair && n < *teams) *teams = n;
+  }
+  if (kPair && dev >= 0 && dev < 64 && pairs[dev] < *teams) *teams = pairs[dev];
+  return cudaSuccess;
+}
+
+template <int N, bool kPair = false>
+cudaError_t launch(Params& p, int num_sms, const CUtensorMap& tq, const CUtensorMap& tkv, cudaStream_t stream) {
+  const cudaError_t e = prepare<N, kPair>(num_sms, p.groups, &p.nteams);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = config<N, kPair>(p.nteams * p.groups, attr, stream);
+  return cudaLaunchKernelEx(&cfg, paged_decode_tc_kernel<N, kPair>, p, tq, tkv);
 }
 
 }  // namespace ptc
@@ -832,15 +925,15 @@ cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_
   p.page_shift = 0;
   while ((1 << p.page_shift) < P) ++p.page_shift;
   p.groups = (a.heads + N - 1) / N;
-  p.nteams = nsm / p.groups > 0 ? nsm / p.groups : 1;
   p.drop_team = g_test_drop_team;
   p.limit_ns = g_test_limit_ns > 0 ? g_test_limit_ns : sm100::kWaitLimitNs;
   CUtensorMap tq, tkv;
   if (!make_q_map(&tq, a, N) || !make_kv_map(&tkv, a.kv))
     return cudaErrorNotSupported;
-  const cudaError_t e = N == 16   ? launch<16>(p, tq, tkv, stream)
-                        : N == 32 ? launch<32>(p, tq, tkv, stream)
-                                  : launch<64>(p, tq, tkv, stream);
+  const cudaError_t e = N == 16         ? launch<16>(p, nsm, tq, tkv, stream)
+                        : N == 32       ? launch<32>(p, nsm, tq, tkv, stream)
+                        : p.groups == 2 ? launch<64, true>(p, nsm, tq, tkv, stream)
+                                        : launch<64>(p, nsm, tq, tkv, stream);
   // No request of this table can be split when it holds no more tiles than a share.
   const int64_t most = ((int64_t)a.kv.max_pages * P + kTile - 1) / kTile;
   if (e != cudaSuccess || p.nteams == 1 || (a.batch == 1 && most <= kMinShare)) return e;
