@@ -2,8 +2,7 @@
 // any page size, and the merge of split requests.
 #include <math.h>
 
-#include "mt_common.cuh"
-#include "mt_internal.h"
+#include "paged.cuh"
 
 namespace mt {
 
@@ -145,29 +144,25 @@ __global__ void __launch_bounds__(32 * kWarps) decode_simt_kernel(const DecodeAr
 
 // Joins split requests: with w_i = exp(lse_i - max lse),
 //     out = sum_i w_i o_i / sum_i w_i,  lse = max lse + ln sum_i w_i.
-// What bounds it is latency (entries, then lse and partials, from L2), so as
-// many partials as possible are loaded at once and the weights made meanwhile.
-// Requests split in a few: W warps take a (request, head, quarter of the dims),
-// a lane four dims, each warp kAheadWarp partials; W grows with the number of
-// partials and until the items fill the card. One long request over all SMs
-// leaves 152 partials a head: there a block takes a (request, head, eighth of
-// the dims), a warp load is 256 bytes of each of two partials. Sums are in a
-// fixed order, so the result is the same in every run.
+// What bounds it is latency (entries, then lse and partials, from L2), so a
+// warp has up to kAhead loads of 512 bytes in flight and makes the weights
+// meanwhile: of R quarters of a head row and the first kAhead / R partials. R
+// is 4 or 2 where requests are split in a few and their heads fill the card;
+// otherwise W warps share the partials of a quarter, W growing with their
+// number and until the items fill the card. One long request over all SMs
+// leaves 152 partials a head and few heads: there a block takes an eighth of a
+// head row, a warp load being 256 bytes of each of two partials, all in flight
+// at once. Sums are in a fixed order, so the result is the same in every run.
 constexpr int kMergeThreads = 256;
 constexpr int kMergeWarps = kMergeThreads / 32;
-constexpr int kMergeBlocksPerSm = 3;
-constexpr int kMaxParts = 1024;
+constexpr int kMergeBlocksPerSm = 2;
+constexpr int kMaxEntries = 512;
+constexpr int kAhead = 16;
 constexpr int kQuarter = kDv / 4;
 constexpr int kEighth = kDv / 8;
-constexpr int kAheadWarp = 8;                      // partials in flight of a lane, one warp (divides 32)
 constexpr int kHalfWarps = kMergeThreads / 16;
-constexpr int kAheadBlock = 10;                    // and of a lane, one block: 160 partials
-
-// Rows and items count in 32 bits: the workspace has fewer than 2^31 rows, and
-// a 64-bit division costs more than an item's arithmetic.
-__device__ __forceinline__ int64_t part_row(const MergeEntry& e, int i, int step, int rows_per_slot) {
-  return (int)((i == 0 ? e.first : e.next + (i - 1) * step) * rows_per_slot);
-}
+constexpr int kAheadBlock = 10;   // partials in flight of a lane of a block: 160 a block
+constexpr int kManyParts = 48;    // partials of a request from which blocks take over
 
 __device__ __forceinline__ float weight(float lse, float mx) {
   return lse == -INFINITY ? 0.f : exp2f((lse - mx) * kLog2e);
@@ -197,13 +192,145 @@ __device__ __forceinline__ void write_dims(const DecodeArgs& a, int64_t row, int
       make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
-__global__ void __launch_bounds__(kMergeThreads, kMergeBlocksPerSm) paged_merge_kernel(const DecodeArgs a, const int entries,
-                                                                    const int step, const int rows_per_slot) {
-  __shared__ MergeEntry list[kMaxParts];
-  __shared__ float wt[kMaxParts];
-  __shared__ float4 acc[kMergeWarps][32];
-  __shared__ float red[kMergeWarps], tots[kMergeWarps];
-  __shared__ int counts[kMergeWarps], sums[kMergeWarps];
+struct MergeShared {
+  MergeEntry list[kMaxEntries];
+  float4 acc[kMergeWarps][32];
+  float wt[kMaxEntries], red[kMergeWarps], tots[kMergeWarps];
+  int counts[kMergeWarps], sums[kMergeWarps];
+};
+
+// Items of R quarters, W = 2^wl warps each (R > 1: W = 1). Counts are in 32
+// bits: a 64-bit division costs more than an item's arithmetic.
+template <int R>
+__device__ __forceinline__ void merge_items(const DecodeArgs& a, MergeShared& sh, unsigned n, int step, int rows, int wl) {
+  constexpr int kParts = kAhead / R;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int W = 1 << wl, sub = warp & (W - 1);
+  const unsigned H = a.heads, items = n * H * (4 / R), per = kMergeWarps >> wl;
+  for (unsigned base = blockIdx.x * per; base < items; base += gridDim.x * per) {
+    const unsigned it = base + (warp >> wl), eh = it / (4 / R), en = eh / H;
+    const bool mine = it < items;
+    const int dim = (int)(it % (4 / R)) * R * kQuarter + 4 * lane, h = (int)(eh - en * H);
+    const MergeEntry e = mine ? sh.list[en] : MergeEntry{0, 0, 0, 0};
+    // the workspace has fewer than 2^31 rows
+    auto row_of = [&](int i) { return (int64_t)((i == 0 ? e.first : e.next + (i - 1) * step) * rows + h); };
+    auto lse_of = [&](int i) { return i < e.n ? __ldcg(a.ws_lse + row_of(i)) : -INFINITY; };
+    float4 v[kParts][R];
+    auto load = [&](int k0) {  // this warp's partials are sub + W k
+#pragma unroll
+      for (int k = 0; k < kParts; ++k)
+        if (sub + ((k0 + k) << wl) < e.n) {
+          const float* src = a.ws_o + row_of(sub + ((k0 + k) << wl)) * kDv + dim;
+#pragma unroll
+          for (int r = 0; r < R; ++r) v[k][r] = __ldcg(reinterpret_cast<const float4*>(src + r * kQuarter));
+        }
+    };
+    load(0);
+    // lane l: partial l for the maximum, this warp's l-th partial for its weight
+    const float seen = lse_of(lane), own = wl == 0 ? seen : lse_of(sub + (lane << wl));
+    float mx = not_nan(seen);
+    for (int i = 32 + lane; i < e.n; i += 32) mx = fmaxf(mx, not_nan(lse_of(i)));
+    mx = warp_max(mx);
+    float4 s[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) s[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float tot = 0.f, w = weight(own, mx);
+    for (int k0 = 0; sub + (k0 << wl) < e.n; k0 += kParts) {
+      if (k0 > 0) {
+        load(k0);
+        if ((k0 & 31) == 0) w = weight(lse_of(sub + ((k0 + lane) << wl)), mx);
+      }
+#pragma unroll
+      for (int k = 0; k < kParts; ++k)
+        if (sub + ((k0 + k) << wl) < e.n) {
+          const float wk = __shfl_sync(kFull, w, (k0 + k) & 31);
+          tot += wk;
+#pragma unroll
+          for (int r = 0; r < R; ++r) add(s[r], wk, v[k][r]);
+        }
+    }
+    if (R == 1 && W > 1) {
+      __syncthreads();  // the item before has been read
+      sh.acc[warp][lane] = s[0];
+      if (lane == 0) sh.tots[warp] = tot;
+      __syncthreads();
+      if (sub == 0)
+        for (int k = 1; k < W; ++k) {
+          tot += sh.tots[warp + k];
+          add(s[0], 1.f, sh.acc[warp + k][lane]);
+        }
+    }
+    if (!mine || sub != 0) continue;
+    const int64_t row = (int64_t)e.b * a.heads + h;
+#pragma unroll
+    for (int r = 0; r < R; ++r) write_dims(a, row, dim + r * kQuarter, tot, s[r]);
+    if (dim == 0) a.lse[row] = tot != 0.f ? mx + logf(tot) : -INFINITY;
+  }
+}
+
+__device__ __forceinline__ void merge_blocks(const DecodeArgs& a, MergeShared& sh, unsigned n, int step, int rows) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, grp = tid >> 4;
+  const unsigned H = a.heads;
+  for (unsigned it = blockIdx.x; it < n * H * 8; it += gridDim.x) {
+    const int dim = (int)(it & 7) * kEighth + 4 * (tid & 15);
+    const unsigned en = (it >> 3) / H;
+    const MergeEntry e = sh.list[en];
+    const int h = (int)((it >> 3) - en * H);
+    auto row_of = [&](int i) { return (int64_t)((i == 0 ? e.first : e.next + (i - 1) * step) * rows + h); };
+    auto part = [&](int i) { return __ldcg(reinterpret_cast<const float4*>(a.ws_o + row_of(i) * kDv + dim)); };
+    float4 v[kAheadBlock];
+#pragma unroll
+    for (int k = 0; k < kAheadBlock; ++k)
+      if (grp + kHalfWarps * k < e.n) v[k] = part(grp + kHalfWarps * k);
+    float mx = -INFINITY;
+    for (int i = tid; i < e.n; i += kMergeThreads) {
+      sh.wt[i] = __ldcg(a.ws_lse + row_of(i));
+      mx = fmaxf(mx, not_nan(sh.wt[i]));
+    }
+    mx = warp_max(mx);
+    if (lane == 0) sh.red[warp] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) mx = fmaxf(mx, sh.red[w]);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    float tot = 0.f;
+#pragma unroll
+    for (int k = 0; k < kAheadBlock; ++k)
+      if (grp + kHalfWarps * k < e.n) {
+        const float w = weight(sh.wt[grp + kHalfWarps * k], mx);
+        tot += w;
+        add(s, w, v[k]);
+      }
+    for (int i = grp + kHalfWarps * kAheadBlock; i < e.n; i += kHalfWarps) {
+      const float w = weight(sh.wt[i], mx);
+      tot += w;
+      add(s, w, part(i));
+    }
+    tot += __shfl_xor_sync(kFull, tot, 16);
+    s.x += __shfl_xor_sync(kFull, s.x, 16);
+    s.y += __shfl_xor_sync(kFull, s.y, 16);
+    s.z += __shfl_xor_sync(kFull, s.z, 16);
+    s.w += __shfl_xor_sync(kFull, s.w, 16);
+    if (lane < 16) sh.acc[warp][lane] = s;
+    if (lane == 0) sh.tots[warp] = tot;
+    __syncthreads();
+    if (tid < 16) {
+#pragma unroll
+      for (int w = 1; w < kMergeWarps; ++w) {
+        tot += sh.tots[w];
+        add(s, 1.f, sh.acc[w][lane]);
+      }
+      const int64_t row = (int64_t)e.b * a.heads + h;
+      write_dims(a, row, dim, tot, s);
+      if (dim == 0) a.lse[row] = tot != 0.f ? mx + logf(tot) : -INFINITY;
+    }
+    __syncthreads();  // wt, red, acc and tots are free for the next item
+  }
+}
+
+__global__ void __launch_bounds__(kMergeThreads, kMergeBlocksPerSm)
+    paged_merge_kernel(const DecodeArgs a, const int entries, const int step, const int rows) {
+  __shared__ MergeShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -213,151 +340,31 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeBlocksPerSm) paged_merge_
     if (base + tid < entries) u = __ldcg(reinterpret_cast<const int4*>(a.ws_entry + base + tid));
     const unsigned any = __ballot_sync(kFull, u.y > 0);
     const int sum = __reduce_add_sync(kFull, u.y);
-    if (lane == 0) counts[warp] = __popc(any), sums[warp] = sum;
+    if (lane == 0) sh.counts[warp] = __popc(any), sh.sums[warp] = sum;
     __syncthreads();
     int at = n + __popc(any & ((1u << lane) - 1));
 #pragma unroll
     for (int w = 0; w < kMergeWarps; ++w) {
-      if (w < warp) at += counts[w];
-      n += counts[w];
-      parts += sums[w];
+      if (w < warp) at += sh.counts[w];
+      n += sh.counts[w];
+      parts += sh.sums[w];
     }
-    if (u.y > 0) list[at] = {u.x, u.y, u.z, u.w};
+    if (u.y > 0) sh.list[at] = {u.x, u.y, u.z, u.w};
     __syncthreads();
   }
-
   if (n == 0) return;
-  const unsigned heads = (unsigned)n * a.heads, H = a.heads;
+  const unsigned heads = (unsigned)n * a.heads, warps = gridDim.x * kMergeWarps;
   const int each = (parts + n - 1) / n;
-
-  if (each <= kMergeWarps * kAheadWarp) {
-    const unsigned items = heads * 4;
-    int wl = 0;  // W = 2^wl
-    while ((1 << wl) < kMergeWarps &&
-           (each > (kAheadWarp << wl) || (items << (wl + 1)) <= gridDim.x * (unsigned)kMergeWarps))
-      ++wl;
-    const int W = 1 << wl;
-    const int sub = warp & (W - 1);
-    const unsigned per = kMergeWarps >> wl;
-    for (unsigned base = blockIdx.x * per; base < items; base += gridDim.x * per) {
-      const unsigned it = base + (warp >> wl);
-      const bool mine = it < items;
-      const int dim = (int)(it & 3) * kQuarter + 4 * lane;
-      const unsigned entry = (it >> 2) / H;
-      const MergeEntry e = mine ? list[entry] : MergeEntry{0, 0, 0, 0};
-      const int h = (int)((it >> 2) - entry * H);
-      const float* src = a.ws_o + h * kDv + dim;
-      float4 v[kAheadWarp];
-      auto load = [&](int k0) {  // this warp's partials are sub + W k
-#pragma unroll
-        for (int k = 0; k < kAheadWarp; ++k)
-          if (sub + ((k0 + k) << wl) < e.n)
-            v[k] = __ldcg(reinterpret_cast<const float4*>(
-                src + part_row(e, sub + ((k0 + k) << wl), step, rows_per_slot) * kDv));
-      };
-      auto lse_of = [&](int i) {
-        return i < e.n ? __ldcg(a.ws_lse + part_row(e, i, step, rows_per_slot) + h) : -INFINITY;
-      };
-      load(0);
-      // lane l: partial l for the maximum, this warp's l-th partial for its weight
-      const float seen = lse_of(lane), own = wl == 0 ? seen : lse_of(sub + (lane << wl));
-      float mx = not_nan(seen);
-      for (int i = 32 + lane; i < e.n; i += 32) mx = fmaxf(mx, not_nan(lse_of(i)));
-      mx = warp_max(mx);
-      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      float tot = 0.f, w = weight(own, mx);
-      for (int k0 = 0; sub + (k0 << wl) < e.n; k0 += kAheadWarp) {
-        if (k0 > 0) {
-          load(k0);
-          if ((k0 & 31) == 0) w = weight(lse_of(sub + ((k0 + lane) << wl)), mx);
-        }
-#pragma unroll
-        for (int k = 0; k < kAheadWarp; ++k)
-          if (sub + ((k0 + k) << wl) < e.n) {
-            const float wk = __shfl_sync(kFull, w, (k0 + k) & 31);
-            tot += wk;
-            add(s, wk, v[k]);
-          }
-      }
-      if (W > 1) {
-        __syncthreads();  // the item before has been read
-        acc[warp][lane] = s;
-        if (lane == 0) tots[warp] = tot;
-        __syncthreads();
-        if (sub == 0)
-          for (int k = 1; k < W; ++k) {
-            tot += tots[warp + k];
-            add(s, 1.f, acc[warp + k][lane]);
-          }
-      }
-      if (mine && sub == 0) {
-        const int64_t row = (int64_t)e.b * a.heads + h;
-        write_dims(a, row, dim, tot, s);
-        if (dim == 0) a.lse[row] = tot != 0.f ? mx + logf(tot) : -INFINITY;
-      }
-    }
-    return;
-  }
-
-  const int grp = tid >> 4, li = tid & 15;
-  for (unsigned it = blockIdx.x; it < heads * 8; it += gridDim.x) {
-    const int dim = (int)(it & 7) * kEighth + 4 * li;
-    const unsigned entry = (it >> 3) / H;
-    const MergeEntry e = list[entry];
-    const int h = (int)((it >> 3) - entry * H);
-    const float* src = a.ws_o + h * kDv + dim;
-    float4 v[kAheadBlock];
-#pragma unroll
-    for (int k = 0; k < kAheadBlock; ++k) {
-      const int i = grp + kHalfWarps * k;
-      if (i < e.n) v[k] = __ldcg(reinterpret_cast<const float4*>(src + part_row(e, i, step, rows_per_slot) * kDv));
-    }
-    float mx = -INFINITY;
-    for (int i = tid; i < e.n; i += kMergeThreads) {
-      const float l = __ldcg(a.ws_lse + part_row(e, i, step, rows_per_slot) + h);
-      wt[i] = l;
-      mx = fmaxf(mx, not_nan(l));
-    }
-    mx = warp_max(mx);
-    if (lane == 0) red[warp] = mx;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) mx = fmaxf(mx, red[w]);
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    float tot = 0.f;
-#pragma unroll
-    for (int k = 0; k < kAheadBlock; ++k) {
-      const int i = grp + kHalfWarps * k;
-      if (i < e.n) {
-        const float w = weight(wt[i], mx);
-        tot += w;
-        add(s, w, v[k]);
-      }
-    }
-    for (int i = grp + kHalfWarps * kAheadBlock; i < e.n; i += kHalfWarps) {
-      const float w = weight(wt[i], mx);
-      tot += w;
-      add(s, w, __ldcg(reinterpret_cast<const float4*>(src + part_row(e, i, step, rows_per_slot) * kDv)));
-    }
-    tot += __shfl_xor_sync(kFull, tot, 16);
-    s.x += __shfl_xor_sync(kFull, s.x, 16);
-    s.y += __shfl_xor_sync(kFull, s.y, 16);
-    s.z += __shfl_xor_sync(kFull, s.z, 16);
-    s.w += __shfl_xor_sync(kFull, s.w, 16);
-    if (lane < 16) acc[warp][lane] = s;
-    if (lane == 0) tots[warp] = tot;
-    __syncthreads();
-    if (tid < 16) {
-#pragma unroll
-      for (int w = 1; w < kMergeWarps; ++w) {
-        tot += tots[w];
-        add(s, 1.f, acc[w][lane]);
-      }
-      const int64_t row = (int64_t)e.b * a.heads + h;
-      write_dims(a, row, dim, tot, s);
-      if (dim == 0) a.lse[row] = tot != 0.f ? mx + logf(tot) : -INFINITY;
-    }
-    __syncthreads();  // wt, red, acc and tots are free for the next item
+  if (each > kManyParts) {
+    merge_blocks(a, sh, n, step, rows);
+  } else if (each <= kAhead / 4 && heads >= warps) {
+    merge_items<4>(a, sh, n, step, rows, 0);
+  } else if (each <= kAhead / 2 && heads * 2 >= warps) {
+    merge_items<2>(a, sh, n, step, rows, 0);
+  } else {
+    int wl = 0;
+    while ((1 << wl) < kMergeWarps && (each > (kAhead << wl) || (heads * 4 << (wl + 1)) <= warps)) ++wl;
+    merge_items<1>(a, sh, n, step, rows, wl);
   }
 }
 

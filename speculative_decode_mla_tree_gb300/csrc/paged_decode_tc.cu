@@ -37,8 +37,7 @@
 
 #include <mutex>
 
-#include "mt_common.cuh"
-#include "mt_internal.h"
+#include "paged.cuh"
 #include "sm100_ptx.cuh"
 
 namespace mt {
@@ -83,8 +82,7 @@ struct Lay {
   static constexpr int kP = kKV + kStages * kStage;     // [N heads][64 keys] bf16, 128B swizzle
   static constexpr int kBars = kP + N * 128;
   static constexpr int kMask = kBars + kNumBars * 8;    // per stage: the tile's visible keys
-  static constexpr int kPlan = kMask + kStages * 8;     // 14 x int64
-  static constexpr int kMisc = kPlan + 14 * 8;          // tmem base, abort flag
+  static constexpr int kMisc = kMask + kStages * 8;     // tmem base, abort flag
   static constexpr int kRed = (kMisc + 8 + 15) / 16 * 16;  // [4][N] fp32
   static constexpr int kVec = kRed + 4 * N * 4;         // [N] fp32
   static constexpr int kUsed = kVec + N * 4;
@@ -99,6 +97,7 @@ struct Lay {
 struct Params {
   DecodeArgs a;
   int page_shift;
+  int most;                     // positions a request's table holds
   int groups;                   // head groups = CTAs per team
   int nteams;
   int drop_team;                // test hook: this team's and later producers issue nothing (-1: off)
@@ -243,11 +242,9 @@ __device__ __forceinline__ bool bar_any(int id, int nthreads, bool v) {
 
 // --------------------------------------------------------------------- plan
 
-__device__ __forceinline__ bool length_ok(const DecodeArgs& a, int len) {
-  return len >= 0 && len <= (int64_t)a.kv.max_pages * a.kv.page_size;
-}
-__device__ __forceinline__ int tiles_of(const DecodeArgs& a, int len) {
-  return length_ok(a, len) ? (int)(((int64_t)len + kTile - 1) / kTile) : 0;
+__device__ __forceinline__ bool length_ok(const Params& p, int len) { return (unsigned)len <= (unsigned)p.most; }
+__device__ __forceinline__ int tiles_of(const Params& p, int len) {
+  return length_ok(p, len) ? (int)(((unsigned)len + kTile - 1) / kTile) : 0;
 }
 
 // A team's walk over its share [s, e) of the line of tiles. Each role keeps
@@ -262,13 +259,14 @@ struct Piece {
   bool ok;
 };
 
-__device__ __forceinline__ bool next_piece(const DecodeArgs& a, Walk& w, Piece& p) {
+__device__ __forceinline__ bool next_piece(const Params& prm, Walk& w, Piece& p) {
+  const DecodeArgs& a = prm.a;
   while (w.b < a.batch && w.o < w.e) {
     p.b = w.b;
     p.o = w.o;
     p.len = __ldg(a.kv.lens + w.b);
-    p.ok = length_ok(a, p.len);
-    p.tiles = tiles_of(a, p.len);
+    p.ok = length_ok(prm, p.len);
+    p.tiles = tiles_of(prm, p.len);
     const int64_t first = w.o + kOverhead;  // the request's tiles start here
     const int64_t t0 = w.s - first, t1 = w.e - first;
     p.t0 = (int)(t0 > 0 ? (t0 < p.tiles ? t0 : p.tiles) : 0);
@@ -280,52 +278,33 @@ __device__ __forceinline__ bool next_piece(const DecodeArgs& a, Walk& w, Piece& 
   return false;
 }
 
-__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  return v;
-}
-
-// The share size and where this team's share starts, by all threads. A batch
-// of up to kThreads requests takes one round of loads and two barriers.
-__device__ Walk make_plan(const Params& p, int team, int64_t* sh, int64_t* share_out) {
-  const DecodeArgs& a = p.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kW = kThreads / 32;
-  auto units = [&](int b) { return b < a.batch ? (int64_t)kOverhead + tiles_of(a, __ldg(a.kv.lens + b)) : 0; };
-  int64_t rest = 0;  // requests behind the first kThreads
-  if (a.batch > kThreads) {
-    for (int b = kThreads + tid; b < a.batch; b += kThreads) rest += units(b);
-    rest = warp_sum64(rest);
-    if (lane == 0) sh[warp] = rest;
-    __syncthreads();
-    rest = 0;
-#pragma unroll
-    for (int w = 0; w < kW; ++w) rest += sh[w];
-    __syncthreads();
-  }
+// The share size and where this team's share starts. Every warp works it out
+// by itself, so that no role waits for another: the 32 lanes sum up equal runs
+// of requests, and the run that holds the start is cut into 32 again (one round
+// of loads and one scan up to 32 requests, two up to 1024).
+__device__ __forceinline__ Walk make_plan(const Params& p, int team, int64_t* share_out) {
+  const int lane = threadIdx.x & 31;
   Walk r;
-  r.b = a.batch;
-  r.o = r.s = r.e = 0;
-  int64_t run = 0;
-  for (int base = 0; base < a.batch; base += kThreads) {
-    const int64_t u = units(base + tid);
+  r.s = r.e = r.o = 0;
+  r.b = p.a.batch;
+  int lo = 0, n = p.a.batch, c;
+  bool first = true;
+  do {
+    c = (n + 31) / 32;
+    int64_t u = 0;
+    for (int k = 0; k < c; ++k) {
+      const int i = lane * c + k;
+      if (i < n) u += kOverhead + tiles_of(p, __ldg(p.a.kv.lens + lo + i));
+    }
     int64_t inc = u;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t v = __shfl_up_sync(kFull, inc, o);
       if (lane >= o) inc += v;
     }
-    if (lane == 31) sh[warp] = inc;
-    __syncthreads();
-    int64_t at = run + inc - u, sum = 0;
-#pragma unroll
-    for (int w = 0; w < kW; ++w) {
-      if (w < warp) at += sh[w];
-      sum += sh[w];
-    }
-    if (base == 0) {
-      const int64_t total = sum + rest;
+    if (first) {
+      first = false;
+      const int64_t total = __shfl_sync(kFull, inc, 31);
       // (a 64-bit division takes longer than the rest of this function)
       int64_t share = total <= INT32_MAX ? (int64_t)(((uint32_t)total + p.nteams - 1) / (uint32_t)p.nteams)
                                          : (total + p.nteams - 1) / p.nteams;
@@ -333,18 +312,15 @@ __device__ Walk make_plan(const Params& p, int team, int64_t* sh, int64_t* share
       *share_out = share;
       r.s = team * share;
       r.e = r.s + share;
-      if (r.s >= total) return r;  // nothing for this team (the same for all threads)
+      if (r.s >= total) return r;  // nothing for this team
     }
-    run += sum;
-    if (u > 0 && at <= r.s && r.s < at + u) {
-      sh[kW] = base + tid;
-      sh[kW + 1] = at;
-    }
-    __syncthreads();
-    if (run > r.s) break;
-  }
-  r.b = (int)sh[kW];
-  r.o = sh[kW + 1];
+    const int64_t at = r.o + inc - u;
+    const int src = __ffs(__ballot_sync(kFull, u > 0 && at <= r.s && r.s < at + u)) - 1;
+    r.o = __shfl_sync(kFull, at, src);
+    lo += src * c;
+    n = min(c, n - src * c);
+  } while (c > 1);
+  r.b = lo;
   return r;
 }
 
@@ -361,7 +337,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBars);
   uint64_t* vmask = reinterpret_cast<uint64_t*>(sm + L::kMask);
-  int64_t* plan = reinterpret_cast<int64_t*>(sm + L::kPlan);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(sm + L::kMisc + 4);
   float* red = reinterpret_cast<float*>(sm + L::kRed);
@@ -389,16 +364,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tq);
     prefetch_tmap(&tkv);
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the merge may be set up from here on; it waits for this grid's completion
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int64_t share = 1;
+  Walk walk = make_plan(p, team, &share);  // its loads run beside the set-up above
   tc_fence_before();
   if (kPair) cluster_sync();  // the other CTA's barriers are there
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  // the merge may be set up from here on; it waits for this grid's completion
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int64_t share;
-  Walk walk = make_plan(p, team, plan, &share);
   Piece pc;
 
   if (warp == kProducerWarp) {
@@ -412,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](int bar, uint32_t parity) {
       if (!dead) dead = __any_sync(kFull, !wait_phase(&bars[bar], parity, abort, limit));
     };
-    while (!dead && next_piece(a, walk, pc)) {
+    while (!dead && next_piece(p, walk, pc)) {
       if (pc.t1 <= pc.t0) continue;
       wait(B_Q_EMPTY, (pieces & 1) ^ 1);
       if (dead) break;
@@ -506,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](int bar, uint32_t parity) {
       if (!dead) dead = __any_sync(kFull, !wait_phase(&bars[bar], parity, abort, limit));
     };
-    while (!dead && next_piece(a, walk, pc)) {
+    while (!dead && next_piece(p, walk, pc)) {
       const int n = __shfl_sync(kFull, pc.t1 - pc.t0, 0);
       if (n <= 0) continue;
       wait(B_Q_FULL, pieces & 1);
@@ -545,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](int bar, uint32_t parity) {
       if (!dead) dead = __any_sync(kFull, !wait_phase(&bars[bar], parity, abort, limit));
     };
-    while (!dead && next_piece(a, walk, pc)) {
+    while (!dead && next_piece(p, walk, pc)) {
       const int n = __shfl_sync(kFull, pc.t1 - pc.t0, 0);
       if (n <= 0) continue;
       wait(B_O_EMPTY, (pieces & 1) ^ 1);
@@ -594,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     MergeEntry entry = {0, 0, 0, 0};
     uint32_t it = 0;
     bool dead = false;
-    while (next_piece(a, walk, pc)) {
+    while (next_piece(p, walk, pc)) {
       const int64_t orow = (int64_t)pc.b * a.heads + grp * N;
       const int nh = min(N, a.heads - grp * N);
       if (pc.t1 <= pc.t0) {  // no keys
@@ -751,20 +726,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_ld_wait();
         tmem_regs_ready(o);
-        const int dim = m * 128 + quad * 32 + lane;
         // all products before the first store: it might change the factors for all the compiler knows
+        float v[NC];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * redh[c]);
+        for (int c = 0; c < NC; ++c) v[c] = __uint_as_float(o[c]) * redh[c];
+        const int dim = m * 128 + quad * 32;
         if (whole) {
           uint16_t* dst = a.out + (orow + c0) * kDv + dim;
 #pragma unroll
-          for (int c = 0; c < NC; ++c)
-            if (c0 + c < nh) dst[c * kDv] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(o[c])));
+          for (int c = 0; c < NC; c += 4) {
+            const float x[4] = {v[c], v[c + 1], v[c + 2], v[c + 3]};
+            store_heads4(dst + c * kDv, lane, x, nh - c0 - c);
+          }
         } else {
-          float* dst = a.ws_o + (wrow + c0) * kDv + dim;
+          float* dst = a.ws_o + (wrow + c0) * kDv + dim + lane;
 #pragma unroll
           for (int c = 0; c < NC; ++c)
-            if (c0 + c < nh) dst[c * kDv] = __uint_as_float(o[c]);
+            if (c0 + c < nh) dst[c * kDv] = v[c];
         }
       }
       tc_fence_before();
@@ -924,6 +902,7 @@ cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_
   p.a = a;
   p.page_shift = 0;
   while ((1 << p.page_shift) < P) ++p.page_shift;
+  p.most = a.kv.max_pages * P;
   p.groups = (a.heads + N - 1) / N;
   p.drop_team = g_test_drop_team;
   p.limit_ns = g_test_limit_ns > 0 ? g_test_limit_ns : sm100::kWaitLimitNs;
