@@ -322,63 +322,81 @@ def mla_tree_verify_noalloc(q, kv_buf, kv_indices, kv_indptr, qo_indptr, packed_
 
 ROPE_PAIRS, ROPE_HALVES = 0, 1
 
-# The paged calls run once per layer and token, where their own time shows:
-# each argument is checked with a handful of attribute reads.
+# The paged calls run once per layer and token, where their own time shows: all
+# arguments are checked in one expression, and a call that fails it goes through
+# the checks again one by one for its message.
 
 
-def _refuse(t, dtype, dev, shape, name, more):
+def _refuse(name, t, dtype, dim, dev, shape=None, whole=False):
+    """Raises what is wrong with one tensor, if anything is."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise MlaTreeError("%s must be a CUDA tensor" % name)
-    if t.get_device() != dev:
+    want = "%s must be %s" % (name, dtype)
+    if t.dtype != dtype:
+        raise MlaTreeError("%s, got %s" % (want, t.dtype))
+    if dev is not None and t.get_device() != dev:
         raise MlaTreeError("%s is on %s, the cache on cuda:%d" % (name, t.device, dev))
-    raise MlaTreeError("%s must be %s %s, %s; got %s %s with strides %s"
-                       % (name, dtype, tuple(shape), more, t.dtype, tuple(t.shape), t.stride()))
+    if t.dim() != dim or shape is not None and tuple(t.shape) != tuple(shape):
+        raise MlaTreeError("%s %s, got %s" % (want, "of %d dimensions" % dim if shape is None else list(shape),
+                                              list(t.shape)))
+    if whole and not t.is_contiguous():
+        raise MlaTreeError("%s must be contiguous" % name)
+    if dim and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise MlaTreeError("%s must have unit stride in its last dimension" % name)
 
 
-def _strided(t, dtype, dev, shape, name):
-    """Strides of a CUDA tensor of that type, device and shape, the last one 1."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
-        _refuse(t, dtype, dev, shape, name, "with unit stride in the last dimension")
-    st = t.stride()
-    if st[-1] != 1 and shape[-1] > 1:
-        _refuse(t, dtype, dev, shape, name, "with unit stride in the last dimension")
-    return st
-
-
-def _whole(t, dtype, dev, shape, name):
-    """Address of a contiguous CUDA tensor of that type, device and shape."""
-    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or t.shape != shape
-            or not t.is_contiguous()):
-        _refuse(t, dtype, dev, shape, name, "contiguous")
-    return t.data_ptr()
-
-
-def _paged(cache, block_table, kv_lens):
-    """((cache arguments), (table arguments), kv_lens, batch, device index), checked."""
-    if not isinstance(cache, torch.Tensor) or not cache.is_cuda:
-        raise MlaTreeError("cache must be a CUDA tensor")
-    if not isinstance(block_table, torch.Tensor) or cache.dim() != 3 or block_table.dim() != 2:
-        raise MlaTreeError("cache must be [num_pages, page_size, 576] and block_table [batch, max_pages]")
+def _refuse_paged(cache, block_table, kv_lens):
+    _refuse("cache", cache, torch.bfloat16, 3, None)
     dev = cache.get_device()
-    pages, size, _ = cache.shape
-    st = _strided(cache, torch.bfloat16, dev, (pages, size, 576), "cache")
-    if size > 1 and st[1] != 576:
-        raise MlaTreeError("cache must hold a page's rows of 576 elements one after another")
-    batch, max_pages = shape = block_table.shape
-    tst = _strided(block_table, torch.int32, dev, shape, "block_table")
-    lens = _whole(kv_lens, torch.int32, dev, (batch,), "kv_lens")
-    return ((cache.data_ptr(), st[0] if pages > 1 else size * 576, pages, size),
-            (block_table.data_ptr(), tst[0] if batch > 1 else max_pages, max_pages), lens, batch, dev)
+    if cache.shape[1] < 1 or cache.shape[2] != 576 or cache.shape[1] > 1 and cache.stride(1) != 576:
+        raise MlaTreeError("cache must be [num_pages, page_size, 576] with a page's rows one after another")
+    _refuse("block_table", block_table, torch.int32, 2, dev)
+    _refuse("kv_lens", kv_lens, torch.int32, 1, dev, (block_table.shape[0],), True)
+    return dev
 
 
-def _status(status, dev):
-    return None if status is None else _whole(status, torch.int32, dev, status.shape, "status")
+def _refuse_append(latent, k_rope, qo_indptr, kv_lens, block_table, cache, rope_table, q_rope, q_out, positions,
+                   norm_weight, status):
+    dev = _refuse_paged(cache, block_table, kv_lens)
+    bf16, i32 = torch.bfloat16, torch.int32
+    _refuse("latent", latent, bf16, 2, dev)
+    t = latent.shape[0]
+    _refuse("latent", latent, bf16, 2, dev, (t, 512))
+    _refuse("k_rope", k_rope, bf16, 2, dev, (t, 64))
+    _refuse("qo_indptr", qo_indptr, i32, 1, dev, (block_table.shape[0] + 1,), True)
+    _refuse("rope_table", rope_table, torch.float32, 2, dev)
+    _refuse("rope_table", rope_table, torch.float32, 2, dev, (rope_table.shape[0], 64), True)
+    if (q_rope is None) != (q_out is None):
+        raise MlaTreeError("q_rope and q_out go together")
+    if q_rope is not None:
+        _refuse("q_rope", q_rope, bf16, 3, dev)
+        _refuse("q_rope", q_rope, bf16, 3, dev, (t, q_rope.shape[1], 64))
+        _refuse("q_out", q_out, bf16, 3, dev, q_rope.shape)
+    if positions is not None:
+        _refuse("positions", positions, i32, 1, dev, (t,), True)
+    if norm_weight is not None:
+        _refuse("norm_weight", norm_weight, bf16, 1, dev, (512,), True)
+    if status is not None:
+        _refuse("status", status, i32, status.dim() if isinstance(status, torch.Tensor) else 1, dev, None, True)
+    raise MlaTreeError("unsupported arguments")
+
+
+def _refuse_decode(q, cache, block_table, kv_lens, out, lse, workspace, status):
+    dev = _refuse_paged(cache, block_table, kv_lens)
+    _refuse("q", q, torch.bfloat16, 3, dev)
+    batch, heads = block_table.shape[0], q.shape[1]
+    _refuse("q", q, torch.bfloat16, 3, dev, (batch, heads, 576))
+    _refuse("out", out, torch.bfloat16, 3, dev, (batch, heads, 512), True)
+    _refuse("lse", lse, torch.float32, 2, dev, (batch, heads), True)
+    _refuse("workspace", workspace, torch.uint8, 1, dev, None, True)
+    if status is not None:
+        _refuse("status", status, torch.int32, status.dim() if isinstance(status, torch.Tensor) else 1, dev, None, True)
+    raise MlaTreeError("unsupported arguments")
 
 
 def _call(dev, stream, fn, *args):
     """fn(*args, stream) with dev current: the stream given, or dev's current one."""
-    now = torch._C._cuda_getDevice()
-    if now != dev:
+    if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return _call(dev, stream, fn, *args)
     return fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
@@ -392,29 +410,55 @@ def mla_paged_append(latent, k_rope, qo_indptr, kv_lens, block_table, cache, rop
     [T, 64] rotated to its position, at position kv_lens[b] - n_b + i of
     request b's pages block_table[b]; and q_out = q_rope [T, H, 64] rotated
     alike (q_out may be q_rope). rope_table: fp32 [positions, 64], cos | sin."""
-    c, table, lens, batch, dev = _paged(cache, block_table, kv_lens)
     bf16, i32 = torch.bfloat16, torch.int32
-    t = latent.shape[0] if isinstance(latent, torch.Tensor) and latent.dim() else 0
-    ls = _strided(latent, bf16, dev, (t, 512), "latent")
-    ks = _strided(k_rope, bf16, dev, (t, 64), "k_rope")
-    indptr = _whole(qo_indptr, i32, dev, (batch + 1,), "qo_indptr")
-    angles = rope_table.shape[0] if isinstance(rope_table, torch.Tensor) and rope_table.dim() else 0
-    rope = _whole(rope_table, torch.float32, dev, (angles, 64), "rope_table")
     heads, q, qs, o, os_ = 0, None, (0, 0), None, (0, 0)
-    if (q_rope is None) != (q_out is None):
-        raise MlaTreeError("q_rope and q_out go together")
-    if q_rope is not None:
-        heads = q_rope.shape[1] if isinstance(q_rope, torch.Tensor) and q_rope.dim() > 1 else 0
-        qs = _strided(q_rope, bf16, dev, (t, heads, 64), "q_rope")
-        os_ = _strided(q_out, bf16, dev, (t, heads, 64), "q_out")
-        if heads:
-            q, o = q_rope.data_ptr(), q_out.data_ptr()
+    try:
+        dev = cache.get_device()
+        pages, size, width = cache.shape
+        batch, max_pages = block_table.shape
+        t = latent.shape[0]
+        angles = rope_table.shape[0]
+        cs, ts, ls, ks = cache.stride(), block_table.stride(), latent.stride(), k_rope.stride()
+        ok = (dev >= 0 and width == 576 and size > 0 and cs[2] == 1 and (cs[1] == 576 or size == 1)
+              and cache.dtype is bf16 and (ts[1] == 1 or max_pages < 2) and block_table.dtype is i32
+              and block_table.get_device() == dev
+              and kv_lens.shape == (batch,) and kv_lens.dtype is i32 and kv_lens.get_device() == dev
+              and kv_lens.is_contiguous()
+              and latent.shape == (t, 512) and ls[1] == 1 and latent.dtype is bf16 and latent.get_device() == dev
+              and k_rope.shape == (t, 64) and ks[1] == 1 and k_rope.dtype is bf16 and k_rope.get_device() == dev
+              and qo_indptr.shape == (batch + 1,) and qo_indptr.dtype is i32 and qo_indptr.get_device() == dev
+              and qo_indptr.is_contiguous()
+              and rope_table.shape == (angles, 64) and rope_table.dtype is torch.float32
+              and rope_table.get_device() == dev and rope_table.is_contiguous()
+              and (q_rope is None) == (q_out is None))
+        if ok and q_rope is not None:
+            heads = q_rope.shape[1]
+            qs, os_ = q_rope.stride(), q_out.stride()
+            ok = (q_rope.shape == (t, heads, 64) and q_out.shape == q_rope.shape and qs[2] == 1 and os_[2] == 1
+                  and q_rope.dtype is bf16 and q_out.dtype is bf16 and q_rope.get_device() == dev
+                  and q_out.get_device() == dev)
+            if heads:
+                q, o = q_rope.data_ptr(), q_out.data_ptr()
+        if ok and positions is not None:
+            ok = (positions.shape == (t,) and positions.dtype is i32 and positions.get_device() == dev
+                  and positions.is_contiguous())
+        if ok and norm_weight is not None:
+            ok = (norm_weight.shape == (512,) and norm_weight.dtype is bf16 and norm_weight.get_device() == dev
+                  and norm_weight.is_contiguous())
+        if ok and status is not None:
+            ok = status.dtype is i32 and status.get_device() == dev and status.is_contiguous()
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _refuse_append(latent, k_rope, qo_indptr, kv_lens, block_table, cache, rope_table, q_rope, q_out, positions,
+                       norm_weight, status)
     rc = _call(dev, stream, (_lib or load()).mla_paged_append,
                latent.data_ptr(), ls[0] if t > 1 else 512, k_rope.data_ptr(), ks[0] if t > 1 else 64,
-               None if norm_weight is None else _whole(norm_weight, bf16, dev, (512,), "norm_weight"), norm_eps,
-               q, qs[0], qs[1], o, os_[0], os_[1], heads, rope, angles, rope_style,
-               None if positions is None else _whole(positions, i32, dev, (t,), "positions"), indptr, lens,
-               batch, t, *table, *c, _status(status, dev))
+               None if norm_weight is None else norm_weight.data_ptr(), norm_eps,
+               q, qs[0], qs[1], o, os_[0], os_[1], heads, rope_table.data_ptr(), angles, rope_style,
+               None if positions is None else positions.data_ptr(), qo_indptr.data_ptr(), kv_lens.data_ptr(),
+               batch, t, block_table.data_ptr(), ts[0] if batch > 1 else max_pages, max_pages, cache.data_ptr(),
+               cs[0] if pages > 1 else size * 576, pages, size, None if status is None else status.data_ptr())
     if rc != MT_OK:
         _check(rc, "mla_paged_append")
 
@@ -429,14 +473,35 @@ def mla_paged_decode(q, cache, block_table, kv_lens, sm_scale, out, lse, workspa
     [B, H, 576] over the first kv_lens[b] positions of request b's pages;
     out [B, H, 512] bf16 and lse [B, H] fp32. workspace: uint8, at least
     mla_paged_decode_workspace_bytes(B, H)."""
-    c, table, lens, batch, dev = _paged(cache, block_table, kv_lens)
-    heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() > 1 else 0
-    qs = _strided(q, torch.bfloat16, dev, (batch, heads, 576), "q")
-    nbytes = workspace.numel() if isinstance(workspace, torch.Tensor) else 0
+    bf16, i32 = torch.bfloat16, torch.int32
+    try:
+        dev = cache.get_device()
+        pages, size, width = cache.shape
+        batch, max_pages = block_table.shape
+        heads, nbytes = q.shape[1], workspace.numel()
+        cs, ts, qs = cache.stride(), block_table.stride(), q.stride()
+        ok = (dev >= 0 and width == 576 and size > 0 and cs[2] == 1 and (cs[1] == 576 or size == 1)
+              and cache.dtype is bf16 and (ts[1] == 1 or max_pages < 2) and block_table.dtype is i32
+              and block_table.get_device() == dev
+              and kv_lens.shape == (batch,) and kv_lens.dtype is i32 and kv_lens.get_device() == dev
+              and kv_lens.is_contiguous()
+              and q.shape == (batch, heads, 576) and qs[2] == 1 and q.dtype is bf16 and q.get_device() == dev
+              and out.shape == (batch, heads, 512) and out.dtype is bf16 and out.get_device() == dev
+              and out.is_contiguous()
+              and lse.shape == (batch, heads) and lse.dtype is torch.float32 and lse.get_device() == dev
+              and lse.is_contiguous()
+              and workspace.dtype is torch.uint8 and workspace.dim() == 1 and workspace.get_device() == dev
+              and workspace.is_contiguous()
+              and (status is None or status.dtype is i32 and status.get_device() == dev and status.is_contiguous()))
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _refuse_decode(q, cache, block_table, kv_lens, out, lse, workspace, status)
     rc = _call(dev, stream, (_lib or load()).mla_paged_decode,
-               q.data_ptr(), qs[0] if batch > 1 else heads * 576, qs[1] if heads > 1 else 576, *c, *table, lens,
-               batch, heads, sm_scale, _whole(out, torch.bfloat16, dev, (batch, heads, 512), "out"),
-               _whole(lse, torch.float32, dev, (batch, heads), "lse"),
-               _whole(workspace, torch.uint8, dev, (nbytes,), "workspace"), nbytes, _status(status, dev))
+               q.data_ptr(), qs[0] if batch > 1 else heads * 576, qs[1] if heads > 1 else 576, cache.data_ptr(),
+               cs[0] if pages > 1 else size * 576, pages, size, block_table.data_ptr(),
+               ts[0] if batch > 1 else max_pages, max_pages, kv_lens.data_ptr(), batch, heads, sm_scale,
+               out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), nbytes,
+               None if status is None else status.data_ptr())
     if rc != MT_OK:
         _check(rc, "mla_paged_decode")

@@ -389,11 +389,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     while (!dead && next_piece(p, walk, pc)) {
       if (pc.t1 <= pc.t0) continue;
-      wait(B_Q_EMPTY, (pieces & 1) ^ 1);
-      if (dead) break;
-      expect_elect(&bars[B_Q_FULL], N * 9 * 128);
-      tma_load_4d_elect(smem_u32(sm + L::kQ), &tq, 0, grp * N, 0, pc.b, &bars[B_Q_FULL]);
-      ++pieces;
       const int32_t* table = a.kv.table + pc.b * a.kv.table_stride;
       // lane l looks after group l of a tile: its page, -1 behind the length or the share
       auto entry = [&](int t) {
@@ -404,6 +399,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       int pages[kAhead + 2];  // of tile t, t + 1, ...
 #pragma unroll
       for (int i = 0; i <= kAhead; ++i) pages[i] = entry(pc.t0 + i);
+      wait(B_Q_EMPTY, (pieces & 1) ^ 1);
+      if (dead) break;
+      expect_elect(&bars[B_Q_FULL], N * 9 * 128);
+      tma_load_4d_elect(smem_u32(sm + L::kQ), &tq, 0, grp * N, 0, pc.b, &bars[B_Q_FULL]);
+      ++pieces;
       for (int t = pc.t0; t < pc.t1 && !dead; ++t, ++it) {
         const int st = it & 1, ph = (it >> 1) & 1;
         const int page = pages[0];
