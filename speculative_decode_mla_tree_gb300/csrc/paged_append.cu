@@ -124,13 +124,13 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
 #pragma unroll
     for (int k = 0; k < kIters; ++k) {
       v[k] = make_uint4(0, 0, 0, 0);
-      if (h0 + 4 * k < a.heads) v[k] = __ldcs(reinterpret_cast<const uint4*>(src + (h0 + 4 * k) * a.q_head));
+      if (h0 + 4 * k < a.heads) v[k] = *reinterpret_cast<const uint4*>(src + (h0 + 4 * k) * a.q_head);
     }
   } else {
     const uint4* src = reinterpret_cast<const uint4*>(a.latent + t64 * a.latent_stride);
-    v[0] = __ldcs(src + lane);
-    v[1] = __ldcs(src + lane + 32);
-    v[2] = __ldcs(reinterpret_cast<const uint4*>(a.k_rope + t64 * a.k_rope_stride) + l);
+    v[0] = src[lane];
+    v[1] = src[lane + 32];
+    v[2] = reinterpret_cast<const uint4*>(a.k_rope + t64 * a.k_rope_stride)[l];
   }
 
   const int b = find_request_warp(a.qo_indptr, a.batch, t, lane);

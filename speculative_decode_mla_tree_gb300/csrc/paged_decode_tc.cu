@@ -330,7 +330,7 @@ __device__ __forceinline__ Walk make_plan(const Params& p, int team, int64_t* sh
 // loads every other quarter of a tile into both.
 template <int N, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_decode_tc_kernel(const Params p, const __grid_constant__ CUtensorMap tq,
+    paged_decode_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tq,
                            const __grid_constant__ CUtensorMap tkv) {
   using L = Lay<N>;
   extern __shared__ uint8_t raw[];
@@ -392,10 +392,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t* table = a.kv.table + pc.b * a.kv.table_stride;
       // lane l looks after group l of a tile: its page, -1 behind the length or the share
       auto entry = [&](int t) {
-        const int64_t row = (int64_t)t * kTile + lane * 8;
-        return lane < 8 && t < pc.t1 && row < pc.len ? __ldg(table + (row >> p.page_shift)) : -1;
+        const unsigned row = (unsigned)t * kTile + lane * 8;
+        return lane < 8 && t < pc.t1 && row < (unsigned)pc.len ? __ldg(table + (row >> p.page_shift)) : -1;
       };
       auto good = [&](int page) { return page >= 0 && page < a.kv.num_pages; };
+      // group g of tile t lies in this group of its page
+      auto place = [&](int t, int g) { return (int)((((unsigned)t * kTile) & (P - 1)) >> 3) + (g & ((P >> 3) - 1)); };
       int pages[kAhead + 2];  // of tile t, t + 1, ...
 #pragma unroll
       for (int i = 0; i <= kAhead; ++i) pages[i] = entry(pc.t0 + i);
@@ -406,28 +408,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++pieces;
       for (int t = pc.t0; t < pc.t1 && !dead; ++t, ++it) {
         const int st = it & 1, ph = (it >> 1) & 1;
-        const int page = pages[0];
-        pages[kAhead + 1] = entry(t + kAhead + 1);
-        const int64_t row = (int64_t)t * kTile + lane * 8;
-        const bool asked = lane < 8 && row < pc.len;
-        const bool ok = asked && good(page);
+        const bool asked = lane < 8 && (unsigned)t * kTile + lane * 8 < (unsigned)pc.len;
+        const bool ok = asked && good(pages[0]);
         if (asked && !ok && grp == 0) flag(a.status, MT_DEV_BAD_SLOT);
-        const unsigned next = __ballot_sync(kFull, good(pages[kAhead]));
-        const unsigned okm = __ballot_sync(kFull, ok);
-        // visible keys: groups whose page is there, positions below the length
-        uint64_t vis = 0;
-#pragma unroll
-        for (int g = 0; g < 8; ++g)
-          if (okm >> g & 1) vis |= 0xffull << (8 * g);
+        const unsigned okm = __ballot_sync(kFull, ok), next = __ballot_sync(kFull, good(pages[kAhead]));
+        // visible keys: groups whose page is there (bit g of okm becomes byte g), positions below the length
+        uint64_t vis = (uint64_t)(((okm >> 4) * 0x00204081u & 0x01010101u) * 0xffu) << 32 |
+                       ((okm & 15) * 0x00204081u & 0x01010101u) * 0xffu;
         const int64_t left = (int64_t)pc.len - (int64_t)t * kTile;
         if (left < kTile) vis &= (1ull << left) - 1;
-        uint64_t* full = &bars[B_KV_FULL + st];
         // a box of two groups lies in one page: they are good or bad together,
         // but the second may start behind the length
-        uint32_t boxes = 0;
+        const uint32_t bytes = per == 2 ? __popc(okm & 0x55) * 2 * kGroup : __popc(okm) * kGroup;
+        uint64_t* full = &bars[B_KV_FULL + st];
+        int id[8], later[8];
 #pragma unroll
-        for (int g = 0; g < 8; ++g)
-          if ((g & (per - 1)) == 0) boxes += okm >> g & 1;
+        for (int g = 0; g < 8; ++g) {
+          id[g] = __shfl_sync(kFull, pages[0], g);
+          later[g] = __shfl_sync(kFull, pages[kAhead], g);
+        }
 #pragma unroll
         for (int q = 0; q < kQuarters; ++q) {
           if (kPair && (q & 1) != grp) continue;  // the other CTA's to load
@@ -436,24 +435,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (q == (kPair ? grp : 0)) {  // every release of the stage came after the softmax had read its old mask
             if (lane == 0) vmask[st] = vis;
             __syncwarp();
-            expect_elect(full, boxes * per * kGroup);
+            expect_elect(full, bytes);
           }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int g = 2 * q + h;
-            const int id = __shfl_sync(kFull, page, g);
-            const int at = (int)((((int64_t)t * kTile) & (P - 1)) >> 3) + (g & ((P >> 3) - 1));
-            if ((h == 0 || per == 1) && (okm >> g & 1)) {
-              if (kPair) tma_load_5d_both_elect(kv0 + st * kStage + g * kGroup, &tkv, 0, 0, 0, at, id, full);
-              else tma_load_5d_elect(kv0 + st * kStage + g * kGroup, &tkv, 0, 0, 0, at, id, full);
+          for (int g = 2 * q; g < 2 * q + 2; ++g)
+            if ((g == 2 * q || per == 1) && (okm >> g & 1)) {
+              if (kPair)
+                tma_load_5d_both_elect(kv0 + st * kStage + g * kGroup, &tkv, 0, 0, 0, place(t, g), id[g], full);
+              else
+                tma_load_5d_elect(kv0 + st * kStage + g * kGroup, &tkv, 0, 0, 0, place(t, g), id[g], full);
             }
-            const int later = __shfl_sync(kFull, pages[kAhead], g);
-            if ((h == 0 || per == 1) && (next >> g & 1))
-              tma_prefetch_5d_elect(&tkv, 0, 0, 0,
-                                    (int)((((int64_t)(t + kAhead) * kTile) & (P - 1)) >> 3) + (g & ((P >> 3) - 1)),
-                                    later);
-          }
         }
+        // off the way of the loads: the tile kAhead behind goes into L2, and its successor's pages are asked for
+#pragma unroll
+        for (int g = 0; g < 8; ++g)
+          if ((!kPair || ((g >> 1) & 1) == grp) && ((g & 1) == 0 || per == 1) && (next >> g & 1))
+            tma_prefetch_5d_elect(&tkv, 0, 0, 0, place(t + kAhead, g), later[g]);
+        pages[kAhead + 1] = entry(t + kAhead + 1);
 #pragma unroll
         for (int i = 0; i <= kAhead; ++i) pages[i] = pages[i + 1];
       }
