@@ -470,15 +470,16 @@ size_t mla_paged_decode_workspace_bytes(int batch, int heads);
  * (NaN included) does not matter.
  * Scores are fp32 sums of bf16 products, the softmax and its sums are fp32,
  * the weights are rounded to bf16 for the product with the values (page
- * sizes that are powers of two from 8 on; they stay fp32 for others), and
- * partial results of a split are fp32. A request's result does not depend on
+ * sizes that are multiples of 8; they stay fp32 for others), and partial
+ * results of a split are fp32. A request's result does not depend on
  * the rest of the batch beyond fp32 rounding of where the splits fall, and
  * is the same in every run.
  *   q:   bf16, element (b, h, 0) at b * q_token_stride + h * q_head_stride
  *        (both at least 576)
  *   out: bf16 [batch, heads, 512], 16-byte aligned; lse: fp32 [batch, heads]
  *   workspace: 256-byte aligned
- * Any page size works; powers of two from 8 on take the tensor-core kernel.
+ * Any page size works; multiples of 8 take the tensor-core kernel, whose
+ * waits are bounded (MT_DEV_TIMEOUT, see mla_tree_test_wait_limits).
  */
 int mla_paged_decode(const mt_bf16* q, int64_t q_token_stride, int64_t q_head_stride,
                      const mt_bf16* cache, int64_t page_stride, int64_t num_pages, int page_size,

@@ -363,7 +363,8 @@ int mla_paged_append(const mt_bf16* latent, int64_t latent_stride, const mt_bf16
   } else if (q_rope || q_out) {
     return MT_EINVAL;
   }
-  if (heads > MT_MAX_PAGED_HEADS) return MT_EUNSUPPORTED;
+  if (heads > MT_MAX_PAGED_HEADS || paged_append_blocks(total_q, heads) > INT32_MAX)
+    return MT_EUNSUPPORTED;
   AppendArgs a;
   a.latent = latent;
   a.latent_stride = latent_stride;

@@ -112,6 +112,7 @@ struct AppendArgs {
   PagedCache kv;
   int32_t* status;
 };
+int64_t paged_append_blocks(int total_q, int heads);  // its grid
 cudaError_t launch_paged_append(const AppendArgs& a, int rope_style, cudaStream_t stream);
 
 // One split request of a decode call, as the attention kernels leave it for

@@ -197,12 +197,17 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
   if (lane < 8) dst[kDv / 8 + lane] = y;
 }
 
+int parts_of(int heads) { return 1 + (heads + kHeadsPerTask - 1) / kHeadsPerTask; }
+
 }  // namespace
 
+int64_t paged_append_blocks(int total_q, int heads) {
+  return ((int64_t)total_q * parts_of(heads) + kWarps - 1) / kWarps;
+}
+
 cudaError_t launch_paged_append(const AppendArgs& a, int rope_style, cudaStream_t stream) {
-  const int parts = 1 + (a.heads + kHeadsPerTask - 1) / kHeadsPerTask;
-  const int64_t blocks = ((int64_t)a.total_q * parts + kWarps - 1) / kWarps;
-  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const int64_t blocks = paged_append_blocks(a.total_q, a.heads);
+  const int parts = parts_of(a.heads);
   // May be scheduled while the stream's previous kernel drains; the kernel
   // waits for its completion before it reads anything.
   cudaLaunchConfig_t cfg = {};

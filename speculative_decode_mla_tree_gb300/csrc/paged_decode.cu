@@ -29,6 +29,7 @@ DecodeLayout decode_layout(int heads, int num_sms) {
 namespace {
 
 constexpr int kWarps = 8;            // heads per CTA of the any-page kernel
+constexpr int kKeys = 4;             // key rows it has in flight a warp
 constexpr unsigned kFull = 0xffffffffu;
 
 // One warp per head, the CTA's warps walk the same keys (so the rows come
@@ -77,41 +78,68 @@ __global__ void __launch_bounds__(32 * kWarps) decode_simt_kernel(const DecodeAr
   for (int i = 0; i < 16; ++i) o[i] = 0.f;
   const int j1 = (int)min((int64_t)len, (int64_t)(s + 1) * split_keys);
   const int32_t* table = a.kv.table + b * a.kv.table_stride;
-  for (int j = s * split_keys; j < j1; ++j) {
-    const int in_table = j / a.kv.page_size;
-    const int page = __ldg(table + in_table);
-    if (page < 0 || page >= a.kv.num_pages) {
-      if (lane == 0) flag(a.status, MT_DEV_BAD_SLOT);
-      continue;
+  for (int j = s * split_keys; j < j1; j += kKeys) {
+    uint4 row[kKeys][3];
+    bool see[kKeys];
+#pragma unroll
+    for (int t = 0; t < kKeys; ++t) {
+      see[t] = j + t < j1;
+      if (!see[t]) continue;
+      const int in_table = (j + t) / a.kv.page_size;
+      const int page = __ldg(table + in_table);
+      see[t] = page >= 0 && page < a.kv.num_pages;
+      if (!see[t]) {
+        if (lane == 0) flag(a.status, MT_DEV_BAD_SLOT);
+        continue;
+      }
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.kv.rows + page * a.kv.page_stride + (int64_t)(j + t - in_table * a.kv.page_size) * kDqk);
+      row[t][0] = __ldg(src + lane);
+      row[t][1] = __ldg(src + lane + 32);
+      row[t][2] = lane < 8 ? __ldg(src + lane + 64) : make_uint4(0, 0, 0, 0);
     }
-    const uint4* row = reinterpret_cast<const uint4*>(
-        a.kv.rows + page * a.kv.page_stride + (int64_t)(j - in_table * a.kv.page_size) * kDqk);
-    float v[16], dot = 0.f;
+    float y[kKeys], mn = m;
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      if (k == 2 && lane >= 8) break;
-      const uint4 u = __ldg(row + lane + 32 * k);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    for (int t = 0; t < kKeys; ++t) {
+      y[t] = 0.f;
+      if (!see[t]) continue;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x0 = bf16_lo(w[i]), x1 = bf16_hi(w[i]);
-        dot = fmaf(q[k][2 * i], x0, fmaf(q[k][2 * i + 1], x1, dot));
-        if (k < 2) {
-          v[8 * k + 2 * i] = x0;
-          v[8 * k + 2 * i + 1] = x1;
-        }
+      for (int k = 0; k < 3; ++k) {
+        const uint32_t w[4] = {row[t][k].x, row[t][k].y, row[t][k].z, row[t][k].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          y[t] = fmaf(q[k][2 * i], bf16_lo(w[i]), fmaf(q[k][2 * i + 1], bf16_hi(w[i]), y[t]));
       }
     }
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) dot += __shfl_xor_sync(kFull, dot, x);
-    const float y = dot * scale;
-    const float mn = fmaxf(m, y);
-    const float c = m == -INFINITY ? 0.f : exp2f(m - mn);
-    const float p = mn == -INFINITY ? 0.f : exp2f(y - mn);
-    m = mn;
-    l = l * c + p;
+    for (int x = 16; x > 0; x >>= 1)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = fmaf(o[i], c, p * v[i]);
+      for (int t = 0; t < kKeys; ++t) y[t] += __shfl_xor_sync(kFull, y[t], x);
+#pragma unroll
+    for (int t = 0; t < kKeys; ++t) {
+      y[t] *= scale;
+      if (see[t]) mn = fmaxf(mn, y[t]);
+    }
+    const float c = m == -INFINITY ? 0.f : exp2f(m - mn);
+    m = mn;
+    l *= c;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] *= c;
+#pragma unroll
+    for (int t = 0; t < kKeys; ++t) {
+      if (!see[t]) continue;
+      const float p = exp2f(y[t] - (mn == -INFINITY ? 0.f : mn));
+      l += p;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t w[4] = {row[t][k].x, row[t][k].y, row[t][k].z, row[t][k].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[8 * k + 2 * i] = fmaf(p, bf16_lo(w[i]), o[8 * k + 2 * i]);
+          o[8 * k + 2 * i + 1] = fmaf(p, bf16_hi(w[i]), o[8 * k + 2 * i + 1]);
+        }
+      }
+    }
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;
   const float lse = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;

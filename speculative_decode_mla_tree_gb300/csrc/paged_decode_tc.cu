@@ -1,5 +1,5 @@
 // Single-token attention over a paged latent cache on the tensor cores
-// (tcgen05 / TMEM / TMA), for page sizes that are powers of two from 8 on.
+// (tcgen05 / TMEM / TMA), for page sizes that are multiples of 8.
 //
 // With one query token per request a tile has only the heads as rows, so both
 // products are taken transposed, keys and value dims in the MMA's M and the
@@ -51,7 +51,7 @@ constexpr int kProducerWarp = 8, kQkWarp = 9, kPvWarp = 10;
 constexpr int kThreads = 352;
 // A tile is eight groups of eight keys, each [9 chunks of 64 dims][8 keys][128
 // bytes] with 128-byte swizzle: 9216 bytes that are one contiguous piece of a
-// page in memory, so any page size from 8 on loads alike.
+// page in memory, so all page sizes load alike.
 constexpr int kGroup = 9 * 1024;
 constexpr int kStage = 8 * kGroup;
 constexpr int kStages = 2;
@@ -96,7 +96,7 @@ struct Lay {
 
 struct Params {
   DecodeArgs a;
-  int page_shift;
+  int page_groups;              // groups of eight rows in a page
   int most;                     // positions a request's table holds
   int groups;                   // head groups = CTAs per team
   int nteams;
@@ -380,8 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
-    const int P = 1 << p.page_shift;
-    const int per = P >= 16 ? 2 : 1;            // groups of a box
+    const int per = p.page_groups % 2 == 0 ? 2 : 1;  // groups of a box: a pair lies in one page, or may not
     const uint32_t kv0 = smem_u32(sm + L::kKV);
     const bool drop = p.drop_team >= 0 && team >= p.drop_team;
     uint32_t it = 0, pieces = 0;
@@ -394,12 +393,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t* table = a.kv.table + pc.b * a.kv.table_stride;
       // lane l looks after group l of a tile: its page, -1 behind the length or the share
       auto entry = [&](int t) {
-        const unsigned row = (unsigned)t * kTile + lane * 8;
-        return lane < 8 && t < pc.t1 && row < (unsigned)pc.len ? __ldg(table + (row >> p.page_shift)) : -1;
+        const unsigned g = (unsigned)t * 8 + lane;
+        return lane < 8 && t < pc.t1 && g * 8 < (unsigned)pc.len ? __ldg(table + g / p.page_groups) : -1;
       };
       auto good = [&](int page) { return page >= 0 && page < a.kv.num_pages; };
-      // group g of tile t lies in this group of its page
-      auto place = [&](int t, int g) { return (int)((((unsigned)t * kTile) & (P - 1)) >> 3) + (g & ((P >> 3) - 1)); };
+      auto place = [&](int t) { return (int)(((unsigned)t * 8 + lane) % p.page_groups); };  // the group in its page
       int pages[kAhead + 2];  // of tile t, t + 1, ...
 #pragma unroll
       for (int i = 0; i <= kAhead; ++i) pages[i] = entry(pc.t0 + i);
@@ -423,11 +421,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // but the second may start behind the length
         const uint32_t bytes = per == 2 ? __popc(okm & 0x55) * 2 * kGroup : __popc(okm) * kGroup;
         uint64_t* full = &bars[B_KV_FULL + st];
-        int id[8], later[8];
+        int id[8], at[8];
+        const int place0 = place(t), place1 = place(t + kAhead);
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
           id[g] = __shfl_sync(kFull, pages[0], g);
-          later[g] = __shfl_sync(kFull, pages[kAhead], g);
+          at[g] = __shfl_sync(kFull, place0, g);
         }
 #pragma unroll
         for (int q = 0; q < kQuarters; ++q) {
@@ -443,16 +442,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int g = 2 * q; g < 2 * q + 2; ++g)
             if ((g == 2 * q || per == 1) && (okm >> g & 1)) {
               if (kPair)
-                tma_load_5d_both_elect(kv0 + st * kStage + g * kGroup, &tkv, 0, 0, 0, place(t, g), id[g], full);
+                tma_load_5d_both_elect(kv0 + st * kStage + g * kGroup, &tkv, 0, 0, 0, at[g], id[g], full);
               else
-                tma_load_5d_elect(kv0 + st * kStage + g * kGroup, &tkv, 0, 0, 0, place(t, g), id[g], full);
+                tma_load_5d_elect(kv0 + st * kStage + g * kGroup, &tkv, 0, 0, 0, at[g], id[g], full);
             }
         }
         // off the way of the loads: the tile kAhead behind goes into L2, and its successor's pages are asked for
 #pragma unroll
-        for (int g = 0; g < 8; ++g)
+        for (int g = 0; g < 8; ++g) {
+          const int ida = __shfl_sync(kFull, pages[kAhead], g), ata = __shfl_sync(kFull, place1, g);
           if ((!kPair || ((g >> 1) & 1) == grp) && ((g & 1) == 0 || per == 1) && (next >> g & 1))
-            tma_prefetch_5d_elect(&tkv, 0, 0, 0, place(t + kAhead, g), later[g]);
+            tma_prefetch_5d_elect(&tkv, 0, 0, 0, ata, ida);
+        }
         pages[kAhead + 1] = entry(t + kAhead + 1);
 #pragma unroll
         for (int i = 0; i <= kAhead; ++i) pages[i] = pages[i + 1];
@@ -820,7 +821,7 @@ bool make_kv_map(CUtensorMap* m, const PagedCache& kv) {
   if (!fn) return false;
   cuuint64_t dims[5] = {64, 8, 9, (cuuint64_t)kv.page_size / 8, (cuuint64_t)kv.num_pages};
   cuuint64_t strides[4] = {kDqk * 2, 128, 8 * kDqk * 2, (cuuint64_t)kv.page_stride * 2};
-  cuuint32_t box[5] = {64, 8, 9, (cuuint32_t)(kv.page_size >= 16 ? 2 : 1), 1};
+  cuuint32_t box[5] = {64, 8, 9, (cuuint32_t)(kv.page_size % 16 == 0 ? 2 : 1), 1};
   cuuint32_t es[5] = {1, 1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, kv.rows, dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -895,13 +896,12 @@ void set_paged_test_hooks(int drop_item, unsigned long long limit_ns) {
 cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_t stream) {
   using namespace ptc;
   const int P = a.kv.page_size;
-  if (P < 8 || (P & (P - 1)) || a.kv.num_pages <= 0) return cudaErrorNotSupported;
+  if (P % 8 != 0 || a.kv.num_pages <= 0) return cudaErrorNotSupported;
   const int N = a.heads <= 16 ? 16 : a.heads <= 32 ? 32 : 64;
   const int nsm = num_sms > 0 ? num_sms : 152;
   Params p;
   p.a = a;
-  p.page_shift = 0;
-  while ((1 << p.page_shift) < P) ++p.page_shift;
+  p.page_groups = P / 8;
   p.most = a.kv.max_pages * P;
   p.groups = (a.heads + N - 1) / N;
   p.drop_team = g_test_drop_team;

@@ -77,6 +77,8 @@ def test_more_than_supported(lib):
     assert _decode(lib, heads=4097, q_tok=4097 * 576) == abi.MT_EUNSUPPORTED
     assert _decode(lib, batch=65536) == abi.MT_EUNSUPPORTED
     assert _append(lib, heads=4097, q_tok=4097 * 192, qo_tok=4097 * 576) == abi.MT_EUNSUPPORTED
+    # more tokens and heads than one grid can take
+    assert _append(lib, total_q=(1 << 31) - 1, heads=4096, q_tok=4096 * 192, qo_tok=4096 * 576) == abi.MT_EUNSUPPORTED
 
 
 def test_empty_calls_launch_nothing(lib):

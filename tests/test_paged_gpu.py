@@ -92,7 +92,7 @@ def run_decode(seed, lens, heads, page, gap=0, q=None):
     return out, lse
 
 
-@pytest.mark.parametrize("page", [8, 16, 32, 64, 128, 256, 1, 3, 48])
+@pytest.mark.parametrize("page", [8, 16, 32, 64, 128, 256, 24, 40, 48, 72, 1, 3, 20])
 def test_decode_pages(page):
     run_decode(page, RAGGED, 16, page)
 
@@ -103,7 +103,7 @@ def test_decode_heads(heads, page):
     run_decode(heads, [1, 100, 0, 513], heads, page)
 
 
-@pytest.mark.parametrize("batch", [1, 2, 151, 152, 153, 400])
+@pytest.mark.parametrize("batch", [1, 2, 151, 152, 153, 400, 1100])
 def test_decode_batches(batch):
     r = torch.randint(0, 130, (batch,), generator=gen(batch)).tolist()
     run_decode(batch, r, 8, 32)
@@ -176,7 +176,7 @@ def test_decode_scores(kind, page):
     check(out, lse, ref.decode(q, flat, table, lens, page, SCALE))
 
 
-@pytest.mark.parametrize("page", [64, 16, 8, 7])
+@pytest.mark.parametrize("page", [64, 16, 8, 24, 7])
 def test_decode_bad_pages_and_lengths(page):
     """A bad page's positions are left out; a bad length leaves its rows as they were."""
     g = gen(10)
@@ -250,6 +250,48 @@ def test_decode_captured_with_other_lengths():
         want = ref.decode(queries, flat, tab, lens, page, SCALE)
         for o, l in outs:
             check(o, l, want)
+
+
+@pytest.mark.parametrize("heads", [8, 64, 128])
+@pytest.mark.parametrize("drop", [0, 3])
+def test_decode_wait_gives_up_then_next_call_is_correct(heads, drop):
+    """With its copies withheld from one share on, the tensor-core kernel
+    reports the timeout and leaves the device usable; the next call is right."""
+    g = gen(14)
+    lens = [1500, 900, 64, 2000]
+    cache, flat, table = paged(g, lens, 32)
+    q = normal(g, 4, heads, 576)
+    args = (q.cuda(), cache, table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    decode(*args, status)
+    assert int(status) == 0
+    abi.mla_tree_test_wait_limits(drop, 1_000_000)
+    try:
+        decode(*args, status)
+        torch.cuda.synchronize()
+    finally:
+        abi.mla_tree_test_wait_limits(-1, 0)
+    assert int(status) == abi.DEV_TIMEOUT
+    status.zero_()
+    out, lse = decode(*args, status)
+    check(out, lse, ref.decode(q, flat, table, lens, 32, SCALE))
+    assert int(status) == 0
+
+
+@pytest.mark.parametrize("page", [64, 6])
+def test_decode_not_a_number(page):
+    """A NaN in a visible key row makes the heads of that request NaN, and no other's."""
+    g = gen(15)
+    lens = [700, 700, 5]
+    cache, flat, table = paged(g, lens, page)
+    flat[ref.slots_of(table[1], page, 300, 301), 3] = float("nan")
+    cache.copy_(flat.view_as(cache))
+    q = normal(g, 3, 16, 576)
+    out, lse = decode(q.cuda(), cache, table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    assert torch.isnan(lse[1]).all() and torch.isnan(out[1]).all()
+    want = ref.decode(q, flat, table, [700, 0, 5], page, SCALE)
+    for b in (0, 2):
+        check(out, lse, want, slice(b, b + 1))
 
 
 # ------------------------------------------------------------------- append
