@@ -47,8 +47,8 @@ using namespace sm100;
 
 constexpr int kTile = 64;                     // keys per tile
 constexpr int kSoftWarps = 8;                 // warps 0-7
-constexpr int kProducerWarp = 8, kQkWarp = 9, kPvWarp = 10;
-constexpr int kThreads = 352;
+constexpr int kProducerWarp = 8, kQkWarp = 9, kPvWarp = 10, kProducer2Warp = 11;
+constexpr int threads_of(bool gather) { return gather ? 384 : 352; }
 // A tile is eight groups of eight keys, each [9 chunks of 64 dims][8 keys][128
 // bytes] with 128-byte swizzle: 9216 bytes that are one contiguous piece of a
 // page in memory, so all page sizes load alike.
@@ -97,6 +97,7 @@ struct Lay {
 struct Params {
   DecodeArgs a;
   int page_groups;              // groups of eight rows in a page
+  int64_t page_rows;            // rows from a page to the next (gather)
   int most;                     // positions a request's table holds
   int groups;                   // head groups = CTAs per team
   int nteams;
@@ -132,6 +133,16 @@ __device__ __forceinline__ void tma_prefetch_5d_elect(const CUtensorMap* map, in
       " @q cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %4, %5}];\n}\n" ::"l"(
           reinterpret_cast<uint64_t>(map)),
       "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
+      : "memory");
+}
+// Four rows of a 2-D map, 64 columns from x on, 128 bytes each one after another.
+__device__ __forceinline__ void tma_gather4_elect(uint32_t dst, const CUtensorMap* map, int x, int r0, int r1, int r2,
+                                                  int r3, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_u32(bar))
       : "memory");
 }
 // The 5-D load into the same place of both CTAs of a pair, signalling each CTA's own barrier.
@@ -330,8 +341,10 @@ __device__ __forceinline__ Walk make_plan(const Params& p, int team, int64_t* sh
 
 // kPair: the two head groups of a team are a cluster of two CTAs, and each
 // loads every other quarter of a tile into both.
-template <int N, bool kPair>
-__global__ void __launch_bounds__(kThreads, 1)
+// kGather: pages that are no whole groups of eight rows; two producer warps
+// bring single rows by gather, each every other quarter of a tile.
+template <int N, bool kPair, bool kGather>
+__global__ void __launch_bounds__(threads_of(kGather), 1)
     paged_decode_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tq,
                            const __grid_constant__ CUtensorMap tkv) {
   using L = Lay<N>;
@@ -361,6 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars[B_S_EMPTY + 1], kSoftWarps);
     if (kPair)
       for (int i = 0; i < kStages * kQuarters; ++i) mbar_init(&bars[B_KV_EMPTY + i], 2);
+    if (kGather)
+      for (int i = 0; i < kStages; ++i) mbar_init(&bars[B_KV_FULL + i], 2);
     fence_mbar_init_cluster();
   } else if (tid == kProducerWarp * 32) {
     prefetch_tmap(&tq);
@@ -378,9 +393,76 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   Piece pc;
 
-  if (warp == kProducerWarp) {
+  if (kGather && (warp == kProducerWarp || warp == kProducer2Warp)) {
+    // --------------------------------------------------- producers, row by row
+    // Producer i takes quarters i and i + 2 of every tile: lane l looks after
+    // row l % 16 of its quarter l / 16. 36 gathers of four rows by 64 dims a
+    // quarter, at 60 cycles and more each what bounds this form.
+    const int me = warp == kProducerWarp ? 0 : 1;
+    const uint32_t kv0 = smem_u32(sm + L::kKV);
+    uint16_t* vmask16 = reinterpret_cast<uint16_t*>(vmask);
+    uint32_t it = 0, pieces = 0;
+    bool dead = p.drop_team >= 0 && team >= p.drop_team;
+    auto wait = [&](int bar, uint32_t parity) {
+      if (!dead) dead = __any_sync(kFull, !wait_phase(&bars[bar], parity, abort, limit));
+    };
+    const int q0 = me + 2 * (lane >> 4);
+    while (!dead && next_piece(p, walk, pc)) {
+      if (pc.t1 <= pc.t0) continue;
+      const int32_t* table = a.kv.table + pc.b * a.kv.table_stride;
+      auto row_of = [&](int t) { return (unsigned)t * kTile + q0 * 16 + (lane & 15); };
+      auto entry = [&](int t) {
+        return t < pc.t1 && row_of(t) < (unsigned)pc.len ? __ldg(table + row_of(t) / a.kv.page_size) : -1;
+      };
+      int page_next = entry(pc.t0);
+      if (me == 0) {
+        wait(B_Q_EMPTY, (pieces & 1) ^ 1);
+        if (dead) break;
+        expect_elect(&bars[B_Q_FULL], N * 9 * 128);
+        tma_load_4d_elect(smem_u32(sm + L::kQ), &tq, 0, grp * N, 0, pc.b, &bars[B_Q_FULL]);
+        ++pieces;
+      }
+      for (int t = pc.t0; t < pc.t1 && !dead; ++t, ++it) {
+        const int st = it & 1, ph = (it >> 1) & 1, page = page_next;
+        page_next = entry(t + 1);
+        const bool asked = row_of(t) < (unsigned)pc.len, ok = asked && page >= 0 && page < a.kv.num_pages;
+        if (asked && !ok && grp == 0) flag(a.status, MT_DEV_BAD_SLOT);
+        const unsigned okm = __ballot_sync(kFull, ok);
+        // a row that is not there is read from the cache's first (and hidden)
+        const int slot = ok ? (int)(page * p.page_rows + row_of(t) % a.kv.page_size) : 0;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          const int q = me + 2 * h;
+          wait(B_KV_EMPTY + st * kQuarters + q, ph ^ 1);
+          if (dead) break;
+          if (h == 0) {  // every release of the stage came after the softmax had read its old mask
+            if (lane < 2) vmask16[st * 4 + me + 2 * lane] = (uint16_t)(okm >> (16 * lane));
+            __syncwarp();
+            expect_elect(&bars[B_KV_FULL + st], 4 * kGroup);
+          }
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            const int src = 16 * h + 4 * k;
+            const int r0 = __shfl_sync(kFull, slot, src), r1 = __shfl_sync(kFull, slot, src + 1);
+            const int r2 = __shfl_sync(kFull, slot, src + 2), r3 = __shfl_sync(kFull, slot, src + 3);
+            const uint32_t dst = kv0 + st * kStage + (2 * q + (k >> 1)) * kGroup + (k & 1) * 512;
+#pragma unroll
+            for (int c = 0; c < 9; ++c)
+              tma_gather4_elect(dst + c * 1024, &tkv, 64 * c, r0, r1, r2, r3, &bars[B_KV_FULL + st]);
+          }
+        }
+      }
+    }
+    if (*abort) {
+      if (pieces) mbar_drain(&bars[B_Q_FULL], (pieces - 1) & 1, kDrainNs);
+      for (uint32_t back = 0; back < kStages; ++back)
+        if (it > back)
+          mbar_drain(&bars[B_KV_FULL + ((it - 1 - back) & 1)], ((it - 1 - back) >> 1) & 1, kDrainNs);
+    }
+  } else if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
     const int per = p.page_groups % 2 == 0 ? 2 : 1;  // groups of a box: a pair lies in one page, or may not
+    const unsigned step_e = 8 / p.page_groups, step_g = 8 % p.page_groups;
     const uint32_t kv0 = smem_u32(sm + L::kKV);
     const bool drop = p.drop_team >= 0 && team >= p.drop_team;
     uint32_t it = 0, pieces = 0;
@@ -391,16 +473,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (!dead && next_piece(p, walk, pc)) {
       if (pc.t1 <= pc.t0) continue;
       const int32_t* table = a.kv.table + pc.b * a.kv.table_stride;
-      // lane l looks after group l of a tile: its page, -1 behind the length or the share
-      auto entry = [&](int t) {
-        const unsigned g = (unsigned)t * 8 + lane;
-        return lane < 8 && t < pc.t1 && g * 8 < (unsigned)pc.len ? __ldg(table + g / p.page_groups) : -1;
+      // Lane l looks after group l of a tile: its page, -1 behind the length or
+      // the share, and its place in the page. (e, g) walk the table one tile
+      // ahead of the pages held: eight groups on is step_e entries and step_g groups.
+      const unsigned g0 = (unsigned)pc.t0 * 8 + lane;
+      unsigned e = g0 / p.page_groups, g = g0 - e * p.page_groups, walked = g0;
+      int pages[kAhead + 2], place[kAhead + 2];  // of tile t, t + 1, ...
+      auto ask = [&](int& page, int& at) {
+        at = (int)g;
+        page = lane < 8 && walked < (unsigned)pc.t1 * 8 && walked * 8 < (unsigned)pc.len ? __ldg(table + e) : -1;
+        walked += 8;
+        e += step_e;
+        g += step_g;
+        if (g >= (unsigned)p.page_groups) g -= p.page_groups, ++e;
       };
       auto good = [&](int page) { return page >= 0 && page < a.kv.num_pages; };
-      auto place = [&](int t) { return (int)(((unsigned)t * 8 + lane) % p.page_groups); };  // the group in its page
-      int pages[kAhead + 2];  // of tile t, t + 1, ...
 #pragma unroll
-      for (int i = 0; i <= kAhead; ++i) pages[i] = entry(pc.t0 + i);
+      for (int i = 0; i <= kAhead; ++i) ask(pages[i], place[i]);
       wait(B_Q_EMPTY, (pieces & 1) ^ 1);
       if (dead) break;
       expect_elect(&bars[B_Q_FULL], N * 9 * 128);
@@ -422,11 +511,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t bytes = per == 2 ? __popc(okm & 0x55) * 2 * kGroup : __popc(okm) * kGroup;
         uint64_t* full = &bars[B_KV_FULL + st];
         int id[8], at[8];
-        const int place0 = place(t), place1 = place(t + kAhead);
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
           id[g] = __shfl_sync(kFull, pages[0], g);
-          at[g] = __shfl_sync(kFull, place0, g);
+          at[g] = __shfl_sync(kFull, place[0], g);
         }
 #pragma unroll
         for (int q = 0; q < kQuarters; ++q) {
@@ -450,13 +538,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // off the way of the loads: the tile kAhead behind goes into L2, and its successor's pages are asked for
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
-          const int ida = __shfl_sync(kFull, pages[kAhead], g), ata = __shfl_sync(kFull, place1, g);
+          const int ida = __shfl_sync(kFull, pages[kAhead], g), ata = __shfl_sync(kFull, place[kAhead], g);
           if ((!kPair || ((g >> 1) & 1) == grp) && ((g & 1) == 0 || per == 1) && (next >> g & 1))
             tma_prefetch_5d_elect(&tkv, 0, 0, 0, ata, ida);
         }
-        pages[kAhead + 1] = entry(t + kAhead + 1);
+        ask(pages[kAhead + 1], place[kAhead + 1]);
 #pragma unroll
-        for (int i = 0; i <= kAhead; ++i) pages[i] = pages[i + 1];
+        for (int i = 0; i <= kAhead; ++i) pages[i] = pages[i + 1], place[i] = place[i + 1];
       }
     }
     if (kPair)  // no arrival of the other CTA may find this one gone
@@ -816,7 +904,7 @@ bool make_q_map(CUtensorMap* m, const DecodeArgs& a, int n) {
 
 // Cache: [64 dims][8 rows][9 chunks][groups of 8 rows][pages], one box is one
 // or two groups.
-bool make_kv_map(CUtensorMap* m, const PagedCache& kv) {
+bool make_box_map(CUtensorMap* m, const PagedCache& kv) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[5] = {64, 8, 9, (cuuint64_t)kv.page_size / 8, (cuuint64_t)kv.num_pages};
@@ -828,11 +916,24 @@ bool make_kv_map(CUtensorMap* m, const PagedCache& kv) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int N, bool kPair>
+// Cache as rows, for gathers of 64 columns of single rows.
+bool make_row_map(CUtensorMap* m, const PagedCache& kv, int64_t rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {kDqk, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {kDqk * 2};
+  cuuint32_t box[2] = {64, 1};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kv.rows, dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int N, bool kPair, bool kGather>
 cudaLaunchConfig_t config(int ctas, cudaLaunchAttribute (&attr)[2], cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads_of(kGather));
   cfg.dynamicSmemBytes = Lay<N>::kBytes;
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -848,7 +949,7 @@ cudaLaunchConfig_t config(int ctas, cudaLaunchAttribute (&attr)[2], cudaStream_t
 
 // Makes the kernel ready on the current device, once; returns how many teams
 // fit at once (pairs: what the device's cluster placement allows).
-template <int N, bool kPair>
+template <int N, bool kPair, bool kGather>
 cudaError_t prepare(int num_sms, int groups, int* teams) {
   static std::mutex mu;
   static int pairs[64] = {};  // per device; 1 where no pairs are counted
@@ -858,16 +959,16 @@ cudaError_t prepare(int num_sms, int groups, int* teams) {
   *teams = num_sms / groups > 0 ? num_sms / groups : 1;
   std::lock_guard<std::mutex> lock(mu);
   if (dev < 0 || dev >= 64 || pairs[dev] == 0) {
-    e = cudaFuncSetAttribute(paged_decode_tc_kernel<N, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(paged_decode_tc_kernel<N, kPair, kGather>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Lay<N>::kBytes);
     if (e != cudaSuccess) return e;
     int n = 1;
     if (kPair) {
       cudaLaunchAttribute attr[2];
-      cudaLaunchConfig_t cfg = config<N, kPair>(2 * *teams, attr, nullptr);
+      cudaLaunchConfig_t cfg = config<N, kPair, kGather>(2 * *teams, attr, nullptr);
       cfg.attrs = attr + 1;
       cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&n, paged_decode_tc_kernel<N, kPair>, &cfg) != cudaSuccess || n <= 0)
+      if (cudaOccupancyMaxActiveClusters(&n, paged_decode_tc_kernel<N, kPair, kGather>, &cfg) != cudaSuccess || n <= 0)
         return cudaErrorNotSupported;
     }
     if (dev >= 0 && dev < 64) pairs[dev] = n;
@@ -877,13 +978,13 @@ cudaError_t prepare(int num_sms, int groups, int* teams) {
   return cudaSuccess;
 }
 
-template <int N, bool kPair = false>
+template <int N, bool kPair = false, bool kGather = false>
 cudaError_t launch(Params& p, int num_sms, const CUtensorMap& tq, const CUtensorMap& tkv, cudaStream_t stream) {
-  const cudaError_t e = prepare<N, kPair>(num_sms, p.groups, &p.nteams);
+  const cudaError_t e = prepare<N, kPair, kGather>(num_sms, p.groups, &p.nteams);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = config<N, kPair>(p.nteams * p.groups, attr, stream);
-  return cudaLaunchKernelEx(&cfg, paged_decode_tc_kernel<N, kPair>, p, tq, tkv);
+  const cudaLaunchConfig_t cfg = config<N, kPair, kGather>(p.nteams * p.groups, attr, stream);
+  return cudaLaunchKernelEx(&cfg, paged_decode_tc_kernel<N, kPair, kGather>, p, tq, tkv);
 }
 
 }  // namespace ptc
@@ -896,23 +997,37 @@ void set_paged_test_hooks(int drop_item, unsigned long long limit_ns) {
 cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_t stream) {
   using namespace ptc;
   const int P = a.kv.page_size;
-  if (P % 8 != 0 || a.kv.num_pages <= 0) return cudaErrorNotSupported;
+  // Pages of whole groups of eight rows go by boxes; others row by row, where
+  // rows can be counted through the pages (32 requests of 8192 keys, 64 heads:
+  // XXX us by gathers, 4.7 ms in the kernel that needs neither).
+  const bool gather = P % 8 != 0;
+  if (a.kv.num_pages <= 0 || (gather && a.kv.page_stride % kDqk != 0)) return cudaErrorNotSupported;
+  const int64_t page_rows = a.kv.page_stride / kDqk;
+  if (gather && page_rows * a.kv.num_pages > INT32_MAX) return cudaErrorNotSupported;
   const int N = a.heads <= 16 ? 16 : a.heads <= 32 ? 32 : 64;
   const int nsm = num_sms > 0 ? num_sms : 152;
   Params p;
   p.a = a;
   p.page_groups = P / 8;
+  p.page_rows = page_rows;
   p.most = a.kv.max_pages * P;
   p.groups = (a.heads + N - 1) / N;
   p.drop_team = g_test_drop_team;
   p.limit_ns = g_test_limit_ns > 0 ? g_test_limit_ns : sm100::kWaitLimitNs;
   CUtensorMap tq, tkv;
-  if (!make_q_map(&tq, a, N) || !make_kv_map(&tkv, a.kv))
+  if (!make_q_map(&tq, a, N)) return cudaErrorNotSupported;
+  if (!(gather ? make_row_map(&tkv, a.kv, (a.kv.num_pages - 1) * page_rows + P) : make_box_map(&tkv, a.kv)))
     return cudaErrorNotSupported;
-  const cudaError_t e = N == 16         ? launch<16>(p, nsm, tq, tkv, stream)
-                        : N == 32       ? launch<32>(p, nsm, tq, tkv, stream)
-                        : p.groups == 2 ? launch<64, true>(p, nsm, tq, tkv, stream)
-                                        : launch<64>(p, nsm, tq, tkv, stream);
+  cudaError_t e;
+  if (gather)
+    e = N == 16   ? launch<16, false, true>(p, nsm, tq, tkv, stream)
+        : N == 32 ? launch<32, false, true>(p, nsm, tq, tkv, stream)
+                  : launch<64, false, true>(p, nsm, tq, tkv, stream);
+  else
+    e = N == 16         ? launch<16>(p, nsm, tq, tkv, stream)
+        : N == 32       ? launch<32>(p, nsm, tq, tkv, stream)
+        : p.groups == 2 ? launch<64, true>(p, nsm, tq, tkv, stream)
+                        : launch<64>(p, nsm, tq, tkv, stream);
   // No request of this table can be split when it holds no more tiles than a share.
   const int64_t most = ((int64_t)a.kv.max_pages * P + kTile - 1) / kTile;
   if (e != cudaSuccess || p.nteams == 1 || (a.batch == 1 && most <= kMinShare)) return e;
