@@ -8,8 +8,7 @@
 //     O^T [512 dims x N heads] += V^T [512 x 64] P^T        (4 x M = 128)
 // K and V^T are the same shared-memory tile, read K-major and MN-major. A CTA
 // serves N = 16, 32 or 64 heads (more heads are groups of 64 in CTAs of their
-// own, side by side; of two groups the CTAs are a cluster, and each loads half
-// of every tile into both by multicast) and walks a contiguous range of 64-key tiles that may
+// own, side by side, which find each other's tiles in L2) and walks a contiguous range of 64-key tiles that may
 // span several requests.
 //
 // Softmax over keys is over TMEM lanes here. Its maximum would cross lanes and
@@ -61,7 +60,6 @@ constexpr float kRescale = 8.f;               // log2 of how far a weight may ex
 constexpr int kOverhead = 2;                  // a request's fixed cost, in tiles
 constexpr int kMinShare = 1;                  // smallest share of a team, in tiles
 constexpr uint64_t kDrainNs = 100000000ull;
-constexpr uint64_t kSettleNs = 50000ull;
 constexpr unsigned kFull = 0xffffffffu;
 
 enum {
@@ -145,16 +143,6 @@ __device__ __forceinline__ void tma_gather4_elect(uint32_t dst, const CUtensorMa
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_u32(bar))
       : "memory");
 }
-// The 5-D load into the same place of both CTAs of a pair, signalling each CTA's own barrier.
-__device__ __forceinline__ void tma_load_5d_both_elect(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
-                                                       int w, int v, uint64_t* bar) {
-  asm volatile(
-      "{\n .reg .pred q;\n .reg .b16 m;\n mov.b16 m, 3;\n elect.sync _|q, 0xffffffff;\n"
-      " @q cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], m;\n}\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(bar))
-      : "memory");
-}
 __device__ __forceinline__ void expect_elect(uint64_t* bar, uint32_t tx) {
   asm volatile(
       "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
@@ -192,16 +180,6 @@ __device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t a, uint3
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a),
                "r"(b), "r"(c), "r"(d)
                : "memory");
-}
-
-// Arrives on the same barrier of CTA `rank` of the cluster.
-__device__ __forceinline__ void mma_commit_to_elect(uint64_t* bar, int rank) {
-  asm volatile(
-      "{\n .reg .pred q;\n .reg .b16 m;\n cvt.u16.u32 m, %1;\n elect.sync _|q, 0xffffffff;\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}\n" ::"r"(
-          smem_u32(bar)),
-      "r"(1u << rank)
-      : "memory");
 }
 
 // Two such blocks; lanes 0-15 give the addresses.
@@ -339,11 +317,9 @@ __device__ __forceinline__ Walk make_plan(const Params& p, int team, int64_t* sh
 
 // ------------------------------------------------------------------- kernel
 
-// kPair: the two head groups of a team are a cluster of two CTAs, and each
-// loads every other quarter of a tile into both.
 // kGather: pages that are no whole groups of eight rows; two producer warps
 // bring single rows by gather, each every other quarter of a tile.
-template <int N, bool kPair, bool kGather>
+template <int N, bool kGather>
 __global__ void __launch_bounds__(threads_of(kGather), 1)
     paged_decode_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tq,
                            const __grid_constant__ CUtensorMap tkv) {
@@ -372,8 +348,6 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
     mbar_init(&bars[B_O_EMPTY], kSoftWarps);
     mbar_init(&bars[B_S_EMPTY], kSoftWarps);
     mbar_init(&bars[B_S_EMPTY + 1], kSoftWarps);
-    if (kPair)
-      for (int i = 0; i < kStages * kQuarters; ++i) mbar_init(&bars[B_KV_EMPTY + i], 2);
     if (kGather)
       for (int i = 0; i < kStages; ++i) mbar_init(&bars[B_KV_FULL + i], 2);
     fence_mbar_init_cluster();
@@ -387,7 +361,6 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
   int64_t share = 1;
   Walk walk = make_plan(p, team, &share);  // its loads run beside the set-up above
   tc_fence_before();
-  if (kPair) cluster_sync();  // the other CTA's barriers are there
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -518,28 +491,23 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
         }
 #pragma unroll
         for (int q = 0; q < kQuarters; ++q) {
-          if (kPair && (q & 1) != grp) continue;  // the other CTA's to load
           wait(B_KV_EMPTY + st * kQuarters + q, ph ^ 1);
           if (dead) break;
-          if (q == (kPair ? grp : 0)) {  // every release of the stage came after the softmax had read its old mask
+          if (q == 0) {  // every release of the stage came after the softmax had read its old mask
             if (lane == 0) vmask[st] = vis;
             __syncwarp();
             expect_elect(full, bytes);
           }
 #pragma unroll
           for (int g = 2 * q; g < 2 * q + 2; ++g)
-            if ((g == 2 * q || per == 1) && (okm >> g & 1)) {
-              if (kPair)
-                tma_load_5d_both_elect(kv0 + st * kStage + g * kGroup, &tkv, 0, 0, 0, at[g], id[g], full);
-              else
-                tma_load_5d_elect(kv0 + st * kStage + g * kGroup, &tkv, 0, 0, 0, at[g], id[g], full);
-            }
+            if ((g == 2 * q || per == 1) && (okm >> g & 1))
+              tma_load_5d_elect(kv0 + st * kStage + g * kGroup, &tkv, 0, 0, 0, at[g], id[g], full);
         }
         // off the way of the loads: the tile kAhead behind goes into L2, and its successor's pages are asked for
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
           const int ida = __shfl_sync(kFull, pages[kAhead], g), ata = __shfl_sync(kFull, place[kAhead], g);
-          if ((!kPair || ((g >> 1) & 1) == grp) && ((g & 1) == 0 || per == 1) && (next >> g & 1))
+          if (((g & 1) == 0 || per == 1) && (next >> g & 1))
             tma_prefetch_5d_elect(&tkv, 0, 0, 0, ata, ida);
         }
         ask(pages[kAhead + 1], place[kAhead + 1]);
@@ -547,10 +515,6 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
         for (int i = 0; i <= kAhead; ++i) pages[i] = pages[i + 1], place[i] = place[i + 1];
       }
     }
-    if (kPair)  // no arrival of the other CTA may find this one gone
-      for (uint32_t back = 0; back < kStages; ++back)
-        for (int q = grp; q < kQuarters; q += 2)
-          if (it > back) wait(B_KV_EMPTY + ((it - 1 - back) & 1) * kQuarters + q, ((it - 1 - back) >> 1) & 1);
     if (*abort) {  // let the copies in flight land (a phase that no copy ends runs out here)
       if (pieces) mbar_drain(&bars[B_Q_FULL], (pieces - 1) & 1, kDrainNs);
       for (uint32_t back = 0; back < kStages; ++back)
@@ -626,8 +590,7 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
           for (int m = 0; m < 4; ++m)
             mma_bf16_ss_elect(tmem + L::kO + m * N, dvs + ((k * 2 * kGroup + m * 2048) >> 4), dp + ((32 * k) >> 4),
                               idesc, j > 0 || k > 0);
-          if (kPair) mma_commit_to_elect(&bars[B_KV_EMPTY + st * kQuarters + k], k & 1);
-          else mma_commit_elect(&bars[B_KV_EMPTY + st * kQuarters + k]);
+          mma_commit_elect(&bars[B_KV_EMPTY + st * kQuarters + k]);
         }
         mma_commit_elect(&bars[B_P_EMPTY]);
       }
@@ -854,14 +817,6 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort) flag(a.status, MT_DEV_TIMEOUT);
-  if (kPair) {
-    if (tid == 0 && *abort) {  // what either CTA sent before it gave up lands within microseconds
-      const uint64_t t0 = global_timer_ns();
-      while (global_timer_ns() - t0 < kSettleNs) {
-      }
-    }
-    cluster_sync();
-  }
   if (warp == kQkWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kCols);
@@ -929,62 +884,33 @@ bool make_row_map(CUtensorMap* m, const PagedCache& kv, int64_t rows) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int N, bool kPair, bool kGather>
-cudaLaunchConfig_t config(int ctas, cudaLaunchAttribute (&attr)[2], cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(threads_of(kGather));
-  cfg.dynamicSmemBytes = Lay<N>::kBytes;
-  cfg.stream = stream;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = kPair ? 2 : 1;
-  return cfg;
-}
-
-// Makes the kernel ready on the current device, once; returns how many teams
-// fit at once (pairs: what the device's cluster placement allows).
-template <int N, bool kPair, bool kGather>
-cudaError_t prepare(int num_sms, int groups, int* teams) {
-  static std::mutex mu;
-  static int pairs[64] = {};  // per device; 1 where no pairs are counted
+template <int N, bool kGather = false>
+cudaError_t launch(const Params& p, const CUtensorMap& tq, const CUtensorMap& tkv, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  *teams = num_sms / groups > 0 ? num_sms / groups : 1;
-  std::lock_guard<std::mutex> lock(mu);
-  if (dev < 0 || dev >= 64 || pairs[dev] == 0) {
-    e = cudaFuncSetAttribute(paged_decode_tc_kernel<N, kPair, kGather>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Lay<N>::kBytes);
-    if (e != cudaSuccess) return e;
-    int n = 1;
-    if (kPair) {
-      cudaLaunchAttribute attr[2];
-      cudaLaunchConfig_t cfg = config<N, kPair, kGather>(2 * *teams, attr, nullptr);
-      cfg.attrs = attr + 1;
-      cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&n, paged_decode_tc_kernel<N, kPair, kGather>, &cfg) != cudaSuccess || n <= 0)
-        return cudaErrorNotSupported;
+  static std::mutex mu;
+  static bool ready[64] = {};  // per device
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 0 || dev >= 64 || !ready[dev]) {
+      e = cudaFuncSetAttribute(paged_decode_tc_kernel<N, kGather>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               Lay<N>::kBytes);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < 64) ready[dev] = true;
     }
-    if (dev >= 0 && dev < 64) pairs[dev] = n;
-    else if (kPair && n < *teams) *teams = n;
   }
-  if (kPair && dev >= 0 && dev < 64 && pairs[dev] < *teams) *teams = pairs[dev];
-  return cudaSuccess;
-}
-
-template <int N, bool kPair = false, bool kGather = false>
-cudaError_t launch(Params& p, int num_sms, const CUtensorMap& tq, const CUtensorMap& tkv, cudaStream_t stream) {
-  const cudaError_t e = prepare<N, kPair, kGather>(num_sms, p.groups, &p.nteams);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = config<N, kPair, kGather>(p.nteams * p.groups, attr, stream);
-  return cudaLaunchKernelEx(&cfg, paged_decode_tc_kernel<N, kPair, kGather>, p, tq, tkv);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.nteams * p.groups));
+  cfg.blockDim = dim3(threads_of(kGather));
+  cfg.dynamicSmemBytes = Lay<N>::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_decode_tc_kernel<N, kGather>, p, tq, tkv);
 }
 
 }  // namespace ptc
@@ -1012,6 +938,7 @@ cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_
   p.page_rows = page_rows;
   p.most = a.kv.max_pages * P;
   p.groups = (a.heads + N - 1) / N;
+  p.nteams = nsm / p.groups > 0 ? nsm / p.groups : 1;
   p.drop_team = g_test_drop_team;
   p.limit_ns = g_test_limit_ns > 0 ? g_test_limit_ns : sm100::kWaitLimitNs;
   CUtensorMap tq, tkv;
@@ -1020,14 +947,13 @@ cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_
     return cudaErrorNotSupported;
   cudaError_t e;
   if (gather)
-    e = N == 16   ? launch<16, false, true>(p, nsm, tq, tkv, stream)
-        : N == 32 ? launch<32, false, true>(p, nsm, tq, tkv, stream)
-                  : launch<64, false, true>(p, nsm, tq, tkv, stream);
+    e = N == 16   ? launch<16, true>(p, tq, tkv, stream)
+        : N == 32 ? launch<32, true>(p, tq, tkv, stream)
+                  : launch<64, true>(p, tq, tkv, stream);
   else
-    e = N == 16         ? launch<16>(p, nsm, tq, tkv, stream)
-        : N == 32       ? launch<32>(p, nsm, tq, tkv, stream)
-        : p.groups == 2 ? launch<64, true>(p, nsm, tq, tkv, stream)
-                        : launch<64>(p, nsm, tq, tkv, stream);
+    e = N == 16   ? launch<16>(p, tq, tkv, stream)
+        : N == 32 ? launch<32>(p, tq, tkv, stream)
+                  : launch<64>(p, tq, tkv, stream);
   // No request of this table can be split when it holds no more tiles than a share.
   const int64_t most = ((int64_t)a.kv.max_pages * P + kTile - 1) / kTile;
   if (e != cudaSuccess || p.nteams == 1 || (a.batch == 1 && most <= kMinShare)) return e;
