@@ -469,8 +469,7 @@ size_t mla_paged_decode_workspace_bytes(int batch, int heads);
  * left unwritten. What cache rows behind a request's last position hold
  * (NaN included) does not matter.
  * Scores are fp32 sums of bf16 products, the softmax and its sums are fp32,
- * the weights are rounded to bf16 for the product with the values (page
- * sizes that are multiples of 8; they stay fp32 for others), and partial
+ * the weights are rounded to bf16 for the product with the values, and partial
  * results of a split are fp32. A request's result does not depend on
  * the rest of the batch beyond fp32 rounding of where the splits fall, and
  * is the same in every run.
@@ -478,8 +477,11 @@ size_t mla_paged_decode_workspace_bytes(int batch, int heads);
  *        (both at least 576)
  *   out: bf16 [batch, heads, 512], 16-byte aligned; lse: fp32 [batch, heads]
  *   workspace: 256-byte aligned
- * Any page size works; multiples of 8 take the tensor-core kernel, whose
- * waits are bounded (MT_DEV_TIMEOUT, see mla_tree_test_wait_limits).
+ * Any page size works. Multiples of 8 are fastest; others are gathered row by
+ * row (1.5 times the time) where page_stride is a multiple of 576 and the cache
+ * has fewer than 2^31 rows, and take a kernel without tensor cores otherwise.
+ * The waits inside the tensor-core kernel are bounded (MT_DEV_TIMEOUT, see
+ * mla_tree_test_wait_limits).
  */
 int mla_paged_decode(const mt_bf16* q, int64_t q_token_stride, int64_t q_head_stride,
                      const mt_bf16* cache, int64_t page_stride, int64_t num_pages, int page_size,

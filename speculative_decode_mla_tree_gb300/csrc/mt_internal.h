@@ -141,6 +141,7 @@ struct DecodeLayout {
   int64_t rows;                 // capacity of ws_lse / ws_o in (slot, head) rows
   size_t lse_off, o_off, total;
 };
+int decode_sms(int num_sms);  // SMs that the decode launches count with (152 where unknown, at most 256)
 DecodeLayout decode_layout(int heads, int num_sms);
 // Tensor-core kernel; returns cudaErrorNotSupported when it cannot serve `a`.
 cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_t stream);

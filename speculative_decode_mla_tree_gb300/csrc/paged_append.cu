@@ -8,6 +8,10 @@
 // angles, so the bound is the bytes: 2304 of the row, 256 a query head and
 // 256 of angles per token.
 //
+// 8832 tokens of 7 prompts with 64 heads take 28.8 us, 167 MB at 5.8 TB/s (85%
+// of the copy rate, which is what reads and writes of HBM in equal parts get);
+// one token of 8 heads 1.8 us, a launch.
+//
 // A task is one warp's share of a token: its cache row, or the rope parts of
 // up to kHeadsPerTask heads. A rope part is 128 bytes, so eight lanes hold
 // one head and a warp instruction moves four heads; a task's heads are all
@@ -23,7 +27,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kHeadsPerTask = 16;   // four 16-byte loads in flight a lane
+constexpr int kHeadsPerTask = 16;   // four 16-byte loads in flight a lane (8 heads: 31.6 us, 32: the same as 16)
 constexpr int kIters = kHeadsPerTask / 4;
 constexpr unsigned kFull = 0xffffffffu;
 

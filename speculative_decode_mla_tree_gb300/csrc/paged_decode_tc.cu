@@ -1,5 +1,5 @@
 // Single-token attention over a paged latent cache on the tensor cores
-// (tcgen05 / TMEM / TMA), for page sizes that are multiples of 8.
+// (tcgen05 / TMEM / TMA).
 //
 // With one query token per request a tile has only the heads as rows, so both
 // products are taken transposed, keys and value dims in the MMA's M and the
@@ -8,15 +8,17 @@
 //     O^T [512 dims x N heads] += V^T [512 x 64] P^T        (4 x M = 128)
 // K and V^T are the same shared-memory tile, read K-major and MN-major. A CTA
 // serves N = 16, 32 or 64 heads (more heads are groups of 64 in CTAs of their
-// own, side by side, which find each other's tiles in L2) and walks a contiguous range of 64-key tiles that may
-// span several requests.
+// own, side by side, which find each other's tiles in L2; loading each tile
+// once for two groups by cluster multicast measured the same, 121 us at 128
+// heads) and walks a contiguous range of 64-key tiles that may span several
+// requests.
 //
 // Softmax over keys is over TMEM lanes here. Its maximum would cross lanes and
 // warps for every tile; instead the reference of each head (the number its
-// weights are relative to) moves only when a score exceeds it by more than
-// 2^8, which is asked with one block-wide OR per tile. Only then are the
-// maxima exchanged and O^T rescaled; after a request's first tile that is
-// rare. Weights stay below 2^8 and the sums fp32, so nothing is lost.
+// weights are relative to) moves only when a score exceeds it by more than 8 in
+// log2, which is asked with one OR over the warps of a half per tile. Only then
+// are the maxima exchanged and O^T rescaled; after a request's first tile that
+// is rare. Weights stay below 2^8 and the sums are fp32, so nothing is lost.
 //
 // Work split: the batch is a line of 64-key tiles (a request adds kOverhead
 // tiles for its query load and epilogue), cut into equal shares, one per team
@@ -24,11 +26,22 @@
 // itself. A request inside one share is finished in place; others leave fp32
 // partials, at most two per CTA, for the merge kernel.
 //
-// Roles (352 threads): eight softmax warps (a TMEM lane quarter and half of
-// the heads each), a TMA producer warp, a warp for each of the two products (the first owns TMEM).
-// Every wait is time-bounded: a
-// timeout sets MT_DEV_TIMEOUT, nothing more is issued, what is in flight is
-// drained and TMEM released.
+// What bounds it. Up to 64 heads, HBM: 73.7 KB a tile at 6782 GB/s of copy
+// bandwidth are 1.65 us an SM, of which the tensor cores need 0.8 us (16 heads)
+// to 1.05 us (64 heads). 4 requests of 200000 keys at 16 heads take 140 us
+// (6.6 TB/s), the 64-request mix of 128 to 131072 keys at 64 heads 225 us (6.3
+// TB/s). A call's fixed part shows in short ones: about 2.5 us until the first
+// load (plan, page numbers), 1.5 us of first loads, 2.5 us for a 128 KB partial
+// at the 28 bytes a cycle that an SM stores, 4 to 8 us of merge. At 128 heads
+// every tile is needed by two SMs, and the latency of a stage's round bounds:
+// loads 0.5 us, scores 0.9 us next to the other stage's P.V, softmax 0.45 us,
+// P.V, 1.4 us per tile with two stages in shared memory.
+//
+// Roles (352 threads): eight softmax warps (a TMEM lane quarter and half of the
+// heads each; four warps took 1.0 us a tile at 64 heads, eight 0.45), a TMA
+// producer warp, and a warp for each of the two products (the first owns TMEM).
+// Every wait is time-bounded: a timeout sets MT_DEV_TIMEOUT, nothing more is
+// issued, what is in flight is drained and TMEM released.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <float.h>
@@ -55,10 +68,17 @@ constexpr int kGroup = 9 * 1024;
 constexpr int kStage = 8 * kGroup;
 constexpr int kStages = 2;
 constexpr int kQuarters = 4;                  // a stage is released by quarters, two groups = one P.V K step
-constexpr int kAhead = 1;                     // a tile's loads go out with the L2 prefetch of the tile so far behind it
+// A tile's loads go out with the L2 prefetch of the tile so far behind it, for
+// two stages of shared memory do not cover HBM's latency: none 233 us on the
+// 64-request mix and 128 us at 128 heads, one 225 and 121, two 228 and 122.
+constexpr int kAhead = 1;
 constexpr float kRescale = 8.f;               // log2 of how far a weight may exceed 1
-constexpr int kOverhead = 2;                  // a request's fixed cost, in tiles
-constexpr int kMinShare = 1;                  // smallest share of a team, in tiles
+// A request's fixed cost in tiles: 1 is 2% slower on the 64-request mix, 4 as
+// much slower on 37 short ragged requests (18.5 us against 17.3).
+constexpr int kOverhead = 2;
+// Smallest share of a team in tiles: 4 saves the merge partials but takes 16 us
+// instead of 12.8 on 8 requests of 1024 to 4096 keys.
+constexpr int kMinShare = 1;
 constexpr uint64_t kDrainNs = 100000000ull;
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -925,13 +945,13 @@ cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_
   const int P = a.kv.page_size;
   // Pages of whole groups of eight rows go by boxes; others row by row, where
   // rows can be counted through the pages (32 requests of 8192 keys, 64 heads:
-  // XXX us by gathers, 4.7 ms in the kernel that needs neither).
+  // 98 us by gathers, 67 us with pages of 64, 4.7 ms in the kernel that needs neither).
   const bool gather = P % 8 != 0;
   if (a.kv.num_pages <= 0 || (gather && a.kv.page_stride % kDqk != 0)) return cudaErrorNotSupported;
   const int64_t page_rows = a.kv.page_stride / kDqk;
   if (gather && page_rows * a.kv.num_pages > INT32_MAX) return cudaErrorNotSupported;
   const int N = a.heads <= 16 ? 16 : a.heads <= 32 ? 32 : 64;
-  const int nsm = num_sms > 0 ? num_sms : 152;
+  const int nsm = decode_sms(num_sms);
   Params p;
   p.a = a;
   p.page_groups = P / 8;

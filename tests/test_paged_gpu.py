@@ -98,9 +98,16 @@ def test_decode_pages(page):
 
 
 @pytest.mark.parametrize("heads", [1, 7, 8, 16, 17, 24, 32, 33, 63, 64, 65, 100, 128, 130, 200])
-@pytest.mark.parametrize("page", [64, 5])
-def test_decode_heads(heads, page):
-    run_decode(heads, [1, 100, 0, 513], heads, page)
+@pytest.mark.parametrize("page,gap", [(64, 0), (5, 0), (5, 8)], ids=["boxes", "rows", "any"])
+def test_decode_heads(heads, page, gap):
+    run_decode(heads, [1, 100, 0, 513], heads, page, gap)
+
+
+@pytest.mark.parametrize("page", [1, 3, 20])
+def test_decode_any_layout(page):
+    """Page strides that are no whole number of rows."""
+    run_decode(page, RAGGED, 16, page, gap=40)
+    run_decode(page, [5000, 1], 24, page, gap=40)
 
 
 @pytest.mark.parametrize("batch", [1, 2, 151, 152, 153, 400, 1100])
@@ -148,13 +155,13 @@ def test_decode_strides(page):
 
 
 @pytest.mark.parametrize("kind", ["peaked", "equal", "far_below", "huge_values", "growing"])
-@pytest.mark.parametrize("page", [64, 1])
-def test_decode_scores(kind, page):
+@pytest.mark.parametrize("page,gap", [(64, 0), (1, 0), (1, 8)], ids=["boxes", "rows", "any"])
+def test_decode_scores(kind, page, gap):
     """Softmaxes that rest on one key, on all alike, on scores far below zero,
     values beyond 16-bit range, maxima that rise with every tile."""
     g = gen(9)
     lens = [1000, 65, 3]
-    cache, flat, table = paged(g, lens, page)
+    cache, flat, table = paged(g, lens, page, gap=gap)
     q = normal(g, 3, 40, 576)
     if kind == "peaked":
         q = q * 16
@@ -171,17 +178,17 @@ def test_decode_scores(kind, page):
             rows = ref.slots_of(table[b], page, 0, n)
             flat[rows, 512:] = (torch.arange(n) / 16.0)[:, None].expand(-1, 64).to(BF)
         q[:, :, 512:] = 1.0
-    cache.copy_(flat.view_as(cache))
+    cache.copy_(flat.view(cache.shape))
     out, lse = decode(q.cuda(), cache, table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"))
     check(out, lse, ref.decode(q, flat, table, lens, page, SCALE))
 
 
-@pytest.mark.parametrize("page", [64, 16, 8, 24, 7])
-def test_decode_bad_pages_and_lengths(page):
+@pytest.mark.parametrize("page,gap", [(64, 0), (16, 0), (8, 0), (24, 0), (7, 0), (7, 8)])
+def test_decode_bad_pages_and_lengths(page, gap):
     """A bad page's positions are left out; a bad length leaves its rows as they were."""
     g = gen(10)
     lens = [500, 200, 70, 64, 90]
-    cache, flat, table = paged(g, lens, page)
+    cache, flat, table = paged(g, lens, page, gap=gap)
     pages = cache.shape[0]
     bad = [-1, pages, -(1 << 31), (1 << 31) - 1]
     table[0, 1], table[0, 500 // page - 1] = bad[0], bad[1]
@@ -254,12 +261,13 @@ def test_decode_captured_with_other_lengths():
 
 @pytest.mark.parametrize("heads", [8, 64, 128])
 @pytest.mark.parametrize("drop", [0, 3])
-def test_decode_wait_gives_up_then_next_call_is_correct(heads, drop):
+@pytest.mark.parametrize("page", [32, 3])
+def test_decode_wait_gives_up_then_next_call_is_correct(heads, drop, page):
     """With its copies withheld from one share on, the tensor-core kernel
     reports the timeout and leaves the device usable; the next call is right."""
     g = gen(14)
     lens = [1500, 900, 64, 2000]
-    cache, flat, table = paged(g, lens, 32)
+    cache, flat, table = paged(g, lens, page)
     q = normal(g, 4, heads, 576)
     args = (q.cuda(), cache, table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"))
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -274,18 +282,18 @@ def test_decode_wait_gives_up_then_next_call_is_correct(heads, drop):
     assert int(status) == abi.DEV_TIMEOUT
     status.zero_()
     out, lse = decode(*args, status)
-    check(out, lse, ref.decode(q, flat, table, lens, 32, SCALE))
+    check(out, lse, ref.decode(q, flat, table, lens, page, SCALE))
     assert int(status) == 0
 
 
-@pytest.mark.parametrize("page", [64, 6])
-def test_decode_not_a_number(page):
+@pytest.mark.parametrize("page,gap", [(64, 0), (6, 0), (6, 8)])
+def test_decode_not_a_number(page, gap):
     """A NaN in a visible key row makes the heads of that request NaN, and no other's."""
     g = gen(15)
     lens = [700, 700, 5]
-    cache, flat, table = paged(g, lens, page)
+    cache, flat, table = paged(g, lens, page, gap=gap)
     flat[ref.slots_of(table[1], page, 300, 301), 3] = float("nan")
-    cache.copy_(flat.view_as(cache))
+    cache.copy_(flat.view(cache.shape))
     q = normal(g, 3, 16, 576)
     out, lse = decode(q.cuda(), cache, table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"))
     assert torch.isnan(lse[1]).all() and torch.isnan(out[1]).all()
