@@ -136,21 +136,28 @@ __device__ __forceinline__ void tma_load_4d_elect(uint32_t dst, const CUtensorMa
       : "memory");
 }
 __device__ __forceinline__ void tma_load_5d_elect(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
-                                                  int v, uint64_t* bar) {
+                                                  int v, uint64_t* bar, uint64_t policy) {
   asm volatile(
       "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
-      " @q cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n}\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(bar))
+      " @q cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;\n}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(bar)), "l"(policy)
       : "memory");
 }
-// Brings a box into L2 only.
-__device__ __forceinline__ void tma_prefetch_5d_elect(const CUtensorMap* map, int x, int y, int z, int w, int v) {
+__device__ __forceinline__ uint64_t l2_policy(bool evict_first) {
+  uint64_t p;
+  if (evict_first) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+// A box into L2 only.
+__device__ __forceinline__ void tma_prefetch_5d_elect(const CUtensorMap* map, int x, int y, int z, int w, int v,
+                                                      uint64_t policy) {
   asm volatile(
       "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
-      " @q cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %4, %5}];\n}\n" ::"l"(
+      " @q cp.async.bulk.prefetch.tensor.5d.L2.global.tile.L2::cache_hint [%0, {%1, %2, %3, %4, %5}], %6;\n}\n" ::"l"(
           reinterpret_cast<uint64_t>(map)),
-      "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
+      "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "l"(policy)
       : "memory");
 }
 // Four rows of a 2-D map, 64 columns from x on, 128 bytes each one after another.
@@ -456,6 +463,11 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
     // ------------------------------------------------------------ producer
     const int per = p.page_groups % 2 == 0 ? 2 : 1;  // groups of a box: a pair lies in one page, or may not
     const unsigned step_e = 8 / p.page_groups, step_g = 8 % p.page_groups;
+    // Keys that one CTA alone reads need not stay in L2: partials, page numbers
+    // and code do (37 ragged requests 17.4 -> 16.5 us, one of 131071 keys 43.9 ->
+    // 42.1, 32 of 8192 66.6 -> 65.4; 4 of 200000 keys 141.7 -> 143.2). With
+    // several head groups the other CTA still reads them.
+    const uint64_t policy = l2_policy(p.groups == 1);
     const uint32_t kv0 = smem_u32(sm + L::kKV);
     const bool drop = p.drop_team >= 0 && team >= p.drop_team;
     uint32_t it = 0, pieces = 0;
@@ -521,14 +533,14 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
 #pragma unroll
           for (int g = 2 * q; g < 2 * q + 2; ++g)
             if ((g == 2 * q || per == 1) && (okm >> g & 1))
-              tma_load_5d_elect(kv0 + st * kStage + g * kGroup, &tkv, 0, 0, 0, at[g], id[g], full);
+              tma_load_5d_elect(kv0 + st * kStage + g * kGroup, &tkv, 0, 0, 0, at[g], id[g], full, policy);
         }
         // off the way of the loads: the tile kAhead behind goes into L2, and its successor's pages are asked for
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
           const int ida = __shfl_sync(kFull, pages[kAhead], g), ata = __shfl_sync(kFull, place[kAhead], g);
           if (((g & 1) == 0 || per == 1) && (next >> g & 1))
-            tma_prefetch_5d_elect(&tkv, 0, 0, 0, ata, ida);
+            tma_prefetch_5d_elect(&tkv, 0, 0, 0, ata, ida, policy);
         }
         ask(pages[kAhead + 1], place[kAhead + 1]);
 #pragma unroll
