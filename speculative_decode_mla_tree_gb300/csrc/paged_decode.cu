@@ -187,8 +187,10 @@ __global__ void __launch_bounds__(32 * kWarps) decode_simt_kernel(const DecodeAr
 // at once. Sums are in a fixed order, so the result is the same in every run.
 // Alone and back to back, from L2: 5.6 us for 24 MB of partials (32 requests of
 // 8192 keys, 64 heads), 7.2 us for 27 MB (the 64-request mix), 6.0 us for 20 MB
-// of one request. With 8 loads in flight and twice the blocks 6.8, 9.5 and 12.9
-// us; bulk copies into shared memory took 10.6, 16.3 and 17.5 us.
+// of one request. With R = 1 alone the first two take 9.2 and 8.9 us (128 heads
+// 19.0 instead of 8.4), with warps in the place of blocks the third 9.7; with 8
+// loads in flight and twice the blocks they take 6.8, 9.5 and 12.9 us, by bulk
+// copies into shared memory 10.6, 16.3 and 17.5.
 constexpr int kMergeThreads = 256;
 constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kMergeBlocksPerSm = 2;

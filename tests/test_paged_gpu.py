@@ -518,3 +518,69 @@ def test_prompt_then_decode_then_tree(heads):
             own = [keep.tolist()]
             want = ref.decode(q[4 * b + node].cpu()[None], flat, own, [len(own[0])], 1, SCALE)
             check(out[4 * b + node][None], lse[4 * b + node][None], want)
+
+
+# ----------------------------------------------------------------- refusals
+
+def _decode_args():
+    g = gen(50)
+    cache, _, table = paged(g, [100, 20], 32)
+    return dict(q=normal(g, 2, 8, 576).cuda(), cache=cache, block_table=table.cuda(),
+                kv_lens=torch.tensor([100, 20], dtype=torch.int32, device="cuda"), sm_scale=SCALE,
+                out=torch.full((2, 8, 512), 7.0, dtype=BF, device="cuda"), lse=torch.full((2, 8), 7.0, device="cuda"),
+                workspace=torch.empty(abi.mla_paged_decode_workspace_bytes(2, 8), dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("name,change", [
+    ("q", lambda t: t.float()), ("q", lambda t: t.cpu()), ("q", lambda t: t[:, :, :575]), ("q", lambda t: t[:1]),
+    ("q", lambda t: None), ("q", lambda t: t.permute(0, 2, 1)), ("q", lambda t: t[0]),
+    ("q", lambda t: t[:, :1].expand(2, 8, 576)),
+    ("cache", lambda t: t.half()), ("cache", lambda t: t.cpu()), ("cache", lambda t: t[:, :, :512]),
+    ("cache", lambda t: t.flatten(0, 1)), ("cache", lambda t: t[:, ::2]), ("cache", lambda t: 5),
+    ("block_table", lambda t: t.long()), ("block_table", lambda t: t.cpu()), ("block_table", lambda t: t[:, ::2]),
+    ("block_table", lambda t: t[:1]), ("block_table", lambda t: t.flatten()),
+    ("kv_lens", lambda t: t.long()), ("kv_lens", lambda t: t[:1]), ("kv_lens", lambda t: [100, 20]),
+    ("out", lambda t: t.float()), ("out", lambda t: t[:, :4]), ("out", lambda t: t.transpose(0, 1).contiguous().transpose(0, 1)),
+    ("lse", lambda t: t.half()), ("lse", lambda t: t[:, :4]), ("workspace", lambda t: t[:-1]),
+    ("workspace", lambda t: t[1:]), ("workspace", lambda t: t.int()), ("workspace", lambda t: None),
+    ("sm_scale", lambda t: float("nan"))])
+def test_decode_refuses(name, change):
+    """What does not fit is refused before anything is launched."""
+    args = _decode_args()
+    out, lse = args["out"], args["lse"]
+    args[name] = change(args[name])
+    with pytest.raises(abi.MlaTreeError):
+        abi.mla_paged_decode(**args)
+    torch.cuda.synchronize()
+    assert (out == 7.0).all() and (lse == 7.0).all()
+
+
+def _append_args():
+    g = gen(51)
+    cache = torch.full((4, 16, 576), 3.0, dtype=BF, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    row = normal(g, 6, 576).cuda()
+    return dict(latent=row[:, :512], k_rope=row[:, 512:], qo_indptr=i32([0, 3, 6]), kv_lens=i32([3, 6]),
+                block_table=i32([[0], [1]]), cache=cache, rope_table=rope_table(64).cuda(),
+                q_rope=normal(g, 6, 4, 64).cuda(), q_out=torch.full((6, 4, 64), 5.0, dtype=BF, device="cuda"),
+                positions=i32([0, 1, 2, 3, 4, 5]), norm_weight=normal(g, 512).cuda())
+
+
+@pytest.mark.parametrize("name,change", [
+    ("latent", lambda t: t.float()), ("latent", lambda t: t[:, :511]), ("latent", lambda t: t[:5]),
+    ("latent", lambda t: t.cpu()), ("latent", lambda t: None), ("k_rope", lambda t: t[:, :63]),
+    ("k_rope", lambda t: t[:5]), ("qo_indptr", lambda t: t[:2]), ("qo_indptr", lambda t: t.long()),
+    ("kv_lens", lambda t: t.repeat(2)[::2]), ("block_table", lambda t: t.float()), ("cache", lambda t: t.float()),
+    ("rope_table", lambda t: t.double()), ("rope_table", lambda t: t[:, :32]), ("rope_table", lambda t: t.t()),
+    ("q_rope", lambda t: None), ("q_out", lambda t: None), ("q_out", lambda t: t[:, :3]),
+    ("q_out", lambda t: t.float()), ("q_rope", lambda t: t[:, :, :32]), ("q_out", lambda t: t[:1].expand(6, 4, 64)),
+    ("positions", lambda t: t.long()), ("positions", lambda t: t[:5]), ("norm_weight", lambda t: t.float()),
+    ("norm_weight", lambda t: t[:511]), ("rope_style", lambda t: 2), ("norm_eps", lambda t: -1.0)])
+def test_append_refuses(name, change):
+    args = _append_args()
+    cache, q_out = args["cache"], args["q_out"]
+    args[name] = change(args.get(name))
+    with pytest.raises(abi.MlaTreeError):
+        abi.mla_paged_append(**args)
+    torch.cuda.synchronize()
+    assert (cache == 3.0).all() and (q_out == 5.0).all()
