@@ -762,10 +762,12 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
         if (~vis != 0) {
           // rows that are no keys of this request count with weight 0, but
           // 0 x NaN is NaN: their values are made 0
-          for (int r = tid >> 6; r < kTile; r += 2 * kHalf / 64)
-            if (!(vis >> r & 1))
-              *reinterpret_cast<uint4*>(sm + L::kKV + st * kStage + (r >> 3) * kGroup + ((tid & 63) >> 3) * 1024 +
-                                        (r & 7) * 128 + (tid & 7) * 16) = make_uint4(0, 0, 0, 0);
+          uint8_t* row0 = sm + L::kKV + st * kStage + (tid >> 6) * 128 + ((tid & 63) >> 3) * 1024 + (tid & 7) * 16;
+          const uint64_t mine = vis >> (tid >> 6);  // this thread's rows: tid / 64 + 4 i
+#pragma unroll
+          for (int i = 0; i < kTile / 4; ++i)
+            if (!(mine >> (4 * i) & 1))
+              *reinterpret_cast<uint4*>(row0 + (i >> 1) * kGroup + (i & 1) * 512) = make_uint4(0, 0, 0, 0);
         }
         fence_async_smem();
         __syncwarp();
@@ -798,35 +800,36 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
       if (!dead) dead = !wait_phase(&bars[B_P_EMPTY], (it - 1) & 1, abort, limit);
       tc_fence_after();
       const bool give_up = __any_sync(kFull, dead || *abort);  // nothing to write
+      constexpr int kM = 32 / NC;               // blocks of 128 dims a thread holds at once
 #pragma unroll 1
-      for (int m = 0; m < 4 && !give_up; ++m) {
-        uint32_t o[NC];
+      for (int m0 = 0; m0 < 4 && !give_up; m0 += kM) {
+        uint32_t o[kM * NC];
 #pragma unroll
-        for (int c = 0; c < NC; c += 8) {
+        for (int c = 0; c < kM * NC; c += 8) {
           uint32_t part[8];
-          tmem_ld8_nw(tmem + lane_base + L::kO + m * N + c0 + c, part);
+          tmem_ld8_nw(tmem + lane_base + L::kO + (m0 + c / NC) * N + c0 + c % NC, part);
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[c + e] = part[e];
         }
         tmem_ld_wait();
         tmem_regs_ready(o);
         // all products before the first store: it might change the factors for all the compiler knows
-        float v[NC];
+        float v[kM * NC];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) v[c] = __uint_as_float(o[c]) * redh[c];
-        const int dim = m * 128 + quad * 32;
+        for (int c = 0; c < kM * NC; ++c) v[c] = __uint_as_float(o[c]) * redh[c % NC];
+        const int dim = m0 * 128 + quad * 32;
         if (whole) {
           uint16_t* dst = a.out + (orow + c0) * kDv + dim;
 #pragma unroll
-          for (int c = 0; c < NC; c += 4) {
+          for (int c = 0; c < kM * NC; c += 4) {
             const float x[4] = {v[c], v[c + 1], v[c + 2], v[c + 3]};
-            store_heads4(dst + c * kDv, lane, x, nh - c0 - c);
+            store_heads4(dst + (c % NC) * kDv + c / NC * 128, lane, x, nh - c0 - c % NC);
           }
         } else {
           float* dst = a.ws_o + (wrow + c0) * kDv + dim + lane;
 #pragma unroll
-          for (int c = 0; c < NC; ++c)
-            if (c0 + c < nh) dst[c * kDv] = v[c];
+          for (int c = 0; c < kM * NC; ++c)
+            if (c0 + c % NC < nh) dst[(c % NC) * kDv + c / NC * 128] = v[c];
         }
       }
       tc_fence_before();
