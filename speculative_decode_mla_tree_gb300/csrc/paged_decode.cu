@@ -185,17 +185,18 @@ __global__ void __launch_bounds__(32 * kWarps) decode_simt_kernel(const DecodeAr
 // leaves 152 partials a head and few heads: there a block takes an eighth of a
 // head row, a warp load being 256 bytes of each of two partials, all in flight
 // at once. Sums are in a fixed order, so the result is the same in every run.
-// Alone and back to back, from L2: 5.6 us for 24 MB of partials (32 requests of
-// 8192 keys, 64 heads), 7.2 us for 27 MB (the 64-request mix), 6.0 us for 20 MB
-// of one request. With R = 1 alone the first two take 9.2 and 8.9 us (128 heads
-// 19.0 instead of 8.4), with warps in the place of blocks the third 9.7; with 8
-// loads in flight and twice the blocks they take 6.8, 9.5 and 12.9 us, by bulk
-// copies into shared memory 10.6, 16.3 and 17.5.
+// Alone and back to back, from L2, it takes 5.8 us for 24 MB of partials (32
+// requests of 8192 keys, 64 heads), 8.5 us for 31 MB (48 requests, 128 heads),
+// 6.1 us for 20 MB of one request and 4.2 us for 37 short ragged ones. With R =
+// 1 alone the first two take 7.0 and 13.0 us, with warps in the place of blocks
+// the third 11.7; 16 loads in flight in two blocks an SM instead of 8 in three
+// take 5.7, 8.6, 6.0 and 5.0; by bulk copies into shared memory the first and
+// third took 10.6 and 17.5.
 constexpr int kMergeThreads = 256;
 constexpr int kMergeWarps = kMergeThreads / 32;
-constexpr int kMergeBlocksPerSm = 2;
+constexpr int kMergeBlocksPerSm = 3;
 constexpr int kMaxEntries = 512;  // two an SM, see decode_sms
-constexpr int kAhead = 16;
+constexpr int kAhead = 8;
 constexpr int kQuarter = kDv / 4;
 constexpr int kEighth = kDv / 8;
 constexpr int kHalfWarps = kMergeThreads / 16;
@@ -395,9 +396,9 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeBlocksPerSm)
   const int each = (parts + n - 1) / n;
   if (each > kManyParts) {
     merge_blocks(a, sh, n, step, rows);
-  } else if (each <= kAhead / 4 && heads >= warps) {
+  } else if (each <= kAhead && heads >= warps) {
     merge_items<4>(a, sh, n, step, rows, 0);
-  } else if (each <= kAhead / 2 && heads * 2 >= warps) {
+  } else if (each <= kAhead && heads * 2 >= warps) {
     merge_items<2>(a, sh, n, step, rows, 0);
   } else {
     int wl = 0;
