@@ -5,6 +5,7 @@ library is missing this module raises instead of computing anything."""
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -322,9 +323,25 @@ def mla_tree_verify_noalloc(q, kv_buf, kv_indices, kv_indptr, qo_indptr, packed_
 
 ROPE_PAIRS, ROPE_HALVES = 0, 1
 
-# The paged calls run once per layer and token, where their own time shows: all
-# arguments are checked in one expression, and a call that fails it goes through
-# the checks again one by one for its message.
+# The paged calls run once per layer and token, where their own time shows: a
+# compiled module (csrc/paged_call.cpp) checks the tensors and calls the
+# library. What does not fit comes back as None and goes through the checks
+# here, one by one, for its message.
+_CALL_PATH = os.path.join(_HERE, "lib", "_paged_call.so")
+_paged_call = None
+
+
+def _load_paged_call():
+    global _paged_call
+    lib = load()
+    if not os.path.exists(_CALL_PATH):
+        raise MlaTreeError("_paged_call.so is not built (%s); run __graft_entry__.build()" % _CALL_PATH)
+    spec = importlib.util.spec_from_file_location("_paged_call", _CALL_PATH)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.bind(*(ctypes.cast(f, P).value for f in (lib.mla_paged_append, lib.mla_paged_decode)))
+    _paged_call = mod
+    return mod
 
 
 def _refuse(name, t, dtype, dim, dev, shape=None, whole=False):
@@ -394,14 +411,6 @@ def _refuse_decode(q, cache, block_table, kv_lens, out, lse, workspace, status):
     raise MlaTreeError("unsupported arguments")
 
 
-def _call(dev, stream, fn, *args):
-    """fn(*args, stream) with dev current: the stream given, or dev's current one."""
-    if torch._C._cuda_getDevice() != dev:
-        with torch.cuda.device(dev):
-            return _call(dev, stream, fn, *args)
-    return fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
-
-
 def mla_paged_append(latent, k_rope, qo_indptr, kv_lens, block_table, cache, rope_table, q_rope=None,
                      q_out=None, positions=None, norm_weight=None, norm_eps=1e-6,
                      rope_style=ROPE_PAIRS, status=None, stream=None):
@@ -409,56 +418,14 @@ def mla_paged_append(latent, k_rope, qo_indptr, kv_lens, block_table, cache, rop
     latent [T, 512] (RMS-normalised where norm_weight is given) and k_rope
     [T, 64] rotated to its position, at position kv_lens[b] - n_b + i of
     request b's pages block_table[b]; and q_out = q_rope [T, H, 64] rotated
-    alike (q_out may be q_rope). rope_table: fp32 [positions, 64], cos | sin."""
-    bf16, i32 = torch.bfloat16, torch.int32
-    heads, q, qs, o, os_ = 0, None, (0, 0), None, (0, 0)
-    try:
-        dev = cache.get_device()
-        pages, size, width = cache.shape
-        batch, max_pages = block_table.shape
-        t = latent.shape[0]
-        angles = rope_table.shape[0]
-        cs, ts, ls, ks = cache.stride(), block_table.stride(), latent.stride(), k_rope.stride()
-        ok = (dev >= 0 and width == 576 and size > 0 and cs[2] == 1 and (cs[1] == 576 or size == 1)
-              and cache.dtype is bf16 and (ts[1] == 1 or max_pages < 2) and block_table.dtype is i32
-              and block_table.get_device() == dev
-              and kv_lens.shape == (batch,) and kv_lens.dtype is i32 and kv_lens.get_device() == dev
-              and kv_lens.is_contiguous()
-              and latent.shape == (t, 512) and ls[1] == 1 and latent.dtype is bf16 and latent.get_device() == dev
-              and k_rope.shape == (t, 64) and ks[1] == 1 and k_rope.dtype is bf16 and k_rope.get_device() == dev
-              and qo_indptr.shape == (batch + 1,) and qo_indptr.dtype is i32 and qo_indptr.get_device() == dev
-              and qo_indptr.is_contiguous()
-              and rope_table.shape == (angles, 64) and rope_table.dtype is torch.float32
-              and rope_table.get_device() == dev and rope_table.is_contiguous()
-              and (q_rope is None) == (q_out is None))
-        if ok and q_rope is not None:
-            heads = q_rope.shape[1]
-            qs, os_ = q_rope.stride(), q_out.stride()
-            ok = (q_rope.shape == (t, heads, 64) and q_out.shape == q_rope.shape and qs[2] == 1 and os_[2] == 1
-                  and q_rope.dtype is bf16 and q_out.dtype is bf16 and q_rope.get_device() == dev
-                  and q_out.get_device() == dev)
-            if heads:
-                q, o = q_rope.data_ptr(), q_out.data_ptr()
-        if ok and positions is not None:
-            ok = (positions.shape == (t,) and positions.dtype is i32 and positions.get_device() == dev
-                  and positions.is_contiguous())
-        if ok and norm_weight is not None:
-            ok = (norm_weight.shape == (512,) and norm_weight.dtype is bf16 and norm_weight.get_device() == dev
-                  and norm_weight.is_contiguous())
-        if ok and status is not None:
-            ok = status.dtype is i32 and status.get_device() == dev and status.is_contiguous()
-    except (AttributeError, ValueError, IndexError):
-        ok = False
-    if not ok:
+    alike (q_out may be q_rope). rope_table: fp32 [positions, 64], cos | sin.
+    Runs on the cache's device, on stream or that device's current one."""
+    rc = (_paged_call or _load_paged_call()).append(
+        latent, k_rope, qo_indptr, kv_lens, block_table, cache, rope_table, q_rope, q_out, positions, norm_weight,
+        norm_eps, rope_style, status, None if stream is None else stream.cuda_stream)
+    if rc is None:
         _refuse_append(latent, k_rope, qo_indptr, kv_lens, block_table, cache, rope_table, q_rope, q_out, positions,
                        norm_weight, status)
-    rc = _call(dev, stream, (_lib or load()).mla_paged_append,
-               latent.data_ptr(), ls[0] if t > 1 else 512, k_rope.data_ptr(), ks[0] if t > 1 else 64,
-               None if norm_weight is None else norm_weight.data_ptr(), norm_eps,
-               q, qs[0], qs[1], o, os_[0], os_[1], heads, rope_table.data_ptr(), angles, rope_style,
-               None if positions is None else positions.data_ptr(), qo_indptr.data_ptr(), kv_lens.data_ptr(),
-               batch, t, block_table.data_ptr(), ts[0] if batch > 1 else max_pages, max_pages, cache.data_ptr(),
-               cs[0] if pages > 1 else size * 576, pages, size, None if status is None else status.data_ptr())
     if rc != MT_OK:
         _check(rc, "mla_paged_append")
 
@@ -472,36 +439,12 @@ def mla_paged_decode(q, cache, block_table, kv_lens, sm_scale, out, lse, workspa
     """Attention of one new token per request over a paged latent cache: q
     [B, H, 576] over the first kv_lens[b] positions of request b's pages;
     out [B, H, 512] bf16 and lse [B, H] fp32. workspace: uint8, at least
-    mla_paged_decode_workspace_bytes(B, H)."""
-    bf16, i32 = torch.bfloat16, torch.int32
-    try:
-        dev = cache.get_device()
-        pages, size, width = cache.shape
-        batch, max_pages = block_table.shape
-        heads, nbytes = q.shape[1], workspace.numel()
-        cs, ts, qs = cache.stride(), block_table.stride(), q.stride()
-        ok = (dev >= 0 and width == 576 and size > 0 and cs[2] == 1 and (cs[1] == 576 or size == 1)
-              and cache.dtype is bf16 and (ts[1] == 1 or max_pages < 2) and block_table.dtype is i32
-              and block_table.get_device() == dev
-              and kv_lens.shape == (batch,) and kv_lens.dtype is i32 and kv_lens.get_device() == dev
-              and kv_lens.is_contiguous()
-              and q.shape == (batch, heads, 576) and qs[2] == 1 and q.dtype is bf16 and q.get_device() == dev
-              and out.shape == (batch, heads, 512) and out.dtype is bf16 and out.get_device() == dev
-              and out.is_contiguous()
-              and lse.shape == (batch, heads) and lse.dtype is torch.float32 and lse.get_device() == dev
-              and lse.is_contiguous()
-              and workspace.dtype is torch.uint8 and workspace.dim() == 1 and workspace.get_device() == dev
-              and workspace.is_contiguous()
-              and (status is None or status.dtype is i32 and status.get_device() == dev and status.is_contiguous()))
-    except (AttributeError, ValueError, IndexError):
-        ok = False
-    if not ok:
+    mla_paged_decode_workspace_bytes(B, H). Runs on the cache's device, on
+    stream or that device's current one."""
+    rc = (_paged_call or _load_paged_call()).decode(
+        q, cache, block_table, kv_lens, sm_scale, out, lse, workspace, status,
+        None if stream is None else stream.cuda_stream)
+    if rc is None:
         _refuse_decode(q, cache, block_table, kv_lens, out, lse, workspace, status)
-    rc = _call(dev, stream, (_lib or load()).mla_paged_decode,
-               q.data_ptr(), qs[0] if batch > 1 else heads * 576, qs[1] if heads > 1 else 576, cache.data_ptr(),
-               cs[0] if pages > 1 else size * 576, pages, size, block_table.data_ptr(),
-               ts[0] if batch > 1 else max_pages, max_pages, kv_lens.data_ptr(), batch, heads, sm_scale,
-               out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), nbytes,
-               None if status is None else status.data_ptr())
     if rc != MT_OK:
         _check(rc, "mla_paged_decode")

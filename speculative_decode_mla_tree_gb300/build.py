@@ -1,7 +1,8 @@
 """Compile the CUDA library in tree: every csrc/*.cu for sm_103a, linked
-into lib/libmla_tree.so (static CUDA runtime). Translation units compile in
-parallel; a unit is rebuilt only when a source or header is newer than its
-object file."""
+into lib/libmla_tree.so (static CUDA runtime), and csrc/paged_call.cpp, the
+paged calls' way in from Python tensors, into lib/_paged_call.so. Translation
+units compile in parallel; a unit is rebuilt only when a source or header is
+newer than its object file."""
 from __future__ import annotations
 
 import glob
@@ -15,6 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "lib")
 OBJDIR = os.path.join(LIBDIR, "obj")
 LIB = os.path.join(LIBDIR, "libmla_tree.so")
+CALL_SRC = os.path.join(CSRC, "paged_call.cpp")
+CALL = os.path.join(LIBDIR, "_paged_call.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -45,11 +48,34 @@ def _compile(src, ptxas_verbose=False):
     return obj, r.stderr
 
 
+def _compile_call():
+    """The extension module, against this interpreter's headers and torch's."""
+    import sysconfig
+
+    import torch
+    newest = max(os.path.getmtime(CALL_SRC), os.path.getmtime(os.path.join(ROOT, "include", "mla_tree.h")))
+    if os.path.exists(CALL) and os.path.getmtime(CALL) >= newest:
+        return CALL
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda", "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(t, "include"),
+           "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"), "-I" + cuda, CALL_SRC, "-o", CALL,
+           "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s\n%s" % (CALL_SRC, " ".join(cmd), r.stderr))
+    return CALL
+
+
 def build(verbose=False, ptxas_verbose=False) -> str:
     os.makedirs(OBJDIR, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
+        call = ex.submit(_compile_call)
         results = list(ex.map(lambda s: _compile(s, ptxas_verbose), srcs))
+        call.result()
     objs = [o for o, _ in results]
     if verbose or ptxas_verbose:
         for (o, log) in results:
