@@ -28,14 +28,14 @@
 //
 // What bounds it. Up to 64 heads, HBM: 73.7 KB a tile at 6782 GB/s of copy
 // bandwidth are 1.65 us an SM, of which the tensor cores need 0.8 us (16 heads)
-// to 1.05 us (64 heads). 4 requests of 200000 keys at 16 heads take 140 us
-// (6.6 TB/s), the 64-request mix of 128 to 131072 keys at 64 heads 225 us (6.3
-// TB/s). A call's fixed part shows in short ones: about 2.5 us until the first
-// load (plan, page numbers), 1.5 us of first loads, 2.5 us for a 128 KB partial
+// to 1.05 us (64 heads). 4 requests of 200000 keys at 16 heads take 141 us (6.5
+// TB/s), the 64-request mix of 128 to 131072 keys at 64 heads 224 us (6.3
+// TB/s). A call's fixed part shows in short ones: 2 to 2.5 us until the first
+// load (plan, page numbers), 1.5 us of first loads, 2.3 us for a 128 KB partial
 // at the 28 bytes a cycle that an SM stores, 4 to 8 us of merge. At 128 heads
-// every tile is needed by two SMs, and the latency of a stage's round bounds:
-// loads 0.5 us, scores 0.9 us next to the other stage's P.V, softmax 0.45 us,
-// P.V, 1.4 us per tile with two stages in shared memory.
+// every tile is needed by two SMs and shared memory bounds: per tile and SM the
+// score products read 144 KB of it, P V 96 KB, and 74 KB are written, 2450
+// cycles at 128 bytes; a tile takes 2750.
 //
 // Roles (352 threads): eight softmax warps (a TMEM lane quarter and half of the
 // heads each; four warps took 1.0 us a tile at 64 heads, eight 0.45), a TMA
