@@ -343,6 +343,15 @@ __device__ __forceinline__ Walk make_plan(const Params& p, int team, int64_t* sh
   return r;
 }
 
+// Shared memory is not left while copies into it are in flight: waits for the
+// last query load and the last tiles' loads (a phase that a give-up broke off
+// runs out after kDrainNs). it: tiles begun.
+__device__ __noinline__ void drain_loads(uint64_t* bars, uint32_t pieces, uint32_t it) {
+  if (pieces) mbar_drain(&bars[B_Q_FULL], (pieces - 1) & 1, kDrainNs);
+  for (uint32_t back = 0; back < kStages; ++back)
+    if (it > back) mbar_drain(&bars[B_KV_FULL + ((it - 1 - back) & 1)], ((it - 1 - back) >> 1) & 1, kDrainNs);
+}
+
 // ------------------------------------------------------------------- kernel
 
 // kGather: pages that are no whole groups of eight rows; two producer warps
@@ -458,12 +467,7 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
         }
       }
     }
-    if (*abort) {
-      if (pieces) mbar_drain(&bars[B_Q_FULL], (pieces - 1) & 1, kDrainNs);
-      for (uint32_t back = 0; back < kStages; ++back)
-        if (it > back)
-          mbar_drain(&bars[B_KV_FULL + ((it - 1 - back) & 1)], ((it - 1 - back) >> 1) & 1, kDrainNs);
-    }
+    drain_loads(bars, pieces, it);
   } else if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
     const int per = p.page_groups % 2 == 0 ? 2 : 1;  // groups of a box: a pair lies in one page, or may not
@@ -552,12 +556,7 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
         for (int i = 0; i <= kAhead; ++i) pages[i] = pages[i + 1], place[i] = place[i + 1];
       }
     }
-    if (*abort) {  // let the copies in flight land (a phase that no copy ends runs out here)
-      if (pieces) mbar_drain(&bars[B_Q_FULL], (pieces - 1) & 1, kDrainNs);
-      for (uint32_t back = 0; back < kStages; ++back)
-        if (it > back)  // `it` counts the tile that was broken off
-          mbar_drain(&bars[B_KV_FULL + ((it - 1 - back) & 1)], ((it - 1 - back) >> 1) & 1, kDrainNs);
-    }
+    drain_loads(bars, pieces, it);
   } else if (warp == kQkWarp) {
     // --------------------------------------------------------------- S = QK
     // The MMA warps run converged and elect a lane per instruction: issued
@@ -594,10 +593,10 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
       }
       ++pieces;
     }
-    if (dead) {
-      mma_commit_elect(&bars[B_DRAIN]);
-      mbar_drain(&bars[B_DRAIN], 0, kDrainNs);
-    }
+    // TMEM is not given back under an MMA (after a give-up of another role
+    // nobody else has waited for the last ones)
+    mma_commit_elect(&bars[B_DRAIN]);
+    mbar_drain(&bars[B_DRAIN], 0, kDrainNs);
   } else if (warp == kPvWarp) {
     // ----------------------------------------------------------- O += V^T P
     // A warp of its own: P.V of a tile must not queue behind QK of the next,
@@ -633,10 +632,8 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
       }
       ++pieces;
     }
-    if (dead) {
-      mma_commit_elect(&bars[B_DRAIN + 1]);
-      mbar_drain(&bars[B_DRAIN + 1], 0, kDrainNs);
-    }
+    mma_commit_elect(&bars[B_DRAIN + 1]);
+    mbar_drain(&bars[B_DRAIN + 1], 0, kDrainNs);
   } else {
     // ------------------------------------------------------ softmax, epilogue
     // Warp w serves TMEM lane quarter w % 4 and one half of the heads, w / 4;
@@ -682,6 +679,7 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
         if (!dead) dead = !wait_phase(&bars[B_KV_FULL + st], ph, abort, limit);
         const uint64_t vis = vmask[st];
         if (!dead) dead = !wait_phase(&bars[B_S_FULL + st], ph, abort, limit);
+        __syncwarp();
         tc_fence_after();
         uint32_t s[NC / 2];
         tmem_ld_frag(tmem + lane_base + L::kS + st * N + c0, s);
@@ -727,6 +725,7 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
           if (t > pc.t0) {  // the first tile's P.V overwrites O
             named_bar_sync(bar_id, kHalf);
             if (!dead) dead = !wait_phase(&bars[B_P_EMPTY], (it & 1) ^ 1, abort, limit);
+            __syncwarp();
             tc_fence_after();
 #pragma unroll 1
             for (int m = 0; m < 4; ++m)
@@ -757,6 +756,7 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
             pk[2 * i + k] = *reinterpret_cast<const uint32_t*>(&h);
           }
         if (!dead) dead = !wait_phase(&bars[B_P_EMPTY], (it & 1) ^ 1, abort, limit);
+        __syncwarp();
         if constexpr (NC == 8) {
           stmatrix2_trans(paddr, pk[0], pk[1]);
         } else {
@@ -779,7 +779,9 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
         if (lane == 0) mbar_arrive(&bars[B_P_FULL]);
       }
 
-      // epilogue: sums over the keys' lanes and warps, then O^T / l
+      // epilogue: sums over the keys' lanes and warps, then O^T / l. The other
+      // warps may still be at the maxima or factors of the last tile.
+      named_bar_sync(bar_id, kHalf);
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
         float v = l[j];
