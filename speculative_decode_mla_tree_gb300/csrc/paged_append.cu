@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kHeadsPerTask = 16;   // four 16-byte loads in flight a lane (8 heads: 31.6 us, 32: the same as 16)
+constexpr int kHeadsPerTask = 16;   // four 16-byte loads in flight a lane (8 heads: 30.0 us for those prompts, 4: 39.9, 32: the same as 16)
 constexpr int kIters = kHeadsPerTask / 4;
 constexpr unsigned kFull = 0xffffffffu;
 
