@@ -80,16 +80,17 @@ __global__ void __launch_bounds__(32 * kWarps) decode_simt_kernel(const DecodeAr
   float o[16], m = -INFINITY, l = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) o[i] = 0.f;
-  const int j1 = (int)min((int64_t)len, (int64_t)(s + 1) * split_keys);
+  // unsigned: the position behind the last of 2^31 - 1 is no int
+  const unsigned j1 = (unsigned)min((int64_t)len, (int64_t)(s + 1) * split_keys);
   const int32_t* table = a.kv.table + b * a.kv.table_stride;
-  for (int j = s * split_keys; j < j1; j += kKeys) {
+  for (unsigned j = (unsigned)s * split_keys; j < j1; j += kKeys) {
     uint4 row[kKeys][3];
     bool see[kKeys];
 #pragma unroll
     for (int t = 0; t < kKeys; ++t) {
       see[t] = j + t < j1;
       if (!see[t]) continue;
-      const int in_table = (j + t) / a.kv.page_size;
+      const unsigned in_table = (j + t) / (unsigned)a.kv.page_size;
       const int page = __ldg(table + in_table);
       see[t] = page >= 0 && page < a.kv.num_pages;
       if (!see[t]) {

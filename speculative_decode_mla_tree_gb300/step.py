@@ -170,7 +170,8 @@ class DecodeStep:
         self.qo_indptr = torch.arange(batch + 1, dtype=torch.int32, device=dev)
         self.out = torch.zeros(batch, heads, 512, dtype=torch.bfloat16, device=dev)
         self.lse = torch.zeros(batch, heads, dtype=torch.float32, device=dev)
-        n = abi.mla_paged_decode_workspace_bytes(batch, heads)
+        with torch.cuda.device_of(cache):  # the size depends on the device
+            n = abi.mla_paged_decode_workspace_bytes(batch, heads)
         self.workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
 
