@@ -18,7 +18,10 @@
 // weights are relative to) moves only when a score exceeds it by more than 8 in
 // log2, which is asked with one OR over the warps of a half per tile. Only then
 // are the maxima exchanged and O^T rescaled; after a request's first tile that
-// is rare. Weights stay below 2^8 and the sums are fp32, so nothing is lost.
+// is rare. Weights stay at most 2^8 and the sums are fp32. References are whole
+// numbers (a maximum rounded up), so another reference changes a weight by a
+// power of two: its rounding to bf16, and with it a request's result, does not
+// depend on where the shares of a batch begin.
 //
 // Work split: the batch is a line of 64-key tiles (a request adds kOverhead
 // tiles for its query load and epilogue), cut into equal shares, one per team
@@ -716,7 +719,7 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
           for (int j = 0; j < kC; ++j) {
             const int c = 8 * (j >> 1) + 2 * (lane & 3) + (j & 1);
             const float m = fmaxf(fmaxf(redh[c], redh[N + c]), fmaxf(redh[2 * N + c], redh[3 * N + c]));
-            const float nr = fmaxf(ref[j], m);
+            const float nr = fmaxf(ref[j], ceilf(m));
             f[j] = ex2_approx(ref[j] - nr);
             ref[j] = nr;
             l[j] *= f[j];
