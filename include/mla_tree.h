@@ -469,7 +469,9 @@ size_t mla_paged_decode_workspace_bytes(int batch, int heads);
  * left unwritten. What cache rows behind a request's last position hold
  * (NaN included) does not matter.
  * Scores are fp32 sums of bf16 products, the softmax and its sums are fp32,
- * the weights are rounded to bf16 for the product with the values, and partial
+ * the weights are rounded to bf16 for the product with the values, whose sum is
+ * divided by that of the same bf16 weights (lse sums the unrounded ones; the
+ * kernel for other layouts, below, rounds none), and partial
  * results of a split are fp32. A request's result does not depend on
  * the rest of the batch beyond the fp32 rounding of sums that are taken in
  * another order where the splits fall elsewhere (about 1 in 100 outputs then

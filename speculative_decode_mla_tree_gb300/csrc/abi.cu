@@ -427,7 +427,7 @@ int mla_paged_decode(const mt_bf16* q, int64_t q_token_stride, int64_t q_head_st
   a.status = dev_status;
   char* ws = (char*)workspace;
   a.ws_entry = (MergeEntry*)ws;
-  a.ws_lse = (float*)(ws + wl.lse_off);
+  a.ws_lse = (float2*)(ws + wl.lse_off);
   a.ws_o = (float*)(ws + wl.o_off);
   const cudaError_t e = launch_paged_decode_tc(a, nsm, (cudaStream_t)stream);
   if (e != cudaErrorNotSupported) return cuda_status(e);

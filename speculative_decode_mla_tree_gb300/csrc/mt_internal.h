@@ -132,7 +132,9 @@ struct DecodeArgs {
   int32_t* status;
   // workspace views
   MergeEntry* ws_entry;
-  float* ws_lse;                // [slots][rows_per_slot]
+  // A partial: o is its weighted sum over the sum l of its weights; x = ln l (with
+  // the maximum), y = the sum of the weights as o's product took them, over l.
+  float2* ws_lse;               // [slots][rows_per_slot]
   float* ws_o;                  // [slots][rows_per_slot][512]
 };
 

@@ -23,7 +23,7 @@ DecodeLayout decode_layout(int heads, int num_sms) {
   w.entries = 2 * nsm;
   w.rows = 2LL * (nsm > groups ? nsm : groups) * (padded_heads(heads) / (heads > 64 ? groups : 1));
   w.lse_off = align256(sizeof(MergeEntry) * (size_t)w.entries);
-  w.o_off = align256(w.lse_off + sizeof(float) * (size_t)w.rows);
+  w.o_off = align256(w.lse_off + sizeof(float2) * (size_t)w.rows);
   w.total = align256(w.o_off + sizeof(float) * (size_t)w.rows * kDv);
   return w;
 }
@@ -172,11 +172,12 @@ __global__ void __launch_bounds__(32 * kWarps) decode_simt_kernel(const DecodeAr
     for (int i = 0; i < 2; ++i)
       dst[2 * (lane + 32 * k) + i] = make_float4(o[8 * k + 4 * i] * inv, o[8 * k + 4 * i + 1] * inv,
                                                  o[8 * k + 4 * i + 2] * inv, o[8 * k + 4 * i + 3] * inv);
-  if (lane == 0) a.ws_lse[row] = lse;
+  if (lane == 0) a.ws_lse[row] = make_float2(lse, 1.f);  // its weights are not rounded
 }
 
-// Joins split requests: with w_i = exp(lse_i - max lse),
-//     out = sum_i w_i o_i / sum_i w_i,  lse = max lse + ln sum_i w_i.
+// Joins split requests: with w_i = exp(lse_i - max lse) and c_i what the sum of
+// partial i's rounded weights is of that of its weights,
+//     out = sum_i w_i o_i / sum_i w_i c_i,  lse = max lse + ln sum_i w_i.
 // What bounds it is latency (entries, then lse and partials, from L2), so a
 // warp has up to kAhead loads of 512 bytes in flight and makes the weights
 // meanwhile: of R quarters of a head row and the first kAhead / R partials. R
@@ -235,7 +236,8 @@ __device__ __forceinline__ void write_dims(const DecodeArgs& a, int64_t row, int
 struct MergeShared {
   MergeEntry list[kMaxEntries];
   float4 acc[kMergeWarps][32];
-  float wt[kMaxEntries], red[kMergeWarps], tots[kMergeWarps];
+  float2 wt[kMaxEntries], tots[kMergeWarps];
+  float red[kMergeWarps];
   int counts[kMergeWarps], sums[kMergeWarps];
 };
 
@@ -254,7 +256,7 @@ __device__ __forceinline__ void merge_items(const DecodeArgs& a, MergeShared& sh
     const MergeEntry e = mine ? sh.list[en] : MergeEntry{0, 0, 0, 0};
     // the workspace has fewer than 2^31 rows
     auto row_of = [&](int i) { return (int64_t)((i == 0 ? e.first : e.next + (i - 1) * step) * rows + h); };
-    auto lse_of = [&](int i) { return i < e.n ? __ldcg(a.ws_lse + row_of(i)) : -INFINITY; };
+    auto lse_of = [&](int i) { return i < e.n ? __ldcg(a.ws_lse + row_of(i)) : make_float2(-INFINITY, 1.f); };
     float4 v[kParts][R];
     auto load = [&](int k0) {  // this warp's partials are sub + W k
 #pragma unroll
@@ -267,24 +269,29 @@ __device__ __forceinline__ void merge_items(const DecodeArgs& a, MergeShared& sh
     };
     load(0);
     // lane l: partial l for the maximum, this warp's l-th partial for its weight
-    const float seen = lse_of(lane), own = wl == 0 ? seen : lse_of(sub + (lane << wl));
-    float mx = not_nan(seen);
-    for (int i = 32 + lane; i < e.n; i += 32) mx = fmaxf(mx, not_nan(lse_of(i)));
+    const float2 seen = lse_of(lane), own = wl == 0 ? seen : lse_of(sub + (lane << wl));
+    float mx = not_nan(seen.x);
+    for (int i = 32 + lane; i < e.n; i += 32) mx = fmaxf(mx, not_nan(lse_of(i).x));
     mx = warp_max(mx);
     float4 s[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) s[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float tot = 0.f, w = weight(own, mx);
+    float tot = 0.f, rounded = 0.f, w = weight(own.x, mx), wc = w * own.y;
     for (int k0 = 0; sub + (k0 << wl) < e.n; k0 += kParts) {
       if (k0 > 0) {
         load(k0);
-        if ((k0 & 31) == 0) w = weight(lse_of(sub + ((k0 + lane) << wl)), mx);
+        if ((k0 & 31) == 0) {
+          const float2 more = lse_of(sub + ((k0 + lane) << wl));
+          w = weight(more.x, mx);
+          wc = w * more.y;
+        }
       }
 #pragma unroll
       for (int k = 0; k < kParts; ++k)
         if (sub + ((k0 + k) << wl) < e.n) {
           const float wk = __shfl_sync(kFull, w, (k0 + k) & 31);
           tot += wk;
+          rounded += __shfl_sync(kFull, wc, (k0 + k) & 31);
 #pragma unroll
           for (int r = 0; r < R; ++r) add(s[r], wk, v[k][r]);
         }
@@ -292,18 +299,19 @@ __device__ __forceinline__ void merge_items(const DecodeArgs& a, MergeShared& sh
     if (R == 1 && W > 1) {
       __syncthreads();  // the item before has been read
       sh.acc[warp][lane] = s[0];
-      if (lane == 0) sh.tots[warp] = tot;
+      if (lane == 0) sh.tots[warp] = make_float2(tot, rounded);
       __syncthreads();
       if (sub == 0)
         for (int k = 1; k < W; ++k) {
-          tot += sh.tots[warp + k];
+          tot += sh.tots[warp + k].x;
+          rounded += sh.tots[warp + k].y;
           add(s[0], 1.f, sh.acc[warp + k][lane]);
         }
     }
     if (!mine || sub != 0) continue;
     const int64_t row = (int64_t)e.b * a.heads + h;
 #pragma unroll
-    for (int r = 0; r < R; ++r) write_dims(a, row, dim + r * kQuarter, tot, s[r]);
+    for (int r = 0; r < R; ++r) write_dims(a, row, dim + r * kQuarter, rounded, s[r]);
     if (dim == 0) a.lse[row] = tot != 0.f ? mx + logf(tot) : -INFINITY;
   }
 }
@@ -325,7 +333,7 @@ __device__ __forceinline__ void merge_blocks(const DecodeArgs& a, MergeShared& s
     float mx = -INFINITY;
     for (int i = tid; i < e.n; i += kMergeThreads) {
       sh.wt[i] = __ldcg(a.ws_lse + row_of(i));
-      mx = fmaxf(mx, not_nan(sh.wt[i]));
+      mx = fmaxf(mx, not_nan(sh.wt[i].x));
     }
     mx = warp_max(mx);
     if (lane == 0) sh.red[warp] = mx;
@@ -333,35 +341,35 @@ __device__ __forceinline__ void merge_blocks(const DecodeArgs& a, MergeShared& s
 #pragma unroll
     for (int w = 0; w < kMergeWarps; ++w) mx = fmaxf(mx, sh.red[w]);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    float tot = 0.f;
+    float tot = 0.f, rounded = 0.f;
+    auto join = [&](const float2& x, const float4& o) {
+      const float w = weight(x.x, mx);
+      tot += w;
+      rounded = fmaf(w, x.y, rounded);
+      add(s, w, o);
+    };
 #pragma unroll
     for (int k = 0; k < kAheadBlock; ++k)
-      if (grp + kHalfWarps * k < e.n) {
-        const float w = weight(sh.wt[grp + kHalfWarps * k], mx);
-        tot += w;
-        add(s, w, v[k]);
-      }
-    for (int i = grp + kHalfWarps * kAheadBlock; i < e.n; i += kHalfWarps) {
-      const float w = weight(sh.wt[i], mx);
-      tot += w;
-      add(s, w, part(i));
-    }
+      if (grp + kHalfWarps * k < e.n) join(sh.wt[grp + kHalfWarps * k], v[k]);
+    for (int i = grp + kHalfWarps * kAheadBlock; i < e.n; i += kHalfWarps) join(sh.wt[i], part(i));
     tot += __shfl_xor_sync(kFull, tot, 16);
+    rounded += __shfl_xor_sync(kFull, rounded, 16);
     s.x += __shfl_xor_sync(kFull, s.x, 16);
     s.y += __shfl_xor_sync(kFull, s.y, 16);
     s.z += __shfl_xor_sync(kFull, s.z, 16);
     s.w += __shfl_xor_sync(kFull, s.w, 16);
     if (lane < 16) sh.acc[warp][lane] = s;
-    if (lane == 0) sh.tots[warp] = tot;
+    if (lane == 0) sh.tots[warp] = make_float2(tot, rounded);
     __syncthreads();
     if (tid < 16) {
 #pragma unroll
       for (int w = 1; w < kMergeWarps; ++w) {
-        tot += sh.tots[w];
+        tot += sh.tots[w].x;
+        rounded += sh.tots[w].y;
         add(s, 1.f, sh.acc[w][lane]);
       }
       const int64_t row = (int64_t)e.b * a.heads + h;
-      write_dims(a, row, dim, tot, s);
+      write_dims(a, row, dim, rounded, s);
       if (dim == 0) a.lse[row] = tot != 0.f ? mx + logf(tot) : -INFINITY;
     }
     __syncthreads();  // wt, red, acc and tots are free for the next item

@@ -21,7 +21,9 @@
 // is rare. Weights stay at most 2^8 and the sums are fp32. References are whole
 // numbers (a maximum rounded up), so another reference changes a weight by a
 // power of two: its rounding to bf16, and with it a request's result, does not
-// depend on where the shares of a batch begin.
+// depend on where the shares of a batch begin. O is divided by the sum of the
+// rounded weights that it is made of, so that it is an average of values (a
+// head that rests on one key gets that key's); lse is made of the unrounded.
 //
 // Work split: the batch is a line of 64-key tiles (a request adds kOverhead
 // tiles for its query load and epilogue), cut into equal shares, one per team
@@ -104,9 +106,9 @@ struct Lay {
   static constexpr int kBars = kP + N * 128;
   static constexpr int kMask = kBars + kNumBars * 8;    // per stage: the tile's visible keys
   static constexpr int kMisc = kMask + kStages * 8;     // tmem base, abort flag
-  static constexpr int kRed = (kMisc + 8 + 15) / 16 * 16;  // [4][N] fp32
-  static constexpr int kVec = kRed + 4 * N * 4;         // [N] fp32
-  static constexpr int kUsed = kVec + N * 4;
+  static constexpr int kRed = (kMisc + 8 + 15) / 16 * 16;  // [4][N] fp32, in the epilogue [7][N]
+  static constexpr int kVec = kRed + 4 * N * 4;         // [N] fp32, in its place while there are tiles
+  static constexpr int kUsed = kRed + 7 * N * 4;
   static constexpr int kBytes = kUsed + 1024;           // slack for aligning the base
   static_assert(kBytes <= 232448, "shared memory budget");
   static_assert(kKV % 1024 == 0 && kP % 1024 == 0 && kRed % 16 == 0 && kVec % 16 == 0, "alignment");
@@ -671,11 +673,11 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
         if (tid < nh) a.lse[orow + tid] = -INFINITY;
         continue;
       }
-      float ref[kC], l[kC];
+      float ref[kC], l[kC], lr[kC];  // sums of the weights and of their roundings
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
         ref[j] = -FLT_MAX;
-        l[j] = 0.f;
+        l[j] = lr[j] = 0.f;
       }
       for (int t = pc.t0; t < pc.t1; ++t, ++it) {
         const int st = it & 1, ph = (it >> 1) & 1;
@@ -723,6 +725,7 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
             f[j] = ex2_approx(ref[j] - nr);
             ref[j] = nr;
             l[j] *= f[j];
+            lr[j] *= f[j];
             if (quad == 0 && lane < 4) vech[c] = f[j];
           }
           if (t > pc.t0) {  // the first tile's P.V overwrites O
@@ -780,31 +783,47 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_P_FULL]);
+        // the product of this tile does not wait for the sums of its weights
+#pragma unroll
+        for (int i = 0; i < NC / 4; ++i) {
+          lr[i & ~1] += bf16_lo(pk[i]);
+          lr[i | 1] += bf16_hi(pk[i]);
+        }
       }
 
-      // epilogue: sums over the keys' lanes and warps, then O^T / l. The other
-      // warps may still be at the maxima or factors of the last tile.
+      // epilogue: sums over the keys' lanes and warps, then O^T over their sum.
+      // The other warps may still be at the maxima or factors of the last tile.
+      // Thread htid finishes column htid; quarter 0's part of its weights' sum
+      // and its reference come by shuffles, for the room in shared memory.
       named_bar_sync(bar_id, kHalf);
+      float col_ref = 0.f, col_l = 0.f;
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
-        float v = l[j];
-        v += __shfl_xor_sync(kFull, v, 4);
-        v += __shfl_xor_sync(kFull, v, 8);
-        v += __shfl_xor_sync(kFull, v, 16);
-        const int c = 8 * (j >> 1) + 2 * (lane & 3) + (j & 1);
-        if (lane < 4) {
-          redh[quad * N + c] = v;
-          if (quad == 0) vech[c] = ref[j];
+        float u = lr[j], v = l[j];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          u += __shfl_xor_sync(kFull, u, o);
+          v += __shfl_xor_sync(kFull, v, o);
         }
+        const int c = 8 * (j >> 1) + 2 * (lane & 3) + (j & 1);
+        if (lane < 4) redh[quad * N + c] = u;
+        if (lane < 4 && quad > 0) redh[(3 + quad) * N + c] = v;
+        const float r = __shfl_sync(kFull, ref[j], lane >> 1 & 3), w = __shfl_sync(kFull, v, lane >> 1 & 3);
+        if (j == 2 * (lane >> 3) + (lane & 1)) col_ref = r, col_l = w;
       }
       named_bar_sync(bar_id, kHalf);
       const bool starts = pc.t0 == 0, whole = starts && pc.t1 == pc.tiles;
       const int64_t wrow = ((int64_t)(2 * team + (starts ? 1 : 0)) * p.groups + grp) * N;
       if (htid < NC) {
-        const float sum = (redh[htid] + redh[N + htid]) + (redh[2 * N + htid] + redh[3 * N + htid]);
-        const float lse = sum != 0.f ? (vech[htid] + log2f(sum)) * kLn2 : -INFINITY;
-        if (c0 + htid < nh && !*abort) (whole ? a.lse[orow + c0 + htid] : a.ws_lse[wrow + c0 + htid]) = lse;
-        redh[htid] = sum != 0.f ? 1.f / sum : 0.f;
+        const float rounded = (redh[htid] + redh[N + htid]) + (redh[2 * N + htid] + redh[3 * N + htid]);
+        const float sum = (col_l + redh[4 * N + htid]) + (redh[5 * N + htid] + redh[6 * N + htid]);
+        const float lse = sum != 0.f ? (col_ref + log2f(sum)) * kLn2 : -INFINITY;
+        const float inv = sum != 0.f ? 1.f / (whole ? rounded : sum) : 0.f;
+        if (c0 + htid < nh && !*abort) {
+          if (whole) a.lse[orow + c0 + htid] = lse;
+          else a.ws_lse[wrow + c0 + htid] = make_float2(lse, rounded * inv);
+        }
+        redh[htid] = inv;
       }
       named_bar_sync(bar_id, kHalf);
       if (!dead) dead = !wait_phase(&bars[B_P_EMPTY], (it - 1) & 1, abort, limit);

@@ -1,5 +1,5 @@
 """How far a decode result may move with what should not matter: the rest of
-the batch."""
+the batch, and the rounding of the weights for the product with the values."""
 import math
 
 import pytest
@@ -68,3 +68,40 @@ def test_decode_alone_as_in_any_batch(heads, page, gap):
         step = 2 * ref.BF16_HALF * torch.maximum(a.abs(), b.abs())
         assert ((a - b).abs() <= step + 640 * 2 * ref.F32_HALF * weight).all()
         assert (a != b).double().mean() <= 0.05, (a != b).double().mean()
+
+
+@LAYOUTS
+@pytest.mark.parametrize("lens", [[65] * 320, [129, 1, 640] * 110, [20011], [2560] * 60],
+                         ids=["two_tiles", "ragged", "long", "batch"])
+def test_decode_average_of_equal_values_is_the_value(lens, page, gap):
+    """All values of a request alike: whatever the weights and however they are
+    rounded, their average is that value, to the few steps of fp32 in which the
+    sums of both sides differ (2^-13 for 20011 keys, under half a step of bf16,
+    2^-9). Every second tile begins with a key at 0, the next one ends with one
+    at 7 to 8 in log2, the rest are far below: within a share that holds both,
+    the larger weight is up to 2^8 and rarely a bf16 value."""
+    g = gen(70)
+    heads = 64
+    cache, flat, table = paged(g, lens, page, gap=gap)
+    value = normal(g, len(lens), 512)
+    q = torch.zeros(len(lens), heads, 576)
+    q[:, :, 512] = 1.0
+    q[:, :, 513] = torch.arange(heads) / 64.0
+    for b, n in enumerate(lens):
+        rows = ref.slots_of(table[b], page, 0, n)
+        late = torch.cat([rows[127::128], rows[-1:]])
+        flat[rows, :512] = value[b]
+        flat[rows, 512:] = 0.0
+        flat[rows, 512] = -100.0
+        flat[rows[::128], 512] = 0.0
+        flat[late, 512] = 7.0
+        flat[late, 513] = 1.0
+    cache.copy_(flat.view(cache.shape))
+    out, lse = decode(q.to(BF).cuda(), cache, table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                      scale=LOG2)
+    assert torch.equal(out.cpu(), value[:, None].expand(-1, heads, -1))
+    for b in sorted(set(lens.index(n) for n in lens)):
+        keys = flat[ref.slots_of(table[b], page, 0, lens[b]), 512:].double()
+        want = torch.logsumexp(q[b, :, 512:].double() @ keys.T * math.log(2.0), -1)
+        # sums of at most 128 + 16 weights in a row a thread, exp2 and log2 to two units in the last place
+        assert ((lse[b].double().cpu() - want).abs() <= 160 * 2 * ref.F32_HALF + want.abs() * 8 * ref.F32_HALF).all()
