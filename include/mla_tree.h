@@ -433,7 +433,10 @@ int mla_tree_verify_noalloc(const mt_bf16* q, const mt_bf16* kv_buf, int64_t num
  *   positions: int32 [total_q] or NULL; norm_weight: bf16 [512] or NULL
  *   qo_indptr: int32 [batch+1], non-decreasing from 0; tokens t >=
  *            qo_indptr[batch] belong to no request and are left out, and
- *            what they would write stays as it was.
+ *            what they would write stays as it was. NULL (total_q == batch,
+ *            else MT_EINVAL) is one token a request, token b for request b,
+ *            where kv_lens[b] == 0 is a slot without a request, whose token is
+ *            left out the same way.
  * Two tokens must not share a cache row (its content is unspecified then).
  * n_b > kv_lens[b], or a qo_indptr that decreases or passes total_q, sets
  * MT_DEV_BAD_INDPTR and leaves out that request; an angle position outside

@@ -380,7 +380,11 @@ def _refuse_append(latent, k_rope, qo_indptr, kv_lens, block_table, cache, rope_
     t = latent.shape[0]
     _refuse("latent", latent, bf16, 2, dev, (t, 512))
     _refuse("k_rope", k_rope, bf16, 2, dev, (t, 64))
-    _refuse("qo_indptr", qo_indptr, i32, 1, dev, (block_table.shape[0] + 1,), True)
+    if qo_indptr is not None:
+        _refuse("qo_indptr", qo_indptr, i32, 1, dev, (block_table.shape[0] + 1,), True)
+    elif t != block_table.shape[0]:
+        raise MlaTreeError("without qo_indptr every request has one token: %d tokens, %d requests"
+                           % (t, block_table.shape[0]))
     _refuse("rope_table", rope_table, torch.float32, 2, dev)
     _refuse("rope_table", rope_table, torch.float32, 2, dev, (rope_table.shape[0], 64), True)
     if (q_rope is None) != (q_out is None):
@@ -419,6 +423,8 @@ def mla_paged_append(latent, k_rope, qo_indptr, kv_lens, block_table, cache, rop
     [T, 64] rotated to its position, at position kv_lens[b] - n_b + i of
     request b's pages block_table[b]; and q_out = q_rope [T, H, 64] rotated
     alike (q_out may be q_rope). rope_table: fp32 [positions, 64], cos | sin.
+    qo_indptr None: token b is request b's only one, and left out with its
+    query where kv_lens[b] is 0 (a slot of a fixed batch that holds no request).
     Runs on the cache's device, on stream or that device's current one."""
     rc = (_paged_call or _load_paged_call()).append(
         latent, k_rope, qo_indptr, kv_lens, block_table, cache, rope_table, q_rope, q_out, positions, norm_weight,

@@ -337,7 +337,8 @@ int mla_paged_append(const mt_bf16* latent, int64_t latent_stride, const mt_bf16
       k_rope_stride % 8)
     return MT_EINVAL;
   if (batch == 0 || total_q == 0) return MT_OK;
-  if (!latent || !k_rope || !rope_table || !qo_indptr || !kv_lens || !block_table || !cache)
+  if (!latent || !k_rope || !rope_table || !kv_lens || !block_table || !cache ||
+      (!qo_indptr && total_q != batch))
     return MT_EINVAL;
   if ((uintptr_t)latent % 16 || (uintptr_t)k_rope % 16 || (uintptr_t)norm_weight % 16 ||
       (uintptr_t)rope_table % 16)

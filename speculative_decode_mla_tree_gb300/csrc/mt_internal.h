@@ -107,7 +107,7 @@ struct AppendArgs {
   const float* table;           // [max_positions, 64] cos | sin
   int64_t max_positions;
   const int32_t* positions;     // or nullptr
-  const int32_t* qo_indptr;
+  const int32_t* qo_indptr;     // or nullptr: one token a request, none where its length is 0
   int batch, total_q;
   PagedCache kv;
   int32_t* status;

@@ -137,8 +137,14 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
     v[2] = reinterpret_cast<const uint4*>(a.k_rope + t64 * a.k_rope_stride)[l];
   }
 
-  const int b = find_request_warp(a.qo_indptr, a.batch, t, lane);
-  const int q0 = __ldg(a.qo_indptr + b), q1 = __ldg(a.qo_indptr + b + 1), len = __ldg(a.kv.lens + b);
+  int b = t, q0 = t, q1 = t + 1;  // one token a request
+  if (a.qo_indptr) {
+    b = find_request_warp(a.qo_indptr, a.batch, t, lane);
+    q0 = __ldg(a.qo_indptr + b);
+    q1 = __ldg(a.qo_indptr + b + 1);
+  }
+  const int len = __ldg(a.kv.lens + b);
+  if (!a.qo_indptr && len == 0) return;  // a slot without a request
   if (b == a.batch - 1 && t >= q1 && q1 >= q0) {
     return;  // behind the last request: belongs to nobody
   }

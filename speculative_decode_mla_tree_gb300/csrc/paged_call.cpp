@@ -96,16 +96,16 @@ PyObject* guarded(int dev, F call) {
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   try {
     if (n != 15 || !g_append) return does_not_fit();
-    Arg latent(a[0]), k_rope(a[1]), indptr(a[2]), rope(a[6]), q(a[7], true), out(a[8], true), pos(a[9], true),
+    Arg latent(a[0]), k_rope(a[1]), indptr(a[2], true), rope(a[6]), q(a[7], true), out(a[8], true), pos(a[9], true),
         weight(a[10], true), status(a[13], true);
     Paged p(a[5], a[4], a[3]);
     if (!p.ok() || !latent.is(at::kBFloat16, 2, p.dev) || !k_rope.is(at::kBFloat16, 2, p.dev) ||
-        !indptr.is(at::kInt, 1, p.dev) || !rope.is(at::kFloat, 2, p.dev) || !q.ok || !out.ok || !pos.ok || !weight.ok ||
+        !indptr.ok || (indptr.t && !indptr.is(at::kInt, 1, p.dev)) || !rope.is(at::kFloat, 2, p.dev) || !q.ok || !out.ok || !pos.ok || !weight.ok ||
         !status_ok(status, p.dev))
       return does_not_fit();
     const int64_t t = latent.t->size(0), angles = rope.t->size(0);
     if (t > INT_MAX || !latent.sizes(t, 512) || !latent.rows() || !k_rope.sizes(t, 64) || !k_rope.rows() ||
-        !indptr.sizes(p.batch + 1) || !rope.sizes(angles, 64) || !rope.t->is_contiguous() || !q.t != !out.t)
+        !(indptr.t ? indptr.sizes(p.batch + 1) : t == p.batch) || !rope.sizes(angles, 64) || !rope.t->is_contiguous() || !q.t != !out.t)
       return does_not_fit();
     int64_t heads = 0;
     if (q.t) {

@@ -153,9 +153,10 @@ class DecodeStep:
     A program fills ``latent`` [B, 512], ``k_rope`` [B, 64] and ``q`` [B, H,
     576] (absorbed latent query, then the rope part as projected: the step
     rotates it in place), keeps ``block_table`` and ``kv_lens`` (lengths with
-    the new token), and reads ``out``
-    and ``lse``. ``q`` holds rotated rope parts after ``run``: refill it
-    before the next step."""
+    the new token), and reads ``out`` and ``lse``. ``q`` holds rotated rope
+    parts after ``run``: refill it before the next step. A slot that holds no
+    request has length 0: nothing is appended for it, its page numbers are not
+    read, its query stays as it is, and it gets 0 and -inf."""
 
     def __init__(self, cache, batch, heads, max_pages, rope_table, sm_scale, norm_weight=None,
                  norm_eps=1e-6, rope_style=abi.ROPE_PAIRS):
@@ -167,7 +168,6 @@ class DecodeStep:
         self.q = torch.zeros(batch, heads, 576, dtype=torch.bfloat16, device=dev)
         self.block_table = torch.zeros(batch, max_pages, dtype=torch.int32, device=dev)
         self.kv_lens = torch.zeros(batch, dtype=torch.int32, device=dev)
-        self.qo_indptr = torch.arange(batch + 1, dtype=torch.int32, device=dev)
         self.out = torch.zeros(batch, heads, 512, dtype=torch.bfloat16, device=dev)
         self.lse = torch.zeros(batch, heads, dtype=torch.float32, device=dev)
         with torch.cuda.device_of(cache):  # the size depends on the device
@@ -177,7 +177,7 @@ class DecodeStep:
 
     def append(self, stream=None):
         q_rope = self.q[:, :, 512:]
-        abi.mla_paged_append(self.latent, self.k_rope, self.qo_indptr, self.kv_lens, self.block_table,
+        abi.mla_paged_append(self.latent, self.k_rope, None, self.kv_lens, self.block_table,
                              self.cache, self.rope_table, q_rope, q_rope, None, self.norm_weight,
                              self.norm_eps, self.rope_style, self.status, stream)
 

@@ -97,3 +97,11 @@ def test_binding_refuses_cpu_tensors():
     with pytest.raises(abi.MlaTreeError, match="cache must be a CUDA tensor"):
         abi.mla_paged_append(z(1, 512, dtype=bf), z(1, 64, dtype=bf), z(2, dtype=torch.int32), lens, table, cache,
                              z(4, 64))
+
+
+def test_append_without_indptr_is_one_token_a_request(lib):
+    """Refused unless there are as many tokens as requests (nothing to launch where there are none)."""
+    for total_q in (1, 3, 4):
+        assert _append(lib, indptr=None, total_q=total_q) == abi.MT_EINVAL
+    assert _append(lib, indptr=None, total_q=0) == abi.MT_OK
+    assert _append(lib, indptr=None, batch=0, total_q=2) == abi.MT_OK
