@@ -477,8 +477,8 @@ size_t mla_paged_decode_workspace_bytes(int batch, int heads);
  * kernel for other layouts, below, rounds none), and partial
  * results of a split are fp32. A request's result does not depend on
  * the rest of the batch beyond the fp32 rounding of sums that are taken in
- * another order where the splits fall elsewhere (about 1 in 100 outputs then
- * rounds to the other neighbouring bf16 value), and is the same in every run.
+ * another order where the splits fall elsewhere (a few outputs in 1000 then
+ * round to the other neighbouring bf16 value), and is the same in every run.
  *   q:   bf16, element (b, h, 0) at b * q_token_stride + h * q_head_stride
  *        (both at least 576)
  *   out: bf16 [batch, heads, 512], 16-byte aligned; lse: fp32 [batch, heads]
