@@ -1,8 +1,8 @@
 """Compile the CUDA library in tree: every csrc/*.cu for sm_103a, linked
-into lib/libmla_tree.so (static CUDA runtime), and csrc/paged_call.cpp, the
-paged calls' way in from Python tensors, into lib/_paged_call.so. Translation
-units compile in parallel; a unit is rebuilt only when a source or header is
-newer than its object file."""
+into lib/libmla_tree.so (static CUDA runtime; needs nvcc and nothing else), and,
+where torch is installed, csrc/paged_call.cpp, the paged calls' way in from
+Python tensors, into lib/_paged_call.so. Translation units compile in parallel;
+a unit is rebuilt only when a source or header is newer than its object file."""
 from __future__ import annotations
 
 import glob
@@ -49,10 +49,14 @@ def _compile(src, ptxas_verbose=False):
 
 
 def _compile_call():
-    """The extension module, against this interpreter's headers and torch's."""
+    """The extension module, against this interpreter's headers and torch's;
+    None without torch, whose tensors are all that it is for."""
     import sysconfig
 
-    import torch
+    try:
+        import torch
+    except ImportError:
+        return None
     newest = max(os.path.getmtime(CALL_SRC), os.path.getmtime(os.path.join(ROOT, "include", "mla_tree.h")))
     if os.path.exists(CALL) and os.path.getmtime(CALL) >= newest:
         return CALL
@@ -75,7 +79,6 @@ def build(verbose=False, ptxas_verbose=False) -> str:
     with ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
         call = ex.submit(_compile_call)
         results = list(ex.map(lambda s: _compile(s, ptxas_verbose), srcs))
-        call.result()
     objs = [o for o, _ in results]
     if verbose or ptxas_verbose:
         for (o, log) in results:
@@ -86,6 +89,7 @@ def build(verbose=False, ptxas_verbose=False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
+    call.result()  # what failed there is raised once the library is in place
     return LIB
 
 
