@@ -10,6 +10,8 @@ import os
 
 import torch
 
+from . import build as _build
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libmla_tree.so")
 
@@ -327,16 +329,16 @@ ROPE_PAIRS, ROPE_HALVES = 0, 1
 # compiled module (csrc/paged_call.cpp) checks the tensors and calls the
 # library. What does not fit comes back as None and goes through the checks
 # here, one by one, for its message.
-_CALL_PATH = os.path.join(_HERE, "lib", "_paged_call.so")
 _paged_call = None
 
 
 def _load_paged_call():
     global _paged_call
     lib = load()
-    if not os.path.exists(_CALL_PATH):
-        raise MlaTreeError("_paged_call.so is not built (%s); run __graft_entry__.build()" % _CALL_PATH)
-    spec = importlib.util.spec_from_file_location("_paged_call", _CALL_PATH)
+    path = _build.call_path()
+    if not os.path.exists(path):
+        raise MlaTreeError("the module for this torch and Python is not built (%s); run __graft_entry__.build()" % path)
+    spec = importlib.util.spec_from_file_location("_paged_call", path)
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
     mod.bind(*(ctypes.cast(f, P).value for f in (lib.mla_paged_append, lib.mla_paged_decode)))

@@ -1,13 +1,16 @@
 """Compile the CUDA library in tree: every csrc/*.cu for sm_103a, linked
 into lib/libmla_tree.so (static CUDA runtime; needs nvcc and nothing else), and,
 where torch is installed, csrc/paged_call.cpp, the paged calls' way in from
-Python tensors, into lib/_paged_call.so. Translation units compile in parallel;
-a unit is rebuilt only when a source or header is newer than its object file."""
+Python tensors, into a lib/_paged_call.*.so (see call_path). Translation units
+compile in parallel; a unit is rebuilt only when a source or header is newer
+than its object file."""
 from __future__ import annotations
 
 import glob
+import hashlib
 import os
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -17,7 +20,6 @@ LIBDIR = os.path.join(HERE, "lib")
 OBJDIR = os.path.join(LIBDIR, "obj")
 LIB = os.path.join(LIBDIR, "libmla_tree.so")
 CALL_SRC = os.path.join(CSRC, "paged_call.cpp")
-CALL = os.path.join(LIBDIR, "_paged_call.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -48,29 +50,54 @@ def _compile(src, ptxas_verbose=False):
     return obj, r.stderr
 
 
+CALL_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-shared"]
+CALL_LIBS = ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
+def _abi_flag():
+    import torch
+    return "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)
+
+
+def call_path():
+    """Where the extension module for this interpreter and this torch is, or will
+    be built. It reads tensors' fields where torch's headers put them, so its
+    name tells the interpreter's ABI, torch's version, the flags and the sources
+    apart: one that was made for anything else is never loaded."""
+    import torch
+    h = hashlib.sha256()
+    for part in [torch.__version__, str(torch.version.git_version), _abi_flag()] + CALL_FLAGS + CALL_LIBS:
+        h.update(part.encode() + b"\0")
+    for path in (CALL_SRC, os.path.join(ROOT, "include", "mla_tree.h")):
+        with open(path, "rb") as f:
+            h.update(f.read() + b"\0")
+    return os.path.join(LIBDIR, "_paged_call.%s%s" % (h.hexdigest()[:16], sysconfig.get_config_var("EXT_SUFFIX")))
+
+
 def _compile_call():
     """The extension module, against this interpreter's headers and torch's;
     None without torch, whose tensors are all that it is for."""
-    import sysconfig
-
     try:
         import torch
     except ImportError:
         return None
-    newest = max(os.path.getmtime(CALL_SRC), os.path.getmtime(os.path.join(ROOT, "include", "mla_tree.h")))
-    if os.path.exists(CALL) and os.path.getmtime(CALL) >= newest:
-        return CALL
+    path = call_path()
+    if os.path.exists(path):
+        return path
+    part = "%s.%d.part" % (path, os.getpid())  # a link that breaks off leaves nothing that looks whole
     t = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda", "include")
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
-           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
-           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(t, "include"),
-           "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"), "-I" + cuda, CALL_SRC, "-o", CALL,
-           "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    cmd = ["g++"] + CALL_FLAGS + [_abi_flag(), "-I" + sysconfig.get_paths()["include"],
+                                  "-I" + os.path.join(t, "include"),
+                                  "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"), "-I" + cuda,
+                                  CALL_SRC, "-o", part, "-L" + os.path.join(t, "lib")] + CALL_LIBS
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
+        if os.path.exists(part):
+            os.remove(part)
         raise RuntimeError("g++ failed for %s:\n%s\n%s" % (CALL_SRC, " ".join(cmd), r.stderr))
-    return CALL
+    os.replace(part, path)
+    return path
 
 
 def build(verbose=False, ptxas_verbose=False) -> str:
