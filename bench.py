@@ -44,6 +44,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -175,15 +176,30 @@ def _code_tokens(text):
     return "".join(out).strip()
 
 
+def _kernel_sources():
+    """Names of the files in csrc that the verify kernels are compiled from:
+    their own and the headers there that these include, one through another."""
+    csrc = os.path.join(ROOT, "speculative_decode_mla_tree_gb300", "csrc")
+    there = set(os.listdir(csrc))
+    todo = [name for name in there if name.startswith("verify")]
+    seen = set(todo)
+    while todo:
+        with open(os.path.join(csrc, todo.pop()), encoding="utf-8") as f:
+            for name in re.findall(r'^[ \t]*#[ \t]*include[ \t]*"([^"]+)"', f.read(), re.M):
+                if name in there and name not in seen:
+                    seen.add(name)
+                    todo.append(name)
+    return sorted(seen)
+
+
 def _kernel_source_hash():
     """Hash of the kernel sources the DRAM traffic in profiles/traffic.json
     was measured on (code only: see _code_tokens)."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "speculative_decode_mla_tree_gb300", "csrc")
-    for name in sorted(os.listdir(csrc)):
-        if name.startswith("verify") or name.endswith((".cuh", ".h")):
-            with open(os.path.join(csrc, name), encoding="utf-8") as f:
-                h.update(_code_tokens(f.read()).encode())
+    for name in _kernel_sources():
+        with open(os.path.join(csrc, name), encoding="utf-8") as f:
+            h.update(_code_tokens(f.read()).encode())
     return h.hexdigest()[:16]
 
 

@@ -7,6 +7,7 @@
 
 #include "../../include/mla_tree.h"
 #include "mt_internal.h"
+#include "paged.h"
 
 namespace mt {
 

@@ -1,7 +1,7 @@
 // What the paged decode kernels share.
 #pragma once
 #include "mt_common.cuh"
-#include "mt_internal.h"
+#include "paged.h"
 
 namespace mt {
 

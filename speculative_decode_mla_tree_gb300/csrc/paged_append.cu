@@ -20,7 +20,7 @@
 // token is found by a 32-way search (one round of loads up to 32 requests,
 // two up to 1024).
 #include "mt_common.cuh"
-#include "mt_internal.h"
+#include "paged.h"
 
 namespace mt {
 namespace {

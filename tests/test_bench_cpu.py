@@ -96,3 +96,30 @@ def test_source_hash_ignores_comments_not_code(bench):
     assert t(base) != t(other)
     assert t(base) != t(lit)      # white space inside a literal is code
     assert "one more" not in t(base) and "// b /* c */" in t(base)
+
+
+def test_committed_traffic_is_of_the_current_sources(bench):
+    """The record's key is that of the sources in this tree: where the verify
+    kernels change, it is counted again."""
+    for n in (2, 3, 4, 5):
+        assert bench._traffic("verify_c%d" % n)
+
+
+def test_traffic_key_follows_what_the_verify_kernels_include(bench, tmp_path, monkeypatch):
+    """A header that no verify source includes leaves the key alone; one that
+    it includes, by itself or through another, does not."""
+    assert "paged.h" not in bench._kernel_sources() and "paged.cuh" not in bench._kernel_sources()
+    csrc = tmp_path / "speculative_decode_mla_tree_gb300" / "csrc"
+    csrc.mkdir(parents=True)
+    (csrc / "verify_a.cu").write_text('#include <math.h>\n#include "one.h"\nint a;\n')
+    (csrc / "one.h").write_text('#  include "two.cuh"\nint one;\n')
+    (csrc / "two.cuh").write_text('#include "../../include/api.h"\n#include "one.h"\nint two;\n')
+    (csrc / "other.cuh").write_text("int other;\n")
+    (csrc / "other.cu").write_text('#include "other.cuh"\n')
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    assert bench._kernel_sources() == ["one.h", "two.cuh", "verify_a.cu"]
+    key = bench._kernel_source_hash()
+    (csrc / "other.cuh").write_text("int changed;\n")
+    assert bench._kernel_source_hash() == key
+    (csrc / "two.cuh").write_text("int changed;\n")
+    assert bench._kernel_source_hash() != key
