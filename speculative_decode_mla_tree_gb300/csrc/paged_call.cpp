@@ -121,11 +121,14 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     mt_stream_t stream;
     if (PyErr_Occurred() || style < 0 || style > 1 || !stream_of(a[14], p.dev, &stream)) return does_not_fit();
     const bool some = heads > 0;
+    // the stride of a dimension of one element addresses nothing and may be anything
+    auto tok = [&](const Arg& x) { return !some ? 0 : t > 1 ? x.stride(0) : 64; };
+    auto head = [&](const Arg& x) { return !some ? 0 : heads > 1 ? x.stride(1) : 64; };
     return guarded(p.dev, [&] {
       return g_append(latent.data<mt_bf16>(), t > 1 ? latent.stride(0) : 512, k_rope.data<mt_bf16>(),
                       t > 1 ? k_rope.stride(0) : 64, weight.data<mt_bf16>(), (float)eps,
-                      some ? q.data<mt_bf16>() : nullptr, some ? q.stride(0) : 0, some ? q.stride(1) : 0,
-                      some ? out.data<mt_bf16>() : nullptr, some ? out.stride(0) : 0, some ? out.stride(1) : 0,
+                      some ? q.data<mt_bf16>() : nullptr, tok(q), head(q),
+                      some ? out.data<mt_bf16>() : nullptr, tok(out), head(out),
                       (int)heads, rope.data<float>(), angles, (int)style, pos.data<int32_t>(),
                       indptr.data<int32_t>(), p.lens.data<int32_t>(), (int)p.batch, (int)t, p.table.data<int32_t>(),
                       p.table_stride(), (int)p.width, p.cache.data<mt_bf16>(), p.page_stride(), p.pages, (int)p.size,

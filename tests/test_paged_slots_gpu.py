@@ -109,3 +109,28 @@ def test_one_token_a_request_needs_as_many_tokens():
     with pytest.raises(abi.MlaTreeError):
         abi.mla_paged_append(row[:, :512], row[:, 512:], None, torch.tensor([5, 6], dtype=torch.int32, device="cuda"),
                              table.cuda(), cache, rope_table(64).cuda())
+
+
+@pytest.mark.parametrize("tokens,heads", [(1, 1), (1, 3), (4, 1)])
+@pytest.mark.parametrize("in_place", [False, True], ids=["apart", "in_place"])
+def test_append_strides_of_single_elements(tokens, heads, in_place):
+    """The stride of a dimension of size 1 says nothing: views that differ in
+    it alone are the same queries."""
+    g = gen(84)
+    cache, _, table = paged(g, [tokens], 16)
+    row, x = normal(g, tokens, 576).cuda(), normal(g, tokens, heads, 64)
+    odd = 64 * heads + (4 if tokens == 1 else 0), 68 if heads == 1 else 64, 1  # no whole 16-byte pieces
+
+    def views(t):
+        return t, t.as_strided(t.shape, odd)
+
+    want = torch.zeros_like(x, device="cuda")
+    rope, n = rope_table(64).cuda(), torch.tensor([tokens], dtype=torch.int32, device="cuda")
+    ptr = torch.tensor([0, tokens], dtype=torch.int32, device="cuda")
+    abi.mla_paged_append(row[:, :512], row[:, 512:], ptr, n, table.cuda(), cache, rope, x.cuda(), want)
+    for k in range(2):
+        for m in range(2):
+            q = x.cuda()
+            out = q if in_place else torch.zeros_like(q)
+            abi.mla_paged_append(row[:, :512], row[:, 512:], ptr, n, table.cuda(), cache, rope, views(q)[k], views(out)[m])
+            assert torch.equal(out, want)
