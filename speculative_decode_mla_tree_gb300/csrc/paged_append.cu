@@ -109,7 +109,8 @@ __device__ __forceinline__ int find_request_warp(const int32_t* indptr, int batc
   return lo;
 }
 
-template <bool kHalves>
+// kOne: one token a request (no qo_indptr), none where its length is 0.
+template <bool kHalves, bool kOne>
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs a, const int parts) {
   const int lane = threadIdx.x & 31, l = lane & 7;
   const int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -137,14 +138,10 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
     v[2] = reinterpret_cast<const uint4*>(a.k_rope + t64 * a.k_rope_stride)[l];
   }
 
-  int b = t, q0 = t, q1 = t + 1;  // one token a request
-  if (a.qo_indptr) {
-    b = find_request_warp(a.qo_indptr, a.batch, t, lane);
-    q0 = __ldg(a.qo_indptr + b);
-    q1 = __ldg(a.qo_indptr + b + 1);
-  }
+  const int b = kOne ? t : find_request_warp(a.qo_indptr, a.batch, t, lane);
+  const int q0 = kOne ? t : __ldg(a.qo_indptr + b), q1 = kOne ? t + 1 : __ldg(a.qo_indptr + b + 1);
   const int len = __ldg(a.kv.lens + b);
-  if (!a.qo_indptr && len == 0) return;  // a slot without a request
+  if (kOne && len == 0) return;
   if (b == a.batch - 1 && t >= q1 && q1 >= q0) {
     return;  // behind the last request: belongs to nobody
   }
@@ -229,9 +226,12 @@ cudaError_t launch_paged_append(const AppendArgs& a, int rope_style, cudaStream_
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return rope_style == MT_ROPE_HALVES
-             ? cudaLaunchKernelEx(&cfg, paged_append_kernel<true>, a, parts)
-             : cudaLaunchKernelEx(&cfg, paged_append_kernel<false>, a, parts);
+  const bool halves = rope_style == MT_ROPE_HALVES;
+  if (!a.qo_indptr)
+    return halves ? cudaLaunchKernelEx(&cfg, paged_append_kernel<true, true>, a, parts)
+                  : cudaLaunchKernelEx(&cfg, paged_append_kernel<false, true>, a, parts);
+  return halves ? cudaLaunchKernelEx(&cfg, paged_append_kernel<true, false>, a, parts)
+                : cudaLaunchKernelEx(&cfg, paged_append_kernel<false, false>, a, parts);
 }
 
 }  // namespace mt
