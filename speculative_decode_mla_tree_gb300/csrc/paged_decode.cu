@@ -41,7 +41,7 @@ constexpr unsigned kFull = 0xffffffffu;
 // pieces l, l + 32 and (l < 8) 64 + l of the query and of every key row, i.e. 16
 // of the 512 value dims. A block takes one split of one request. Bound by its
 // fp32 arithmetic, about 2200 operations a key and head: 32 requests of 8192
-// keys at 64 heads take 4.7 ms.
+// keys at 64 heads take 4.6 ms.
 __global__ void __launch_bounds__(32 * kWarps) decode_simt_kernel(const DecodeArgs a, const int splits,
                                                                   const int split_keys) {
   const int lane = threadIdx.x & 31;
@@ -187,13 +187,13 @@ __global__ void __launch_bounds__(32 * kWarps) decode_simt_kernel(const DecodeAr
 // leaves 152 partials a head and few heads: there a block takes an eighth of a
 // head row, a warp load being 256 bytes of each of two partials, all in flight
 // at once. Sums are in a fixed order, so the result is the same in every run.
-// Alone and back to back, from L2, it takes 5.8 us for 24 MB of partials (32
-// requests of 8192 keys, 64 heads), 8.5 us for 31 MB (48 requests, 128 heads),
-// 6.1 us for 20 MB of one request and 4.2 us for 37 short ragged ones. With R =
-// 1 alone the first two take 7.0 and 13.0 us, with warps in the place of blocks
-// the third 11.7; 16 loads in flight in two blocks an SM instead of 8 in three
-// take 5.7, 8.6, 6.0 and 5.0; by bulk copies into shared memory the first and
-// third took 10.6 and 17.5.
+// Alone and back to back, from L2, it takes 4.9 us for 24 MB of partials (32
+// requests of 8192 keys, 64 heads), 5.3 us for 31 MB (48 requests, 128 heads),
+// 5.8 us for 20 MB of one request and 4.4 us for 37 short ragged ones. With R =
+// 1 alone the first two take 5.9 and 10.4 us, with warps in the place of blocks
+// the third 9.9; 16 loads in flight in two blocks an SM instead of 8 in three
+// take 4.6, 5.9, 5.8 and 5.0; by bulk copies into shared memory an earlier form
+// took 10.6 instead of 5.8 for the first, 17.5 instead of 6.1 for the third.
 constexpr int kMergeThreads = 256;
 constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kMergeBlocksPerSm = 3;
@@ -203,7 +203,10 @@ constexpr int kQuarter = kDv / 4;
 constexpr int kEighth = kDv / 8;
 constexpr int kHalfWarps = kMergeThreads / 16;
 constexpr int kAheadBlock = 10;   // partials in flight of a lane of a block: 160 a block
-constexpr int kManyParts = 48;    // partials of a request from which blocks take over
+// Partials of a request from which blocks take over: 24 is slower where requests
+// leave 27 to 32 (5 of 26214 keys, 64 heads: a whole call 46.7 us against 42.0, 6 of
+// 21845: 48.2 against 41.8), 96 where they leave 77 (2 of 65536: 44.9 against 41.9).
+constexpr int kManyParts = 48;
 
 __device__ __forceinline__ float weight(float lse, float mx) {
   return lse == -INFINITY ? 0.f : exp2f((lse - mx) * kLog2e);

@@ -9,7 +9,7 @@
 // K and V^T are the same shared-memory tile, read K-major and MN-major. A CTA
 // serves N = 16, 32 or 64 heads (more heads are groups of 64 in CTAs of their
 // own, side by side, which find each other's tiles in L2; loading each tile
-// once for two groups by cluster multicast measured the same, 121 us at 128
+// once for two groups by cluster multicast measured the same, 120 us at 128
 // heads) and walks a contiguous range of 64-key tiles that may span several
 // requests.
 //
@@ -34,16 +34,19 @@
 // What bounds it. Up to 64 heads, HBM: 73.7 KB a tile at 6782 GB/s of copy
 // bandwidth are 1.65 us an SM, of which the tensor cores need 0.8 us (16 heads)
 // to 1.05 us (64 heads). 4 requests of 200000 keys at 16 heads take 141 us (6.5
-// TB/s), the 64-request mix of 128 to 131072 keys at 64 heads 224 us (6.3
+// TB/s), the 64-request mix of 128 to 131072 keys at 64 heads 225 us (6.3
 // TB/s). A call's fixed part shows in short ones: 2 to 2.5 us until the first
 // load (plan, page numbers), 1.5 us of first loads, 2.3 us for a 128 KB partial
-// at the 28 bytes a cycle that an SM stores, 4 to 8 us of merge. At 128 heads
+// at the 28 bytes a cycle that an SM stores, 4 to 6 us of merge. Each request of
+// a share also costs it a pause: the next one's query and keys are asked for
+// when this one's score products are done (256 requests of 500 keys at 64 heads
+// take 47.9 us, 1.8 times the time of their bytes). At 128 heads
 // every tile is needed by two SMs and shared memory bounds: per tile and SM the
 // score products read 144 KB of it, P V 96 KB, and 74 KB are written, 2450
-// cycles at 128 bytes; a tile takes 2750.
+// cycles at 128 bytes; a tile takes about 2800.
 //
 // Roles (352 threads): eight softmax warps (a TMEM lane quarter and half of the
-// heads each; four warps took 1.0 us a tile at 64 heads, eight 0.45), a TMA
+// heads each; four warps took 1.0 us a tile at 64 heads, eight half of it), a TMA
 // producer warp, and a warp for each of the two products (the first owns TMEM).
 // Every wait is time-bounded: a timeout sets MT_DEV_TIMEOUT, nothing more is
 // issued, what is in flight is drained and TMEM released.
@@ -74,15 +77,17 @@ constexpr int kStage = 8 * kGroup;
 constexpr int kStages = 2;
 constexpr int kQuarters = 4;                  // a stage is released by quarters, two groups = one P.V K step
 // A tile's loads go out with the L2 prefetch of the tile so far behind it, for
-// two stages of shared memory do not cover HBM's latency: none 233 us on the
-// 64-request mix and 128 us at 128 heads, one 225 and 121, two 228 and 122.
+// two stages of shared memory do not cover HBM's latency: none 232.5 us on the
+// 64-request mix and 125.5 us at 128 heads, one 225.4 and 120.7, two 225.9 and 120.8.
 constexpr int kAhead = 1;
 constexpr float kRescale = 8.f;               // log2 of how far a weight may exceed 1
-// A request's fixed cost in tiles: 1 is 2% slower on the 64-request mix, 4 as
-// much slower on 37 short ragged requests (18.5 us against 17.3).
+// A request's fixed cost in tiles: 1 takes 227.2 us instead of 225.4 on the
+// 64-request mix and 16.8 instead of 15.2 on 37 short ragged requests; 4 takes 16.8
+// there, too, and 14.6 instead of 12.5 on 8 requests of 1024 to 4096 keys.
 constexpr int kOverhead = 2;
-// Smallest share of a team in tiles: 4 saves the merge partials but takes 16 us
-// instead of 12.8 on 8 requests of 1024 to 4096 keys.
+// Smallest share of a team in tiles: 4 saves the merge partials but takes 15.6 us
+// instead of 12.5 on those 8 requests, 18.9 instead of 14.9 on one of 1000 keys at
+// 64 heads.
 constexpr int kMinShare = 1;
 constexpr uint64_t kDrainNs = 100000000ull;
 constexpr unsigned kFull = 0xffffffffu;
@@ -416,7 +421,8 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
     // --------------------------------------------------- producers, row by row
     // Producer i takes quarters i and i + 2 of every tile: lane l looks after
     // row l % 16 of its quarter l / 16. 36 gathers of four rows by 64 dims a
-    // quarter, at 60 cycles and more each what bounds this form.
+    // quarter bound this form: 144 a tile, 3.0 us of it, 21 ns a gather from two
+    // warps (four warps that do nothing else reach 16 ns on an SM).
     const int me = warp == kProducerWarp ? 0 : 1;
     const uint32_t kv0 = smem_u32(sm + L::kKV);
     uint16_t* vmask16 = reinterpret_cast<uint16_t*>(vmask);
@@ -990,7 +996,7 @@ cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_
   const int P = a.kv.page_size;
   // Pages of whole groups of eight rows go by boxes; others row by row, where
   // rows can be counted through the pages (32 requests of 8192 keys, 64 heads:
-  // 98 us by gathers, 67 us with pages of 64, 4.7 ms in the kernel that needs neither).
+  // 96 us by gathers, 64 us with pages of 64, 4.6 ms in the kernel that needs neither).
   const bool gather = P % 8 != 0;
   if (a.kv.num_pages <= 0 || (gather && a.kv.page_stride % kDqk != 0)) return cudaErrorNotSupported;
   const int64_t page_rows = a.kv.page_stride / kDqk;
