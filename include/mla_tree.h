@@ -67,6 +67,8 @@ enum {
 #define MT_DEV_TIMEOUT      0x10  /* a bounded wait inside a kernel gave up */
 #define MT_DEV_MISMATCH     0x20  /* validate mode: the two kernels disagree beyond the tolerance */
 #define MT_DEV_BAD_POSITION 0x40  /* rope position outside the angle table */
+#define MT_DEV_BAD_TOKEN    0x80  /* token outside the vocabulary */
+#define MT_DEV_NO_PAGES     0x100 /* fewer free pages than a call needs */
 
 #define MT_D_QK 576
 #define MT_D_V 512
@@ -498,6 +500,166 @@ int mla_paged_decode(const mt_bf16* q, int64_t q_token_stride, int64_t q_head_st
                      const int32_t* kv_lens, int batch, int heads, float sm_scale,
                      mt_bf16* out, float* lse, void* workspace, size_t workspace_bytes,
                      int32_t* dev_status, mt_stream_t stream);
+
+/*
+ * mla_paged_decode over a sliding window and a few first tokens that stay
+ * visible: position j < kv_lens[b] takes part if j < sinks or j >= kv_lens[b]
+ * - window (window >= 1, sinks >= 0, else MT_EINVAL). Everything else is
+ * mla_paged_decode's: arguments, workspace, arithmetic, bad pages, requests of
+ * length 0, page sizes and how fast they are. Table entries of pages that hold
+ * no visible position are never read: such pages may have been given away
+ * (mla_pages_fit does that). Time goes by the visible positions.
+ */
+int mla_paged_decode_window(const mt_bf16* q, int64_t q_token_stride, int64_t q_head_stride,
+                            const mt_bf16* cache, int64_t page_stride, int64_t num_pages,
+                            int page_size, const int32_t* block_table, int64_t table_stride,
+                            int max_pages, const int32_t* kv_lens, int window, int sinks, int batch,
+                            int heads, float sm_scale, mt_bf16* out, float* lse, void* workspace,
+                            size_t workspace_bytes, int32_t* dev_status, mt_stream_t stream);
+
+/* Types of logits (logits_type). */
+#define MT_LOGITS_BF16 0
+#define MT_LOGITS_FP16 1
+#define MT_LOGITS_FP32 2
+
+#define MT_MAX_TOP 32             /* alternatives a row (more: MT_EUNSUPPORTED) */
+
+/*
+ * Log probabilities of given tokens, entropy and most likely tokens of rows of
+ * logits. For row r, x_v = logits[r * row_stride + v], v < vocab:
+ *     lse[r]         = ln sum_v exp(x_v)
+ *     logprobs[r, g] = x_tok - lse[r],   tok = tokens[r * token_stride + g]
+ *     entropy[r]     = -sum_v p_v ln p_v,   p_v = exp(x_v - lse[r]), 0 ln 0 = 0
+ *     top_ids[r, i]  = the token of the i-th largest x_v, i < top_k, equal
+ *                      values by the lower token (0 equals -0; NaN comes first)
+ *     top_logprobs[r, i] = its x_v - lse[r]
+ * Sums are fp32 (the reference of the exponent is the maximum so far). A row
+ * whose values are all -inf has lse -inf, entropy 0 and log probabilities -inf;
+ * one that holds NaN or +inf has NaN for all of them (its top_ids are as above).
+ * Token -1 asks for nothing and gets -inf; one outside [-1, vocab) sets
+ * MT_DEV_BAD_TOKEN and gets -inf.
+ *   logits: of logits_type, aligned to its elements; row_stride in elements,
+ *            any (rows may overlap, or be the same row)
+ *   tokens: int32; NULL with tokens_per_row 0, and logprobs then, too
+ *   lse, entropy, top_logprobs: NULL leaves them out; top_ids: NULL with top_k 0
+ *   top_k:  0 .. MT_MAX_TOP, not above vocab (MT_EINVAL)
+ * Every result is the same in every run. No workspace.
+ */
+int mla_token_logprobs(const void* logits, int logits_type, int64_t row_stride, int rows, int vocab,
+                       const int32_t* tokens, int64_t token_stride, int tokens_per_row, int top_k,
+                       float* logprobs, float* lse, float* entropy, int32_t* top_ids,
+                       float* top_logprobs, int32_t* dev_status, mt_stream_t stream);
+
+/*
+ * Which nodes of the draft trees stay. Request b owns nodes t = qo_indptr[b] +
+ * i, i < n_b, with parents and order as for tree_mask_pack; tokens[t] is what
+ * was drafted there, and targets[t * target_stride] is the token that the model
+ * chose after node t (its most likely, or one drawn from its distribution:
+ * then the tokens that come out are drawn from the model's own). From cur =
+ * -1, want = first[b]: the lowest child of cur with tokens == want is taken,
+ * and its target is wanted next, until there is none or max_accept are taken.
+ *     path[b, k]     = the k-th node taken, k < counts[b]; -1 behind
+ *     next_tokens[b] = what is wanted in the end: the token to go on with
+ *     new_lens[b]    = kv_lens[b] - n_b + counts[b]
+ * first NULL: the token of each request's node 0 (a root that was decided
+ * before), -1 where it has none. kv_lens holds the lengths with the drafts;
+ * new_lens may be kv_lens.
+ *   path: int32 [batch, max_accept]; counts, next_tokens, new_lens: int32 [batch]
+ * A parent out of range sets MT_DEV_BAD_PARENT (that node is not taken); more
+ * than MT_MAX_TREE nodes set MT_DEV_TREE_TOO_BIG, a decreasing qo_indptr, one
+ * that passes total_q, or more nodes than kv_lens[b] MT_DEV_BAD_INDPTR: such a
+ * request takes nothing, with next_tokens -1 and new_lens kv_lens.
+ */
+int mla_tree_accept(const int32_t* parents, const int32_t* tokens, const int32_t* targets,
+                    int64_t target_stride, const int32_t* first, const int32_t* qo_indptr,
+                    const int32_t* kv_lens, int batch, int total_q, int max_accept, int32_t* path,
+                    int32_t* counts, int32_t* next_tokens, int32_t* new_lens, int32_t* dev_status,
+                    mt_stream_t stream);
+
+/*
+ * Moves the accepted rows up, in every layer: with base = kv_lens[b] -
+ * counts[b] (kv_lens: the new lengths), the row of position base + path[b, k]
+ * goes to position base + k, k = 0, 1, ... in order. What mla_tree_accept
+ * returns is what this takes. Rows behind the new length keep what they held
+ * last. Layer l's cache is at cache + l * layer_stride (16-byte aligned);
+ * geometry, table and their checks are those of the paged calls.
+ * A path that does not rise sets MT_DEV_BAD_PARENT and ends there; counts
+ * outside [0, max_accept] or a bad length set MT_DEV_BAD_INDPTR (the request is
+ * left as it is); a bad page leaves out the moves that touch it.
+ */
+int mla_paged_compact(const int32_t* path, int64_t path_stride, int max_accept, const int32_t* counts,
+                      const int32_t* kv_lens, int batch, const int32_t* block_table,
+                      int64_t table_stride, int max_pages, mt_bf16* cache, int64_t page_stride,
+                      int64_t num_pages, int page_size, int layers, int64_t layer_stride,
+                      int32_t* dev_status, mt_stream_t stream);
+
+/*
+ * Pages of a paged cache, held by reference: refs[p] (int32 [num_pages]) is
+ * the number of table entries that hold page p, 0 where it is free. Request b
+ * holds the entries j < held[b] of its row that are not -1; entries from
+ * held[b] on mean nothing. Calls that change refs have to be ordered.
+ *
+ * Fork: row r < new_batch of the new table holds the pages of row parents[r] of
+ * the old one (none for -1), with its held and kv_lens; rows of the old table
+ * that are nobody's parent give their pages back. So one call forks, drops and
+ * reorders. The tables, held and kv_lens of both sides may not overlap.
+ * A parent outside [-1, old_batch) sets MT_DEV_BAD_PARENT and counts as -1, a
+ * held entry outside [0, max_pages] MT_DEV_BAD_INDPTR and counts as 0, a page
+ * number that is neither -1 nor a page MT_DEV_BAD_SLOT and is copied as it is.
+ */
+int mla_pages_fork(const int32_t* parents, const int32_t* kv_lens, const int32_t* held,
+                   const int32_t* block_table, int64_t table_stride, int old_batch, int max_pages,
+                   int32_t* refs, int64_t num_pages, int32_t* new_lens, int32_t* new_held,
+                   int32_t* new_table, int64_t new_table_stride, int new_batch,
+                   int32_t* dev_status, mt_stream_t stream);
+
+/*
+ * Bytes of workspace mla_pages_fit needs (0 for arguments it would reject);
+ * its content does not matter. Calls that may overlap need their own.
+ */
+size_t mla_pages_fit_workspace_bytes(int batch, int64_t num_pages);
+
+/*
+ * Makes positions kv_lens[b] .. want_lens[b] - 1 writable and gives back what
+ * is not needed. Of request b's row,
+ *   - pages behind want_lens[b] are given back;
+ *   - with window > 0, so are the pages that lie wholly between the first
+ *     `sinks` positions and the window of the token at position kv_lens[b]
+ *     (the last `window` positions, its own among them), from the highest down
+ *     to the first that is gone already;
+ *   - each page that holds a position to be written is there and held by nobody
+ *     else: a column without one gets a free page, and one whose page others
+ *     hold, too, gets a free page in its place. Where all that hold a page want
+ *     to write to it in the same call, the lowest request keeps it.
+ * Free pages (those given back by this call among them) are taken lowest
+ * first, in the order of requests, then columns. held[b] becomes
+ * ceil(want_lens[b] / page_size); an entry without a page is -1.
+ *     copies[b] = (source page, destination page, rows)
+ * names the copy that the request's rows before kv_lens[b] need in a page that
+ * was replaced, (-1, -1, 0) where there is none: mla_paged_copy carries it out,
+ * before the next append.
+ * Where the free pages do not suffice for all requests, the call sets
+ * MT_DEV_NO_PAGES and changes nothing (copies are all (-1, -1, 0)). A bad
+ * length (below 0, or want_lens beyond the table) or held entry sets
+ * MT_DEV_BAD_INDPTR and leaves that request as it is; a page number that is
+ * neither -1 nor a page sets MT_DEV_BAD_SLOT and counts as -1.
+ *   copies: int32 [batch, 3]; workspace: 16-byte aligned
+ */
+int mla_pages_fit(const int32_t* kv_lens, const int32_t* want_lens, int32_t* held,
+                  int32_t* block_table, int64_t table_stride, int batch, int max_pages, int32_t* refs,
+                  int64_t num_pages, int page_size, int window, int sinks, int32_t* copies,
+                  void* workspace, size_t workspace_bytes, int32_t* dev_status, mt_stream_t stream);
+
+/*
+ * Copies the first copies[i][2] rows of page copies[i][0] to page copies[i][1],
+ * i < n, in every layer (copies: int32 [n, 3]; entries with destination -1 are
+ * left out). A page that is written may be neither read nor written by another
+ * entry. A page number or a count of rows out of range sets MT_DEV_BAD_SLOT
+ * and leaves out that entry.
+ */
+int mla_paged_copy(const int32_t* copies, int64_t n, mt_bf16* cache, int64_t page_stride,
+                   int64_t num_pages, int page_size, int layers, int64_t layer_stride,
+                   int32_t* dev_status, mt_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(_HERE, "lib", "libmla_tree.so")
 
 MT_OK, MT_EINVAL, MT_EUNSUPPORTED, MT_EWORKSPACE, MT_ECUDA = 0, -1, -2, -3, -4
 DEV_BAD_SLOT, DEV_BAD_PARENT, DEV_BAD_INDPTR, DEV_TREE_TOO_BIG, DEV_TIMEOUT = 1, 2, 4, 8, 16
-DEV_MISMATCH, DEV_BAD_POSITION = 32, 64
+DEV_MISMATCH, DEV_BAD_POSITION, DEV_BAD_TOKEN, DEV_NO_PAGES = 32, 64, 128, 256
 PATH_AUTO, PATH_SIMT, PATH_TC = 0, 1, 2
 
 EXPORTS = ["mla_tree_abi_version", "mla_tree_status_string", "mla_tree_draft_kv_scatter",
@@ -25,7 +25,9 @@ EXPORTS = ["mla_tree_abi_version", "mla_tree_status_string", "mla_tree_draft_kv_
            "mla_tree_verify_workspace_bytes", "mla_tree_verify_launch_count", "mla_tree_verify",
            "mla_tree_verify_bits", "mla_tree_verify_masked", "mla_tree_verify_validate_workspace_bytes",
            "mla_tree_verify_validate", "mla_tree_verify_noalloc", "mla_tree_test_wait_limits",
-           "mla_paged_append", "mla_paged_decode_workspace_bytes", "mla_paged_decode"]
+           "mla_paged_append", "mla_paged_decode_workspace_bytes", "mla_paged_decode",
+           "mla_paged_decode_window", "mla_token_logprobs", "mla_tree_accept", "mla_paged_compact",
+           "mla_pages_fork", "mla_pages_fit_workspace_bytes", "mla_pages_fit", "mla_paged_copy"]
 MT_ESCRATCH = -5
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -91,6 +93,23 @@ def load():
     lib.mla_paged_decode.restype = I32
     lib.mla_paged_decode.argtypes = [P, I64, I64, P, I64, I64, I32, P, I64, I32, P, I32, I32, F32,
                                      P, P, P, SZ, P, P]
+    lib.mla_paged_decode_window.restype = I32
+    lib.mla_paged_decode_window.argtypes = [P, I64, I64, P, I64, I64, I32, P, I64, I32, P, I32, I32, I32, I32, F32,
+                                            P, P, P, SZ, P, P]
+    lib.mla_token_logprobs.restype = I32
+    lib.mla_token_logprobs.argtypes = [P, I32, I64, I32, I32, P, I64, I32, I32, P, P, P, P, P, P, P]
+    lib.mla_tree_accept.restype = I32
+    lib.mla_tree_accept.argtypes = [P, P, P, I64, P, P, P, I32, I32, I32, P, P, P, P, P, P]
+    lib.mla_paged_compact.restype = I32
+    lib.mla_paged_compact.argtypes = [P, I64, I32, P, P, I32, P, I64, I32, P, I64, I64, I32, I32, I64, P, P]
+    lib.mla_pages_fork.restype = I32
+    lib.mla_pages_fork.argtypes = [P, P, P, P, I64, I32, I32, P, I64, P, P, P, I64, I32, P, P]
+    lib.mla_pages_fit_workspace_bytes.restype = SZ
+    lib.mla_pages_fit_workspace_bytes.argtypes = [I32, I64]
+    lib.mla_pages_fit.restype = I32
+    lib.mla_pages_fit.argtypes = [P, P, P, P, I64, I32, I32, P, I64, I32, I32, I32, P, P, SZ, P, P]
+    lib.mla_paged_copy.restype = I32
+    lib.mla_paged_copy.argtypes = [P, I64, P, I64, I64, I32, I32, I64, P, P]
     _lib = lib
     return lib
 
@@ -325,7 +344,7 @@ def mla_tree_verify_noalloc(q, kv_buf, kv_indices, kv_indptr, qo_indptr, packed_
 
 ROPE_PAIRS, ROPE_HALVES = 0, 1
 
-# The paged calls run once per layer and token, where their own time shows: a
+# The calls of a decoding loop run once per token or layer, where their own time shows: a
 # compiled module (csrc/paged_call.cpp) checks the tensors and calls the
 # library. What does not fit comes back as None and goes through the checks
 # here, one by one, for its message.
@@ -341,12 +360,14 @@ def _load_paged_call():
     spec = importlib.util.spec_from_file_location("_paged_call", path)
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
-    mod.bind(*(ctypes.cast(f, P).value for f in (lib.mla_paged_append, lib.mla_paged_decode)))
+    mod.bind(*(ctypes.cast(f, P).value for f in (
+        lib.mla_paged_append, lib.mla_paged_decode, lib.mla_paged_decode_window, lib.mla_token_logprobs, lib.mla_tree_accept,
+        lib.mla_paged_compact, lib.mla_pages_fork, lib.mla_pages_fit, lib.mla_paged_copy)))
     _paged_call = mod
     return mod
 
 
-def _refuse(name, t, dtype, dim, dev, shape=None, whole=False):
+def _refuse(name, t, dtype, dim, dev, shape=None, whole=False, other="cache"):
     """Raises what is wrong with one tensor, if anything is."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise MlaTreeError("%s must be a CUDA tensor" % name)
@@ -354,7 +375,7 @@ def _refuse(name, t, dtype, dim, dev, shape=None, whole=False):
     if t.dtype != dtype:
         raise MlaTreeError("%s, got %s" % (want, t.dtype))
     if dev is not None and t.get_device() != dev:
-        raise MlaTreeError("%s is on %s, the cache on cuda:%d" % (name, t.device, dev))
+        raise MlaTreeError("%s is on %s, the %s on cuda:%d" % (name, t.device, other, dev))
     if t.dim() != dim or shape is not None and tuple(t.shape) != tuple(shape):
         raise MlaTreeError("%s %s, got %s" % (want, "of %d dimensions" % dim if shape is None else list(shape),
                                               list(t.shape)))
@@ -456,3 +477,225 @@ def mla_paged_decode(q, cache, block_table, kv_lens, sm_scale, out, lse, workspa
         _refuse_decode(q, cache, block_table, kv_lens, out, lse, workspace, status)
     if rc != MT_OK:
         _check(rc, "mla_paged_decode")
+
+
+def mla_paged_decode_window(q, cache, block_table, kv_lens, window, sinks, sm_scale, out, lse, workspace, status=None,
+                            stream=None):
+    """mla_paged_decode where request b sees its last ``window`` positions and
+    its first ``sinks`` alone. Table entries of pages that hold none of them are
+    not read."""
+    rc = (_paged_call or _load_paged_call()).decode_window(
+        q, cache, block_table, kv_lens, window, sinks, sm_scale, out, lse, workspace, status,
+        None if stream is None else stream.cuda_stream)
+    if rc is None:
+        _refuse_int("window", window)
+        _refuse_int("sinks", sinks)
+        _refuse_decode(q, cache, block_table, kv_lens, out, lse, workspace, status)
+    if rc != MT_OK:
+        _check(rc, "mla_paged_decode_window")
+
+
+def _refuse_int(name, v):
+    if not isinstance(v, int) or not -(1 << 31) <= v < 1 << 31:
+        raise MlaTreeError("%s must be a 32-bit int, got %r" % (name, v))
+
+
+def _refuse_status(status, dev, other):
+    if status is not None:
+        _refuse("status", status, torch.int32, status.dim() if isinstance(status, torch.Tensor) else 1, dev, None, True, other)
+    raise MlaTreeError("unsupported arguments")
+
+
+def _refuse_logprobs(logits, tokens, logprobs, lse, entropy, top_ids, top_logprobs, status):
+    types = (torch.bfloat16, torch.float16, torch.float32)
+    if isinstance(logits, torch.Tensor) and logits.dtype not in types:
+        raise MlaTreeError("logits must be bf16, fp16 or fp32, got %s" % logits.dtype)
+    _refuse("logits", logits, getattr(logits, "dtype", None), 2, None)
+    dev, rows, on = logits.get_device(), logits.shape[0], "logits"
+    if logits.shape[1] < 1:
+        raise MlaTreeError("logits must have a vocabulary, got %s" % list(logits.shape))
+    if (tokens is None) != (logprobs is None):
+        raise MlaTreeError("tokens and logprobs go together")
+    if tokens is not None:
+        dim = 2 if isinstance(tokens, torch.Tensor) and tokens.dim() == 2 else 1
+        _refuse("tokens", tokens, torch.int32, dim, dev, None, False, on)
+        if tokens.shape[0] != rows:
+            raise MlaTreeError("tokens must have the logits' %d rows, got %s" % (rows, list(tokens.shape)))
+        _refuse("logprobs", logprobs, torch.float32, dim, dev, tokens.shape, True, on)
+    for name, v in (("lse", lse), ("entropy", entropy)):
+        if v is not None:
+            _refuse(name, v, torch.float32, 1, dev, (rows,), True, on)
+    if top_ids is None and top_logprobs is not None:
+        raise MlaTreeError("top_logprobs needs top_ids")
+    if top_ids is not None:
+        _refuse("top_ids", top_ids, torch.int32, 2, dev, None, True, on)
+        _refuse("top_ids", top_ids, torch.int32, 2, dev, (rows, top_ids.shape[1]), True, on)
+        if top_logprobs is not None:
+            _refuse("top_logprobs", top_logprobs, torch.float32, 2, dev, top_ids.shape, True, on)
+    _refuse_status(status, dev, on)
+
+
+def mla_token_logprobs(logits, tokens=None, logprobs=None, lse=None, entropy=None, top_ids=None, top_logprobs=None,
+                       status=None, stream=None):
+    """Rows of logits [T, V] (bf16, fp16 or fp32; any row stride): the log
+    probabilities of tokens [T] or [T, G] (-1: none), the rows' log sums of exp
+    and entropies [T], and their k <= 32 most likely tokens, top_ids [T, k] and
+    top_logprobs, equal ones by the lower token. What is None is left out. Runs
+    on the logits' device, on stream or that device's current one."""
+    rc = (_paged_call or _load_paged_call()).logprobs(
+        logits, tokens, logprobs, lse, entropy, top_ids, top_logprobs, status,
+        None if stream is None else stream.cuda_stream)
+    if rc is None:
+        _refuse_logprobs(logits, tokens, logprobs, lse, entropy, top_ids, top_logprobs, status)
+    if rc != MT_OK:
+        _check(rc, "mla_token_logprobs")
+
+
+def _refuse_accept(parents, tokens, targets, qo_indptr, kv_lens, path, counts, next_tokens, new_lens, first, status):
+    i32, on = torch.int32, "parents"
+    _refuse("parents", parents, i32, 1, None, None, True)
+    dev, t = parents.get_device(), parents.shape[0]
+    _refuse("path", path, i32, 2, dev, None, True, on)
+    batch = path.shape[0]
+    _refuse("tokens", tokens, i32, 1, dev, (t,), True, on)
+    if isinstance(targets, torch.Tensor) and targets.dim() == 1:
+        targets = targets.as_strided(targets.shape, (1,)) if targets.is_cuda else targets  # any stride
+    _refuse("targets", targets, i32, 1, dev, (t,), False, on)
+    _refuse("qo_indptr", qo_indptr, i32, 1, dev, (batch + 1,), True, on)
+    for name, v in (("kv_lens", kv_lens), ("counts", counts), ("next_tokens", next_tokens), ("new_lens", new_lens)):
+        _refuse(name, v, i32, 1, dev, (batch,), True, on)
+    if first is not None:
+        _refuse("first", first, i32, 1, dev, (batch,), True, on)
+    _refuse_status(status, dev, on)
+
+
+def mla_tree_accept(parents, tokens, targets, qo_indptr, kv_lens, path, counts, next_tokens, new_lens, first=None,
+                    status=None, stream=None):
+    """Walks request b's draft tree (nodes qo_indptr[b] .., parents as for
+    tree_mask_pack) along the tokens that the model chose: from the prefix, the
+    lowest child whose tokens entry is wanted, then its targets entry is wanted.
+    path [B, most] gets the nodes taken (-1 behind), counts [B] how many,
+    next_tokens [B] the token to go on with, new_lens [B] kv_lens without the
+    nodes that were not taken (new_lens may be kv_lens). targets may have any
+    stride (a column of top_ids); first [B] is what the prefix wants, None the
+    token of each request's node 0."""
+    rc = (_paged_call or _load_paged_call()).accept(
+        parents, tokens, targets, qo_indptr, kv_lens, path, counts, next_tokens, new_lens, first, status,
+        None if stream is None else stream.cuda_stream)
+    if rc is None:
+        _refuse_accept(parents, tokens, targets, qo_indptr, kv_lens, path, counts, next_tokens, new_lens, first, status)
+    if rc != MT_OK:
+        _check(rc, "mla_tree_accept")
+
+
+def _refuse_layers(cache):
+    dim = 4 if isinstance(cache, torch.Tensor) and cache.dim() == 4 else 3
+    _refuse("cache", cache, torch.bfloat16, dim, None)
+    if cache.shape[-2] < 1 or cache.shape[-1] != 576 or cache.shape[-2] > 1 and cache.stride(-2) != 576:
+        raise MlaTreeError("cache must be [num_pages, page_size, 576] or [layers, num_pages, page_size, 576] "
+                           "with a page's rows one after another")
+    return cache.get_device()
+
+
+def _refuse_compact(path, counts, kv_lens, block_table, cache, status):
+    dev = _refuse_layers(cache)
+    _refuse("block_table", block_table, torch.int32, 2, dev)
+    batch = block_table.shape[0]
+    _refuse("path", path, torch.int32, 2, dev)
+    _refuse("path", path, torch.int32, 2, dev, (batch, path.shape[1]))
+    _refuse("counts", counts, torch.int32, 1, dev, (batch,), True)
+    _refuse("kv_lens", kv_lens, torch.int32, 1, dev, (batch,), True)
+    _refuse_status(status, dev, "cache")
+
+
+def mla_paged_compact(path, counts, kv_lens, block_table, cache, status=None, stream=None):
+    """Moves the rows of the nodes that mla_tree_accept took up behind the
+    prefix, in a cache [num_pages, page_size, 576] or, for all layers at once,
+    [layers, num_pages, page_size, 576]: position base + path[b, k] to base + k,
+    base = kv_lens[b] - counts[b] (kv_lens: the new lengths)."""
+    rc = (_paged_call or _load_paged_call()).compact(path, counts, kv_lens, block_table, cache, status,
+                                                     None if stream is None else stream.cuda_stream)
+    if rc is None:
+        _refuse_compact(path, counts, kv_lens, block_table, cache, status)
+    if rc != MT_OK:
+        _check(rc, "mla_paged_compact")
+
+
+def _refuse_rows(table, refs, names):
+    _refuse("refs", refs, torch.int32, 1, None, None, True)
+    dev, on = refs.get_device(), "refs"
+    for name, v in zip(names, table):
+        _refuse(name, v, torch.int32, 2, dev, None, False, on)
+    return dev
+
+
+def _refuse_fork(parents, kv_lens, held, block_table, refs, new_lens, new_held, new_table, status):
+    i32, on = torch.int32, "refs"
+    dev = _refuse_rows((block_table, new_table), refs, ("block_table", "new_table"))
+    old, rows = block_table.shape[0], new_table.shape[0]
+    _refuse("new_table", new_table, i32, 2, dev, (rows, block_table.shape[1]), False, on)
+    for name, v, n in (("parents", parents, rows), ("kv_lens", kv_lens, old), ("held", held, old),
+                       ("new_lens", new_lens, rows), ("new_held", new_held, rows)):
+        _refuse(name, v, i32, 1, dev, (n,), True, on)
+    _refuse_status(status, dev, on)
+
+
+def mla_pages_fork(parents, kv_lens, held, block_table, refs, new_lens, new_held, new_table, status=None, stream=None):
+    """Row r of new_table shares the pages of row parents[r] of block_table
+    (-1: none), with its kv_lens and held; rows that are nobody's parent give
+    their pages back. refs [num_pages] counts the holders of each page. The new
+    tensors are others than the old ones."""
+    rc = (_paged_call or _load_paged_call()).fork(parents, kv_lens, held, block_table, refs, new_lens, new_held, new_table,
+                                                  status, None if stream is None else stream.cuda_stream)
+    if rc is None:
+        _refuse_fork(parents, kv_lens, held, block_table, refs, new_lens, new_held, new_table, status)
+    if rc != MT_OK:
+        _check(rc, "mla_pages_fork")
+
+
+def _refuse_fit(kv_lens, want_lens, held, block_table, refs, page_size, copies, workspace, window, sinks, status):
+    i32, on = torch.int32, "refs"
+    for name, v in (("page_size", page_size), ("window", window), ("sinks", sinks)):
+        _refuse_int(name, v)
+    dev = _refuse_rows((block_table,), refs, ("block_table",))
+    batch = block_table.shape[0]
+    for name, v in (("kv_lens", kv_lens), ("want_lens", want_lens), ("held", held)):
+        _refuse(name, v, i32, 1, dev, (batch,), True, on)
+    _refuse("copies", copies, i32, 2, dev, (batch, 3), True, on)
+    _refuse("workspace", workspace, torch.uint8, 1, dev, None, True, on)
+    _refuse_status(status, dev, on)
+
+
+def mla_pages_fit_workspace_bytes(batch, num_pages):
+    return int(load().mla_pages_fit_workspace_bytes(batch, num_pages))
+
+
+def mla_pages_fit(kv_lens, want_lens, held, block_table, refs, page_size, copies, workspace, window=0, sinks=0,
+                  status=None, stream=None):
+    """Gives each request pages of its own for positions kv_lens .. want_lens -
+    1 and takes back those behind want_lens and, with a window, those that lie
+    wholly between the first sinks positions and the window of position kv_lens.
+    copies [B, 3] gets (source page, destination page, rows) where a shared page
+    was replaced, for mla_paged_copy. Without enough free pages DEV_NO_PAGES is
+    set and nothing changes. workspace: uint8, mla_pages_fit_workspace_bytes(B,
+    num_pages)."""
+    rc = (_paged_call or _load_paged_call()).fit(kv_lens, want_lens, held, block_table, refs, page_size, copies, workspace,
+                                                 window, sinks, status, None if stream is None else stream.cuda_stream)
+    if rc is None:
+        _refuse_fit(kv_lens, want_lens, held, block_table, refs, page_size, copies, workspace, window, sinks, status)
+    if rc != MT_OK:
+        _check(rc, "mla_pages_fit")
+
+
+def mla_paged_copy(copies, cache, status=None, stream=None):
+    """Copies the first copies[i, 2] rows of page copies[i, 0] to page copies[i,
+    1] (-1: none), in a cache [num_pages, page_size, 576] or in every layer of
+    [layers, num_pages, page_size, 576]."""
+    rc = (_paged_call or _load_paged_call()).copy(copies, cache, status, None if stream is None else stream.cuda_stream)
+    if rc is None:
+        dev = _refuse_layers(cache)
+        _refuse("copies", copies, torch.int32, 2, dev)
+        _refuse("copies", copies, torch.int32, 2, dev, (copies.shape[0], 3), True)
+        _refuse_status(status, dev, "cache")
+    if rc != MT_OK:
+        _check(rc, "mla_paged_copy")

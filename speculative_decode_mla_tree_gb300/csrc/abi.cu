@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include "../../include/mla_tree.h"
+#include "logits.h"
 #include "mt_internal.h"
 #include "paged.h"
 
@@ -397,12 +398,15 @@ size_t mla_paged_decode_workspace_bytes(int batch, int heads) {
   return decode_layout(heads, sm_count()).total;
 }
 
-int mla_paged_decode(const mt_bf16* q, int64_t q_token_stride, int64_t q_head_stride,
-                     const mt_bf16* cache, int64_t page_stride, int64_t num_pages, int page_size,
-                     const int32_t* block_table, int64_t table_stride, int max_pages,
-                     const int32_t* kv_lens, int batch, int heads, float sm_scale,
-                     mt_bf16* out, float* lse, void* workspace, size_t workspace_bytes,
-                     int32_t* dev_status, mt_stream_t stream) {
+}  // extern "C"
+
+// window 0: every position.
+static int decode_common(const mt_bf16* q, int64_t q_token_stride, int64_t q_head_stride,
+                         const mt_bf16* cache, int64_t page_stride, int64_t num_pages, int page_size,
+                         const int32_t* block_table, int64_t table_stride, int max_pages,
+                         const int32_t* kv_lens, int window, int sinks, int batch, int heads, float sm_scale,
+                         mt_bf16* out, float* lse, void* workspace, size_t workspace_bytes,
+                         int32_t* dev_status, mt_stream_t stream) {
   if (batch < 0 || heads <= 0 || !isfinite(sm_scale) || q_token_stride < MT_D_QK ||
       q_token_stride % 8 || q_head_stride < MT_D_QK || q_head_stride % 8 ||
       !paged_cache_ok(cache, page_stride, num_pages, page_size, table_stride, max_pages))
@@ -421,6 +425,8 @@ int mla_paged_decode(const mt_bf16* q, int64_t q_token_stride, int64_t q_head_st
   a.q_head = q_head_stride;
   a.kv = {const_cast<mt_bf16*>(cache), page_stride, num_pages, page_size, block_table, table_stride,
           max_pages, kv_lens};
+  a.window = window;
+  a.sinks = sinks;
   a.batch = batch;
   a.heads = heads;
   a.sm_scale = sm_scale;
@@ -434,6 +440,176 @@ int mla_paged_decode(const mt_bf16* q, int64_t q_token_stride, int64_t q_head_st
   const cudaError_t e = launch_paged_decode_tc(a, nsm, (cudaStream_t)stream);
   if (e != cudaErrorNotSupported) return cuda_status(e);
   return cuda_status(launch_paged_decode_simt(a, nsm, (cudaStream_t)stream));
+}
+
+// Layers of a paged cache.
+static bool layers_ok(int layers, int64_t layer_stride) {
+  return layers >= 0 && (layers <= 1 || (layer_stride >= 0 && layer_stride % 8 == 0 && layer_stride <= INT64_MAX / 4 / layers));
+}
+
+extern "C" {
+
+int mla_paged_decode(const mt_bf16* q, int64_t q_token_stride, int64_t q_head_stride,
+                     const mt_bf16* cache, int64_t page_stride, int64_t num_pages, int page_size,
+                     const int32_t* block_table, int64_t table_stride, int max_pages,
+                     const int32_t* kv_lens, int batch, int heads, float sm_scale,
+                     mt_bf16* out, float* lse, void* workspace, size_t workspace_bytes,
+                     int32_t* dev_status, mt_stream_t stream) {
+  return decode_common(q, q_token_stride, q_head_stride, cache, page_stride, num_pages, page_size, block_table,
+                       table_stride, max_pages, kv_lens, 0, 0, batch, heads, sm_scale, out, lse, workspace,
+                       workspace_bytes, dev_status, stream);
+}
+
+int mla_paged_decode_window(const mt_bf16* q, int64_t q_token_stride, int64_t q_head_stride,
+                            const mt_bf16* cache, int64_t page_stride, int64_t num_pages,
+                            int page_size, const int32_t* block_table, int64_t table_stride,
+                            int max_pages, const int32_t* kv_lens, int window, int sinks, int batch,
+                            int heads, float sm_scale, mt_bf16* out, float* lse, void* workspace,
+                            size_t workspace_bytes, int32_t* dev_status, mt_stream_t stream) {
+  if (window < 1 || sinks < 0) return MT_EINVAL;
+  return decode_common(q, q_token_stride, q_head_stride, cache, page_stride, num_pages, page_size, block_table,
+                       table_stride, max_pages, kv_lens, window, sinks, batch, heads, sm_scale, out, lse,
+                       workspace, workspace_bytes, dev_status, stream);
+}
+
+int mla_token_logprobs(const void* logits, int logits_type, int64_t row_stride, int rows, int vocab,
+                       const int32_t* tokens, int64_t token_stride, int tokens_per_row, int top_k,
+                       float* logprobs, float* lse, float* entropy, int32_t* top_ids,
+                       float* top_logprobs, int32_t* dev_status, mt_stream_t stream) {
+  if (logits_type != MT_LOGITS_BF16 && logits_type != MT_LOGITS_FP16 && logits_type != MT_LOGITS_FP32) return MT_EINVAL;
+  const int size = logits_type == MT_LOGITS_FP32 ? 4 : 2;
+  if (rows < 0 || vocab < 1 || tokens_per_row < 0 || top_k < 0 || top_k > vocab) return MT_EINVAL;
+  if (row_stride < 0 || (rows > 1 && row_stride > INT64_MAX / 8 / rows)) return MT_EINVAL;
+  if (token_stride < 0 || (rows > 1 && token_stride > INT64_MAX / 8 / rows)) return MT_EINVAL;
+  if (tokens_per_row > 0 ? !tokens || !logprobs : tokens || logprobs) return MT_EINVAL;
+  if (top_k > 0 ? !top_ids : top_ids || top_logprobs) return MT_EINVAL;
+  if (top_k > MT_MAX_TOP) return MT_EUNSUPPORTED;
+  if (rows == 0) return MT_OK;
+  if (!logits || (uintptr_t)logits % size) return MT_EINVAL;
+  const int nsm = sm_count();
+  if ((int64_t)rows * logprob_parts(rows, vocab, nsm) > INT32_MAX) return MT_EUNSUPPORTED;
+  LogprobArgs a;
+  a.logits = logits;
+  a.row_stride = row_stride;
+  a.rows = rows;
+  a.vocab = vocab;
+  a.tokens = tokens;
+  a.token_stride = token_stride;
+  a.per_row = tokens_per_row;
+  a.top_k = top_k;
+  a.logprobs = logprobs;
+  a.lse = lse;
+  a.entropy = entropy;
+  a.top_ids = top_ids;
+  a.top_logprobs = top_logprobs;
+  a.status = dev_status;
+  return cuda_status(launch_token_logprobs(a, logits_type, nsm, (cudaStream_t)stream));
+}
+
+int mla_tree_accept(const int32_t* parents, const int32_t* tokens, const int32_t* targets,
+                    int64_t target_stride, const int32_t* first, const int32_t* qo_indptr,
+                    const int32_t* kv_lens, int batch, int total_q, int max_accept, int32_t* path,
+                    int32_t* counts, int32_t* next_tokens, int32_t* new_lens, int32_t* dev_status,
+                    mt_stream_t stream) {
+  if (batch < 0 || total_q < 0 || max_accept < 0 || target_stride < 0 ||
+      (total_q > 1 && target_stride > INT64_MAX / 8 / total_q))
+    return MT_EINVAL;
+  if (batch == 0) return MT_OK;
+  if (!qo_indptr || !kv_lens || !counts || !next_tokens || !new_lens) return MT_EINVAL;
+  if (total_q > 0 && (!parents || !tokens || !targets)) return MT_EINVAL;
+  if (max_accept > 0 && !path) return MT_EINVAL;
+  if (batch > 65535) return MT_EUNSUPPORTED;
+  const AcceptArgs a = {parents, tokens, targets, target_stride, first, qo_indptr, kv_lens, batch, total_q,
+                        max_accept, path, counts, next_tokens, new_lens, dev_status};
+  return cuda_status(launch_tree_accept(a, (cudaStream_t)stream));
+}
+
+int mla_paged_compact(const int32_t* path, int64_t path_stride, int max_accept, const int32_t* counts,
+                      const int32_t* kv_lens, int batch, const int32_t* block_table,
+                      int64_t table_stride, int max_pages, mt_bf16* cache, int64_t page_stride,
+                      int64_t num_pages, int page_size, int layers, int64_t layer_stride,
+                      int32_t* dev_status, mt_stream_t stream) {
+  if (batch < 0 || max_accept < 0 || path_stride < max_accept || !layers_ok(layers, layer_stride) ||
+      !paged_cache_ok(cache, page_stride, num_pages, page_size, table_stride, max_pages))
+    return MT_EINVAL;
+  if (batch == 0 || max_accept == 0 || layers == 0) return MT_OK;
+  if (!path || !counts || !kv_lens || (max_pages > 0 && !block_table) || (num_pages > 0 && !cache)) return MT_EINVAL;
+  if (batch > 65535) return MT_EUNSUPPORTED;
+  CompactArgs a;
+  a.path = path;
+  a.path_stride = path_stride;
+  a.max_accept = max_accept;
+  a.counts = counts;
+  a.kv = {cache, page_stride, num_pages, page_size, block_table, table_stride, max_pages, kv_lens};
+  a.batch = batch;
+  a.layers = layers;
+  a.layer_stride = layer_stride;
+  a.status = dev_status;
+  return cuda_status(launch_paged_compact(a, (cudaStream_t)stream));
+}
+
+int mla_pages_fork(const int32_t* parents, const int32_t* kv_lens, const int32_t* held,
+                   const int32_t* block_table, int64_t table_stride, int old_batch, int max_pages,
+                   int32_t* refs, int64_t num_pages, int32_t* new_lens, int32_t* new_held,
+                   int32_t* new_table, int64_t new_table_stride, int new_batch,
+                   int32_t* dev_status, mt_stream_t stream) {
+  if (old_batch < 0 || new_batch < 0 || max_pages < 0 || table_stride < max_pages || new_table_stride < max_pages ||
+      table_stride > INT64_MAX >> 20 || new_table_stride > INT64_MAX >> 20 || num_pages < 0 || num_pages > INT32_MAX)
+    return MT_EINVAL;
+  if (old_batch == 0 && new_batch == 0) return MT_OK;
+  if (old_batch > 0 && (!kv_lens || !held || (max_pages > 0 && !block_table))) return MT_EINVAL;
+  if (new_batch > 0 && (!parents || !new_lens || !new_held || (max_pages > 0 && !new_table))) return MT_EINVAL;
+  if (num_pages > 0 && !refs) return MT_EINVAL;
+  if (old_batch > 65535 || new_batch > 65535) return MT_EUNSUPPORTED;
+  if (old_batch > 0 && new_batch > 0) {
+    auto apart = [](const int32_t* x, int64_t n, const int32_t* y, int64_t m) {
+      return n == 0 || m == 0 || (uintptr_t)(x + n) <= (uintptr_t)y || (uintptr_t)(y + m) <= (uintptr_t)x;
+    };
+    const int64_t cells = max_pages ? (old_batch - 1) * table_stride + max_pages : 0;
+    const int64_t new_cells = max_pages ? (new_batch - 1) * new_table_stride + max_pages : 0;
+    if (!apart(kv_lens, old_batch, new_lens, new_batch) || !apart(held, old_batch, new_held, new_batch) ||
+        !apart(block_table, cells, new_table, new_cells))
+      return MT_EINVAL;
+  }
+  const ForkArgs a = {parents, kv_lens, held, block_table, table_stride, old_batch, max_pages, refs, num_pages,
+                      new_lens, new_held, new_table, new_table_stride, new_batch, dev_status};
+  return cuda_status(launch_pages_fork(a, (cudaStream_t)stream));
+}
+
+size_t mla_pages_fit_workspace_bytes(int batch, int64_t num_pages) {
+  if (batch < 0 || batch > 65535 || num_pages < 0 || num_pages > INT32_MAX) return 0;
+  return pages_fit_workspace(batch, num_pages);
+}
+
+int mla_pages_fit(const int32_t* kv_lens, const int32_t* want_lens, int32_t* held,
+                  int32_t* block_table, int64_t table_stride, int batch, int max_pages, int32_t* refs,
+                  int64_t num_pages, int page_size, int window, int sinks, int32_t* copies,
+                  void* workspace, size_t workspace_bytes, int32_t* dev_status, mt_stream_t stream) {
+  if (batch < 0 || max_pages < 0 || table_stride < max_pages || num_pages < 0 || num_pages > INT32_MAX ||
+      page_size < 1 || (int64_t)max_pages * page_size > INT32_MAX || window < 0 || sinks < 0)
+    return MT_EINVAL;
+  if (batch == 0) return MT_OK;
+  if (!kv_lens || !want_lens || !held || !copies || (max_pages > 0 && !block_table) || (num_pages > 0 && !refs))
+    return MT_EINVAL;
+  if (batch > 65535) return MT_EUNSUPPORTED;
+  if (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < pages_fit_workspace(batch, num_pages))
+    return MT_EWORKSPACE;
+  const FitArgs a = {kv_lens, want_lens, held, block_table, table_stride, batch, max_pages, refs, num_pages,
+                     page_size, window, sinks, copies, (int32_t*)workspace, dev_status};
+  return cuda_status(launch_pages_fit(a, (cudaStream_t)stream));
+}
+
+int mla_paged_copy(const int32_t* copies, int64_t n, mt_bf16* cache, int64_t page_stride,
+                   int64_t num_pages, int page_size, int layers, int64_t layer_stride,
+                   int32_t* dev_status, mt_stream_t stream) {
+  if (n < 0 || !layers_ok(layers, layer_stride) ||
+      !paged_cache_ok(cache, page_stride, num_pages, page_size, 0, 0))
+    return MT_EINVAL;
+  if (n == 0 || layers == 0) return MT_OK;
+  if (!copies || (num_pages > 0 && !cache)) return MT_EINVAL;
+  const CopyArgs a = {copies, n, cache, page_stride, layer_stride, num_pages, page_size, layers, dev_status};
+  if (paged_copy_blocks(a) < 0) return MT_EUNSUPPORTED;
+  return cuda_status(launch_paged_copy(a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

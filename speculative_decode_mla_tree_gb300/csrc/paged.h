@@ -53,6 +53,7 @@ struct DecodeArgs {
   const uint16_t* q;
   int64_t q_tok, q_head;
   PagedCache kv;
+  int window, sinks;            // positions below sinks and the last window; window 0: all
   int batch, heads;
   float sm_scale;
   uint16_t* out;                // bf16 [batch, heads, 512]
@@ -82,5 +83,69 @@ cudaError_t launch_paged_decode_simt(const DecodeArgs& a, int num_sms, cudaStrea
 // after the first.
 cudaError_t launch_paged_merge(const DecodeArgs& a, int entries, int step, int rows_per_slot,
                                int num_sms, cudaStream_t stream);
+
+// ------------------------------------------------- what surrounds the attention
+
+struct AcceptArgs {
+  const int32_t *parents, *tokens, *targets;
+  int64_t target_stride;
+  const int32_t* first;         // [batch] or nullptr: each request's node 0
+  const int32_t *qo_indptr, *kv_lens;
+  int batch, total_q, max_accept;
+  int32_t *path, *counts, *next_tokens, *new_lens;
+  int32_t* status;
+};
+cudaError_t launch_tree_accept(const AcceptArgs& a, cudaStream_t stream);
+
+struct CompactArgs {
+  const int32_t* path;
+  int64_t path_stride;
+  int max_accept;
+  const int32_t* counts;
+  PagedCache kv;                // of the first layer; lens: with the accepted rows
+  int batch, layers;
+  int64_t layer_stride;         // elements
+  int32_t* status;
+};
+cudaError_t launch_paged_compact(const CompactArgs& a, cudaStream_t stream);
+
+struct ForkArgs {
+  const int32_t *parents, *lens, *held, *table;
+  int64_t table_stride;
+  int old_batch, max_pages;
+  int32_t* refs;
+  int64_t num_pages;
+  int32_t *new_lens, *new_held, *new_table;
+  int64_t new_table_stride;
+  int new_batch;
+  int32_t* status;
+};
+cudaError_t launch_pages_fork(const ForkArgs& a, cudaStream_t stream);
+
+struct FitArgs {
+  const int32_t *lens, *want;
+  int32_t *held, *table;
+  int64_t table_stride;
+  int batch, max_pages;
+  int32_t* refs;
+  int64_t num_pages;
+  int page_size, window, sinks;
+  int32_t* copies;              // [batch, 3] source page, destination page, rows
+  int32_t* ws;
+  int32_t* status;
+};
+size_t pages_fit_workspace(int batch, int64_t num_pages);
+cudaError_t launch_pages_fit(const FitArgs& a, cudaStream_t stream);
+
+struct CopyArgs {
+  const int32_t* copies;        // [n, 3]
+  int64_t n;
+  uint16_t* rows;
+  int64_t page_stride, layer_stride, num_pages;
+  int page_size, layers;
+  int32_t* status;
+};
+int64_t paged_copy_blocks(const CopyArgs& a);  // its grid; -1: more than one takes
+cudaError_t launch_paged_copy(const CopyArgs& a, cudaStream_t stream);
 
 }  // namespace mt

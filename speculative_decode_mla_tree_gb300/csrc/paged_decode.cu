@@ -42,14 +42,20 @@ constexpr unsigned kFull = 0xffffffffu;
 // of the 512 value dims. A block takes one split of one request. Bound by its
 // fp32 arithmetic, about 2200 operations a key and head: 32 requests of 8192
 // keys at 64 heads take 4.6 ms.
+//
+// kWindow: the visible positions are counted one after another, those behind
+// the gap between the first tokens and the window by `gap` less.
+template <bool kWindow>
 __global__ void __launch_bounds__(32 * kWarps) decode_simt_kernel(const DecodeArgs a, const int splits,
                                                                   const int split_keys) {
   const int lane = threadIdx.x & 31;
   const int b = blockIdx.y, s = blockIdx.z;
   const int h = blockIdx.x * kWarps + (threadIdx.x >> 5);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int len = __ldg(a.kv.lens + b);
+  int len = __ldg(a.kv.lens + b);
   const bool ok = len >= 0 && len <= (int64_t)a.kv.max_pages * a.kv.page_size;
+  const unsigned gap = kWindow && len > a.window && len - a.window > a.sinks ? len - a.window - a.sinks : 0;
+  len -= gap;
   const int used = ok ? (int)(((int64_t)len + split_keys - 1) / split_keys) : 0;  // splits with keys
   if (blockIdx.x == 0 && s == 0 && threadIdx.x == 0) {
     if (!ok) flag(a.status, MT_DEV_BAD_INDPTR);
@@ -90,7 +96,8 @@ __global__ void __launch_bounds__(32 * kWarps) decode_simt_kernel(const DecodeAr
     for (int t = 0; t < kKeys; ++t) {
       see[t] = j + t < j1;
       if (!see[t]) continue;
-      const unsigned in_table = (j + t) / (unsigned)a.kv.page_size;
+      const unsigned at = kWindow && j + t >= (unsigned)a.sinks ? j + t + gap : j + t;
+      const unsigned in_table = at / (unsigned)a.kv.page_size;
       const int page = __ldg(table + in_table);
       see[t] = page >= 0 && page < a.kv.num_pages;
       if (!see[t]) {
@@ -98,7 +105,7 @@ __global__ void __launch_bounds__(32 * kWarps) decode_simt_kernel(const DecodeAr
         continue;
       }
       const uint4* src = reinterpret_cast<const uint4*>(
-          a.kv.rows + page * a.kv.page_stride + (int64_t)(j + t - in_table * a.kv.page_size) * kDqk);
+          a.kv.rows + page * a.kv.page_stride + (int64_t)(at - in_table * a.kv.page_size) * kDqk);
       row[t][0] = __ldg(src + lane);
       row[t][1] = __ldg(src + lane + 32);
       row[t][2] = lane < 8 ? __ldg(src + lane + 64) : make_uint4(0, 0, 0, 0);
@@ -438,9 +445,10 @@ cudaError_t launch_paged_merge(const DecodeArgs& a, int entries, int step, int r
 cudaError_t launch_paged_decode_simt(const DecodeArgs& a, int num_sms, cudaStream_t stream) {
   const int nsm = decode_sms(num_sms);
   const int hb = (a.heads + kWarps - 1) / kWarps;
-  // Splits by the table's width, which the host knows: as many as two CTAs an
+  // Splits by the table's width (or the window's), which the host knows: as many as two CTAs an
   // SM, none below 64 keys. batch * splits stays within the workspace's rows.
-  const int64_t cap = (int64_t)a.kv.max_pages * a.kv.page_size;
+  int64_t cap = (int64_t)a.kv.max_pages * a.kv.page_size;
+  if (a.window > 0 && cap > (int64_t)a.window + a.sinks) cap = (int64_t)a.window + a.sinks;
   int64_t splits = 2LL * nsm / ((int64_t)a.batch * hb);
   if (splits > (cap + 63) / 64) splits = (cap + 63) / 64;
   if (splits < 1) splits = 1;
@@ -454,7 +462,8 @@ cudaError_t launch_paged_decode_simt(const DecodeArgs& a, int num_sms, cudaStrea
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, decode_simt_kernel, a, (int)splits, (int)keys);
+  cudaError_t e = a.window > 0 ? cudaLaunchKernelEx(&cfg, decode_simt_kernel<true>, a, (int)splits, (int)keys)
+                               : cudaLaunchKernelEx(&cfg, decode_simt_kernel<false>, a, (int)splits, (int)keys);
   if (e != cudaSuccess || splits == 1) return e;
   return launch_paged_merge(a, a.batch, 1, a.heads, nsm, stream);
 }

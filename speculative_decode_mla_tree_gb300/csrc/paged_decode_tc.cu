@@ -993,6 +993,7 @@ void set_paged_test_hooks(int drop_item, unsigned long long limit_ns) {
 
 cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_t stream) {
   using namespace ptc;
+  if (a.window > 0) return cudaErrorNotSupported;
   const int P = a.kv.page_size;
   // Pages of whole groups of eight rows go by boxes; others row by row, where
   // rows can be counted through the pages (32 requests of 8192 keys, 64 heads:
