@@ -130,6 +130,7 @@ struct Params {
   int groups;                   // head groups = CTAs per team
   int nteams;
   int merge;                    // 1: a merge launch follows
+  int window, sinks, sink_rows, unit;  // window form, see View
   int drop_team;                // test hook: this team's and later producers issue nothing (-1: off)
   unsigned long long limit_ns;  // bound of every wait
 };
@@ -272,8 +273,20 @@ __device__ __forceinline__ bool bar_any(int id, int nthreads, bool v) {
 // --------------------------------------------------------------------- plan
 
 __device__ __forceinline__ bool length_ok(const Params& p, int len) { return (unsigned)len <= (unsigned)p.most; }
+
+// What of a request is walked. With a window, positions come in units of one
+// box (16 or 8 rows, 1 with gathers), and the units between the first `sinks`
+// positions and the window, in which no position is visible, are not counted:
+// row v of the walk is position v, or v + gap behind the first sink_rows (sinks,
+// rounded up to units). Of the units at the edges the visible positions are
+// those below sinks and from start on.
+template <bool kWindow>
+__device__ __forceinline__ int gap_of(const Params& p, int len) {
+  return kWindow && len > p.window ? max(0, ((len - p.window) & -p.unit) - p.sink_rows) : 0;
+}
+template <bool kWindow>
 __device__ __forceinline__ int tiles_of(const Params& p, int len) {
-  return length_ok(p, len) ? (int)(((unsigned)len + kTile - 1) / kTile) : 0;
+  return length_ok(p, len) ? (int)(((unsigned)len - gap_of<kWindow>(p, len) + kTile - 1) / kTile) : 0;
 }
 
 // A team's walk over its share [s, e) of the line of tiles. Each role keeps
@@ -283,11 +296,13 @@ struct Walk {
   int b;
 };
 struct Piece {
-  int b, len, tiles, t0, t1;
+  int b, len, tiles, t0, t1;  // len: rows of the walk
+  int gap, start;             // with a window
   int64_t o;
   bool ok;
 };
 
+template <bool kWindow>
 __device__ __forceinline__ bool next_piece(const Params& prm, Walk& w, Piece& p) {
   const DecodeArgs& a = prm.a;
   while (w.b < a.batch && w.o < w.e) {
@@ -295,7 +310,12 @@ __device__ __forceinline__ bool next_piece(const Params& prm, Walk& w, Piece& p)
     p.o = w.o;
     p.len = __ldg(a.kv.lens + w.b);
     p.ok = length_ok(prm, p.len);
-    p.tiles = tiles_of(prm, p.len);
+    p.tiles = tiles_of<kWindow>(prm, p.len);
+    if (kWindow) {
+      p.start = max(0, p.len - prm.window);
+      p.gap = gap_of<kWindow>(prm, p.len);
+      p.len -= p.gap;
+    }
     const int64_t first = w.o + kOverhead;  // the request's tiles start here
     const int64_t t0 = w.s - first, t1 = w.e - first;
     p.t0 = (int)(t0 > 0 ? (t0 < p.tiles ? t0 : p.tiles) : 0);
@@ -311,6 +331,7 @@ __device__ __forceinline__ bool next_piece(const Params& prm, Walk& w, Piece& p)
 // by itself, so that no role waits for another: the 32 lanes sum up equal runs
 // of requests, and the run that holds the start is cut into 32 again (one round
 // of loads and one scan up to 32 requests, two up to 1024).
+template <bool kWindow>
 __device__ __forceinline__ Walk make_plan(const Params& p, int team, int64_t* share_out) {
   const int lane = threadIdx.x & 31;
   Walk r;
@@ -323,7 +344,7 @@ __device__ __forceinline__ Walk make_plan(const Params& p, int team, int64_t* sh
     int64_t u = 0;
     for (int k = 0; k < c; ++k) {
       const int i = lane * c + k;
-      if (i < n) u += kOverhead + tiles_of(p, __ldg(p.a.kv.lens + lo + i));
+      if (i < n) u += kOverhead + tiles_of<kWindow>(p, __ldg(p.a.kv.lens + lo + i));
     }
     int64_t inc = u;
 #pragma unroll
@@ -366,7 +387,7 @@ __device__ __noinline__ void drain_loads(uint64_t* bars, uint32_t pieces, uint32
 
 // kGather: pages that are no whole groups of eight rows; two producer warps
 // bring single rows by gather, each every other quarter of a tile.
-template <int N, bool kGather>
+template <int N, bool kGather, bool kWindow>
 __global__ void __launch_bounds__(threads_of(kGather), 1)
     paged_decode_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tq,
                            const __grid_constant__ CUtensorMap tkv) {
@@ -410,7 +431,7 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
   // the early signal is worth 0.5 us).
   if (!p.merge) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int64_t share = 1;
-  Walk walk = make_plan(p, team, &share);  // its loads run beside the set-up above
+  Walk walk = make_plan<kWindow>(p, team, &share);  // its loads run beside the set-up above
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -432,12 +453,15 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
       if (!dead) dead = __any_sync(kFull, !wait_phase(&bars[bar], parity, abort, limit));
     };
     const int q0 = me + 2 * (lane >> 4);
-    while (!dead && next_piece(p, walk, pc)) {
+    while (!dead && next_piece<kWindow>(p, walk, pc)) {
       if (pc.t1 <= pc.t0) continue;
       const int32_t* table = a.kv.table + pc.b * a.kv.table_stride;
       auto row_of = [&](int t) { return (unsigned)t * kTile + q0 * 16 + (lane & 15); };
+      auto place_of = [&](int t) {  // of that row, as a position
+        return kWindow && row_of(t) >= (unsigned)p.sink_rows ? row_of(t) + pc.gap : row_of(t);
+      };
       auto entry = [&](int t) {
-        return t < pc.t1 && row_of(t) < (unsigned)pc.len ? __ldg(table + row_of(t) / a.kv.page_size) : -1;
+        return t < pc.t1 && row_of(t) < (unsigned)pc.len ? __ldg(table + place_of(t) / a.kv.page_size) : -1;
       };
       int page_next = entry(pc.t0);
       if (me == 0) {
@@ -454,7 +478,7 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
         if (asked && !ok && grp == 0) flag(a.status, MT_DEV_BAD_SLOT);
         const unsigned okm = __ballot_sync(kFull, ok);
         // a row that is not there is read from the cache's first (and hidden)
-        const int slot = ok ? (int)(page * p.page_rows + row_of(t) % a.kv.page_size) : 0;
+        const int slot = ok ? (int)(page * p.page_rows + place_of(t) % a.kv.page_size) : 0;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           const int q = me + 2 * h;
@@ -495,7 +519,7 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
     auto wait = [&](int bar, uint32_t parity) {
       if (!dead) dead = __any_sync(kFull, !wait_phase(&bars[bar], parity, abort, limit));
     };
-    while (!dead && next_piece(p, walk, pc)) {
+    while (!dead && next_piece<kWindow>(p, walk, pc)) {
       if (pc.t1 <= pc.t0) continue;
       const int32_t* table = a.kv.table + pc.b * a.kv.table_stride;
       // Lane l looks after group l of a tile: its page, -1 behind the length or
@@ -505,9 +529,15 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
       unsigned e = g0 / p.page_groups, g = g0 - e * p.page_groups, walked = g0;
       int pages[kAhead + 2], place[kAhead + 2];  // of tile t, t + 1, ...
       auto ask = [&](int& page, int& at) {
+        if (kWindow) {  // behind the gap, which may begin anywhere
+          const unsigned at_group = walked * 8 < (unsigned)p.sink_rows ? walked : walked + (unsigned)pc.gap / 8;
+          e = at_group / p.page_groups;
+          g = at_group - e * p.page_groups;
+        }
         at = (int)g;
         page = lane < 8 && walked < (unsigned)pc.t1 * 8 && walked * 8 < (unsigned)pc.len ? __ldg(table + e) : -1;
         walked += 8;
+        if (kWindow) return;
         e += step_e;
         g += step_g;
         if (g >= (unsigned)p.page_groups) g -= p.page_groups, ++e;
@@ -531,6 +561,14 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
                        ((okm & 15) * 0x00204081u & 0x01010101u) * 0xffu;
         const int64_t left = (int64_t)pc.len - (int64_t)t * kTile;
         if (left < kTile) vis &= (1ull << left) - 1;
+        if (kWindow) {
+          auto seen = [&](unsigned row) {
+            const unsigned at = row < (unsigned)p.sink_rows ? row : row + pc.gap;
+            return at < (unsigned)p.sinks || at >= (unsigned)pc.start;
+          };
+          const unsigned row = (unsigned)t * kTile + lane;
+          vis &= (uint64_t)__ballot_sync(kFull, seen(row + 32)) << 32 | __ballot_sync(kFull, seen(row));
+        }
         // a box of two groups lies in one page: they are good or bad together,
         // but the second may start behind the length
         const uint32_t bytes = per == 2 ? __popc(okm & 0x55) * 2 * kGroup : __popc(okm) * kGroup;
@@ -581,7 +619,7 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
     auto wait = [&](int bar, uint32_t parity) {
       if (!dead) dead = __any_sync(kFull, !wait_phase(&bars[bar], parity, abort, limit));
     };
-    while (!dead && next_piece(p, walk, pc)) {
+    while (!dead && next_piece<kWindow>(p, walk, pc)) {
       const int n = __shfl_sync(kFull, pc.t1 - pc.t0, 0);
       if (n <= 0) continue;
       wait(B_Q_FULL, pieces & 1);
@@ -620,7 +658,7 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
     auto wait = [&](int bar, uint32_t parity) {
       if (!dead) dead = __any_sync(kFull, !wait_phase(&bars[bar], parity, abort, limit));
     };
-    while (!dead && next_piece(p, walk, pc)) {
+    while (!dead && next_piece<kWindow>(p, walk, pc)) {
       const int n = __shfl_sync(kFull, pc.t1 - pc.t0, 0);
       if (n <= 0) continue;
       wait(B_O_EMPTY, (pieces & 1) ^ 1);
@@ -666,7 +704,7 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
     MergeEntry entry = {0, 0, 0, 0};
     uint32_t it = 0;
     bool dead = false;
-    while (next_piece(p, walk, pc)) {
+    while (next_piece<kWindow>(p, walk, pc)) {
       const int64_t orow = (int64_t)pc.b * a.heads + grp * N;
       const int nh = min(N, a.heads - grp * N);
       if (pc.t1 <= pc.t0) {  // no keys
@@ -955,7 +993,7 @@ bool make_row_map(CUtensorMap* m, const PagedCache& kv, int64_t rows) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int N, bool kGather = false>
+template <int N, bool kGather, bool kWindow>
 cudaError_t launch(const Params& p, const CUtensorMap& tq, const CUtensorMap& tkv, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -965,7 +1003,7 @@ cudaError_t launch(const Params& p, const CUtensorMap& tq, const CUtensorMap& tk
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev < 0 || dev >= 64 || !ready[dev]) {
-      e = cudaFuncSetAttribute(paged_decode_tc_kernel<N, kGather>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      e = cudaFuncSetAttribute(paged_decode_tc_kernel<N, kGather, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                Lay<N>::kBytes);
       if (e != cudaSuccess) return e;
       if (dev >= 0 && dev < 64) ready[dev] = true;
@@ -981,7 +1019,14 @@ cudaError_t launch(const Params& p, const CUtensorMap& tq, const CUtensorMap& tk
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_decode_tc_kernel<N, kGather>, p, tq, tkv);
+  return cudaLaunchKernelEx(&cfg, paged_decode_tc_kernel<N, kGather, kWindow>, p, tq, tkv);
+}
+
+template <bool kGather, bool kWindow>
+cudaError_t launch(int n, const Params& p, const CUtensorMap& tq, const CUtensorMap& tkv, cudaStream_t stream) {
+  return n == 16   ? launch<16, kGather, kWindow>(p, tq, tkv, stream)
+         : n == 32 ? launch<32, kGather, kWindow>(p, tq, tkv, stream)
+                   : launch<64, kGather, kWindow>(p, tq, tkv, stream);
 }
 
 }  // namespace ptc
@@ -993,7 +1038,6 @@ void set_paged_test_hooks(int drop_item, unsigned long long limit_ns) {
 
 cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_t stream) {
   using namespace ptc;
-  if (a.window > 0) return cudaErrorNotSupported;
   const int P = a.kv.page_size;
   // Pages of whole groups of eight rows go by boxes; others row by row, where
   // rows can be counted through the pages (32 requests of 8192 keys, 64 heads:
@@ -1011,8 +1055,19 @@ cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_
   p.most = a.kv.max_pages * P;
   p.groups = (a.heads + N - 1) / N;
   p.nteams = nsm / p.groups > 0 ? nsm / p.groups : 1;
+  p.window = a.window;
+  p.sinks = a.sinks;
+  p.unit = gather ? 1 : P % 16 == 0 ? 16 : 8;
+  int64_t rows = p.most;
+  if (a.window > 0) {  // beyond the table it does not matter how many tokens stay
+    p.sinks = a.sinks < p.most ? a.sinks : p.most;
+    const int64_t sink_rows = ((int64_t)p.sinks + p.unit - 1) / p.unit * p.unit;
+    p.sink_rows = sink_rows < INT32_MAX ? (int)sink_rows : INT32_MAX;
+    const int64_t walked = sink_rows + a.window + p.unit;
+    if (walked < rows) rows = walked;
+  }
   // No request of this table can be split when it holds no more tiles than a share.
-  const int64_t tiles = ((int64_t)p.most + kTile - 1) / kTile;
+  const int64_t tiles = (rows + kTile - 1) / kTile;
   p.merge = p.nteams > 1 && (a.batch > 1 || tiles > kMinShare);
   p.drop_team = g_test_drop_team;
   p.limit_ns = g_test_limit_ns > 0 ? g_test_limit_ns : sm100::kWaitLimitNs;
@@ -1020,15 +1075,9 @@ cudaError_t launch_paged_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_
   if (!make_q_map(&tq, a, N)) return cudaErrorNotSupported;
   if (!(gather ? make_row_map(&tkv, a.kv, (a.kv.num_pages - 1) * page_rows + P) : make_box_map(&tkv, a.kv)))
     return cudaErrorNotSupported;
-  cudaError_t e;
-  if (gather)
-    e = N == 16   ? launch<16, true>(p, tq, tkv, stream)
-        : N == 32 ? launch<32, true>(p, tq, tkv, stream)
-                  : launch<64, true>(p, tq, tkv, stream);
-  else
-    e = N == 16   ? launch<16>(p, tq, tkv, stream)
-        : N == 32 ? launch<32>(p, tq, tkv, stream)
-                  : launch<64>(p, tq, tkv, stream);
+  const cudaError_t e = a.window > 0 ? (gather ? launch<true, true>(N, p, tq, tkv, stream) : launch<false, true>(N, p, tq, tkv, stream))
+                        : gather     ? launch<true, false>(N, p, tq, tkv, stream)
+                                     : launch<false, false>(N, p, tq, tkv, stream);
   if (e != cudaSuccess || !p.merge) return e;
   return launch_paged_merge(a, p.nteams, 2, p.groups * N, nsm, stream);
 }

@@ -156,11 +156,14 @@ class DecodeStep:
     the new token), and reads ``out`` and ``lse``. ``q`` holds rotated rope
     parts after ``run``: refill it before the next step. A slot that holds no
     request has length 0: nothing is appended for it, its page numbers are not
-    read, its query stays as it is, and it gets 0 and -inf."""
+    read, its query stays as it is, and it gets 0 and -inf. With a window, the
+    heads see the last ``window`` positions (the new one among them) and the
+    first ``sinks`` alone."""
 
     def __init__(self, cache, batch, heads, max_pages, rope_table, sm_scale, norm_weight=None,
-                 norm_eps=1e-6, rope_style=abi.ROPE_PAIRS):
+                 norm_eps=1e-6, rope_style=abi.ROPE_PAIRS, window=0, sinks=0):
         dev = cache.device
+        self.window, self.sinks = window, sinks
         self.cache, self.rope_table, self.norm_weight = cache, rope_table, norm_weight
         self.sm_scale, self.norm_eps, self.rope_style = sm_scale, norm_eps, rope_style
         self.latent = torch.zeros(batch, 512, dtype=torch.bfloat16, device=dev)
@@ -182,6 +185,10 @@ class DecodeStep:
                              self.norm_eps, self.rope_style, self.status, stream)
 
     def attend(self, stream=None):
+        if self.window:
+            abi.mla_paged_decode_window(self.q, self.cache, self.block_table, self.kv_lens, self.window, self.sinks,
+                                        self.sm_scale, self.out, self.lse, self.workspace, self.status, stream)
+            return
         abi.mla_paged_decode(self.q, self.cache, self.block_table, self.kv_lens, self.sm_scale, self.out,
                              self.lse, self.workspace, self.status, stream)
 
