@@ -8,14 +8,16 @@
 // order. A value is read once from HBM.
 //
 // Most likely tokens are ordered by value, then by lower place: a key of 64 bits,
-// the value's bits made monotone above the inverted place, says both. A bound
-// that k known keys reach lets nearly all values by with one comparison per 16
-// bytes: it comes from the first chunk (each warp's q-th best thread, q = ceil(k /
-// warps), the least of which at least k values reach), and is raised to the
-// exact k-th key when 1, 2, 4, ... chunks have passed. What reaches it goes into a
-// list; ranks are counted there. Values that keep rising can overflow the
-// list, and NaN are not seen by the comparisons: then the keys are found by a
-// second walk over the row, step by step, for which any content will do.
+// the value's bits made monotone above the inverted place, says both. On the way
+// over the row a thread keeps the largest value of its vectors (of 16 bytes), that
+// vector's place, and the second largest. At the end each warp's q-th best thread (q
+// = ceil(k / warps)) gives a bound: the least of them is reached by at least k
+// values. Threads that reach it look at their vector again; the few whose second
+// does, too, have all theirs looked at again by the whole block. What reaches the
+// bound, about 20 values for k up to 8 and 100 for 32, gets its rank by
+// counting. Where a row holds NaN, which comparisons do not see, or so many equal or
+// grouped values that the list of these overflows, the keys are found by a second
+// walk over the row, step by step, for which any content will do.
 //
 // Few rows are split over clusters of up to 8 CTAs, which join through
 // distributed shared memory: no workspace and no second launch.
@@ -115,23 +117,30 @@ __device__ __forceinline__ float exponent(float x, float ref) {
   return y;
 }
 
-__device__ __forceinline__ void raise(Sums& a, float m) {  // a.m < m
+__device__ __forceinline__ void raise(Sums& a, float m) {  // to a maximum that is not lower
   const float d = exponent(reference(a.m), reference(m)), f = ex2(d);
   a.t = f * fmaf(d, a.s, a.t);
   a.s *= f;
   a.m = m;
-}
-__device__ __forceinline__ void join(Sums& a, Sums b) {
-  if (b.m > a.m) raise(a, b.m);
-  else if (a.m > b.m) raise(b, a.m);
-  a.s += b.s;
-  a.t += b.t;
 }
 __device__ __forceinline__ void add_one(Sums& a, float x) {
   if (x > a.m) raise(a, x);
   const float y = exponent(x, reference(a.m)), e = ex2(y);
   a.s += e;
   a.t = fmaf(e, y, a.t);
+}
+// Of n sums in shared memory, in their order.
+__device__ __forceinline__ Sums join(const Sums* v, int n) {
+  Sums r = {v[0].m, 0.f, 0.f};
+  for (int i = 1; i < n; ++i) r.m = fmaxf(r.m, v[i].m);
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) {
+    Sums u = v[i];
+    raise(u, r.m);
+    r.s += u.s;
+    r.t += u.t;
+  }
+  return r;
 }
 
 struct Shared {
@@ -140,7 +149,8 @@ struct Shared {
   Key parts[kMaxParts * kMaxTop];    // of the row's parts, in the first one's
   Key bound[kWarps];
   Sums sums[kWarps], part_sums[kMaxParts];
-  int count, over;
+  int again[kThreads];                 // threads whose vectors are looked at again
+  int count, agains;
 };
 
 __device__ __forceinline__ Key larger(Key a, Key b) { return a > b ? a : b; }
@@ -170,8 +180,13 @@ __device__ __noinline__ void prune(Shared& sh, int k) {
     const Key key = i < k ? sh.best[i] : sh.list[i - k];
     if (key == 0) continue;
     int r = 0;
+#pragma unroll 4
     for (int j = 0; j < k; ++j) r += sh.best[j] > key;
-    for (int j = 0; j < n && r < k; ++j) r += sh.list[j] > key;
+    for (int j0 = 0; j0 < n && r < k; j0 += 32) {
+      const int j1 = min(j0 + 32, n);
+#pragma unroll 8
+      for (int j = j0; j < j1; ++j) r += sh.list[j] > key;
+    }
     if (r < k) sh.better[r] = key;  // keys are distinct: each rank is one key's
   }
   __syncthreads();
@@ -179,22 +194,23 @@ __device__ __noinline__ void prune(Shared& sh, int k) {
     sh.best[threadIdx.x] = sh.better[threadIdx.x];
     sh.better[threadIdx.x] = 0;
   }
-  if (threadIdx.x == 0) {
-    if (sh.count > kCap) sh.over = 1;
-    sh.count = 0;
-  }
+  if (threadIdx.x == 0) sh.count = 0;
   __syncthreads();
 }
 
-// A bound that at least k of the threads' keys reach: each warp's q-th best.
-__device__ __forceinline__ Key common_bound(Shared& sh, Key k, int q) {
-  const Key w = warp_qth(k, q);
+// A bound that at least k of the threads' keys reach, the first `lanes` of which
+// are there: the least of the q-th best of each warp that is full of them (0
+// where there is none).
+__device__ __forceinline__ Key common_bound(Shared& sh, Key own, int k, int lanes) {
+  const int full = min(lanes / 32, kWarps);
+  if (full == 0) return 0;
+  const Key w = warp_qth(own, (k + full - 1) / full);
   if ((threadIdx.x & 31) == 0) sh.bound[threadIdx.x >> 5] = w;
   __syncthreads();
   Key b = sh.bound[0];
 #pragma unroll
-  for (int i = 1; i < kWarps; ++i) b = b < sh.bound[i] ? b : sh.bound[i];
-  __syncthreads();
+  for (int i = 1; i < kWarps; ++i)
+    if (i < full) b = b < sh.bound[i] ? b : sh.bound[i];
   return b;
 }
 
@@ -212,12 +228,12 @@ struct Share {
 // the best k so far and by the step's own common bound, after which the list
 // holds what is left.
 template <typename T>
-__device__ __noinline__ void find_top(Shared& sh, const Share<T>& p, int k, int q) {
+__device__ __noinline__ void find_top(Shared& sh, const Share<T>& p, int k) {
   constexpr int E = Vec<T>::kN;
   const int tid = threadIdx.x;
   __syncthreads();
-  if (tid < k) sh.best[tid] = 0;
-  if (tid == 0) sh.count = 0, sh.over = 0;
+  if (tid < kMaxTop) sh.best[tid] = sh.better[tid] = 0;
+  if (tid == 0) sh.count = 0;
   __syncthreads();
   if (tid < p.head) push(sh, make_key(Vec<T>::one(p.row[tid]), tid));
   if (tid < p.tail) push(sh, make_key(Vec<T>::one(p.row[p.tail0 + tid]), p.tail0 + tid));
@@ -231,7 +247,7 @@ __device__ __noinline__ void find_top(Shared& sh, const Share<T>& p, int k, int 
 #pragma unroll
       for (int i = 0; i < E; ++i) own = larger(own, make_key(x[i], p.first + v * E + i));
     }
-    const Key b = larger(sh.best[k - 1] + 1, common_bound(sh, own, q));
+    const Key b = larger(sh.best[k - 1] + 1, common_bound(sh, own, k, p.hi - v0));
     if (own >= b && v < p.hi)
 #pragma unroll
       for (int i = 0; i < E; ++i) {
@@ -260,10 +276,12 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t r = blockIdx.x / parts;
   const int part = parts > 1 ? (int)cluster_rank() : 0;
-  const int k = a.top_k, q = (k + kWarps - 1) / kWarps;
-  if (parts > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  if (tid < kMaxTop) sh.best[tid] = 0;
-  if (tid == 0) sh.count = 0, sh.over = 0;
+  const int k = a.top_k;
+  if (tid == 0) sh.count = sh.agains = 0;
+  if (parts > 1) {
+    if (part == 0) sh.parts[tid] = 0;
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();
@@ -290,32 +308,30 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
   if (tid < p.head) ends(tid);
   if (tid < p.tail) ends(p.tail0 + tid);
 
-  float bound = -INFINITY;  // values up to this cannot be among the best
+  float top = -INFINITY, second = -INFINITY;
+  int at = p.lo + tid;
   uint4 next[kUnroll];
   auto load = [&](int v0) {
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i)
-      if (v0 + i * kThreads + tid < p.hi) next[i] = load16(p.vec + v0 + i * kThreads + tid);
+      if (v0 + i * kThreads < p.hi) next[i] = load16(p.vec + v0 + i * kThreads);
   };
-  load(p.lo);
-  int chunk = 0;
-  for (int v0 = p.lo; v0 < p.hi; v0 += kUnroll * kThreads, ++chunk) {
+  load(p.lo + tid);
+  for (int v0 = p.lo + tid; v0 < p.hi; v0 += kUnroll * kThreads) {
     uint4 now[kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) now[i] = next[i];
     load(v0 + kUnroll * kThreads);
-    float top = -INFINITY;
-    int at = 0;
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const int v = v0 + i * kThreads + tid;
-      if (v >= p.hi) break;
+      if (v0 + i * kThreads >= p.hi) break;
       float x[E];
       Vec<T>::unpack(now[i], x);
       float m = x[0];
 #pragma unroll
       for (int j = 1; j < E; ++j) m = fmaxf(m, x[j]);
-      if (m > top || i == 0) top = m, at = v;
+      second = fmaxf(second, fminf(m, top));
+      if (m > top) top = m, at = v0 + i * kThreads;
       if (m > u.m) raise(u, m);
       const float ref = reference(u.m);
 #pragma unroll
@@ -325,77 +341,88 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
         u.t = fmaf(e, y, u.t);
       }
     }
-    if (k == 0) continue;
-    bool some = v0 + tid < p.hi;
-    Key b = 0;
-    if (chunk == 0) {
-      // wherever in its vector the value is, its key is at least that of the last place
-      b = common_bound(sh, some ? make_key(top, p.first + at * E + E - 1) : 0, q);
-      some = some && make_key(top, p.first + at * E) >= b;
-    } else {
-      some = some && top > bound;  // an equal value has a higher place than those that are there
-    }
-    if (some) {
-#pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
-        const int v = v0 + i * kThreads + tid;
-        if (v >= p.hi) break;
-        float x[E];
-        Vec<T>::unpack(now[i], x);
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          const Key key = make_key(x[j], p.first + v * E + j);
-          if (chunk == 0 ? key >= b : x[j] > bound) push(sh, key);
-        }
-      }
-    }
-    if ((chunk & (chunk + 1)) == 0) {
-      prune(sh, k);
-      if (sh.best[k - 1]) bound = value_of(sh.best[k - 1]);
-    }
   }
-  if (k > 0) prune(sh, k);
 
-  // this CTA's sums, in a fixed order
+  // this CTA's sums, in a fixed order, and the bound
+  float m = u.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+  raise(u, m);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    Sums w;
-    w.m = __shfl_xor_sync(kFull, u.m, o);
-    w.s = __shfl_xor_sync(kFull, u.s, o);
-    w.t = __shfl_xor_sync(kFull, u.t, o);
-    join(u, w);
+    u.s += __shfl_xor_sync(kFull, u.s, o);
+    u.t += __shfl_xor_sync(kFull, u.t, o);
   }
   if (lane == 0) sh.sums[warp] = u;
+  const bool some = p.lo + tid < p.hi;
+  // wherever in its vector the value is, its key is at least that of the last place
+  Key b = 0;
+  if (k > 0) b = common_bound(sh, some ? make_key(top, p.first + at * E + E - 1) : 0, k, p.hi - p.lo);
   __syncthreads();
-  u = sh.sums[0];
-#pragma unroll
-  for (int i = 1; i < kWarps; ++i) join(u, sh.sums[i]);
-  if (k > 0 && (u.s != u.s || sh.over)) find_top<T>(sh, p, k, q);
+  u = join(sh.sums, kWarps);
 
-  Key key = tid < k ? sh.best[tid] : 0;  // of rank tid
-  int rank = tid;
+  int n = 0;                           // keys in the list
+  bool sorted = false;                 // or k in best
+  if (k > 0) {
+    auto look = [&](int v) {
+      float x[E];
+      Vec<T>::unpack(load16(p.vec + v), x);
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const Key key = make_key(x[j], p.first + v * E + j);
+        if (key >= b) push(sh, key);
+      }
+    };
+    if (some && make_key(top, p.first + at * E) >= b) {
+      if (b && second >= value_of(b)) sh.again[atomicAdd(&sh.agains, 1)] = tid;
+      else look(at);
+    }
+    __syncthreads();
+    const int each = (p.hi - p.lo + kThreads - 1) / kThreads, items = sh.agains * each;
+    for (int i = tid; i < items; i += kThreads) {
+      const int v = p.lo + sh.again[i / each] + i % each * kThreads;
+      if (v < p.hi) look(v);
+    }
+    if (items) __syncthreads();
+    n = sh.count;
+    if (n > kCap || u.s != u.s) {
+      find_top<T>(sh, p, k);
+      n = k;
+      sorted = true;
+    }
+  }
+  auto rank_of = [&](Key key) {
+    int r = 0;
+    for (int j0 = 0; j0 < n && r < k; j0 += 32) {
+      const int j1 = min(j0 + 32, n);
+#pragma unroll 8
+      for (int j = j0; j < j1; ++j) r += sh.list[j] > key;
+    }
+    return r;
+  };
+
+  Key key = 0;
+  int rank = k;
   if (parts > 1) {
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // the first CTA runs
-    const uint32_t to = in_first(&sh.parts[part * kMaxTop + tid]), sums = in_first(&sh.part_sums[part]);
-    if (tid < k) asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(key) : "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // the first CTA runs
+    for (int i = tid; i < n; i += kThreads) {
+      key = sorted ? sh.best[i] : sh.list[i];
+      rank = sorted ? i : rank_of(key);
+      if (rank < k)
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(in_first(&sh.parts[part * kMaxTop + rank])), "l"(key) : "memory");
+    }
     if (tid == 0) {
+      const uint32_t sums = in_first(&sh.part_sums[part]);
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(sums), "f"(u.m) : "memory");
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(sums + 4), "f"(u.s) : "memory");
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(sums + 8), "f"(u.t) : "memory");
     }
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (part != 0) return;
-    u = sh.part_sums[0];
-    for (int i = 1; i < parts; ++i) join(u, sh.part_sums[i]);
-    key = 0;
-    rank = k;
-    if ((tid & (kMaxTop - 1)) < k && tid < parts * kMaxTop) {
-      key = sh.parts[tid];
-      rank = 0;
-      for (int i = 0; i < parts; ++i)
-        for (int j = 0; j < k; ++j) rank += sh.parts[i * kMaxTop + j] > key;
-    }
+    u = join(sh.part_sums, parts);
+    sorted = false;
   }
 
   const bool none = u.m == -INFINITY && u.s == u.s;
@@ -407,9 +434,25 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
       a.entropy[r] = h < 0.f ? 0.f : h;
     }
   }
-  if (key && rank < k) {
+  auto put = [&](int rank, Key key) {
+    if (!key || rank >= k) return;
     a.top_ids[r * k + rank] = place_of(key);
     if (a.top_logprobs) a.top_logprobs[r * k + rank] = none ? -INFINITY : value_of(key) - lse;
+  };
+  if (parts > 1) {
+    if (tid < parts * kMaxTop && (tid & (kMaxTop - 1)) < k) {
+      key = sh.parts[tid];
+      rank = 0;
+      for (int i = 0; i < parts; ++i)
+#pragma unroll 4
+        for (int j = 0; j < k; ++j) rank += sh.parts[i * kMaxTop + j] > key;
+      put(rank, key);
+    }
+  } else {
+    for (int i = tid; i < n; i += kThreads) {
+      key = sorted ? sh.best[i] : sh.list[i];
+      put(sorted ? i : rank_of(key), key);
+    }
   }
   for (int g = tid; g < a.per_row; g += kThreads) {
     const int token = a.tokens[r * a.token_stride + g];
