@@ -481,13 +481,12 @@ int mla_token_logprobs(const void* logits, int logits_type, int64_t row_stride, 
   if (rows < 0 || vocab < 1 || tokens_per_row < 0 || top_k < 0 || top_k > vocab) return MT_EINVAL;
   if (row_stride < 0 || (rows > 1 && row_stride > INT64_MAX / 8 / rows)) return MT_EINVAL;
   if (token_stride < 0 || (rows > 1 && token_stride > INT64_MAX / 8 / rows)) return MT_EINVAL;
-  if (tokens_per_row > 0 ? !tokens || !logprobs : tokens || logprobs) return MT_EINVAL;
-  if (top_k > 0 ? !top_ids : top_ids || top_logprobs) return MT_EINVAL;
   if (top_k > MT_MAX_TOP) return MT_EUNSUPPORTED;
   if (rows == 0) return MT_OK;
+  if (tokens_per_row > 0 ? !tokens || !logprobs : tokens || logprobs) return MT_EINVAL;
+  if (top_k > 0 ? !top_ids : top_ids || top_logprobs) return MT_EINVAL;
   if (!logits || (uintptr_t)logits % size) return MT_EINVAL;
   const int nsm = sm_count();
-  if ((int64_t)rows * logprob_parts(rows, vocab, nsm) > INT32_MAX) return MT_EUNSUPPORTED;
   LogprobArgs a;
   a.logits = logits;
   a.row_stride = row_stride;

@@ -19,7 +19,6 @@ struct LogprobArgs {
   float* top_logprobs;          // [rows, top_k] or nullptr
   int32_t* status;
 };
-int logprob_parts(int rows, int vocab, int num_sms);  // CTAs that share a row
 cudaError_t launch_token_logprobs(const LogprobArgs& a, int logits_type, int num_sms, cudaStream_t stream);
 
 }  // namespace mt

@@ -32,12 +32,11 @@
 namespace mt {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;            // 16-byte loads of a chunk a thread
+// 16-byte loads of a chunk a thread, one chunk ahead (2048 rows of 131072 bf16 values: 2
+// take 111 us, 4 98, 8 99; 256 rows of 100003 fp32 values 29, 26, 32)
+constexpr int kUnroll = 4;
 constexpr int kMaxTop = MT_MAX_TOP;   // 32
 constexpr int kMaxParts = 8;
-constexpr int kCap = 2048 + 16;       // one step's values of 16 bits, and the ends
 constexpr unsigned kFull = 0xffffffffu;
 
 typedef unsigned long long Key;
@@ -55,21 +54,72 @@ __device__ __forceinline__ float value_of(Key k) {
 __device__ __forceinline__ Key make_key(float x, uint32_t place) { return (Key)ordered(x) << 32 | (uint32_t)~place; }
 __device__ __forceinline__ int place_of(Key k) { return (int)~(uint32_t)k; }
 
+// Two fp32 numbers, for instructions on both.
+typedef unsigned long long Pair;
+__device__ __forceinline__ Pair pair(float x, float y) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 halves(Pair p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Values by 16 bytes. raised(): as fp32, none below kFloor (so that exp's
+// argument is finite); largest(): ignores NaN. Rows whose maximum is below
+// kLow, where kFloor would count, are summed another way.
 template <typename T>
 struct Vec;
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int kN = 8;
+  static constexpr float kFloor = -0x1.2cp+126f, kLow = -0.9e38f;  // 0xfe96, about -1e38
   static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[2 * i] = bf16_lo(w[i]), x[2 * i + 1] = bf16_hi(w[i]);
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ float largest(const uint4& u) {
+    const uint32_t m = max2(max2(u.x, u.y), max2(u.z, u.w));
+    return fmaxf(bf16_lo(m), bf16_hi(m));
+  }
+  static __device__ __forceinline__ void raised(const uint4& u, Pair (&x)[4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t r;  // NaN stays NaN
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w[i]), "r"(0xfe96fe96u));
+      x[i] = pair(bf16_lo(r), bf16_hi(r));
+    }
   }
   static __device__ __forceinline__ float one(__nv_bfloat16 v) { return __bfloat162float(v); }
 };
 template <>
 struct Vec<__half> {
   static constexpr int kN = 8;
+  static constexpr float kFloor = -65504.f, kLow = -65000.f;
   static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -78,13 +128,46 @@ struct Vec<__half> {
       x[2 * i] = f.x, x[2 * i + 1] = f.y;
     }
   }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ float largest(const uint4& u) {
+    const uint32_t m = max2(max2(u.x, u.y), max2(u.z, u.w));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+    return fmaxf(f.x, f.y);
+  }
+  static __device__ __forceinline__ void raised(const uint4& u, Pair (&x)[4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t r;  // 0xfbff: -65504
+      asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(w[i]), "r"(0xfbfffbffu));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r));
+      x[i] = pair(f.x, f.y);
+    }
+  }
   static __device__ __forceinline__ float one(__half v) { return __half2float(v); }
 };
 template <>
 struct Vec<float> {
   static constexpr int kN = 4;
+  static constexpr float kFloor = -1e38f, kLow = -0.9e38f;
   static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[4]) {
     x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
+  }
+  static __device__ __forceinline__ float largest(const uint4& u) {
+    float x[4];
+    unpack(u, x);
+    return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+  }
+  static __device__ __forceinline__ void raised(const uint4& u, Pair (&x)[2]) {
+    float v[4];
+    unpack(u, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("max.NaN.f32 %0, %1, %2;" : "=f"(v[i]) : "f"(v[i]), "f"(kFloor));
+    x[0] = pair(v[0], v[1]), x[1] = pair(v[2], v[3]);
   }
   static __device__ __forceinline__ float one(float v) { return v; }
 };
@@ -129,24 +212,42 @@ __device__ __forceinline__ void add_one(Sums& a, float x) {
   a.s += e;
   a.t = fmaf(e, y, a.t);
 }
-// Of n sums in shared memory, in their order.
-__device__ __forceinline__ Sums join(const Sums* v, int n) {
-  Sums r = {v[0].m, 0.f, 0.f};
-  for (int i = 1; i < n; ++i) r.m = fmaxf(r.m, v[i].m);
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) {
-    Sums u = v[i];
-    raise(u, r.m);
-    r.s += u.s;
-    r.t += u.t;
+__device__ __forceinline__ Sums warp_sums(Sums a) {
+  float m = a.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+  raise(a, m);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a.s += __shfl_xor_sync(kFull, a.s, o);
+    a.t += __shfl_xor_sync(kFull, a.t, o);
   }
-  return r;
+  return a;
+}
+// Of n <= 8 sums in shared memory; all lanes of a warp, eight of which have one each.
+__device__ __forceinline__ Sums join(const Sums* v, int n) {
+  const int i = threadIdx.x & 7;
+  Sums a = {-INFINITY, 0.f, 0.f};
+  if (i < n) a = v[i];
+  float m = a.m;
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+  raise(a, m);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) {
+    a.s += __shfl_xor_sync(kFull, a.s, o);
+    a.t += __shfl_xor_sync(kFull, a.t, o);
+  }
+  return a;
 }
 
+template <int kThreads>
 struct Shared {
+  static constexpr int kWarps = kThreads / 32;
+  static constexpr int kCap = kThreads * 8 + 16;  // one vector of 16-bit values a thread, and the ends
   Key list[kCap];
   Key best[kMaxTop], better[kMaxTop];  // the k best so far, in order (0: none); 0, but for prune
-  Key parts[kMaxParts * kMaxTop];    // of the row's parts, in the first one's
+  Key parts[kMaxParts][kMaxTop];    // of the row's parts, in the first one's
   Key bound[kWarps];
   Sums sums[kWarps], part_sums[kMaxParts];
   int again[kThreads];                 // threads whose vectors are looked at again
@@ -167,15 +268,17 @@ __device__ __forceinline__ Key warp_qth(Key k, int q) {
   return r;
 }
 
-__device__ __forceinline__ void push(Shared& sh, Key k) {
+template <int kThreads>
+__device__ __forceinline__ void push(Shared<kThreads>& sh, Key k) {
   const int at = atomicAdd(&sh.count, 1);
-  if (at < kCap) sh.list[at] = k;
+  if (at < sh.kCap) sh.list[at] = k;
 }
 
 // The k best of best and list become best; the list is empty then. All threads.
-__device__ __noinline__ void prune(Shared& sh, int k) {
+template <int kThreads>
+__device__ __noinline__ void prune(Shared<kThreads>& sh, int k) {
   __syncthreads();
-  const int n = min(sh.count, kCap);
+  const int n = min(sh.count, sh.kCap);
   for (int i = threadIdx.x; i < n + k; i += kThreads) {
     const Key key = i < k ? sh.best[i] : sh.list[i - k];
     if (key == 0) continue;
@@ -199,17 +302,23 @@ __device__ __noinline__ void prune(Shared& sh, int k) {
 }
 
 // A bound that at least k of the threads' keys reach, the first `lanes` of which
-// are there: the least of the q-th best of each warp that is full of them (0
-// where there is none).
-__device__ __forceinline__ Key common_bound(Shared& sh, Key own, int k, int lanes) {
-  const int full = min(lanes / 32, kWarps);
-  if (full == 0) return 0;
+// are there: the least of the q-th best of each warp that is full of them, or of
+// the first warp's (0 where they are fewer than k). warp_bound leaves its warp's
+// for common_bound, a barrier later.
+template <int kThreads>
+__device__ __forceinline__ int bound_warps(int lanes) { return max(1, min(lanes / 32, kThreads / 32)); }
+template <int kThreads>
+__device__ __forceinline__ void warp_bound(Shared<kThreads>& sh, Key own, int k, int lanes) {
+  const int full = bound_warps<kThreads>(lanes);
   const Key w = warp_qth(own, (k + full - 1) / full);
   if ((threadIdx.x & 31) == 0) sh.bound[threadIdx.x >> 5] = w;
-  __syncthreads();
+}
+template <int kThreads>
+__device__ __forceinline__ Key common_bound(const Shared<kThreads>& sh, int lanes) {
+  const int full = bound_warps<kThreads>(lanes);
   Key b = sh.bound[0];
 #pragma unroll
-  for (int i = 1; i < kWarps; ++i)
+  for (int i = 1; i < kThreads / 32; ++i)
     if (i < full) b = b < sh.bound[i] ? b : sh.bound[i];
   return b;
 }
@@ -227,8 +336,8 @@ struct Share {
 // The keys of a row of any content: one vector a thread at a time, bounded by
 // the best k so far and by the step's own common bound, after which the list
 // holds what is left.
-template <typename T>
-__device__ __noinline__ void find_top(Shared& sh, const Share<T>& p, int k) {
+template <typename T, int kThreads>
+__device__ __noinline__ void find_top(Shared<kThreads>& sh, const Share<T>& p, int k) {
   constexpr int E = Vec<T>::kN;
   const int tid = threadIdx.x;
   __syncthreads();
@@ -247,7 +356,9 @@ __device__ __noinline__ void find_top(Shared& sh, const Share<T>& p, int k) {
 #pragma unroll
       for (int i = 0; i < E; ++i) own = larger(own, make_key(x[i], p.first + v * E + i));
     }
-    const Key b = larger(sh.best[k - 1] + 1, common_bound(sh, own, k, p.hi - v0));
+    warp_bound(sh, own, k, p.hi - v0);
+    __syncthreads();
+    const Key b = larger(sh.best[k - 1] + 1, common_bound(sh, p.hi - v0));
     if (own >= b && v < p.hi)
 #pragma unroll
       for (int i = 0; i < E; ++i) {
@@ -256,6 +367,27 @@ __device__ __noinline__ void find_top(Shared& sh, const Share<T>& p, int k) {
       }
   }
   prune(sh, k);
+}
+
+// The sums of a share of any content, by every value's distance from a maximum that may be anything.
+template <typename T, int kThreads>
+__device__ __noinline__ Sums careful_sums(Shared<kThreads>& sh, const Share<T>& p) {
+  constexpr int E = Vec<T>::kN;
+  const int tid = threadIdx.x;
+  Sums u = {-INFINITY, 0.f, 0.f};
+  if (tid < p.head) add_one(u, Vec<T>::one(p.row[tid]));
+  if (tid < p.tail) add_one(u, Vec<T>::one(p.row[p.tail0 + tid]));
+  for (int v = p.lo + tid; v < p.hi; v += kThreads) {
+    float x[E];
+    Vec<T>::unpack(load16(p.vec + v), x);
+#pragma unroll 1
+    for (int j = 0; j < E; ++j) add_one(u, x[j]);
+  }
+  u = warp_sums(u);
+  __syncthreads();
+  if ((tid & 31) == 0) sh.sums[tid >> 5] = u;
+  __syncthreads();
+  return join(sh.sums, kThreads / 32);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -269,17 +401,17 @@ __device__ __forceinline__ uint32_t in_first(const void* p) {  // its place in t
   return r;
 }
 
-template <typename T>
+template <typename T, int kThreads>
 __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobArgs a, const int parts) {
-  constexpr int E = Vec<T>::kN;
-  __shared__ Shared sh;
+  constexpr int E = Vec<T>::kN, kWarps = kThreads / 32;
+  __shared__ Shared<kThreads> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t r = blockIdx.x / parts;
   const int part = parts > 1 ? (int)cluster_rank() : 0;
   const int k = a.top_k;
   if (tid == 0) sh.count = sh.agains = 0;
   if (parts > 1) {
-    if (part == 0) sh.parts[tid] = 0;
+    for (int i = tid; part == 0 && i < kMaxParts * kMaxTop; i += kThreads) sh.parts[0][i] = 0;
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -299,6 +431,17 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
   p.first = head;
   p.head = part == 0 ? head : 0;
 
+  // the given tokens' values are asked for ahead of the row
+  auto value_at = [&](int g, bool& there) {
+    const int token = __ldg(a.tokens + r * a.token_stride + g);
+    there = token >= 0 && token < a.vocab;
+    if (there) return Vec<T>::one(p.row[token]);
+    if (token != -1) flag(a.status, MT_DEV_BAD_TOKEN);
+    return 0.f;
+  };
+  bool asked = false;
+  const float given = part == 0 && tid < a.per_row ? value_at(tid, asked) : 0.f;
+
   Sums u = {-INFINITY, 0.f, 0.f};
   auto ends = [&](int place) {
     const float x = Vec<T>::one(p.row[place]);
@@ -309,6 +452,8 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
   if (tid < p.tail) ends(p.tail0 + tid);
 
   float top = -INFINITY, second = -INFINITY;
+  Pair s2 = 0, t2 = 0, neg = pair(-Vec<T>::kFloor, -Vec<T>::kFloor);
+  const Pair log2e = pair(kLog2e, kLog2e);
   int at = p.lo + tid;
   uint4 next[kUnroll];
   auto load = [&](int v0) {
@@ -325,56 +470,70 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
       if (v0 + i * kThreads >= p.hi) break;
-      float x[E];
-      Vec<T>::unpack(now[i], x);
-      float m = x[0];
-#pragma unroll
-      for (int j = 1; j < E; ++j) m = fmaxf(m, x[j]);
+      const float m = Vec<T>::largest(now[i]);
       second = fmaxf(second, fminf(m, top));
-      if (m > top) top = m, at = v0 + i * kThreads;
-      if (m > u.m) raise(u, m);
-      const float ref = reference(u.m);
+      if (m > top) {
+        // sums in pairs, relative to the largest so far (not below the floor)
+        const float ref = fmaxf(m, Vec<T>::kFloor), d = fmaxf((fmaxf(top, Vec<T>::kFloor) - ref) * kLog2e, -1e4f);
+        const Pair d2 = pair(d, d), f2 = pair(ex2(d), ex2(d));
+        t2 = mul2(f2, fma2(d2, s2, t2));
+        s2 = mul2(f2, s2);
+        neg = pair(-ref, -ref);
+        top = m, at = v0 + i * kThreads;
+      }
+      Pair x[E / 2];
+      Vec<T>::raised(now[i], x);
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const float y = exponent(x[j], ref), e = ex2(y);
-        u.s += e;
-        u.t = fmaf(e, y, u.t);
+      for (int j = 0; j < E / 2; ++j) {
+        const Pair y = mul2(add2(x[j], neg), log2e);
+        const float2 h = halves(y);
+        const Pair e = pair(ex2(h.x), ex2(h.y));
+        s2 = add2(s2, e);
+        t2 = fma2(e, y, t2);
       }
     }
   }
 
   // this CTA's sums, in a fixed order, and the bound
-  float m = u.m;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-  raise(u, m);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    u.s += __shfl_xor_sync(kFull, u.s, o);
-    u.t += __shfl_xor_sync(kFull, u.t, o);
+  {
+    const float2 hs = halves(s2), ht = halves(t2);
+    Sums w = {top, hs.x + hs.y, ht.x + ht.y};
+    if (top == -INFINITY && w.s == w.s) w.s = w.t = 0.f;  // counted as the floor
+    const float m = fmaxf(u.m, w.m);
+    raise(u, m);
+    raise(w, m);
+    u.s += w.s;
+    u.t += w.t;
+    u = warp_sums(u);
   }
   if (lane == 0) sh.sums[warp] = u;
   const bool some = p.lo + tid < p.hi;
   // wherever in its vector the value is, its key is at least that of the last place
-  Key b = 0;
-  if (k > 0) b = common_bound(sh, some ? make_key(top, p.first + at * E + E - 1) : 0, k, p.hi - p.lo);
+  if (k > 0) warp_bound(sh, some ? make_key(top, p.first + at * E + E - 1) : 0, k, p.hi - p.lo);
   __syncthreads();
   u = join(sh.sums, kWarps);
+  const Key b = k > 0 ? common_bound(sh, p.hi - p.lo) : 0;
+  const bool odd = u.s != u.s || u.t != u.t;  // NaN, +inf, or a maximum that differences from are infinite
+  if (odd || (u.m < Vec<T>::kLow && u.m > -INFINITY)) u = careful_sums<T, kThreads>(sh, p);
 
   int n = 0;                           // keys in the list
   bool sorted = false;                 // or k in best
   if (k > 0) {
+    const float least = b ? value_of(b) : -INFINITY;
     auto look = [&](int v) {
       float x[E];
       Vec<T>::unpack(load16(p.vec + v), x);
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const Key key = make_key(x[j], p.first + v * E + j);
-        if (key >= b) push(sh, key);
-      }
+      for (int j = 0; j < E; ++j)
+        if (x[j] >= least) {
+          const Key key = make_key(x[j], p.first + v * E + j);
+          if (key >= b) push(sh, key);
+        }
     };
     if (some && make_key(top, p.first + at * E) >= b) {
-      if (b && second >= value_of(b)) sh.again[atomicAdd(&sh.agains, 1)] = tid;
+      // the second value where it equals the first comes behind it
+      const bool behind = second == least && top == least && p.first + (int64_t)(at + kThreads) * E > place_of(b);
+      if (b && second >= least && !behind) sh.again[atomicAdd(&sh.agains, 1)] = tid;
       else look(at);
     }
     __syncthreads();
@@ -385,8 +544,8 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
     }
     if (items) __syncthreads();
     n = sh.count;
-    if (n > kCap || u.s != u.s) {
-      find_top<T>(sh, p, k);
+    if (n > sh.kCap || odd) {
+      find_top<T, kThreads>(sh, p, k);
       n = k;
       sorted = true;
     }
@@ -409,7 +568,7 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
       key = sorted ? sh.best[i] : sh.list[i];
       rank = sorted ? i : rank_of(key);
       if (rank < k)
-        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(in_first(&sh.parts[part * kMaxTop + rank])), "l"(key) : "memory");
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(in_first(&sh.parts[part][rank])), "l"(key) : "memory");
     }
     if (tid == 0) {
       const uint32_t sums = in_first(&sh.part_sums[part]);
@@ -440,12 +599,13 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
     if (a.top_logprobs) a.top_logprobs[r * k + rank] = none ? -INFINITY : value_of(key) - lse;
   };
   if (parts > 1) {
-    if (tid < parts * kMaxTop && (tid & (kMaxTop - 1)) < k) {
-      key = sh.parts[tid];
+    for (int t = tid; t < parts * kMaxTop; t += kThreads) {
+      if (t % kMaxTop >= k) continue;
+      key = sh.parts[t / kMaxTop][t % kMaxTop];
       rank = 0;
       for (int i = 0; i < parts; ++i)
 #pragma unroll 4
-        for (int j = 0; j < k; ++j) rank += sh.parts[i * kMaxTop + j] > key;
+        for (int j = 0; j < k; ++j) rank += sh.parts[i][j] > key;
       put(rank, key);
     }
   } else {
@@ -455,18 +615,12 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
     }
   }
   for (int g = tid; g < a.per_row; g += kThreads) {
-    const int token = a.tokens[r * a.token_stride + g];
-    float lp = -INFINITY;
-    if (token >= 0 && token < a.vocab) {
-      if (!none) lp = Vec<T>::one(p.row[token]) - lse;
-    } else if (token != -1) {
-      flag(a.status, MT_DEV_BAD_TOKEN);
-    }
-    a.logprobs[r * a.per_row + g] = lp;
+    const float x = g == tid ? given : value_at(g, asked);
+    a.logprobs[r * a.per_row + g] = none || !asked ? -INFINITY : x - lse;
   }
 }
 
-template <typename T>
+template <typename T, int kThreads>
 cudaError_t launch(const LogprobArgs& a, int parts, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)a.rows * parts));
@@ -478,24 +632,46 @@ cudaError_t launch(const LogprobArgs& a, int parts, cudaStream_t stream) {
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim = {(unsigned)parts, 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T>, a, parts);
+  cfg.numAttrs = parts > 1 ? 2 : 1;  // clusters of one start more slowly than plain blocks
+  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, kThreads>, a, parts);
+}
+
+// CTAs of a row: up to two an SM of at least 4096 values (128 rows of 131072 bf16
+// values: 2 parts 14.5 us, 1 15.6, 4 15.7, 8 22.2), or four of 160 KB (256 rows of
+// 100003 fp32 values: 2 parts 26.3, 1 29.1; 256 of 131072 bf16 values, 128 KB each
+// in 2 parts: 22.0, 1 20.5).
+int parts_of(int rows, int vocab, int size, int num_sms) {
+  int parts = 1;
+  while (parts < kMaxParts) {
+    const int64_t blocks = 2LL * parts * rows, values = vocab / (2 * parts);
+    if (!(blocks <= 2LL * num_sms && values >= 4096) && !(blocks <= 4LL * num_sms && values * size >= 160000)) break;
+    parts *= 2;
+  }
+  return parts;
+}
+
+template <typename T>
+cudaError_t launch(const LogprobArgs& a, int num_sms, cudaStream_t stream) {
+  // Blocks that all fit at once have 256 threads, for the time of one row; where
+  // they follow one another the work of its end counts, which goes by the warp (2048 rows of
+  // 131072 bf16 values: 256 threads 101 us, 128 98, 64 113; 8192 of 32000: 134, 108, 101;
+  // 8192 of 4000: 77, 43, 31; but 32 rows of 131072 in 4 parts: 9.1, 10.5, 15.8).
+  const int parts = parts_of(a.rows, a.vocab, sizeof(T), num_sms);
+  // For more than 8 alternatives few warps give a low bound (2048 rows, 32 of them: 256
+  // threads 116 us, 128 128).
+  const bool follow = (int64_t)a.rows * parts > 4LL * num_sms, small = a.vocab * sizeof(T) <= 65536, few = a.top_k <= 8;
+  if (follow && small && few) return launch<T, 64>(a, parts, stream);
+  if (follow && (small || few)) return launch<T, 128>(a, parts, stream);
+  return launch<T, 256>(a, parts, stream);
 }
 
 }  // namespace
 
-int logprob_parts(int rows, int vocab, int num_sms) {
-  const int64_t room = 4LL * (num_sms > 0 ? num_sms : 152);
-  int parts = 1;
-  while (parts < kMaxParts && 2LL * parts * rows <= room && vocab / (2 * parts) >= 4096) parts *= 2;
-  return parts;
-}
-
 cudaError_t launch_token_logprobs(const LogprobArgs& a, int logits_type, int num_sms, cudaStream_t stream) {
-  const int parts = logprob_parts(a.rows, a.vocab, num_sms);
-  return logits_type == MT_LOGITS_BF16   ? launch<__nv_bfloat16>(a, parts, stream)
-         : logits_type == MT_LOGITS_FP16 ? launch<__half>(a, parts, stream)
-                                         : launch<float>(a, parts, stream);
+  if (num_sms <= 0) num_sms = 152;
+  return logits_type == MT_LOGITS_BF16   ? launch<__nv_bfloat16>(a, num_sms, stream)
+         : logits_type == MT_LOGITS_FP16 ? launch<__half>(a, num_sms, stream)
+                                         : launch<float>(a, num_sms, stream);
 }
 
 }  // namespace mt
