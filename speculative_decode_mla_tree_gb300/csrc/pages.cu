@@ -122,7 +122,7 @@ __device__ __forceinline__ int block_scan(FitShared& sh, int v, int* total) {
 // What a call asks of one request.
 struct Wish {
   int len, held, need;          // need: columns behind the call
-  int w0;                       // first column that is written to
+  int w0, w1;                   // columns that are written to
   int gap0, gap1;               // columns between the first tokens and the window
   int32_t* row;
   bool ok;
@@ -136,6 +136,7 @@ __device__ __forceinline__ Wish wish_of(const FitArgs& a, int b) {
   w.ok = w.len >= 0 && want >= 0 && want <= (int64_t)a.max_pages * a.page_size && w.held >= 0 && w.held <= a.max_pages;
   w.need = (int)(((int64_t)want + a.page_size - 1) / a.page_size);
   w.w0 = w.len / a.page_size;
+  w.w1 = want > w.len ? w.need : w.w0;
   w.gap0 = w.gap1 = 0;
   if (a.window > 0 && (int64_t)w.len + 1 > a.window) {
     w.gap0 = (int)(((int64_t)a.sinks + a.page_size - 1) / a.page_size);
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(kFitThreads) pages_fit_kernel(const FitArgs a)
       if (lane == 0) flag(a.status, MT_DEV_BAD_INDPTR);
       continue;
     }
-    for (int c = w.w0 + lane; c < min(w.need, w.held); c += 32) {
+    for (int c = w.w0 + lane; c < min(w.w1, w.held); c += 32) {
       const int p = w.row[c];
       if (known(p)) {
         if (__ldcg(a.refs + p) > 1) w.row[c] = -2 - p;
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(kFitThreads) pages_fit_kernel(const FitArgs a)
   for (int b = first; b < a.batch; b += warps) {
     const Wish w = wish_of(a, b);
     if (!w.ok) continue;
-    for (int c = w.w0 + lane; c < min(w.need, w.held); c += 32)
+    for (int c = w.w0 + lane; c < min(w.w1, w.held); c += 32)
       if (w.row[c] < -1) atomicSub(a.refs + (-2 - w.row[c]), 1);
     given_back(a, w, lane, [&](int, int p) {
       if (known(p)) atomicSub(a.refs + p, 1);
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(kFitThreads) pages_fit_kernel(const FitArgs a)
   for (int b = first; b < a.batch; b += warps) {
     const Wish w = wish_of(a, b);
     if (!w.ok) continue;
-    for (int c = w.w0 + lane; c < min(w.need, w.held); c += 32)
+    for (int c = w.w0 + lane; c < min(w.w1, w.held); c += 32)
       if (w.row[c] < -1 && __ldcg(a.refs + (-2 - w.row[c])) <= 0) atomicMin(a.refs + (-2 - w.row[c]), kClaim + b);
   }
   all();
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(kFitThreads) pages_fit_kernel(const FitArgs a)
     const Wish w = wish_of(a, b);
     int need = 0;
     if (w.ok)
-      for (int c = w.w0 + lane; c < w.need; c += 32) {
+      for (int c = w.w0 + lane; c < w.w1; c += 32) {
         int p = c < w.held ? w.row[c] : -1;
         if (p < -1 && __ldcg(a.refs + (-2 - p)) == kClaim + b) {  // keeps it: nobody else finds itself there
           p = -2 - p;
@@ -270,7 +271,7 @@ __global__ void __launch_bounds__(kFitThreads) pages_fit_kernel(const FitArgs a)
     const Wish w = wish_of(a, b);
     int copy[3] = {-1, -1, 0};
     if (w.ok && !enough) {
-      for (int c = w.w0 + lane; c < min(w.need, w.held); c += 32)
+      for (int c = w.w0 + lane; c < min(w.w1, w.held); c += 32)
         if (w.row[c] < -1) {
           const int p = -2 - w.row[c];
           w.row[c] = p;
@@ -281,12 +282,12 @@ __global__ void __launch_bounds__(kFitThreads) pages_fit_kernel(const FitArgs a)
       });
     } else if (w.ok) {
       given_back(a, w, lane, [&](int c, int) { w.row[c] = -1; });
-      for (int c = w.held + lane; c < min(w.w0, w.need); c += 32) w.row[c] = -1;
+      for (int c = w.held + lane; c < (w.w1 > w.w0 ? w.w0 : w.need); c += 32) w.row[c] = -1;
       int at = __ldcg(before + b);
-      for (int c0 = w.w0; c0 < w.need; c0 += 32) {
+      for (int c0 = w.w0; c0 < w.w1; c0 += 32) {
         const int c = c0 + lane;
-        const int p = c < w.held && c < w.need ? w.row[c] : -1;
-        const bool take = c < w.need && p < 0;
+        const int p = c < w.held && c < w.w1 ? w.row[c] : -1;
+        const bool take = c < w.w1 && p < 0;
         const unsigned m = __ballot_sync(kFull, take);
         if (take) {
           const int page = __ldcg(frees + at + __popc(m & ((1u << lane) - 1)));

@@ -2,7 +2,8 @@
 verify step: draft-KV scatter, KV index marshaling, tree-mask packing and
 tree-verify attention (``VerifyStep``); and those of one plain decoding step
 over a paged cache: append with rotation and single-token attention
-(``DecodeStep``). Buffers are allocated once, so a step can be replayed or
+(``DecodeStep``). What follows a verify step over such a cache
+(``AcceptStep``), and the pages that branches share (``Pages``). Buffers are allocated once, so a step can be replayed or
 captured into a CUDA graph; refilling the input buffers in place (``load``)
 gives a new step of the same shape."""
 from __future__ import annotations
@@ -195,3 +196,103 @@ class DecodeStep:
     def run(self, stream=None):
         self.append(stream)
         self.attend(stream)
+
+
+class AcceptStep:
+    """What follows a verify step over a paged cache whose draft rows were
+    appended (mla_paged_append with positions, the rows of a tree one after
+    another): the logits of the trees' nodes say which nodes stay, and their
+    rows move up behind the prefix, in every layer.
+
+    cache is [num_pages, page_size, 576], or [layers, num_pages, page_size, 576]
+    for all layers at once. A program fills ``logits`` [T, vocab] (node after
+    node), ``parents`` and ``tokens`` [T], ``first`` [B] (the token that the
+    prefix wants: that of node 0 where a tree has one root), keeps
+    ``block_table`` and ``kv_lens`` (lengths with the drafts), and reads
+    ``counts``, ``path``, ``next_tokens``, and for every node ``top_ids`` and
+    ``top_logprobs`` [T, top_k], ``lse`` and ``entropy``. ``kv_lens`` holds the
+    new lengths after ``run``. Where ``targets`` [T] is given, the walk follows it
+    (tokens drawn from the logits, say) instead of the most likely tokens."""
+
+    def __init__(self, cache, tree_sizes, max_pages, vocab, max_accept=None, top_k=1, dtype=torch.bfloat16, targets=None):
+        dev = cache.device
+        batch, total = len(tree_sizes), sum(tree_sizes)
+        most = max(tree_sizes) if max_accept is None else max_accept
+        ints = lambda *n: torch.zeros(n, dtype=torch.int32, device=dev)  # noqa: E731
+        self.cache = cache
+        self.qo_indptr = torch.tensor([0] + list(tree_sizes), device=dev).cumsum(0).to(torch.int32)
+        self.logits = torch.zeros(total, vocab, dtype=dtype, device=dev)
+        self.parents, self.tokens, self.first, self.kv_lens = ints(total), ints(total), ints(batch), ints(batch)
+        self.block_table = ints(batch, max_pages)
+        self.path, self.counts, self.next_tokens = ints(batch, most), ints(batch), ints(batch)
+        self.top_ids, self.top_logprobs = ints(total, top_k), torch.zeros(total, top_k, device=dev)
+        self.lse, self.entropy = torch.zeros(total, device=dev), torch.zeros(total, device=dev)
+        self.targets = self.top_ids[:, 0] if targets is None else targets
+        self.status = ints(1)
+
+    def score(self, stream=None):
+        abi.mla_token_logprobs(self.logits, None, None, self.lse, self.entropy, self.top_ids, self.top_logprobs, self.status,
+                               stream)
+
+    def accept(self, stream=None):
+        abi.mla_tree_accept(self.parents, self.tokens, self.targets, self.qo_indptr, self.kv_lens, self.path, self.counts,
+                            self.next_tokens, self.kv_lens, self.first, self.status, stream)
+
+    def compact(self, stream=None):
+        abi.mla_paged_compact(self.path, self.counts, self.kv_lens, self.block_table, self.cache, self.status, stream)
+
+    def run(self, stream=None):
+        self.score(stream)
+        self.accept(stream)
+        self.compact(stream)
+
+
+class Pages:
+    """The pages of a cache [layers, num_pages, page_size, 576] and who holds
+    them: ``refs`` [num_pages], and for each of ``batch`` branches a row of
+    ``block_table``, ``held`` and ``kv_lens``, on two sides that ``fork`` swaps
+    (two forks to a captured graph, then, or one graph for each side).
+
+    ``fork``: branch r goes on from branch ``parents[r]`` (-1: from nothing).
+    ``fit``: after ``want_lens`` has been set, positions kv_lens .. want_lens - 1
+    may be written, pages that are not needed are free, and rows in pages that
+    were shared are copied. ``advance``: they have been written. DecodeStep reads
+    a side's table and lengths."""
+
+    def __init__(self, layers, num_pages, page_size, batch, max_pages, window=0, sinks=0, device="cuda"):
+        ints = lambda *n: torch.zeros(n, dtype=torch.int32, device=device)  # noqa: E731
+        self.page_size, self.window, self.sinks, self.now = page_size, window, sinks, 0
+        self.cache = torch.zeros(layers, num_pages, page_size, 576, dtype=torch.bfloat16, device=device)
+        self.refs = ints(num_pages)
+        self._tables = [ints(batch, max_pages) - 1, ints(batch, max_pages) - 1]
+        self._held, self._lens = [ints(batch), ints(batch)], [ints(batch), ints(batch)]
+        self.parents, self.want_lens, self.copies = ints(batch), ints(batch), ints(batch, 3)
+        n = abi.mla_pages_fit_workspace_bytes(batch, num_pages)
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=device)
+        self.status = ints(1)
+
+    @property
+    def block_table(self):
+        return self._tables[self.now]
+
+    @property
+    def held(self):
+        return self._held[self.now]
+
+    @property
+    def kv_lens(self):
+        return self._lens[self.now]
+
+    def fork(self, stream=None):
+        a, b = self.now, 1 - self.now
+        abi.mla_pages_fork(self.parents, self._lens[a], self._held[a], self._tables[a], self.refs, self._lens[b],
+                           self._held[b], self._tables[b], self.status, stream)
+        self.now = b
+
+    def fit(self, stream=None):
+        abi.mla_pages_fit(self.kv_lens, self.want_lens, self.held, self.block_table, self.refs, self.page_size, self.copies,
+                          self.workspace, self.window, self.sinks, self.status, stream)
+        abi.mla_paged_copy(self.copies, self.cache, self.status, stream)
+
+    def advance(self):
+        self.kv_lens.copy_(self.want_lens)
