@@ -63,18 +63,25 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const ForkArgs
 
 // -------------------------------------------------------------------- fit
 //
-// One cluster works through steps with a cluster barrier between them; a warp
-// looks after a request (requests warp, warp + warps, ...), a lane after a
-// column of it. A cell that holds a page p that others hold too, and will be
-// written to, is marked by -2 - p until it is known what becomes of it:
-//   1  mark; 2  take back the references of marked cells and of pages given back;
+// What a call decides about one page depends on every request that holds it, so
+// the steps are separated by barriers; all but the search for free pages are
+// the first block's, four lanes a request, whose barriers are cheap:
+//   1  mark: a cell that will be written to and whose page p others hold, too,
+//      becomes -2 - p; count what each request needs;
+//   2  take back the references of marked cells and of pages given back;
 //   3  where nobody is left, all that held the page asked for one of their own:
 //      the lowest of them keeps it (a minimum over refs[p], which is below 0 then);
-//   4  count what each request needs; 5  sums of needs and of free pages;
-//   6  write the free pages down in order; 7  hand them out, or put everything back.
+//   4  tell who keeps; sums of the needs before each request;
+//   5  write the lowest free pages down in order, by all blocks;
+//   6  hand them out, or put everything back.
+// Bound by the latency of these steps (a round to L2 each), and of the search,
+// which reads refs up to the last page that it takes.
 constexpr int kFitThreads = 1024;
 constexpr int kFitWarps = kFitThreads / 32;
+constexpr int kLanes = 4;             // of a request
+constexpr int kAtOnce = kFitThreads / kLanes;
 constexpr int kFitCtas = 8;
+constexpr int kScan = 8;              // pages a thread looks at at a time
 constexpr int kClaim = -(1 << 30);
 
 struct FitShared {
@@ -91,8 +98,9 @@ __device__ __forceinline__ uint32_t cta() {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void all() {
-  __syncwarp();
+__device__ __forceinline__ void all(int n) {
+  __syncthreads();
+  if (n == 1) return;
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -109,14 +117,15 @@ __device__ __forceinline__ int block_scan(FitShared& sh, int v, int* total) {
   __syncthreads();
   if (lane == 31) sh.sums[warp] = inc;
   __syncthreads();
-  int s = sh.sums[lane], at = s;
+  int at = sh.sums[lane];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int u = __shfl_up_sync(kFull, at, o);
     if (lane >= o) at += u;
   }
+  const int before = __shfl_sync(kFull, at, warp > 0 ? warp - 1 : 0);
   *total = __shfl_sync(kFull, at, 31);
-  return inc - v + (warp > 0 ? __shfl_sync(kFull, at, warp - 1) : 0);
+  return inc - v + (warp > 0 ? before : 0);
 }
 
 // What a call asks of one request.
@@ -132,15 +141,15 @@ __device__ __forceinline__ Wish wish_of(const FitArgs& a, int b) {
   Wish w;
   w.len = __ldg(a.lens + b);
   const int want = __ldg(a.want + b);
-  w.held = __ldcg(a.held + b);
+  w.held = a.held[b];
   w.ok = w.len >= 0 && want >= 0 && want <= (int64_t)a.max_pages * a.page_size && w.held >= 0 && w.held <= a.max_pages;
-  w.need = (int)(((int64_t)want + a.page_size - 1) / a.page_size);
+  w.need = (int)(((unsigned)want + a.page_size - 1) / (unsigned)a.page_size);
   w.w0 = w.len / a.page_size;
   w.w1 = want > w.len ? w.need : w.w0;
   w.gap0 = w.gap1 = 0;
-  if (a.window > 0 && (int64_t)w.len + 1 > a.window) {
-    w.gap0 = (int)(((int64_t)a.sinks + a.page_size - 1) / a.page_size);
-    w.gap1 = (int)(((int64_t)w.len + 1 - a.window) / a.page_size);
+  if (a.window > 0 && w.len >= a.window) {
+    w.gap0 = (int)(((unsigned)a.sinks + a.page_size - 1) / (unsigned)a.page_size);
+    w.gap1 = (w.len - a.window + 1) / a.page_size;
   }
   w.gap1 = min(w.gap1, min(w.held, w.need));
   w.row = a.table + b * a.table_stride;
@@ -148,158 +157,178 @@ __device__ __forceinline__ Wish wish_of(const FitArgs& a, int b) {
 }
 
 // f(column, page) for this lane's pages that request w gives back: those
-// behind its need, and those of the gap down to the first that is gone.
+// behind its need, and those of the gap down to the first that is gone. group:
+// the lanes of the request, lane: this one's place among them.
 template <typename F>
-__device__ __forceinline__ void given_back(const FitArgs& a, const Wish& w, int lane, F f) {
-  for (int c = w.need + lane; c < w.held; c += 32) f(c, w.row[c]);
-  for (int top = w.gap1; top > w.gap0; top -= 32) {
+__device__ __forceinline__ void given_back(const Wish& w, unsigned group, int lane, F f) {
+  for (int c = w.need + lane; c < w.held; c += kLanes) f(c, w.row[c]);
+  for (int top = w.gap1; top > w.gap0; top -= kLanes) {
     const int c = top - 1 - lane;
     const int p = c >= w.gap0 ? w.row[c] : -1;
-    const unsigned gone = __ballot_sync(kFull, p == -1);
-    if (gone == 0 || lane < __ffs(gone) - 1) f(c, p);
+    const unsigned gone = __ballot_sync(group, p == -1);
+    if ((gone & ((2u << (threadIdx.x & 31)) - 1)) == 0) f(c, p);
     if (gone) break;
   }
 }
 
 __global__ void __launch_bounds__(kFitThreads) pages_fit_kernel(const FitArgs a) {
   __shared__ FitShared sh;
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int n = ctas(), me = cta(), warps = n * kFitWarps, first = me * kFitWarps + (tid >> 5);
+  const int tid = threadIdx.x, lane = tid % kLanes;
+  const unsigned group = ((1u << kLanes) - 1) << (tid & 31 & ~(kLanes - 1));
+  const int n = ctas(), me = cta();
   int32_t* const frees = a.ws;              // [num_pages] the lowest free pages, in order
   int32_t* const before = frees + a.num_pages;  // [batch] needs, then their sums before each request
-  int32_t* const totals = before + a.batch;     // [2][n] needs, free pages
+  int32_t* const totals = before + a.batch;     // needs; then free pages of each block
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   auto known = [&](int p) { return p >= 0 && p < a.num_pages; };
+  // this thread's part of the requests, in the first block
+  const int b0 = me == 0 ? tid / kLanes : a.batch;
+  Wish mine = {};
+  if (b0 < a.batch) mine = wish_of(a, b0);
 
-  for (int b = first; b < a.batch; b += warps) {
-    const Wish w = wish_of(a, b);
+  for (int b = b0; b < a.batch; b += kAtOnce) {
+    const Wish w = b == b0 ? mine : wish_of(a, b);
+    int need = 0;
     if (!w.ok) {
       if (lane == 0) flag(a.status, MT_DEV_BAD_INDPTR);
-      continue;
-    }
-    for (int c = w.w0 + lane; c < min(w.w1, w.held); c += 32) {
-      const int p = w.row[c];
-      if (known(p)) {
-        if (__ldcg(a.refs + p) > 1) w.row[c] = -2 - p;
-      } else if (p != -1) {
-        flag(a.status, MT_DEV_BAD_SLOT);
-        w.row[c] = -1;
+    } else {
+      for (int c = w.w0 + lane; c < w.w1; c += kLanes) {
+        const int p = c < w.held ? w.row[c] : -1;
+        if (known(p)) {
+          if (__ldcg(a.refs + p) <= 1) continue;
+          w.row[c] = -2 - p;
+        } else if (p != -1) {
+          flag(a.status, MT_DEV_BAD_SLOT);
+          w.row[c] = -1;
+        }
+        ++need;
       }
     }
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) need += __shfl_xor_sync(group, need, o);
+    if (lane == 0) before[b] = need;
   }
-  all();
-  for (int b = first; b < a.batch; b += warps) {
-    const Wish w = wish_of(a, b);
+  __syncthreads();
+  for (int b = b0; b < a.batch; b += kAtOnce) {
+    const Wish w = b == b0 ? mine : wish_of(a, b);
     if (!w.ok) continue;
-    for (int c = w.w0 + lane; c < min(w.w1, w.held); c += 32)
+    for (int c = w.w0 + lane; c < min(w.w1, w.held); c += kLanes)
       if (w.row[c] < -1) atomicSub(a.refs + (-2 - w.row[c]), 1);
-    given_back(a, w, lane, [&](int, int p) {
+    given_back(w, group, lane, [&](int, int p) {
       if (known(p)) atomicSub(a.refs + p, 1);
       else if (p != -1) flag(a.status, MT_DEV_BAD_SLOT);
     });
   }
-  all();
-  for (int b = first; b < a.batch; b += warps) {
-    const Wish w = wish_of(a, b);
+  __syncthreads();
+  bool claims = false;  // a page that nobody is left to hold
+  for (int b = b0; b < a.batch; b += kAtOnce) {
+    const Wish w = b == b0 ? mine : wish_of(a, b);
     if (!w.ok) continue;
-    for (int c = w.w0 + lane; c < min(w.w1, w.held); c += 32)
-      if (w.row[c] < -1 && __ldcg(a.refs + (-2 - w.row[c])) <= 0) atomicMin(a.refs + (-2 - w.row[c]), kClaim + b);
-  }
-  all();
-  for (int b = first; b < a.batch; b += warps) {
-    const Wish w = wish_of(a, b);
-    int need = 0;
-    if (w.ok)
-      for (int c = w.w0 + lane; c < w.w1; c += 32) {
-        int p = c < w.held ? w.row[c] : -1;
-        if (p < -1 && __ldcg(a.refs + (-2 - p)) == kClaim + b) {  // keeps it: nobody else finds itself there
-          p = -2 - p;
-          a.refs[p] = 1;
-          w.row[c] = p;
-        }
-        need += p < 0;
+    for (int c = w.w0 + lane; c < min(w.w1, w.held); c += kLanes)
+      if (w.row[c] < -1 && __ldcg(a.refs + (-2 - w.row[c])) <= 0) {
+        atomicMin(a.refs + (-2 - w.row[c]), kClaim + b);
+        claims = true;
       }
-    need = __reduce_add_sync(kFull, need);
-    if (lane == 0) before[b] = need;
   }
-  all();
-
-  // this CTA's runs of requests and of pages
-  const int b0 = (int)((int64_t)a.batch * me / n), b1 = (int)((int64_t)a.batch * (me + 1) / n);
+  if (__syncthreads_or(claims)) {
+    for (int b = b0; b < a.batch; b += kAtOnce) {
+      const Wish w = b == b0 ? mine : wish_of(a, b);
+      if (!w.ok) continue;
+      int keeps = 0;
+      for (int c = w.w0 + lane; c < min(w.w1, w.held); c += kLanes) {
+        const int p = w.row[c];
+        if (p < -1 && __ldcg(a.refs + (-2 - p)) == kClaim + b) {  // nobody else finds itself there
+          a.refs[-2 - p] = 1;
+          w.row[c] = -2 - p;
+          ++keeps;
+        }
+      }
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) keeps += __shfl_xor_sync(group, keeps, o);
+      if (lane == 0 && keeps) before[b] -= keeps;
+    }
+    __syncthreads();
+  }
+  int64_t asked = 0;
+  if (me == 0) {
+    for (int b = 0; b < a.batch; b += kFitThreads) {
+      int sum;
+      const int v = b + tid < a.batch ? before[b + tid] : 0;
+      const int at = block_scan(sh, v, &sum);
+      if (b + tid < a.batch) before[b + tid] = (int)asked + at;
+      asked = min(asked + sum, (int64_t)INT32_MAX);  // more than there can be
+    }
+    if (n > 1 && tid == 0) totals[0] = (int)asked;
+  }
+  // Free pages: with several blocks each first counts those of its run of pages.
   const int p0 = (int)(a.num_pages * me / n), p1 = (int)(a.num_pages * (me + 1) / n);
-  int needs = 0, free = 0;
-  for (int b = b0 + tid; b < b1; b += kFitThreads) needs += __ldcg(before + b);
+  int at = 0, there = 0;
+  all(n);
+  if (n > 1) {
+    int free = 0, sum;
 #pragma unroll 8
-  for (int p = p0 + tid; p < p1; p += kFitThreads) free += __ldcg(a.refs + p) == 0;
-  int all_needs, all_free;
-  block_scan(sh, needs, &all_needs);
-  block_scan(sh, free, &all_free);
-  if (tid == 0) {
-    totals[me] = all_needs;
-    totals[n + me] = all_free;
-  }
-  all();
-  int64_t asked = 0, there = 0;
-  int need_at = 0, free_at = 0;             // before this CTA's runs
-  for (int i = 0; i < n; ++i) {
-    const int x = __ldcg(totals + i), y = __ldcg(totals + n + i);
-    if (i < me) need_at += x, free_at += y;
-    asked += x;
-    there += y;
-  }
-  const bool enough = asked <= there;
-  if (enough) {
-    for (int b = b0; b < b1; b += kFitThreads) {
-      int sum;
-      const int at = block_scan(sh, b + tid < b1 ? __ldcg(before + b + tid) : 0, &sum);
-      if (b + tid < b1) before[b + tid] = need_at + at;
-      need_at += sum;
-    }
-    for (int p = p0; p < p1 && free_at < asked; p += kFitThreads) {
-      int sum;
-      const bool is = p + tid < p1 && __ldcg(a.refs + p + tid) == 0;
-      const int at = free_at + block_scan(sh, is, &sum);
-      if (is && at < asked) frees[at] = p + tid;
-      free_at += sum;
+    for (int p = p0 + tid; p < p1; p += kFitThreads) free += __ldcg(a.refs + p) == 0;
+    block_scan(sh, free, &sum);
+    if (tid == 0) totals[1 + me] = sum;
+    asked = __ldcg(totals);
+    all(n);
+    for (int i = 0; i < n; ++i) {
+      const int x = __ldcg(totals + 1 + i);
+      if (i < me) at += x;
+      there += x;
     }
   }
-  all();
+  if (n == 1 || asked <= there)
+    for (int p = p0; p < p1 && at < asked; p += kFitThreads * kScan) {
+      int is = 0, sum;
+#pragma unroll
+      for (int i = 0; i < kScan; ++i) {
+        const int q = p + tid * kScan + i;
+        if (q < p1 && __ldcg(a.refs + q) == 0) is |= 1 << i;
+      }
+      int r = at + block_scan(sh, __popc(is), &sum);
+      for (; is && r < asked; is &= is - 1, ++r) frees[r] = p + tid * kScan + __ffs(is) - 1;
+      at += sum;
+    }
+  const bool enough = n == 1 ? asked <= at : asked <= there;
+  all(n);
 
   if (!enough && me == 0 && tid == 0) flag(a.status, MT_DEV_NO_PAGES);
-  for (int b = first; b < a.batch; b += warps) {
-    const Wish w = wish_of(a, b);
+  for (int b = b0; b < a.batch; b += kAtOnce) {
+    const Wish w = b == b0 ? mine : wish_of(a, b);
     int copy[3] = {-1, -1, 0};
     if (w.ok && !enough) {
-      for (int c = w.w0 + lane; c < min(w.w1, w.held); c += 32)
+      for (int c = w.w0 + lane; c < min(w.w1, w.held); c += kLanes)
         if (w.row[c] < -1) {
           const int p = -2 - w.row[c];
           w.row[c] = p;
           atomicAdd(a.refs + p, 1);
         }
-      given_back(a, w, lane, [&](int, int p) {
+      given_back(w, group, lane, [&](int, int p) {
         if (known(p)) atomicAdd(a.refs + p, 1);
       });
     } else if (w.ok) {
-      given_back(a, w, lane, [&](int c, int) { w.row[c] = -1; });
-      for (int c = w.held + lane; c < (w.w1 > w.w0 ? w.w0 : w.need); c += 32) w.row[c] = -1;
-      int at = __ldcg(before + b);
-      for (int c0 = w.w0; c0 < w.w1; c0 += 32) {
+      given_back(w, group, lane, [&](int c, int) { w.row[c] = -1; });
+      for (int c = w.held + lane; c < (w.w1 > w.w0 ? w.w0 : w.need); c += kLanes) w.row[c] = -1;
+      int rank = before[b];
+      for (int c0 = w.w0; c0 < w.w1; c0 += kLanes) {
         const int c = c0 + lane;
         const int p = c < w.held && c < w.w1 ? w.row[c] : -1;
         const bool take = c < w.w1 && p < 0;
-        const unsigned m = __ballot_sync(kFull, take);
+        const unsigned m = __ballot_sync(group, take);
         if (take) {
-          const int page = __ldcg(frees + at + __popc(m & ((1u << lane) - 1)));
+          const int page = __ldcg(frees + rank + __popc(m & ((1u << (tid & 31)) - 1)));
           w.row[c] = page;
           a.refs[page] = 1;
           if (c == w.w0 && p < -1 && w.len % a.page_size > 0) copy[0] = -2 - p, copy[1] = page, copy[2] = w.len % a.page_size;
         }
-        at += __popc(m);
+        rank += __popc(m);
       }
+      __syncwarp(group);  // all lanes have read held
       if (lane == 0) a.held[b] = w.need;
     }
-    if (lane == 0) {  // column w0 is lane 0's
+    if (lane == 0) {  // column w0 is its
 #pragma unroll
       for (int i = 0; i < 3; ++i) a.copies[3 * b + i] = copy[i];
     }
@@ -350,7 +379,7 @@ void configure(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, unsigned bloc
 }  // namespace
 
 size_t pages_fit_workspace(int batch, int64_t num_pages) {
-  return ((size_t)num_pages + (size_t)batch + 2 * kFitCtas) * sizeof(int32_t);
+  return ((size_t)num_pages + (size_t)batch + 1 + kFitCtas) * sizeof(int32_t);
 }
 
 int64_t paged_copy_blocks(const CopyArgs& a) {
@@ -369,7 +398,7 @@ cudaError_t launch_pages_fork(const ForkArgs& a, cudaStream_t stream) {
 cudaError_t launch_pages_fit(const FitArgs& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  const unsigned ctas = a.num_pages > 16384 || a.batch > 64 ? kFitCtas : 1;
+  const unsigned ctas = a.num_pages > 32768 ? kFitCtas : 1;
   configure(cfg, attr, ctas, kFitThreads, stream);
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim = {ctas, 1, 1};
