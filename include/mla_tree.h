@@ -581,7 +581,8 @@ int mla_tree_accept(const int32_t* parents, const int32_t* tokens, const int32_t
  * counts[b] (kv_lens: the new lengths), the row of position base + path[b, k]
  * goes to position base + k, k = 0, 1, ... in order. What mla_tree_accept
  * returns is what this takes. Rows behind the new length keep what they held
- * last. Layer l's cache is at cache + l * layer_stride (16-byte aligned);
+ * last. Layer l's cache is at cache + l * layer_stride (16-byte aligned; no two
+ * layers' pages may overlap, but one layer's may lie between another's);
  * geometry, table and their checks are those of the paged calls.
  * A path that does not rise sets MT_DEV_BAD_PARENT and ends there; counts
  * outside [0, max_accept] or a bad length set MT_DEV_BAD_INDPTR (the request is

@@ -442,9 +442,17 @@ static int decode_common(const mt_bf16* q, int64_t q_token_stride, int64_t q_hea
   return cuda_status(launch_paged_decode_simt(a, nsm, (cudaStream_t)stream));
 }
 
-// Layers of a paged cache.
-static bool layers_ok(int layers, int64_t layer_stride) {
-  return layers >= 0 && (layers <= 1 || (layer_stride >= 0 && layer_stride % 8 == 0 && layer_stride <= INT64_MAX / 4 / layers));
+// Layers of a paged cache, no two of whose pages may share elements: the wider
+// stride has to step over all that the narrower one spans (either may be the layers').
+static bool layers_ok(int layers, int64_t layer_stride, int64_t num_pages, int64_t page_stride, int page_size) {
+  if (layers < 0) return false;
+  if (layers <= 1 || num_pages <= 0) return true;
+  if (layer_stride <= 0 || layer_stride % 8 || layer_stride > INT64_MAX / 4 / layers) return false;
+  const int64_t page = (int64_t)page_size * MT_D_QK;
+  if (num_pages == 1) return layer_stride >= page;
+  const bool inside = layer_stride < page_stride;  // a page of all layers, then the next
+  const int64_t lo = inside ? layer_stride : page_stride, hi = inside ? page_stride : layer_stride;
+  return lo >= page && hi >= lo * ((inside ? layers : num_pages) - 1) + page;
 }
 
 extern "C" {
@@ -528,8 +536,9 @@ int mla_paged_compact(const int32_t* path, int64_t path_stride, int max_accept, 
                       int64_t table_stride, int max_pages, mt_bf16* cache, int64_t page_stride,
                       int64_t num_pages, int page_size, int layers, int64_t layer_stride,
                       int32_t* dev_status, mt_stream_t stream) {
-  if (batch < 0 || max_accept < 0 || path_stride < max_accept || !layers_ok(layers, layer_stride) ||
-      !paged_cache_ok(cache, page_stride, num_pages, page_size, table_stride, max_pages))
+  if (batch < 0 || max_accept < 0 || path_stride < max_accept ||
+      !paged_cache_ok(cache, page_stride, num_pages, page_size, table_stride, max_pages) ||
+      !layers_ok(layers, layer_stride, num_pages, page_stride, page_size))
     return MT_EINVAL;
   if (batch == 0 || max_accept == 0 || layers == 0) return MT_OK;
   if (!path || !counts || !kv_lens || (max_pages > 0 && !block_table) || (num_pages > 0 && !cache)) return MT_EINVAL;
@@ -601,8 +610,8 @@ int mla_pages_fit(const int32_t* kv_lens, const int32_t* want_lens, int32_t* hel
 int mla_paged_copy(const int32_t* copies, int64_t n, mt_bf16* cache, int64_t page_stride,
                    int64_t num_pages, int page_size, int layers, int64_t layer_stride,
                    int32_t* dev_status, mt_stream_t stream) {
-  if (n < 0 || !layers_ok(layers, layer_stride) ||
-      !paged_cache_ok(cache, page_stride, num_pages, page_size, 0, 0))
+  if (n < 0 || !paged_cache_ok(cache, page_stride, num_pages, page_size, 0, 0) ||
+      !layers_ok(layers, layer_stride, num_pages, page_stride, page_size))
     return MT_EINVAL;
   if (n == 0 || layers == 0) return MT_OK;
   if (!copies || (num_pages > 0 && !cache)) return MT_EINVAL;

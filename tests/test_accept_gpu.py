@@ -184,6 +184,20 @@ def test_compact(layers, page, gap, layer_gap):
     assert torch.equal(after[hole].view(torch.int16), before[hole].view(torch.int16))
 
 
+def test_compact_layers_inside_pages():
+    """[pages, layers, page, 576] in memory, seen as [layers, pages, page, 576]."""
+    g = torch.Generator()
+    g.manual_seed(4)
+    store = torch.randn(6, 5, 8, 576, generator=g).to(BF).cuda()
+    cache = store.transpose(0, 1)
+    table, path = [[3, 1, 0]], [[0, 2, 7, 12]]
+    want = moved(cache, table, 8, [9], [4], path)
+    abi.mla_paged_compact(ints(path), ints([4]), ints([9]), ints(table), cache)
+    assert torch.equal(cache.cpu(), want)
+    with pytest.raises(abi.MlaTreeError, match="invalid"):
+        abi.mla_paged_compact(ints(path), ints([4]), ints([9]), ints(table), store[:, :1].transpose(0, 1).expand(3, 6, 8, 576))
+
+
 def test_compact_bad_input():
     page, table = 4, [[0, 1, 2], [3, 77, 5], [6, 7, 8]]
     g = torch.Generator()
