@@ -310,7 +310,7 @@ __device__ __forceinline__ int bound_warps(int lanes) { return max(1, min(lanes 
 template <int kThreads>
 __device__ __forceinline__ void warp_bound(Shared<kThreads>& sh, Key own, int k, int lanes) {
   const int full = bound_warps<kThreads>(lanes);
-  const Key w = warp_qth(own, (k + full - 1) / full);
+  const Key w = warp_qth(own, full == kThreads / 32 ? (k + kThreads / 32 - 1) / (kThreads / 32) : (k + full - 1) / full);
   if ((threadIdx.x & 31) == 0) sh.bound[threadIdx.x >> 5] = w;
 }
 template <int kThreads>
@@ -431,30 +431,12 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
   p.first = head;
   p.head = part == 0 ? head : 0;
 
-  // the given tokens' values are asked for ahead of the row
-  auto value_at = [&](int g, bool& there) {
-    const int token = __ldg(a.tokens + r * a.token_stride + g);
-    there = token >= 0 && token < a.vocab;
-    if (there) return Vec<T>::one(p.row[token]);
-    if (token != -1) flag(a.status, MT_DEV_BAD_TOKEN);
-    return 0.f;
-  };
-  bool asked = false;
-  const float given = part == 0 && tid < a.per_row ? value_at(tid, asked) : 0.f;
-
-  Sums u = {-INFINITY, 0.f, 0.f};
-  auto ends = [&](int place) {
-    const float x = Vec<T>::one(p.row[place]);
-    add_one(u, x);
-    if (k > 0) push(sh, make_key(x, place));
-  };
-  if (tid < p.head) ends(tid);
-  if (tid < p.tail) ends(p.tail0 + tid);
-
   float top = -INFINITY, second = -INFINITY;
   Pair s2 = 0, t2 = 0, neg = pair(-Vec<T>::kFloor, -Vec<T>::kFloor);
   const Pair log2e = pair(kLog2e, kLog2e);
   int at = p.lo + tid;
+  constexpr bool kKeep = kThreads == 256;  // for the time of one row; it costs registers and moves
+  uint4 best = make_uint4(0, 0, 0, 0);     // the vector there
   uint4 next[kUnroll];
   auto load = [&](int v0) {
 #pragma unroll
@@ -462,6 +444,23 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
       if (v0 + i * kThreads < p.hi) next[i] = load16(p.vec + v0 + i * kThreads);
   };
   load(p.lo + tid);
+  // the given tokens' values are asked for behind the first of the row
+  auto value_at = [&](int g, bool& there) {
+    const int token = __ldg(a.tokens + r * a.token_stride + g);
+    there = token >= 0 && token < a.vocab;
+    if (!there && token != -1) flag(a.status, MT_DEV_BAD_TOKEN);
+    return p.row[there ? token : 0];
+  };
+  bool asked = false;
+  T given = T(0.f);
+  if (part == 0 && tid < a.per_row) given = value_at(tid, asked);
+  Sums u = {-INFINITY, 0.f, 0.f};
+  if (tid < p.head + p.tail) {
+    const int place = tid < p.head ? tid : p.tail0 + tid - p.head;
+    const float x = Vec<T>::one(p.row[place]);
+    add_one(u, x);
+    if (k > 0) push(sh, make_key(x, place));
+  }
   for (int v0 = p.lo + tid; v0 < p.hi; v0 += kUnroll * kThreads) {
     uint4 now[kUnroll];
 #pragma unroll
@@ -480,6 +479,7 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
         s2 = mul2(f2, s2);
         neg = pair(-ref, -ref);
         top = m, at = v0 + i * kThreads;
+        if (kKeep) best = now[i];
       }
       Pair x[E / 2];
       Vec<T>::raised(now[i], x);
@@ -511,18 +511,15 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
   // wherever in its vector the value is, its key is at least that of the last place
   if (k > 0) warp_bound(sh, some ? make_key(top, p.first + at * E + E - 1) : 0, k, p.hi - p.lo);
   __syncthreads();
-  u = join(sh.sums, kWarps);
   const Key b = k > 0 ? common_bound(sh, p.hi - p.lo) : 0;
-  const bool odd = u.s != u.s || u.t != u.t;  // NaN, +inf, or a maximum that differences from are infinite
-  if (odd || (u.m < Vec<T>::kLow && u.m > -INFINITY)) u = careful_sums<T, kThreads>(sh, p);
 
   int n = 0;                           // keys in the list
   bool sorted = false;                 // or k in best
   if (k > 0) {
     const float least = b ? value_of(b) : -INFINITY;
-    auto look = [&](int v) {
+    auto look = [&](int v, const uint4& u) {
       float x[E];
-      Vec<T>::unpack(load16(p.vec + v), x);
+      Vec<T>::unpack(u, x);
 #pragma unroll
       for (int j = 0; j < E; ++j)
         if (x[j] >= least) {
@@ -534,21 +531,24 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
       // the second value where it equals the first comes behind it
       const bool behind = second == least && top == least && p.first + (int64_t)(at + kThreads) * E > place_of(b);
       if (b && second >= least && !behind) sh.again[atomicAdd(&sh.agains, 1)] = tid;
-      else look(at);
+      else look(at, kKeep && top > -INFINITY ? best : load16(p.vec + at));
     }
     __syncthreads();
     const int each = (p.hi - p.lo + kThreads - 1) / kThreads, items = sh.agains * each;
     for (int i = tid; i < items; i += kThreads) {
       const int v = p.lo + sh.again[i / each] + i % each * kThreads;
-      if (v < p.hi) look(v);
+      if (v < p.hi) look(v, load16(p.vec + v));
     }
     if (items) __syncthreads();
     n = sh.count;
-    if (n > sh.kCap || odd) {
-      find_top<T, kThreads>(sh, p, k);
-      n = k;
-      sorted = true;
-    }
+  }
+  u = join(sh.sums, kWarps);
+  const bool odd = u.s != u.s || u.t != u.t;  // NaN, +inf, or a maximum that differences from are infinite
+  if (odd || (u.m < Vec<T>::kLow && u.m > -INFINITY)) u = careful_sums<T, kThreads>(sh, p);
+  if (k > 0 && (n > sh.kCap || odd)) {
+    find_top<T, kThreads>(sh, p, k);
+    n = k;
+    sorted = true;
   }
   auto rank_of = [&](Key key) {
     int r = 0;
@@ -585,11 +585,12 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
   }
 
   const bool none = u.m == -INFINITY && u.s == u.s;
-  const float lse = none ? -INFINITY : u.m + logf(u.s);
+  const float log_s = __log2f(u.s);
+  const float lse = none ? -INFINITY : fmaf(log_s, kLn2, u.m);
   if (tid == 0) {
     if (a.lse) a.lse[r] = lse;
     if (a.entropy) {
-      const float h = none ? 0.f : (log2f(u.s) - u.t / u.s) * kLn2;
+      const float h = none ? 0.f : (log_s - u.t / u.s) * kLn2;
       a.entropy[r] = h < 0.f ? 0.f : h;
     }
   }
@@ -599,14 +600,19 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
     if (a.top_logprobs) a.top_logprobs[r * k + rank] = none ? -INFINITY : value_of(key) - lse;
   };
   if (parts > 1) {
-    for (int t = tid; t < parts * kMaxTop; t += kThreads) {
-      if (t % kMaxTop >= k) continue;
-      key = sh.parts[t / kMaxTop][t % kMaxTop];
+    // eight lanes a key, each of which counts in one part
+    for (int t = tid; t < parts * k * 8; t += kThreads) {
+      const int i = t >> 3, from = i / k, in = t & 7;
+      key = sh.parts[from][i - from * k];
       rank = 0;
-      for (int i = 0; i < parts; ++i)
-#pragma unroll 4
-        for (int j = 0; j < k; ++j) rank += sh.parts[i][j] > key;
-      put(rank, key);
+      if (in < parts)
+#pragma unroll 8
+        for (int j = 0; j < k; ++j) rank += sh.parts[in][j] > key;
+      const unsigned eight = 0xffu << (lane & 24);
+      rank += __shfl_xor_sync(eight, rank, 1);
+      rank += __shfl_xor_sync(eight, rank, 2);
+      rank += __shfl_xor_sync(eight, rank, 4);
+      if (in == 0) put(rank, key);
     }
   } else {
     for (int i = tid; i < n; i += kThreads) {
@@ -615,8 +621,8 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
     }
   }
   for (int g = tid; g < a.per_row; g += kThreads) {
-    const float x = g == tid ? given : value_at(g, asked);
-    a.logprobs[r * a.per_row + g] = none || !asked ? -INFINITY : x - lse;
+    const T x = g == tid ? given : value_at(g, asked);
+    a.logprobs[r * a.per_row + g] = none || !asked ? -INFINITY : Vec<T>::one(x) - lse;
   }
 }
 
