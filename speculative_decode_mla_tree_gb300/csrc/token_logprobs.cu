@@ -3,14 +3,15 @@
 //
 // With m = max x, e_v = exp(x_v - m), S = sum e_v and T = sum e_v (x_v - m):
 //     lse = m + ln S,   ln p_v = x_v - lse,   H = -sum p_v ln p_v = ln S - T / S.
-// Each thread keeps a running m, S and T of its own (S' = f S, T' = f (T +
-// (m - m') S), f = exp(m - m'), where m rises to m'), joined at the end in a fixed
-// order. A value is read once from HBM.
+// Each thread keeps an S and T of its own relative to a value m that follows its
+// maximum in steps (S' = f S, T' = f (T + (m - m') S), f = exp(m - m'), where a
+// value more than kSlack above m makes it m'), joined at the end, relative to
+// the maximum, in a fixed order. A value is read once from HBM.
 //
 // Most likely tokens are ordered by value, then by lower place: a key of 64 bits,
 // the value's bits made monotone above the inverted place, says both. On the way
-// over the row a thread keeps the largest value of its vectors (of 16 bytes), that
-// vector's place, and the second largest. At the end each warp's q-th best thread (q
+// over the row a thread keeps the two vectors (of 16 bytes) with the largest values
+// and the third largest value of one. At the end each warp's q-th best thread (q
 // = ceil(k / warps)) gives a bound: the least of them is reached by at least k
 // values. Threads that reach it look at their vector again; the few whose second
 // does, too, have all theirs looked at again by the whole block. What reaches the
@@ -21,6 +22,12 @@
 //
 // Few rows are split over clusters of up to 8 CTAs, which join through
 // distributed shared memory: no workspace and no second launch.
+//
+// What bounds it: with many rows HBM, and beside it the 16 exp a cycle of an SM (58
+// us of the 95 that 2048 rows of 131072 bf16 values take, 5.7 TB/s; fp32 rows of
+// half as many reach 6.7 TB/s). The best tokens cost 5 us of them for k = 5, 14 for
+// 32. 128 such rows take 13.3 us, 10.4 without tokens, where HBM needs 5: the start,
+// a ramp, and the joins. One row takes 5 to 6.6 us, nearly all of it latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <float.h>
@@ -32,9 +39,10 @@
 namespace mt {
 namespace {
 
-// 16-byte loads of a chunk a thread, one chunk ahead (2048 rows of 131072 bf16 values: 2
-// take 111 us, 4 98, 8 99; 256 rows of 100003 fp32 values 29, 26, 32)
+// 16-byte loads of a chunk a thread, one chunk ahead (with 2
+// 2048 rows of 131072 bf16 values take 13% longer, with 8 1%; 256 rows of 100003 fp32 values 11% and 20%)
 constexpr int kUnroll = 4;
+constexpr float kSlack = 4.f;         // larger ones cost bits of the entropy (a difference), smaller ones branches
 constexpr int kMaxTop = MT_MAX_TOP;   // 32
 constexpr int kMaxParts = 8;
 constexpr unsigned kFull = 0xffffffffu;
@@ -247,7 +255,7 @@ struct Shared {
   static constexpr int kCap = kThreads * 8 + 16;  // one vector of 16-bit values a thread, and the ends
   Key list[kCap];
   Key best[kMaxTop], better[kMaxTop];  // the k best so far, in order (0: none); 0, but for prune
-  Key parts[kMaxParts][kMaxTop];    // of the row's parts, in the first one's
+  Key parts[kMaxParts][kMaxTop + 1];  // of the row's parts, in the first one's (columns in banks of their own)
   Key bound[kWarps];
   Sums sums[kWarps], part_sums[kMaxParts];
   int again[kThreads];                 // threads whose vectors are looked at again
@@ -411,7 +419,7 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
   const int k = a.top_k;
   if (tid == 0) sh.count = sh.agains = 0;
   if (parts > 1) {
-    for (int i = tid; part == 0 && i < kMaxParts * kMaxTop; i += kThreads) sh.parts[0][i] = 0;
+    for (int i = tid; part == 0 && i < kMaxParts * (kMaxTop + 1); i += kThreads) sh.parts[0][i] = 0;
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -431,12 +439,12 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
   p.first = head;
   p.head = part == 0 ? head : 0;
 
-  float top = -INFINITY, second = -INFINITY;
-  Pair s2 = 0, t2 = 0, neg = pair(-Vec<T>::kFloor, -Vec<T>::kFloor);
+  float top = -INFINITY, second = -INFINITY, third = -INFINITY;
+  // sums in pairs, relative to a value that the largest so far is not far above (nor the value below the floor)
+  float ref = Vec<T>::kFloor, limit = -INFINITY;
+  Pair s2 = 0, t2 = 0, neg = pair(-ref, -ref);
   const Pair log2e = pair(kLog2e, kLog2e);
-  int at = p.lo + tid;
-  constexpr bool kKeep = kThreads == 256;  // for the time of one row; it costs registers and moves
-  uint4 best = make_uint4(0, 0, 0, 0);     // the vector there
+  int at = p.lo + tid, at2 = at;
   uint4 next[kUnroll];
   auto load = [&](int v0) {
 #pragma unroll
@@ -470,16 +478,23 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
     for (int i = 0; i < kUnroll; ++i) {
       if (v0 + i * kThreads >= p.hi) break;
       const float m = Vec<T>::largest(now[i]);
+      // without a branch: over 32 lanes one would be taken nearly every time
+      const int v = v0 + i * kThreads;
+      const bool first = m > top, next_best = m > second;
+      third = fmaxf(third, fminf(m, second));
       second = fmaxf(second, fminf(m, top));
-      if (m > top) {
-        // sums in pairs, relative to the largest so far (not below the floor)
-        const float ref = fmaxf(m, Vec<T>::kFloor), d = fmaxf((fmaxf(top, Vec<T>::kFloor) - ref) * kLog2e, -1e4f);
+      at2 = first ? at : next_best ? v : at2;
+      top = fmaxf(top, m);
+      at = first ? v : at;
+      if (m > limit) {
+        // sums relative to this value from here on
+        const float to = fmaxf(m, Vec<T>::kFloor), d = fmaxf((ref - to) * kLog2e, -1e4f);
         const Pair d2 = pair(d, d), f2 = pair(ex2(d), ex2(d));
         t2 = mul2(f2, fma2(d2, s2, t2));
         s2 = mul2(f2, s2);
+        ref = to;
         neg = pair(-ref, -ref);
-        top = m, at = v0 + i * kThreads;
-        if (kKeep) best = now[i];
+        limit = m + kSlack;
       }
       Pair x[E / 2];
       Vec<T>::raised(now[i], x);
@@ -497,9 +512,9 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
   // this CTA's sums, in a fixed order, and the bound
   {
     const float2 hs = halves(s2), ht = halves(t2);
-    Sums w = {top, hs.x + hs.y, ht.x + ht.y};
-    if (top == -INFINITY && w.s == w.s) w.s = w.t = 0.f;  // counted as the floor
-    const float m = fmaxf(u.m, w.m);
+    Sums w = {ref, hs.x + hs.y, ht.x + ht.y};
+    if (top == -INFINITY && w.s == w.s) w = {-INFINITY, 0.f, 0.f};  // counted as the floor
+    const float m = fmaxf(u.m, fmaxf(w.m, top));
     raise(u, m);
     raise(w, m);
     u.s += w.s;
@@ -528,10 +543,24 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
         }
     };
     if (some && make_key(top, p.first + at * E) >= b) {
-      // the second value where it equals the first comes behind it
-      const bool behind = second == least && top == least && p.first + (int64_t)(at + kThreads) * E > place_of(b);
-      if (b && second >= least && !behind) sh.again[atomicAdd(&sh.agains, 1)] = tid;
-      else look(at, kKeep && top > -INFINITY ? best : load16(p.vec + at));
+      // Which of its vectors can reach the bound: `at`, at2 where `two`, others
+      // where `all`. Where one's largest value equals the bound's, its place
+      // decides: those that equal the first or second come behind these.
+      auto before = [&](int v) { return p.first + (int64_t)v * E <= place_of(b); };
+      bool two = false, all = false;
+      if (least > -INFINITY) {
+        two = second > least || (second == least && before(at2));
+        all = third > least || (third == least && (third < second || before(at2 + kThreads)));
+      } else if (b) {  // too few values are not -inf, and of those that are nobody kept a place
+        all = top > -INFINITY || before(at + kThreads);
+      }
+      if (all) {
+        sh.again[atomicAdd(&sh.agains, 1)] = tid;
+      } else {
+        const uint4 one = load16(p.vec + at), other = load16(p.vec + at2);  // (there is no place without a vector)
+        look(at, one);
+        if (two) look(at2, other);
+      }
     }
     __syncthreads();
     const int each = (p.hi - p.lo + kThreads - 1) / kThreads, items = sh.agains * each;
@@ -550,26 +579,30 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
     n = k;
     sorted = true;
   }
-  auto rank_of = [&](Key key) {
-    int r = 0;
-    for (int j0 = 0; j0 < n && r < k; j0 += 32) {
-      const int j1 = min(j0 + 32, n);
-#pragma unroll 8
-      for (int j = j0; j < j1; ++j) r += sh.list[j] > key;
+  // f(rank, key) for the k best of the list, from eight lanes a key, each of which
+  // counts a part of those that are larger.
+  auto ranked = [&](auto f) {
+    const int in = tid & 7;
+    const unsigned eight = 0xffu << (lane & 24);
+    for (int i = tid >> 3; i < n; i += kThreads / 8) {
+      const Key key = sorted ? sh.best[i] : sh.list[i];
+      int r = sorted ? i : 0;
+      if (!sorted) {
+#pragma unroll 4
+        for (int j = in; j < n; j += 8) r += sh.list[j] > key;
+        r += __shfl_xor_sync(eight, r, 1);
+        r += __shfl_xor_sync(eight, r, 2);
+        r += __shfl_xor_sync(eight, r, 4);
+      }
+      if (in == 0 && r < k && key) f(r, key);
     }
-    return r;
   };
 
-  Key key = 0;
-  int rank = k;
   if (parts > 1) {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // the first CTA runs
-    for (int i = tid; i < n; i += kThreads) {
-      key = sorted ? sh.best[i] : sh.list[i];
-      rank = sorted ? i : rank_of(key);
-      if (rank < k)
-        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(in_first(&sh.parts[part][rank])), "l"(key) : "memory");
-    }
+    ranked([&](int r, Key key) {
+      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(in_first(&sh.parts[part][r])), "l"(key) : "memory");
+    });
     if (tid == 0) {
       const uint32_t sums = in_first(&sh.part_sums[part]);
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(sums), "f"(u.m) : "memory");
@@ -581,7 +614,6 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (part != 0) return;
     u = join(sh.part_sums, parts);
-    sorted = false;
   }
 
   const bool none = u.m == -INFINITY && u.s == u.s;
@@ -595,30 +627,27 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
     }
   }
   auto put = [&](int rank, Key key) {
-    if (!key || rank >= k) return;
     a.top_ids[r * k + rank] = place_of(key);
     if (a.top_logprobs) a.top_logprobs[r * k + rank] = none ? -INFINITY : value_of(key) - lse;
   };
   if (parts > 1) {
     // eight lanes a key, each of which counts in one part
+    const float per_k = __fdividef(1.f, (float)k);
     for (int t = tid; t < parts * k * 8; t += kThreads) {
-      const int i = t >> 3, from = i / k, in = t & 7;
-      key = sh.parts[from][i - from * k];
-      rank = 0;
+      const int i = t >> 3, from = (int)((i + 0.5f) * per_k), in = t & 7;
+      const Key key = sh.parts[from][i - from * k];
+      int r = 0;
       if (in < parts)
-#pragma unroll 8
-        for (int j = 0; j < k; ++j) rank += sh.parts[in][j] > key;
+#pragma unroll 4
+        for (int j = 0; j < k; ++j) r += sh.parts[in][j] > key;
       const unsigned eight = 0xffu << (lane & 24);
-      rank += __shfl_xor_sync(eight, rank, 1);
-      rank += __shfl_xor_sync(eight, rank, 2);
-      rank += __shfl_xor_sync(eight, rank, 4);
-      if (in == 0) put(rank, key);
+      r += __shfl_xor_sync(eight, r, 1);
+      r += __shfl_xor_sync(eight, r, 2);
+      r += __shfl_xor_sync(eight, r, 4);
+      if (in == 0 && r < k && key) put(r, key);
     }
   } else {
-    for (int i = tid; i < n; i += kThreads) {
-      key = sorted ? sh.best[i] : sh.list[i];
-      put(sorted ? i : rank_of(key), key);
-    }
+    ranked(put);
   }
   for (int g = tid; g < a.per_row; g += kThreads) {
     const T x = g == tid ? given : value_at(g, asked);
