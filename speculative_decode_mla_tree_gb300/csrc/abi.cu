@@ -425,7 +425,8 @@ static int decode_common(const mt_bf16* q, int64_t q_token_stride, int64_t q_hea
   a.q_head = q_head_stride;
   a.kv = {const_cast<mt_bf16*>(cache), page_stride, num_pages, page_size, block_table, table_stride,
           max_pages, kv_lens};
-  a.window = window;
+  const int64_t most = (int64_t)max_pages * page_size;  // a window or sinks as long as the table leave nothing out
+  a.window = window >= most || sinks >= most ? 0 : window;
   a.sinks = sinks;
   a.batch = batch;
   a.heads = heads;

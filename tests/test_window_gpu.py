@@ -113,6 +113,50 @@ def test_batches(batch):
     run(batch, torch.randint(0, 900, (batch,), generator=g).tolist(), 8, 32, 100, 20)
 
 
+@pytest.mark.parametrize("heads", [8, 24, 64, 128])
+@pytest.mark.parametrize("batch,window,sinks", [(1, 500, 4), (9, 500, 4), (14, 100, 0), (30, 100, 0), (60, 60, 3), (3, 1500, 0)])
+@pytest.mark.parametrize("page", [16, 9])
+def test_one_cluster_a_request(heads, batch, window, sinks, page):
+    """Requests of no tile, one, fewer than the cluster has CTAs, and more."""
+    g = torch.Generator()
+    g.manual_seed(batch)
+    lens = torch.randint(0, window + 300, (batch,), generator=g).tolist()
+    lens[0] = window + 250
+    lens[-1] = 5
+    lens[batch // 2] = 0
+    run(batch + heads, lens, heads, page, window, sinks)
+
+
+def test_same_in_every_run():
+    for heads, window in ((8, 400), (64, 100), (64, 3000)):
+        a = run(1, [5000, 90, 700, 0], heads, 64, window, 4)
+        b = run(1, [5000, 90, 700, 0], heads, 64, window, 4)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_timeout_in_a_cluster():
+    """A wait that runs out is said; nothing is written for that request, and the next call is right."""
+    g = torch.Generator()
+    g.manual_seed(5)
+    cache, flat, table, slots, counts = windowed(g, [900, 900], 64, 500, 4)
+    q = torch.randn(2, 8, 576, generator=g).to(BF)
+    n = torch.tensor([900, 900], dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    abi.mla_tree_test_wait_limits(9, 50_000_000)  # of the second request's eight parts, all but the first
+    try:
+        out, lse = decode(q.cuda(), cache, table.cuda(), n, 500, 4, status)
+        assert int(status) == abi.DEV_TIMEOUT
+    finally:
+        abi.mla_tree_test_wait_limits(-1, 0)
+    want = ref.decode(q, flat, slots, counts, 1, SCALE)
+    check(out[:1], lse[:1], tuple(w[:1] for w in want))
+    assert (out[1] == 7).all() and (lse[1] == 7).all()
+    status.zero_()
+    out, lse = decode(q.cuda(), cache, table.cuda(), n, 500, 4, status)
+    check(out, lse, want)
+    assert int(status) == 0
+
+
 @pytest.mark.parametrize("page", [64, 16, 7])
 def test_long_window_is_split(page):
     run(page, [40000, 12345], 16, page, 9000, 70)
@@ -121,17 +165,20 @@ def test_long_window_is_split(page):
 @pytest.mark.parametrize("heads,page", [(8, 64), (64, 16), (16, 5)])
 @pytest.mark.parametrize("window,sinks", [(1 << 20, 0), ((1 << 31) - 1, (1 << 31) - 1), (1, (1 << 31) - 1), (1001, 0), (1, 1000)])
 def test_all_visible_is_the_plain_call(heads, page, window, sinks):
-    """Bit for bit: the same tiles in the same shares."""
+    """Bit for bit where the table holds no more; else within the rounding of other splits."""
     g = torch.Generator()
     g.manual_seed(heads)
     lens = [0, 1, 500, 1001]
-    cache, flat, table, _, _ = windowed(g, lens, page, 1 << 20, 0)
-    q = torch.randn(4, heads, 576, generator=g).to(BF).cuda()
+    cache, flat, table, slots, counts = windowed(g, lens, page, 1 << 20, 0)
+    q = torch.randn(4, heads, 576, generator=g).to(BF)
     t, n = table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
-    out, lse = decode(q, cache, t, n, window, sinks)
+    out, lse = decode(q.cuda(), cache, t, n, window, sinks)
+    check(out, lse, ref.decode(q, flat, slots, counts, 1, SCALE))
+    if max(window, sinks) < table.shape[1] * page:
+        return
     ws = torch.zeros(abi.mla_paged_decode_workspace_bytes(4, heads), dtype=torch.uint8, device="cuda")
     out2, lse2 = torch.empty_like(out), torch.empty_like(lse)
-    abi.mla_paged_decode(q, cache, t, n, SCALE, out2, lse2, ws)
+    abi.mla_paged_decode(q.cuda(), cache, t, n, SCALE, out2, lse2, ws)
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
 
 
