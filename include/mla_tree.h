@@ -563,7 +563,7 @@ int mla_token_logprobs(const void* logits, int logits_type, int64_t row_stride, 
  *     new_lens[b]    = kv_lens[b] - n_b + counts[b]
  * first NULL: the token of each request's node 0 (a root that was decided
  * before), -1 where it has none. kv_lens holds the lengths with the drafts;
- * new_lens may be kv_lens.
+ * new_lens may be kv_lens, and next_tokens may be first.
  *   path: int32 [batch, max_accept]; counts, next_tokens, new_lens: int32 [batch]
  * A parent out of range sets MT_DEV_BAD_PARENT (that node is not taken); more
  * than MT_MAX_TREE nodes set MT_DEV_TREE_TOO_BIG, a decreasing qo_indptr, one
@@ -580,7 +580,8 @@ int mla_tree_accept(const int32_t* parents, const int32_t* tokens, const int32_t
  * Moves the accepted rows up, in every layer: with base = kv_lens[b] -
  * counts[b] (kv_lens: the new lengths), the row of position base + path[b, k]
  * goes to position base + k, k = 0, 1, ... in order. What mla_tree_accept
- * returns is what this takes. Rows behind the new length keep what they held
+ * returns is what this takes. The pages of these positions must be the
+ * request's own (mla_pages_fit makes them so). Rows behind the new length keep what they held
  * last. Layer l's cache is at cache + l * layer_stride (16-byte aligned; no two
  * layers' pages may overlap, but one layer's may lie between another's);
  * geometry, table and their checks are those of the paged calls.
@@ -613,6 +614,8 @@ int mla_pages_fork(const int32_t* parents, const int32_t* kv_lens, const int32_t
                    int32_t* refs, int64_t num_pages, int32_t* new_lens, int32_t* new_held,
                    int32_t* new_table, int64_t new_table_stride, int new_batch,
                    int32_t* dev_status, mt_stream_t stream);
+
+#define MT_MAX_FIT_PAGES (1 << 30)  /* pages of mla_pages_fit (more: MT_EUNSUPPORTED) */
 
 /*
  * Bytes of workspace mla_pages_fit needs (0 for arguments it would reject);

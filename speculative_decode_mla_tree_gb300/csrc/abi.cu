@@ -586,7 +586,7 @@ int mla_pages_fork(const int32_t* parents, const int32_t* kv_lens, const int32_t
 }
 
 size_t mla_pages_fit_workspace_bytes(int batch, int64_t num_pages) {
-  if (batch < 0 || batch > 65535 || num_pages < 0 || num_pages > INT32_MAX) return 0;
+  if (batch < 0 || batch > 65535 || num_pages < 0 || num_pages > MT_MAX_FIT_PAGES) return 0;
   return pages_fit_workspace(batch, num_pages);
 }
 
@@ -600,7 +600,7 @@ int mla_pages_fit(const int32_t* kv_lens, const int32_t* want_lens, int32_t* hel
   if (batch == 0) return MT_OK;
   if (!kv_lens || !want_lens || !held || !copies || (max_pages > 0 && !block_table) || (num_pages > 0 && !refs))
     return MT_EINVAL;
-  if (batch > 65535) return MT_EUNSUPPORTED;
+  if (batch > 65535 || num_pages > MT_MAX_FIT_PAGES) return MT_EUNSUPPORTED;
   if (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < pages_fit_workspace(batch, num_pages))
     return MT_EWORKSPACE;
   const FitArgs a = {kv_lens, want_lens, held, block_table, table_stride, batch, max_pages, refs, num_pages,

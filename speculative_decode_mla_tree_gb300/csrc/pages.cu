@@ -347,7 +347,8 @@ __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const CopyArgs
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const unsigned piece = blockIdx.x % pieces, i = blockIdx.x / pieces / a.layers, layer = blockIdx.x / pieces % a.layers;
-  const int src = __ldg(a.copies + 3 * i), dst = __ldg(a.copies + 3 * i + 1), rows = __ldg(a.copies + 3 * i + 2);
+  const int32_t* entry = a.copies + 3 * (int64_t)i;
+  const int src = __ldg(entry), dst = __ldg(entry + 1), rows = __ldg(entry + 2);
   if (dst == -1) return;
   if (src < 0 || src >= a.num_pages || dst < 0 || dst >= a.num_pages || rows < 0 || rows > a.page_size) {
     if (threadIdx.x == 0 && layer == 0 && piece == 0) flag(a.status, MT_DEV_BAD_SLOT);

@@ -96,6 +96,19 @@ def test_equal_siblings_and_many_requests():
     check_accept(trees, [len(t[0]) + 3 for t in trees], 12, [0] * 1500)
 
 
+def test_next_tokens_over_first():
+    """A loop that keeps one buffer for the tokens to go on with."""
+    r = random.Random(8)
+    trees = [forest(r, n, 2) for n in (9, 0, 300, 1)]
+    n = [len(t[0]) for t in trees]
+    flat = [ints([x for t in trees for x in t[i]]) for i in range(3)]
+    keep = ints([1, 1, 0, 1])
+    path, counts = torch.zeros(4, 6, dtype=torch.int32, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda")
+    abi.mla_tree_accept(*flat, ints([0, n[0], n[0], n[0] + n[2], sum(n)]), ints(n), path, counts, keep, counts.clone(), first=keep)
+    want = [walk(*t, f, 6) for t, f in zip(trees, (1, 1, 0, 1))]
+    assert keep.tolist() == [w[1] for w in want] and counts.tolist() == [len(w[0]) for w in want]
+
+
 def test_targets_of_any_stride():
     r = random.Random(6)
     t = forest(r, 50, 2)

@@ -93,7 +93,7 @@ def test_workspaces(lib):
     assert n > 0
     for kw in (dict(ws=None), dict(ws=FAKE + 8), dict(ws_bytes=n - 1)):
         assert call(lib, "mla_pages_fit", **kw) == abi.MT_EWORKSPACE
-    for bad in ((-1, 10), (65536, 10), (2, -1), (2, 1 << 31)):
+    for bad in ((-1, 10), (65536, 10), (2, -1), (2, (1 << 30) + 1), (2, 1 << 31)):
         assert abi.mla_pages_fit_workspace_bytes(*bad) == 0
     n = abi.mla_paged_decode_workspace_bytes(2, 8)
     assert call(lib, "mla_paged_decode_window", ws_bytes=n - 1) == abi.MT_EWORKSPACE
@@ -108,6 +108,7 @@ def test_more_than_supported(lib):
     assert call(lib, "mla_pages_fork", old=65536, table=1 << 40) == abi.MT_EUNSUPPORTED
     assert call(lib, "mla_pages_fork", new=65536, new_table=1 << 40) == abi.MT_EUNSUPPORTED
     assert call(lib, "mla_pages_fit", batch=65536) == abi.MT_EUNSUPPORTED
+    assert call(lib, "mla_pages_fit", num_pages=(1 << 30) + 1) == abi.MT_EUNSUPPORTED
     assert call(lib, "mla_paged_copy", n=1 << 31) == abi.MT_EUNSUPPORTED
     assert call(lib, "mla_paged_copy", layers=BIG) == abi.MT_EUNSUPPORTED
 
