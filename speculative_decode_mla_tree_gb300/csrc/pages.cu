@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const ForkArgs
 //
 // What a call decides about one page depends on every request that holds it, so
 // the steps are separated by barriers; all but the search for free pages are
-// the first block's, four lanes a request, whose barriers are cheap:
+// the first block's, whose barriers are cheap:
 //   1  mark: a cell that will be written to and whose page p others hold, too,
 //      becomes -2 - p; count what each request needs;
 //   2  take back the references of marked cells and of pages given back;
@@ -74,18 +74,25 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const ForkArgs
 //   4  tell who keeps; sums of the needs before each request;
 //   5  write the lowest free pages down in order, by all blocks;
 //   6  hand them out, or put everything back.
-// Bound by the latency of these steps (a round to L2 each), and of the search,
-// which reads refs up to the last page that it takes.
-constexpr int kFitThreads = 1024;
+// A decoding step writes to one column of a request: a thread looks after it, and
+// keeps what it needs again in registers. A warp does for requests of more
+// columns (prompts). Bound by latency: each step is one or two rounds to L2, and
+// the instructions and barriers of many warps in one SM cost as much as these (256
+// requests: 10.4 us in the kernel with four lanes each, 9.1 with one of 1024 threads,
+// 7.4 with one of 256). The search reads refs up to the last page that it takes.
+constexpr int kFitThreads = 1024;     // or kFewThreads, for up to as many requests
+constexpr int kFewThreads = 256;
 constexpr int kFitWarps = kFitThreads / 32;
-constexpr int kLanes = 4;             // of a request
-constexpr int kAtOnce = kFitThreads / kLanes;
 constexpr int kFitCtas = 8;
-constexpr int kScan = 8;              // pages a thread looks at at a time
+constexpr int kScan = 32;             // pages a thread looks at at a time
 constexpr int kClaim = -(1 << 30);
+
+constexpr int kNear = 2048;           // numbers of each kind in shared memory
 
 struct FitShared {
   int sums[kFitWarps];
+  int before[kNear], frees[kNear];
+  int longs;
 };
 
 __device__ __forceinline__ uint32_t ctas() {
@@ -117,7 +124,7 @@ __device__ __forceinline__ int block_scan(FitShared& sh, int v, int* total) {
   __syncthreads();
   if (lane == 31) sh.sums[warp] = inc;
   __syncthreads();
-  int at = sh.sums[lane];
+  int at = lane < (int)blockDim.x / 32 ? sh.sums[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int u = __shfl_up_sync(kFull, at, o);
@@ -156,103 +163,208 @@ __device__ __forceinline__ Wish wish_of(const FitArgs& a, int b) {
   return w;
 }
 
-// f(column, page) for this lane's pages that request w gives back: those
-// behind its need, and those of the gap down to the first that is gone. group:
-// the lanes of the request, lane: this one's place among them.
-template <typename F>
-__device__ __forceinline__ void given_back(const Wish& w, unsigned group, int lane, F f) {
-  for (int c = w.need + lane; c < w.held; c += kLanes) f(c, w.row[c]);
-  for (int top = w.gap1; top > w.gap0; top -= kLanes) {
-    const int c = top - 1 - lane;
-    const int p = c >= w.gap0 ? w.row[c] : -1;
-    const unsigned gone = __ballot_sync(group, p == -1);
-    if ((gone & ((2u << (threadIdx.x & 31)) - 1)) == 0) f(c, p);
-    if (gone) break;
+// One request in the hands of L lanes (1 or 32).
+template <int L>
+struct Job {
+  const FitArgs& a;
+  int b;
+  Wish w;
+  int cell;  // this lane's first column: its page, -1, or a mark
+  int gap;   // this lane's first column of the gap, from above
+
+  __device__ __forceinline__ Job(const FitArgs& args, int request) : a(args), b(request), w(wish_of(args, request)), cell(-1), gap(-1) {
+    if (!w.ok) return;
+    if (w.w0 + lane() < min(w.w1, w.held)) cell = w.row[w.w0 + lane()];
+    if (w.gap1 - 1 - lane() >= w.gap0) gap = w.row[w.gap1 - 1 - lane()];
   }
-}
+  static __device__ __forceinline__ int lane() { return L == 1 ? 0 : threadIdx.x & 31; }
+  static __device__ __forceinline__ unsigned ballot(bool v) { return L == 1 ? (unsigned)v : __ballot_sync(kFull, v); }
+  static __device__ __forceinline__ int sum(int v) { return L == 1 ? v : __reduce_add_sync(kFull, v); }
+  __device__ __forceinline__ bool known(int p) const { return p >= 0 && p < a.num_pages; }
+  __device__ __forceinline__ int get(int c) const { return c == w.w0 + lane() ? cell : w.row[c]; }
+  __device__ __forceinline__ void set(int c, int v) {
+    if (c == w.w0 + lane()) cell = v;
+    else w.row[c] = v;
+  }
+  // f(column, page) for this lane's pages that are given back: those behind
+  // the need, and those of the gap down to the first that is gone.
+  template <typename F>
+  __device__ __forceinline__ void given_back(F f) {
+    for (int c = w.need + lane(); c < w.held; c += L) f(c, w.row[c]);
+    for (int top = w.gap1; top > w.gap0; top -= L) {
+      const int c = top - 1 - lane();
+      const int p = c < w.gap0 ? -1 : top == w.gap1 ? gap : w.row[c];
+      const unsigned gone = ballot(p == -1);
+      if ((gone & ((2u << lane()) - 1)) == 0) f(c, p);
+      if (gone) break;
+    }
+  }
+  // f(column, mark) for the marked ones.
+  template <typename F>
+  __device__ __forceinline__ void marked(F f) {
+    if (!w.ok) return;
+    for (int c = w.w0 + lane(); c < min(w.w1, w.held); c += L)
+      if (const int p = get(c); p < -1) f(c, -2 - p);
+  }
+
+  __device__ __forceinline__ int mark() {
+    int need = 0;
+    if (!w.ok) {
+      if (lane() == 0) flag(a.status, MT_DEV_BAD_INDPTR);
+      return 0;
+    }
+    for (int c = w.w0 + lane(); c < w.w1; c += L) {
+      const int p = c < w.held ? get(c) : -1;
+      if (known(p)) {
+        if (__ldcg(a.refs + p) <= 1) continue;
+        set(c, -2 - p);
+      } else if (p != -1) {
+        flag(a.status, MT_DEV_BAD_SLOT);
+        set(c, -1);
+      }
+      ++need;
+    }
+    return sum(need);
+  }
+  // What the next step's Job of this request has to find in the table.
+  __device__ __forceinline__ void leave() {
+    if ((L > 1 || b >= (int)blockDim.x) && w.ok && w.w0 + lane() < min(w.w1, w.held)) w.row[w.w0 + lane()] = cell;
+  }
+  __device__ __forceinline__ void take_back() {
+    marked([&](int, int p) { atomicSub(a.refs + p, 1); });
+    if (w.ok)
+      given_back([&](int, int p) {
+        if (known(p)) atomicSub(a.refs + p, 1);
+        else if (p != -1) flag(a.status, MT_DEV_BAD_SLOT);
+      });
+  }
+  __device__ __forceinline__ bool claim() {
+    bool any = false;
+    marked([&](int, int p) {
+      if (__ldcg(a.refs + p) > 0) return;
+      atomicMin(a.refs + p, kClaim + b);
+      any = true;
+    });
+    return any;
+  }
+  __device__ __forceinline__ int keep() {
+    int kept = 0;
+    marked([&](int c, int p) {
+      if (__ldcg(a.refs + p) != kClaim + b) return;  // nobody else finds itself there
+      a.refs[p] = 1;
+      set(c, p);
+      ++kept;
+    });
+    return sum(kept);
+  }
+  __device__ __forceinline__ void put_back() {
+    marked([&](int c, int p) {
+      w.row[c] = p;
+      atomicAdd(a.refs + p, 1);
+    });
+    if (w.ok)
+      given_back([&](int, int p) {
+        if (known(p)) atomicAdd(a.refs + p, 1);
+      });
+    say(-1, -1, 0);
+  }
+  __device__ __forceinline__ void hand_out(const int32_t* pages) {
+    int src = -1, dst = -1, rows = 0;
+    if (w.ok) {
+      given_back([&](int c, int) { w.row[c] = -1; });
+      for (int c = w.held + lane(); c < (w.w1 > w.w0 ? w.w0 : w.need); c += L) w.row[c] = -1;
+      for (int c0 = w.w0; c0 < w.w1; c0 += L) {
+        const int c = c0 + lane();
+        const int p = c < w.held && c < w.w1 ? get(c) : -1;
+        const bool take = c < w.w1 && p < 0;
+        const unsigned m = ballot(take);
+        if (take) {
+          const int page = pages[__popc(m & ((1u << lane()) - 1))];
+          w.row[c] = page;
+          a.refs[page] = 1;
+          if (c == w.w0 && p < -1 && w.len % a.page_size > 0) src = -2 - p, dst = page, rows = w.len % a.page_size;
+        }
+        pages += __popc(m);
+      }
+      if (lane() == 0) a.held[b] = w.need;  // (the other lanes have long read it)
+    }
+    say(src, dst, rows);
+  }
+  __device__ __forceinline__ void say(int src, int dst, int rows) {
+    if (lane() != 0) return;  // column w0 is lane 0's
+    a.copies[3 * b] = src;
+    a.copies[3 * b + 1] = dst;
+    a.copies[3 * b + 2] = rows;
+  }
+};
 
 __global__ void __launch_bounds__(kFitThreads) pages_fit_kernel(const FitArgs a) {
   __shared__ FitShared sh;
-  const int tid = threadIdx.x, lane = tid % kLanes;
-  const unsigned group = ((1u << kLanes) - 1) << (tid & 31 & ~(kLanes - 1));
+  const int tid = threadIdx.x, threads = blockDim.x;
   const int n = ctas(), me = cta();
-  int32_t* const frees = a.ws;              // [num_pages] the lowest free pages, in order
-  int32_t* const before = frees + a.num_pages;  // [batch] needs, then their sums before each request
-  int32_t* const totals = before + a.batch;     // needs; then free pages of each block
+  int32_t* frees = a.ws;                    // [num_pages] the lowest free pages, in order
+  int32_t* before = a.ws + a.num_pages;     // [batch] needs, then their sums before each request
+  int32_t* const longs = before + a.batch;  // [batch] the requests of many columns
+  int32_t* const is_long = longs + a.batch; // [batch] whether it is one, from request `threads` on
+  int32_t* const totals = is_long + a.batch;  // needs; then free pages of each block
+  if (a.batch <= kNear) before = sh.before;
+  if (tid == 0) sh.longs = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  auto known = [&](int p) { return p >= 0 && p < a.num_pages; };
-  // this thread's part of the requests, in the first block
-  const int b0 = me == 0 ? tid / kLanes : a.batch;
-  Wish mine = {};
-  if (b0 < a.batch) mine = wish_of(a, b0);
 
-  for (int b = b0; b < a.batch; b += kAtOnce) {
-    const Wish w = b == b0 ? mine : wish_of(a, b);
-    int need = 0;
-    if (!w.ok) {
-      if (lane == 0) flag(a.status, MT_DEV_BAD_INDPTR);
-    } else {
-      for (int c = w.w0 + lane; c < w.w1; c += kLanes) {
-        const int p = c < w.held ? w.row[c] : -1;
-        if (known(p)) {
-          if (__ldcg(a.refs + p) <= 1) continue;
-          w.row[c] = -2 - p;
-        } else if (p != -1) {
-          flag(a.status, MT_DEV_BAD_SLOT);
-          w.row[c] = -1;
-        }
-        ++need;
-      }
-    }
-#pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) need += __shfl_xor_sync(group, need, o);
-    if (lane == 0) before[b] = need;
-  }
+  int64_t asked = 0;
+  // Requests tid, tid + threads, ... are this thread's, but for those that a
+  // warp takes: of several columns to write or give back, or with a window that has
+  // just come to bear. The first one's state stays in registers.
+  const bool has = me == 0 && tid < a.batch;
+  auto many = [&](const Job<1>& j) {
+    const Wish& w = j.w;
+    return w.ok && (w.w1 - w.w0 > 2 || w.held - w.need > 2 || (w.gap1 - 4 >= w.gap0 && j.gap != -1 && w.row[w.gap1 - 4] != -1));
+  };
+  Job<1> mine(a, has ? tid : 0);
+  const bool single = has && !many(mine);
   __syncthreads();
-  for (int b = b0; b < a.batch; b += kAtOnce) {
-    const Wish w = b == b0 ? mine : wish_of(a, b);
-    if (!w.ok) continue;
-    for (int c = w.w0 + lane; c < min(w.w1, w.held); c += kLanes)
-      if (w.row[c] < -1) atomicSub(a.refs + (-2 - w.row[c]), 1);
-    given_back(w, group, lane, [&](int, int p) {
-      if (known(p)) atomicSub(a.refs + p, 1);
-      else if (p != -1) flag(a.status, MT_DEV_BAD_SLOT);
-    });
-  }
+  auto each = [&](auto f) {
+    if (me != 0) return;
+    if (single) f(mine);
+    for (int b = tid + threads; b < a.batch; b += threads) {
+      if (is_long[b]) continue;
+      Job<1> j(a, b);
+      f(j);
+    }
+    for (int i = tid >> 5; i < sh.longs; i += threads / 32) {
+      Job<32> j(a, longs[i]);
+      f(j);
+    }
+  };
+  if (has && !single) longs[atomicAdd(&sh.longs, 1)] = tid;
+  if (me == 0)
+    for (int b = tid + threads; b < a.batch; b += threads) {
+      is_long[b] = many(Job<1>(a, b));
+      if (is_long[b]) longs[atomicAdd(&sh.longs, 1)] = b;
+    }
+  __syncthreads();
+
+  each([&](auto& j) {
+    const int need = j.mark();
+    if (j.lane() == 0) before[j.b] = need;
+    j.leave();
+  });
+  __syncthreads();
+  each([&](auto& j) { j.take_back(); });
   __syncthreads();
   bool claims = false;  // a page that nobody is left to hold
-  for (int b = b0; b < a.batch; b += kAtOnce) {
-    const Wish w = b == b0 ? mine : wish_of(a, b);
-    if (!w.ok) continue;
-    for (int c = w.w0 + lane; c < min(w.w1, w.held); c += kLanes)
-      if (w.row[c] < -1 && __ldcg(a.refs + (-2 - w.row[c])) <= 0) {
-        atomicMin(a.refs + (-2 - w.row[c]), kClaim + b);
-        claims = true;
-      }
-  }
+  each([&](auto& j) { claims |= j.claim(); });
   if (__syncthreads_or(claims)) {
-    for (int b = b0; b < a.batch; b += kAtOnce) {
-      const Wish w = b == b0 ? mine : wish_of(a, b);
-      if (!w.ok) continue;
-      int keeps = 0;
-      for (int c = w.w0 + lane; c < min(w.w1, w.held); c += kLanes) {
-        const int p = w.row[c];
-        if (p < -1 && __ldcg(a.refs + (-2 - p)) == kClaim + b) {  // nobody else finds itself there
-          a.refs[-2 - p] = 1;
-          w.row[c] = -2 - p;
-          ++keeps;
-        }
-      }
-#pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1) keeps += __shfl_xor_sync(group, keeps, o);
-      if (lane == 0 && keeps) before[b] -= keeps;
-    }
+    each([&](auto& j) {
+      const int kept = j.keep();
+      if (kept && j.lane() == 0) before[j.b] -= kept;
+      j.leave();
+    });
     __syncthreads();
   }
-  int64_t asked = 0;
   if (me == 0) {
-    for (int b = 0; b < a.batch; b += kFitThreads) {
+    for (int b = 0; b < a.batch; b += threads) {
       int sum;
       const int v = b + tid < a.batch ? before[b + tid] : 0;
       const int at = block_scan(sh, v, &sum);
@@ -261,14 +373,16 @@ __global__ void __launch_bounds__(kFitThreads) pages_fit_kernel(const FitArgs a)
     }
     if (n > 1 && tid == 0) totals[0] = (int)asked;
   }
+  if (n == 1 && asked <= kNear) frees = sh.frees;
   // Free pages: with several blocks each first counts those of its run of pages.
-  const int p0 = (int)(a.num_pages * me / n), p1 = (int)(a.num_pages * (me + 1) / n);
+  const int p0 = (int)(a.num_pages * me / n) & -4, p1 = me + 1 < n ? (int)(a.num_pages * (me + 1) / n) & -4 : (int)a.num_pages;
+  const bool whole = ((uintptr_t)(a.refs + p0) & 15) == 0;  // runs of four in one load
   int at = 0, there = 0;
   all(n);
   if (n > 1) {
     int free = 0, sum;
 #pragma unroll 8
-    for (int p = p0 + tid; p < p1; p += kFitThreads) free += __ldcg(a.refs + p) == 0;
+    for (int p = p0 + tid; p < p1; p += threads) free += __ldcg(a.refs + p) == 0;
     block_scan(sh, free, &sum);
     if (tid == 0) totals[1 + me] = sum;
     asked = __ldcg(totals);
@@ -280,12 +394,20 @@ __global__ void __launch_bounds__(kFitThreads) pages_fit_kernel(const FitArgs a)
     }
   }
   if (n == 1 || asked <= there)
-    for (int p = p0; p < p1 && at < asked; p += kFitThreads * kScan) {
-      int is = 0, sum;
+    for (int p = p0; p < p1 && at < asked; p += threads * kScan) {
+      unsigned is = 0;
+      int sum;
+      const int q0 = p + tid * kScan;
+      if (q0 + kScan <= p1 && whole) {
 #pragma unroll
-      for (int i = 0; i < kScan; ++i) {
-        const int q = p + tid * kScan + i;
-        if (q < p1 && __ldcg(a.refs + q) == 0) is |= 1 << i;
+        for (int i = 0; i < kScan; i += 4) {
+          const int4 r = __ldcg(reinterpret_cast<const int4*>(a.refs + q0 + i));
+          is |= (unsigned)((r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3) << i;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kScan; ++i)
+          if (q0 + i < p1 && __ldcg(a.refs + q0 + i) == 0) is |= 1u << i;
       }
       int r = at + block_scan(sh, __popc(is), &sum);
       for (; is && r < asked; is &= is - 1, ++r) frees[r] = p + tid * kScan + __ffs(is) - 1;
@@ -294,45 +416,12 @@ __global__ void __launch_bounds__(kFitThreads) pages_fit_kernel(const FitArgs a)
   const bool enough = n == 1 ? asked <= at : asked <= there;
   all(n);
 
-  if (!enough && me == 0 && tid == 0) flag(a.status, MT_DEV_NO_PAGES);
-  for (int b = b0; b < a.batch; b += kAtOnce) {
-    const Wish w = b == b0 ? mine : wish_of(a, b);
-    int copy[3] = {-1, -1, 0};
-    if (w.ok && !enough) {
-      for (int c = w.w0 + lane; c < min(w.w1, w.held); c += kLanes)
-        if (w.row[c] < -1) {
-          const int p = -2 - w.row[c];
-          w.row[c] = p;
-          atomicAdd(a.refs + p, 1);
-        }
-      given_back(w, group, lane, [&](int, int p) {
-        if (known(p)) atomicAdd(a.refs + p, 1);
-      });
-    } else if (w.ok) {
-      given_back(w, group, lane, [&](int c, int) { w.row[c] = -1; });
-      for (int c = w.held + lane; c < (w.w1 > w.w0 ? w.w0 : w.need); c += kLanes) w.row[c] = -1;
-      int rank = before[b];
-      for (int c0 = w.w0; c0 < w.w1; c0 += kLanes) {
-        const int c = c0 + lane;
-        const int p = c < w.held && c < w.w1 ? w.row[c] : -1;
-        const bool take = c < w.w1 && p < 0;
-        const unsigned m = __ballot_sync(group, take);
-        if (take) {
-          const int page = __ldcg(frees + rank + __popc(m & ((1u << (tid & 31)) - 1)));
-          w.row[c] = page;
-          a.refs[page] = 1;
-          if (c == w.w0 && p < -1 && w.len % a.page_size > 0) copy[0] = -2 - p, copy[1] = page, copy[2] = w.len % a.page_size;
-        }
-        rank += __popc(m);
-      }
-      __syncwarp(group);  // all lanes have read held
-      if (lane == 0) a.held[b] = w.need;
-    }
-    if (lane == 0) {  // column w0 is its
-#pragma unroll
-      for (int i = 0; i < 3; ++i) a.copies[3 * b + i] = copy[i];
-    }
+  if (enough) {
+    each([&](auto& j) { j.hand_out(frees + before[j.b]); });
+    return;
   }
+  if (me == 0 && tid == 0) flag(a.status, MT_DEV_NO_PAGES);
+  each([&](auto& j) { j.put_back(); });
 }
 
 // ------------------------------------------------------------------- copy
@@ -380,7 +469,7 @@ void configure(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, unsigned bloc
 }  // namespace
 
 size_t pages_fit_workspace(int batch, int64_t num_pages) {
-  return ((size_t)num_pages + (size_t)batch + 1 + kFitCtas) * sizeof(int32_t);
+  return ((size_t)num_pages + 3 * (size_t)batch + 1 + kFitCtas) * sizeof(int32_t);
 }
 
 int64_t paged_copy_blocks(const CopyArgs& a) {
@@ -400,7 +489,7 @@ cudaError_t launch_pages_fit(const FitArgs& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
   const unsigned ctas = a.num_pages > 32768 ? kFitCtas : 1;
-  configure(cfg, attr, ctas, kFitThreads, stream);
+  configure(cfg, attr, ctas, a.batch <= kFewThreads ? kFewThreads : kFitThreads, stream);
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim = {ctas, 1, 1};
   cfg.numAttrs = 2;

@@ -114,7 +114,8 @@ def fit(m, table, held, lens, refs, want, window=0, sinks=0):
 
 
 @pytest.mark.parametrize("batch,page,width,pages", [(1, 1, 40, 50), (3, 4, 30, 90), (8, 16, 12, 70), (40, 8, 20, 500),
-                                                    (65, 64, 9, 400), (300, 4, 9, 2000), (20, 8, 16, 40000)])
+                                                    (65, 64, 9, 400), (300, 4, 9, 2000), (20, 8, 16, 40000),
+                                                    (1300, 4, 9, 9000), (2100, 2, 40, 50000)])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (9, 2), (30, 17)])
 def test_lives_of_branches(batch, page, width, pages, window, sinks):
     """Prompts, single tokens, forks, drops, cuts and reorderings by chance, every state compared."""
