@@ -90,15 +90,15 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
   return r;
 }
 
-// Values by 16 bytes. raised(): as fp32, none below kFloor (so that exp's
-// argument is finite); largest(): ignores NaN. Rows whose maximum is below
-// kLow, where kFloor would count, are summed another way.
+// Values by 16 bytes. raised(): as fp32, -inf and the lowest of the type raised
+// to a floor, so that exp's argument is finite; largest(): ignores NaN. kLow is
+// above the floor.
 template <typename T>
 struct Vec;
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int kN = 8;
-  static constexpr float kFloor = -0x1.2cp+126f, kLow = -0.9e38f;  // 0xfe96, about -1e38
+  static constexpr float kLow = -0.9e38f;
   static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -117,7 +117,7 @@ struct Vec<__nv_bfloat16> {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      uint32_t r;  // NaN stays NaN
+      uint32_t r;  // NaN stays NaN; 0xfe96: about -1e38
       asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w[i]), "r"(0xfe96fe96u));
       x[i] = pair(bf16_lo(r), bf16_hi(r));
     }
@@ -127,7 +127,7 @@ struct Vec<__nv_bfloat16> {
 template <>
 struct Vec<__half> {
   static constexpr int kN = 8;
-  static constexpr float kFloor = -65504.f, kLow = -65000.f;
+  static constexpr float kLow = -65000.f;
   static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -161,7 +161,7 @@ struct Vec<__half> {
 template <>
 struct Vec<float> {
   static constexpr int kN = 4;
-  static constexpr float kFloor = -1e38f, kLow = -0.9e38f;
+  static constexpr float kLow = -0.9e38f;
   static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[4]) {
     x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
   }
@@ -174,7 +174,7 @@ struct Vec<float> {
     float v[4];
     unpack(u, v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) asm("max.NaN.f32 %0, %1, %2;" : "=f"(v[i]) : "f"(v[i]), "f"(kFloor));
+    for (int i = 0; i < 4; ++i) asm("max.NaN.f32 %0, %1, %2;" : "=f"(v[i]) : "f"(v[i]), "f"(-1e38f));
     x[0] = pair(v[0], v[1]), x[1] = pair(v[2], v[3]);
   }
   static __device__ __forceinline__ float one(float v) { return v; }
@@ -440,18 +440,20 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
   p.head = part == 0 ? head : 0;
 
   float top = -INFINITY, second = -INFINITY, third = -INFINITY;
-  // sums in pairs, relative to a value that the largest so far is not far above (nor the value below the floor)
-  float ref = Vec<T>::kFloor, limit = -INFINITY;
-  Pair s2 = 0, t2 = 0, neg = pair(-ref, -ref);
+  // Sums in pairs, relative to 2^ref: an exponent is one fma, rounded once. The
+  // largest value so far is not far above ref (values up to kLow are as good as
+  // masked here; a row of them alone is summed again).
+  float ref = 0.f, limit = Vec<T>::kLow;
+  Pair s2 = 0, t2 = 0, neg = 0;
   const Pair log2e = pair(kLog2e, kLog2e);
   int at = p.lo + tid, at2 = at;
-  uint4 next[kUnroll];
-  auto load = [&](int v0) {
+  auto load = [&](uint4 (&u)[kUnroll], int v0) {
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i)
-      if (v0 + i * kThreads < p.hi) next[i] = load16(p.vec + v0 + i * kThreads);
+      if (v0 + i * kThreads < p.hi) u[i] = load16(p.vec + v0 + i * kThreads);
   };
-  load(p.lo + tid);
+  uint4 next[kUnroll];
+  load(next, p.lo + tid);
   // the given tokens' values are asked for behind the first of the row
   auto value_at = [&](int g, bool& there) {
     const int token = __ldg(a.tokens + r * a.token_stride + g);
@@ -473,13 +475,13 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
     uint4 now[kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) now[i] = next[i];
-    load(v0 + kUnroll * kThreads);
+    load(next, v0 + kUnroll * kThreads);
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      if (v0 + i * kThreads >= p.hi) break;
+      const int v = v0 + i * kThreads;
+      if (v >= p.hi) break;
       const float m = Vec<T>::largest(now[i]);
       // without a branch: over 32 lanes one would be taken nearly every time
-      const int v = v0 + i * kThreads;
       const bool first = m > top, next_best = m > second;
       third = fmaxf(third, fminf(m, second));
       second = fmaxf(second, fminf(m, top));
@@ -487,20 +489,19 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
       top = fmaxf(top, m);
       at = first ? v : at;
       if (m > limit) {
-        // sums relative to this value from here on
-        const float to = fmaxf(m, Vec<T>::kFloor), d = fmaxf((ref - to) * kLog2e, -1e4f);
+        const float to = m * kLog2e, d = fmaxf(fminf(ref - to, 0.f), -1e4f);
         const Pair d2 = pair(d, d), f2 = pair(ex2(d), ex2(d));
         t2 = mul2(f2, fma2(d2, s2, t2));
         s2 = mul2(f2, s2);
         ref = to;
-        neg = pair(-ref, -ref);
+        neg = pair(-to, -to);
         limit = m + kSlack;
       }
       Pair x[E / 2];
       Vec<T>::raised(now[i], x);
 #pragma unroll
       for (int j = 0; j < E / 2; ++j) {
-        const Pair y = mul2(add2(x[j], neg), log2e);
+        const Pair y = fma2(x[j], log2e, neg);
         const float2 h = halves(y);
         const Pair e = pair(ex2(h.x), ex2(h.y));
         s2 = add2(s2, e);
@@ -512,9 +513,13 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
   // this CTA's sums, in a fixed order, and the bound
   {
     const float2 hs = halves(s2), ht = halves(t2);
-    Sums w = {ref, hs.x + hs.y, ht.x + ht.y};
-    if (top == -INFINITY && w.s == w.s) w = {-INFINITY, 0.f, 0.f};  // counted as the floor
-    const float m = fmaxf(u.m, fmaxf(w.m, top));
+    Sums w = {top, hs.x + hs.y, ht.x + ht.y};
+    if (top > Vec<T>::kLow) {  // relative to the largest value: 2^(ref - top log2 e), of at most kSlack
+      const float d = -fmaf(top, kLog2e, -ref), f = ex2(d);
+      w.t = f * fmaf(d, w.s, w.t);
+      w.s *= f;
+    }
+    const float m = fmaxf(u.m, top);
     raise(u, m);
     raise(w, m);
     u.s += w.s;
