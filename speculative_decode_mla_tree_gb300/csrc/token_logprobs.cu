@@ -45,6 +45,7 @@ constexpr int kUnroll = 4;
 constexpr float kSlack = 4.f;         // larger ones cost bits of the entropy (a difference), smaller ones branches
 constexpr int kMaxTop = MT_MAX_TOP;   // 32
 constexpr int kMaxParts = 8;
+constexpr int kFew = 256;             // keys whose ranks are counted without another look (6 to 150 are usual)
 constexpr unsigned kFull = 0xffffffffu;
 
 typedef unsigned long long Key;
@@ -331,6 +332,50 @@ __device__ __forceinline__ Key common_bound(const Shared<kThreads>& sh, int lane
   return b;
 }
 
+// Whether these bounds are of one value.
+template <int kThreads>
+__device__ __forceinline__ bool all_equal(const Shared<kThreads>& sh, int lanes) {
+  const int full = bound_warps<kThreads>(lanes);
+  bool same = true;
+#pragma unroll
+  for (int i = 1; i < kThreads / 32; ++i)
+    if (i < full) same = same && sh.bound[i] >> 32 == sh.bound[0] >> 32;
+  return same && full > 1;
+}
+
+// Another bound: k keys of one warp. Where many values are the same (a masked
+// row's), their places make this the closer one. All threads.
+template <int kThreads>
+__device__ __noinline__ Key one_warps_bound(Shared<kThreads>& sh, Key own, int k) {
+  const Key w = warp_qth(own, k);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh.bound[threadIdx.x >> 5] = w;
+  __syncthreads();
+  Key b = 0;
+  for (int i = 0; i < kThreads / 32; ++i) b = larger(b, sh.bound[i]);
+  return b;
+}
+
+// Leaves those of the list's n keys that reach b. All threads.
+template <int kThreads>
+__device__ __noinline__ int drop_below(Shared<kThreads>& sh, Key b, int n) {
+  constexpr int kEach = (Shared<kThreads>::kCap + kThreads - 1) / kThreads;
+  Key held[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int at = i * kThreads + threadIdx.x;
+    held[i] = at < n ? sh.list[at] : 0;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) sh.count = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    if (held[i] && held[i] >= b) push(sh, held[i]);
+  __syncthreads();
+  return sh.count;
+}
+
 // This CTA's share of a row: vectors [lo, hi), vector v being the 16 bytes from
 // place first + v * kN on, and the places before the first 16-byte boundary
 // (head of them, in the first part) and behind the last (tail, in the last).
@@ -529,9 +574,14 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
   if (lane == 0) sh.sums[warp] = u;
   const bool some = p.lo + tid < p.hi;
   // wherever in its vector the value is, its key is at least that of the last place
-  if (k > 0) warp_bound(sh, some ? make_key(top, p.first + at * E + E - 1) : 0, k, p.hi - p.lo);
+  const Key own = some ? make_key(top, p.first + at * E + E - 1) : 0;
+  if (k > 0) warp_bound(sh, own, k, p.hi - p.lo);
   __syncthreads();
-  const Key b = k > 0 ? common_bound(sh, p.hi - p.lo) : 0;
+  Key b = 0;
+  if (k > 0) {
+    b = common_bound(sh, p.hi - p.lo);
+    if (b && (value_of(b) == -INFINITY || all_equal(sh, p.hi - p.lo))) b = larger(b, one_warps_bound(sh, own, k));
+  }
 
   int n = 0;                           // keys in the list
   bool sorted = false;                 // or k in best
@@ -575,6 +625,7 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
     }
     if (items) __syncthreads();
     n = sh.count;
+    if (n > kFew && n <= sh.kCap) n = drop_below(sh, one_warps_bound(sh, own, k), n);
   }
   u = join(sh.sums, kWarps);
   const bool odd = u.s != u.s || u.t != u.t;  // NaN, +inf, or a maximum that differences from are infinite
