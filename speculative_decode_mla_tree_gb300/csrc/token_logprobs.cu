@@ -16,18 +16,19 @@
 // values. Threads that reach it look at their vector again; the few whose second
 // does, too, have all theirs looked at again by the whole block. What reaches the
 // bound, about 20 values for k up to 8 and 100 for 32, gets its rank by
-// counting. Where a row holds NaN, which comparisons do not see, or so many equal or
-// grouped values that the list of these overflows, the keys are found by a second
-// walk over the row, step by step, for which any content will do.
+// counting. Where the bounds of all warps are the same value, or -inf, k keys of a
+// single warp are the closer bound. Where a row holds NaN, which comparisons do not
+// see, or so many equal or grouped values that the list overflows, the keys are
+// found by a second walk over the row, step by step, for which any content will do.
 //
 // Few rows are split over clusters of up to 8 CTAs, which join through
 // distributed shared memory: no workspace and no second launch.
 //
-// What bounds it: with many rows HBM, and beside it the 16 exp a cycle of an SM (58
-// us of the 95 that 2048 rows of 131072 bf16 values take, 5.7 TB/s; fp32 rows of
-// half as many reach 6.7 TB/s). The best tokens cost 5 us of them for k = 5, 14 for
-// 32. 128 such rows take 13.3 us, 10.4 without tokens, where HBM needs 5: the start,
-// a ramp, and the joins. One row takes 5 to 6.6 us, nearly all of it latency.
+// What bounds it: with many rows HBM, and beside it the issue slots (2.7 of 4
+// instructions a cycle): 2048 rows of 131072 bf16 values take 92 us, 5.8 TB/s, fp32
+// rows of half as many 81, 6.6 TB/s. The best tokens cost 5 us of them for k = 5, 20
+// for 32. 128 such rows take 13 us, 9.8 without tokens, where HBM needs 5: the start,
+// a ramp, and the joins. One row takes 5 to 6.4 us, nearly all of it latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <float.h>
@@ -387,8 +388,8 @@ struct Share {
 };
 
 // The keys of a row of any content: one vector a thread at a time, bounded by
-// the best k so far and by the step's own common bound, after which the list
-// holds what is left.
+// the best k so far and by the step's own bounds, after which the list holds what
+// is left.
 template <typename T, int kThreads>
 __device__ __noinline__ void find_top(Shared<kThreads>& sh, const Share<T>& p, int k) {
   constexpr int E = Vec<T>::kN;
@@ -411,7 +412,8 @@ __device__ __noinline__ void find_top(Shared<kThreads>& sh, const Share<T>& p, i
     }
     warp_bound(sh, own, k, p.hi - v0);
     __syncthreads();
-    const Key b = larger(sh.best[k - 1] + 1, common_bound(sh, p.hi - v0));
+    Key b = larger(sh.best[k - 1] + 1, common_bound(sh, p.hi - v0));
+    b = larger(b, one_warps_bound(sh, own, k));
     if (own >= b && v < p.hi)
 #pragma unroll
       for (int i = 0; i < E; ++i) {
