@@ -426,10 +426,13 @@ __global__ void __launch_bounds__(kFitThreads) pages_fit_kernel(const FitArgs a)
 
 // ------------------------------------------------------------------- copy
 //
-// The first rows of pages to other pages, in every layer. HBM bound: a block
-// moves up to 28 rows, eight 16-byte loads a thread in flight.
+// The first rows of pages to other pages, in every layer. HBM bound (19200 rows in 8
+// layers 53.8 us, 6.6 TB/s). A page is cut into pieces until there are kCopyBlocks
+// blocks: entries that copy nothing or little cost theirs (256 entries of which 83 copy
+// 31 rows each in 8 layers: 8.0 us in two blocks an entry and layer, 9.2 in four).
+constexpr int kCopyBlocks = 16 * 152;
 constexpr int kCopyThreads = 256;
-constexpr int kCopyAhead = 8;
+constexpr int kCopyAhead = 6;
 constexpr int kCopyVecs = kCopyThreads * kCopyAhead;
 
 __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const CopyArgs a, const unsigned pieces) {
@@ -443,16 +446,18 @@ __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const CopyArgs
     if (threadIdx.x == 0 && layer == 0 && piece == 0) flag(a.status, MT_DEV_BAD_SLOT);
     return;
   }
-  const int64_t n = (int64_t)rows * kRowVec, v0 = (int64_t)piece * kCopyVecs + threadIdx.x;
+  const int64_t n = (int64_t)rows * kRowVec;
   const uint4* from = reinterpret_cast<const uint4*>(a.rows + layer * a.layer_stride + src * a.page_stride);
   uint4* to = reinterpret_cast<uint4*>(a.rows + layer * a.layer_stride + dst * a.page_stride);
-  uint4 v[kCopyAhead];
+  for (int64_t v0 = (int64_t)piece * kCopyVecs + threadIdx.x; v0 < n; v0 += (int64_t)pieces * kCopyVecs) {
+    uint4 v[kCopyAhead];
 #pragma unroll
-  for (int k = 0; k < kCopyAhead; ++k)
-    if (v0 + k * kCopyThreads < n) v[k] = from[v0 + k * kCopyThreads];
+    for (int k = 0; k < kCopyAhead; ++k)
+      if (v0 + k * kCopyThreads < n) v[k] = from[v0 + k * kCopyThreads];
 #pragma unroll
-  for (int k = 0; k < kCopyAhead; ++k)
-    if (v0 + k * kCopyThreads < n) to[v0 + k * kCopyThreads] = v[k];
+    for (int k = 0; k < kCopyAhead; ++k)
+      if (v0 + k * kCopyThreads < n) to[v0 + k * kCopyThreads] = v[k];
+  }
 }
 
 void configure(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, unsigned blocks, int threads, cudaStream_t stream) {
@@ -472,8 +477,15 @@ size_t pages_fit_workspace(int batch, int64_t num_pages) {
   return ((size_t)num_pages + 3 * (size_t)batch + 1 + kFitCtas) * sizeof(int32_t);
 }
 
+static int64_t copy_pieces(const CopyArgs& a) {
+  const int64_t all = ((int64_t)a.page_size * kRowVec + kCopyVecs - 1) / kCopyVecs;
+  const int64_t some = (kCopyBlocks + a.n * a.layers - 1) / (a.n * a.layers);
+  return some < all ? some : all;
+}
+
 int64_t paged_copy_blocks(const CopyArgs& a) {
-  const int64_t pieces = ((int64_t)a.page_size * kRowVec + kCopyVecs - 1) / kCopyVecs;
+  if (a.n > INT32_MAX) return -1;
+  const int64_t pieces = copy_pieces(a);
   const int64_t each = pieces * a.layers;
   return each > INT32_MAX || a.n > INT32_MAX / each ? -1 : a.n * each;
 }
@@ -500,7 +512,7 @@ cudaError_t launch_paged_copy(const CopyArgs& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
   configure(cfg, &attr, (unsigned)paged_copy_blocks(a), kCopyThreads, stream);
-  return cudaLaunchKernelEx(&cfg, paged_copy_kernel, a, (unsigned)(((int64_t)a.page_size * kRowVec + kCopyVecs - 1) / kCopyVecs));
+  return cudaLaunchKernelEx(&cfg, paged_copy_kernel, a, (unsigned)copy_pieces(a));
 }
 
 }  // namespace mt
