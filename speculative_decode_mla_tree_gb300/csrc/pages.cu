@@ -3,6 +3,8 @@
 // refs[p] counts the table entries that hold page p; a page with 0 is free.
 // There is no other state, so no list can go stale, and "the lowest free pages,
 // in the order of requests and columns" says exactly which pages a call takes.
+#include <limits.h>
+
 #include "mt_common.cuh"
 #include "paged.h"
 
@@ -68,12 +70,12 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const ForkArgs
 // the first block's, whose barriers are cheap:
 //   1  mark: a cell that will be written to and whose page p others hold, too,
 //      becomes -2 - p; count what each request needs;
-//   2  take back the references of marked cells and of pages given back;
+//   2  take back the references of marked cells and of pages given back, and find
+//      the lowest request that marked a page;
 //   3  where nobody is left, all that held the page asked for one of their own:
-//      the lowest of them keeps it (a minimum over refs[p], which is below 0 then);
-//   4  tell who keeps; sums of the needs before each request;
-//   5  write the lowest free pages down in order, by all blocks;
-//   6  hand them out, or put everything back.
+//      that lowest one keeps it; sums of the needs before each request;
+//   4  write the lowest free pages down in order, by all blocks;
+//   5  hand them out, or put everything back.
 // A decoding step writes to one column of a request: a thread looks after it, and
 // keeps what it needs again in registers. A warp does for requests of more
 // columns (prompts). Bound by latency: each step is one or two rounds to L2, and
@@ -85,7 +87,6 @@ constexpr int kFewThreads = 256;
 constexpr int kFitWarps = kFitThreads / 32;
 constexpr int kFitCtas = 8;
 constexpr int kScan = 32;             // pages a thread looks at at a time
-constexpr int kClaim = -(1 << 30);
 
 constexpr int kNear = 2048;           // numbers of each kind in shared memory
 
@@ -180,6 +181,7 @@ struct Job {
   static __device__ __forceinline__ int lane() { return L == 1 ? 0 : threadIdx.x & 31; }
   static __device__ __forceinline__ unsigned ballot(bool v) { return L == 1 ? (unsigned)v : __ballot_sync(kFull, v); }
   static __device__ __forceinline__ int sum(int v) { return L == 1 ? v : __reduce_add_sync(kFull, v); }
+  __device__ __forceinline__ int32_t* lowest() const { return a.ws + a.num_pages; }  // [num_pages], of marked pages
   __device__ __forceinline__ bool known(int p) const { return p >= 0 && p < a.num_pages; }
   __device__ __forceinline__ int get(int c) const { return c == w.w0 + lane() ? cell : w.row[c]; }
   __device__ __forceinline__ void set(int c, int v) {
@@ -218,6 +220,7 @@ struct Job {
       if (known(p)) {
         if (__ldcg(a.refs + p) <= 1) continue;
         set(c, -2 - p);
+        lowest()[p] = INT_MAX;
       } else if (p != -1) {
         flag(a.status, MT_DEV_BAD_SLOT);
         set(c, -1);
@@ -230,28 +233,28 @@ struct Job {
   __device__ __forceinline__ void leave() {
     if ((L > 1 || b >= (int)blockDim.x) && w.ok && w.w0 + lane() < min(w.w1, w.held)) w.row[w.w0 + lane()] = cell;
   }
-  __device__ __forceinline__ void take_back() {
-    marked([&](int, int p) { atomicSub(a.refs + p, 1); });
+  __device__ __forceinline__ bool take_back() {
+    bool any = false;
+    marked([&](int, int p) {
+      atomicSub(a.refs + p, 1);
+      atomicMin(lowest() + p, b);
+      any = true;
+    });
     if (w.ok)
       given_back([&](int, int p) {
         if (known(p)) atomicSub(a.refs + p, 1);
         else if (p != -1) flag(a.status, MT_DEV_BAD_SLOT);
       });
-  }
-  __device__ __forceinline__ bool claim() {
-    bool any = false;
-    marked([&](int, int p) {
-      if (__ldcg(a.refs + p) > 0) return;
-      atomicMin(a.refs + p, kClaim + b);
-      any = true;
-    });
     return any;
   }
   __device__ __forceinline__ int keep() {
     int kept = 0;
     marked([&](int c, int p) {
-      if (__ldcg(a.refs + p) != kClaim + b) return;  // nobody else finds itself there
-      a.refs[p] = 1;
+      const int left = __ldcg(a.refs + p), low = __ldcg(lowest() + p);
+      if (left > 0 || low != b) return;
+      // A row that holds a page twice keeps it in one column: a warp's lanes have to agree.
+      if (L == 1) a.refs[p] = 1;
+      else if (atomicCAS(a.refs + p, left, 1) != left) return;
       set(c, p);
       ++kept;
     });
@@ -303,7 +306,7 @@ __global__ void __launch_bounds__(kFitThreads) pages_fit_kernel(const FitArgs a)
   const int tid = threadIdx.x, threads = blockDim.x;
   const int n = ctas(), me = cta();
   int32_t* frees = a.ws;                    // [num_pages] the lowest free pages, in order
-  int32_t* before = a.ws + a.num_pages;     // [batch] needs, then their sums before each request
+  int32_t* before = a.ws + 2 * a.num_pages; // (behind Job::lowest) [batch] needs, then their sums before each request
   int32_t* const longs = before + a.batch;  // [batch] the requests of many columns
   int32_t* const is_long = longs + a.batch; // [batch] whether it is one, from request `threads` on
   int32_t* const totals = is_long + a.batch;  // needs; then free pages of each block
@@ -351,11 +354,9 @@ __global__ void __launch_bounds__(kFitThreads) pages_fit_kernel(const FitArgs a)
     j.leave();
   });
   __syncthreads();
-  each([&](auto& j) { j.take_back(); });
-  __syncthreads();
-  bool claims = false;  // a page that nobody is left to hold
-  each([&](auto& j) { claims |= j.claim(); });
-  if (__syncthreads_or(claims)) {
+  bool any = false;
+  each([&](auto& j) { any |= j.take_back(); });
+  if (__syncthreads_or(any)) {
     each([&](auto& j) {
       const int kept = j.keep();
       if (kept && j.lane() == 0) before[j.b] -= kept;
@@ -474,7 +475,7 @@ void configure(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, unsigned bloc
 }  // namespace
 
 size_t pages_fit_workspace(int batch, int64_t num_pages) {
-  return ((size_t)num_pages + 3 * (size_t)batch + 1 + kFitCtas) * sizeof(int32_t);
+  return (2 * (size_t)num_pages + 3 * (size_t)batch + 1 + kFitCtas) * sizeof(int32_t);
 }
 
 static int64_t copy_pieces(const CopyArgs& a) {

@@ -171,6 +171,24 @@ def test_all_writers_share_a_page():
     assert copies == [[1, 2, 4], [-1, -1, 0], [1, 3, 4]] and refs.tolist()[:4] == [3, 1, 1, 1]
 
 
+@pytest.mark.parametrize("columns", [2, 20])
+def test_a_page_twice_in_a_row_is_kept_once(columns):
+    """Entries count, not requests: whoever keeps a page keeps it in one column."""
+    m = Model(64, 4, 2, columns)
+    m.rows = [[7 if c in (0, columns - 1) else 20 + c for c in range(columns)] for _ in range(2)]
+    for row in m.rows:
+        for p in row:
+            m.refs[p] += 1
+    m.held, m.lens = [columns] * 2, [0] * 2
+    table, held, lens, refs = state(m)
+    copies, status = fit(m, table, held, lens, refs, [4 * columns] * 2)
+    assert status == 0 and held.tolist() == [columns] * 2
+    rows = table.tolist()
+    assert sorted(rows[0])[0] == 0 and sum(row.count(7) for row in rows) == 1 and 7 in rows[0]
+    assert len(set(rows[0] + rows[1])) == 2 * columns
+    assert refs.tolist() == [int(p in rows[0] + rows[1]) for p in range(64)]
+
+
 def test_exactly_enough_and_one_too_few():
     m = Model(6, 4, 2, 5)
     table, held, lens, refs = state(m)
