@@ -569,6 +569,8 @@ int mla_token_logprobs(const void* logits, int logits_type, int64_t row_stride, 
  * than MT_MAX_TREE nodes set MT_DEV_TREE_TOO_BIG, a decreasing qo_indptr, one
  * that passes total_q, or more nodes than kv_lens[b] MT_DEV_BAD_INDPTR: such a
  * request takes nothing, with next_tokens -1 and new_lens kv_lens.
+ * More than 65535 requests return MT_EUNSUPPORTED, here and in
+ * mla_paged_compact.
  */
 int mla_tree_accept(const int32_t* parents, const int32_t* tokens, const int32_t* targets,
                     int64_t target_stride, const int32_t* first, const int32_t* qo_indptr,
@@ -608,6 +610,7 @@ int mla_paged_compact(const int32_t* path, int64_t path_stride, int max_accept, 
  * A parent outside [-1, old_batch) sets MT_DEV_BAD_PARENT and counts as -1, a
  * held entry outside [0, max_pages] MT_DEV_BAD_INDPTR and counts as 0, a page
  * number that is neither -1 nor a page MT_DEV_BAD_SLOT and is copied as it is.
+ * More than 65535 rows of a side return MT_EUNSUPPORTED.
  */
 int mla_pages_fork(const int32_t* parents, const int32_t* kv_lens, const int32_t* held,
                    const int32_t* block_table, int64_t table_stride, int old_batch, int max_pages,
@@ -646,7 +649,9 @@ size_t mla_pages_fit_workspace_bytes(int batch, int64_t num_pages);
  * MT_DEV_NO_PAGES and changes nothing (copies are all (-1, -1, 0)). A bad
  * length (below 0, or want_lens beyond the table) or held entry sets
  * MT_DEV_BAD_INDPTR and leaves that request as it is; a page number that is
- * neither -1 nor a page sets MT_DEV_BAD_SLOT and counts as -1.
+ * neither -1 nor a page sets MT_DEV_BAD_SLOT and counts as -1 (and may be -1
+ * afterwards). A page that stands twice in a row is held twice.
+ * More than 65535 requests return MT_EUNSUPPORTED.
  *   copies: int32 [batch, 3]; workspace: 16-byte aligned
  */
 int mla_pages_fit(const int32_t* kv_lens, const int32_t* want_lens, int32_t* held,
