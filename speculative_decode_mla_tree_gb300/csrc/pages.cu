@@ -79,20 +79,23 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const ForkArgs
 // A decoding step writes to one column of a request: a thread looks after it, and
 // keeps what it needs again in registers. A warp does for requests of more
 // columns (prompts). Bound by latency: each step is one or two rounds to L2, and
-// the instructions and barriers of many warps in one SM cost as much as these (256
-// requests: 10.4 us in the kernel with four lanes each, 9.1 with one of 1024 threads,
-// 7.4 with one of 256). The search reads refs up to the last page that it takes.
-constexpr int kFitThreads = 1024;     // or kFewThreads, for up to as many requests
-constexpr int kFewThreads = 256;
+// the instructions and barriers of many warps in one SM cost as much as these, so a
+// block has few threads (256 requests: 10.4 us in the kernel with four lanes each, 9.1
+// with one of 1024 threads, 7.4 with one of 256; 512 requests that each replace a page
+// 10.2 us with 1024 threads, 8.6 with 512) and the registers to ask early for what the
+// search needs (32 beams forked, fitted and copied 10.8 -> 9.2 us, 256 19.6 -> 17.9).
+// The search reads refs up to the last page that it takes.
+constexpr int kFitThreads = 1024;     // or the fewest of 256 and 512 that are as many as the requests
 constexpr int kFitWarps = kFitThreads / 32;
 constexpr int kFitCtas = 8;
-constexpr int kScan = 32;             // pages a thread looks at at a time
+constexpr int kScan = 32;             // pages a thread looks at at a time (bits of a word)
 
 constexpr int kNear = 2048;           // numbers of each kind in shared memory
 
 struct FitShared {
   int sums[kFitWarps];
   int before[kNear], frees[kNear];
+  unsigned kept[kFitThreads];           // bits of the pages that a search looks at first
   int longs;
 };
 
@@ -247,7 +250,7 @@ struct Job {
       });
     return any;
   }
-  __device__ __forceinline__ int keep() {
+  __device__ __forceinline__ int keep(unsigned* bits, int words) {
     int kept = 0;
     marked([&](int c, int p) {
       const int left = __ldcg(a.refs + p), low = __ldcg(lowest() + p);
@@ -255,6 +258,7 @@ struct Job {
       // A row that holds a page twice keeps it in one column: a warp's lanes have to agree.
       if (L == 1) a.refs[p] = 1;
       else if (atomicCAS(a.refs + p, left, 1) != left) return;
+      if (p / 32 < words) atomicOr(&bits[p / 32], 1u << p % 32);
       set(c, p);
       ++kept;
     });
@@ -301,9 +305,12 @@ struct Job {
   }
 };
 
-__global__ void __launch_bounds__(kFitThreads) pages_fit_kernel(const FitArgs a) {
+template <int threads>
+__global__ void __launch_bounds__(threads, 1) pages_fit_kernel(const FitArgs a) {
+  constexpr bool kMany = threads == kFitThreads;  // more requests than threads, it may be
+  constexpr bool kEarly = !kMany;                 // its registers cost more than it gains there
   __shared__ FitShared sh;
-  const int tid = threadIdx.x, threads = blockDim.x;
+  const int tid = threadIdx.x;
   const int n = ctas(), me = cta();
   int32_t* frees = a.ws;                    // [num_pages] the lowest free pages, in order
   int32_t* before = a.ws + 2 * a.num_pages; // (behind Job::lowest) [batch] needs, then their sums before each request
@@ -312,6 +319,7 @@ __global__ void __launch_bounds__(kFitThreads) pages_fit_kernel(const FitArgs a)
   int32_t* const totals = is_long + a.batch;  // needs; then free pages of each block
   if (a.batch <= kNear) before = sh.before;
   if (tid == 0) sh.longs = 0;
+  if (kEarly) sh.kept[tid] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -330,7 +338,7 @@ __global__ void __launch_bounds__(kFitThreads) pages_fit_kernel(const FitArgs a)
   auto each = [&](auto f) {
     if (me != 0) return;
     if (single) f(mine);
-    for (int b = tid + threads; b < a.batch; b += threads) {
+    for (int b = tid + threads; kMany && b < a.batch; b += threads) {
       if (is_long[b]) continue;
       Job<1> j(a, b);
       f(j);
@@ -341,31 +349,49 @@ __global__ void __launch_bounds__(kFitThreads) pages_fit_kernel(const FitArgs a)
     }
   };
   if (has && !single) longs[atomicAdd(&sh.longs, 1)] = tid;
-  if (me == 0)
+  if (kMany && me == 0)
     for (int b = tid + threads; b < a.batch; b += threads) {
       is_long[b] = many(Job<1>(a, b));
       if (is_long[b]) longs[atomicAdd(&sh.longs, 1)] = b;
     }
   __syncthreads();
 
+  bool any = false;
   each([&](auto& j) {
     const int need = j.mark();
     if (j.lane() == 0) before[j.b] = need;
+    any |= need > 0;
     j.leave();
   });
-  __syncthreads();
-  bool any = false;
+  const bool some = __syncthreads_or(any);  // of the first block's requests
+  any = false;
   each([&](auto& j) { any |= j.take_back(); });
-  if (__syncthreads_or(any)) {
+  any = __syncthreads_or(any);
+  // One block asks for the first references of its search together with those
+  // that decide what is kept, and strikes out what is kept afterwards.
+  const bool early = kEarly && n == 1 && some && ((uintptr_t)a.refs & 15) == 0;
+  int4 refs[kScan / 4];
+  int ends[3];                              // behind the last run of four
+  const int end0 = (int)a.num_pages & -4;
+  if (early) {
+#pragma unroll
+    for (int i = 0; i < kScan / 4; ++i) {
+      const int q = tid * kScan + 4 * i;
+      refs[i] = q < end0 ? __ldcg(reinterpret_cast<const int4*>(a.refs + q)) : make_int4(1, 1, 1, 1);
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) ends[i] = tid == end0 / kScan && end0 + i < a.num_pages ? __ldcg(a.refs + end0 + i) : 1;
+  }
+  if (any) {
     each([&](auto& j) {
-      const int kept = j.keep();
+      const int kept = j.keep(sh.kept, kEarly ? threads : 0);
       if (kept && j.lane() == 0) before[j.b] -= kept;
       j.leave();
     });
     __syncthreads();
   }
   if (me == 0) {
-    for (int b = 0; b < a.batch; b += threads) {
+    for (int b = 0; b < a.batch && some; b += threads) {
       int sum;
       const int v = b + tid < a.batch ? before[b + tid] : 0;
       const int at = block_scan(sh, v, &sum);
@@ -376,7 +402,8 @@ __global__ void __launch_bounds__(kFitThreads) pages_fit_kernel(const FitArgs a)
   }
   if (n == 1 && asked <= kNear) frees = sh.frees;
   // Free pages: with several blocks each first counts those of its run of pages.
-  const int p0 = (int)(a.num_pages * me / n) & -4, p1 = me + 1 < n ? (int)(a.num_pages * (me + 1) / n) & -4 : (int)a.num_pages;
+  const int pages = (int)a.num_pages, run = (pages / n + 4) & -4;
+  const int p0 = min(run * me, pages), p1 = min(p0 + run, pages);
   const bool whole = ((uintptr_t)(a.refs + p0) & 15) == 0;  // runs of four in one load
   int at = 0, there = 0;
   all(n);
@@ -399,12 +426,19 @@ __global__ void __launch_bounds__(kFitThreads) pages_fit_kernel(const FitArgs a)
       unsigned is = 0;
       int sum;
       const int q0 = p + tid * kScan;
-      if (q0 + kScan <= p1 && whole) {
+      auto four = [&](int i, const int4& r) { is |= (unsigned)((r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3) << i; };
+      if (early && p == 0) {
 #pragma unroll
-        for (int i = 0; i < kScan; i += 4) {
-          const int4 r = __ldcg(reinterpret_cast<const int4*>(a.refs + q0 + i));
-          is |= (unsigned)((r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3) << i;
+        for (int i = 0; i < kScan / 4; ++i) {
+          asm volatile("" : "+r"(refs[i].x), "+r"(refs[i].y), "+r"(refs[i].z), "+r"(refs[i].w));  // not looked at earlier
+          four(4 * i, refs[i]);
         }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) is |= (unsigned)(ends[i] == 0) << (end0 % kScan + i);
+        is &= ~sh.kept[tid];
+      } else if (q0 + kScan <= p1 && whole) {
+#pragma unroll
+        for (int i = 0; i < kScan; i += 4) four(i, __ldcg(reinterpret_cast<const int4*>(a.refs + q0 + i)));
       } else {
 #pragma unroll
         for (int i = 0; i < kScan; ++i)
@@ -502,11 +536,12 @@ cudaError_t launch_pages_fit(const FitArgs& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
   const unsigned ctas = a.num_pages > 32768 ? kFitCtas : 1;
-  configure(cfg, attr, ctas, a.batch <= kFewThreads ? kFewThreads : kFitThreads, stream);
+  const auto kernel = a.batch <= 256 ? pages_fit_kernel<256> : a.batch <= 512 ? pages_fit_kernel<512> : pages_fit_kernel<kFitThreads>;
+  configure(cfg, attr, ctas, a.batch <= 256 ? 256 : a.batch <= 512 ? 512 : kFitThreads, stream);
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim = {ctas, 1, 1};
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, pages_fit_kernel, a);
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 cudaError_t launch_paged_copy(const CopyArgs& a, cudaStream_t stream) {

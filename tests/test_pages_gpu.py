@@ -189,6 +189,26 @@ def test_a_page_twice_in_a_row_is_kept_once(columns):
     assert refs.tolist() == [int(p in rows[0] + rows[1]) for p in range(64)]
 
 
+@pytest.mark.parametrize("batch", [3, 300, 600])
+@pytest.mark.parametrize("more", [0, 1, 2, 3, 29, 8192 * 2 + 5])
+@pytest.mark.parametrize("off", [0, 1])
+def test_pools_of_any_size_and_address(batch, more, off):
+    """Branches that all write to a shared page and need another one, in pools that are just as large."""
+    m = Model(2 + 2 * batch + more, 4, batch, 5)
+    store = torch.zeros(len(m.refs) + off, dtype=torch.int32, device="cuda")
+    m.rows = [[0, 1, -1, -1, -1] for _ in range(batch)]
+    m.refs[0], m.refs[1] = batch, batch
+    m.held, m.lens = [2] * batch, [6] * batch
+    table, held, lens, refs = state(m)
+    refs = store[off:].copy_(refs)
+    for want in [[6] * batch, [7] * batch, [9] * batch, [10] * batch]:
+        copies, status = fit(m, table, held, lens, refs, want)
+        assert status == 0 and copies == [list(c) for c in m.fit(want)]
+        m.lens = want
+        lens = ints(want)
+        same(m, table, held, refs)
+
+
 def test_exactly_enough_and_one_too_few():
     m = Model(6, 4, 2, 5)
     table, held, lens, refs = state(m)
