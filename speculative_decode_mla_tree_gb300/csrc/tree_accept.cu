@@ -82,13 +82,16 @@ constexpr int kMoveThreads = kColumns * kLayersPerBlock;
 constexpr int kRound = 64;                  // moves planned at a time
 constexpr int kAhead = 8;
 
-__global__ void __launch_bounds__(kMoveThreads) paged_compact_kernel(const CompactArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, 4) paged_compact_kernel(const CompactArgs a) {
   __shared__ int64_t from[kRound], to[kRound];
   __shared__ int moves;
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
   const int layer = blockIdx.x * kLayersPerBlock + tid / kColumns, column = tid % kColumns;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int32_t* path = a.path + b * a.path_stride;
+  int node0 = -1;                           // the first nodes do not wait for the count
+  if (tid < 32 && lane < a.max_accept) node0 = __ldg(path + lane);
   const int count = __ldg(a.counts + b), len = __ldg(a.kv.lens + b);
   const int64_t cap = (int64_t)a.kv.max_pages * a.kv.page_size;
   if (count < 0 || count > a.max_accept || len < count || len > cap) {
@@ -96,7 +99,6 @@ __global__ void __launch_bounds__(kMoveThreads) paged_compact_kernel(const Compa
     return;
   }
   const int base = len - count;
-  const int32_t* path = a.path + b * a.path_stride;
   const int32_t* table = a.kv.table + b * a.kv.table_stride;
   uint4* rows = reinterpret_cast<uint4*>(a.kv.rows + layer * a.layer_stride) + column;
   for (int k0 = 0; k0 < count; k0 += kRound) {
@@ -104,15 +106,17 @@ __global__ void __launch_bounds__(kMoveThreads) paged_compact_kernel(const Compa
     if (tid < 32) {
       int n = 0;
       bool end = false;
+      int last = __shfl_up_sync(0xffffffffu, node0, 1);
+      if (lane == 0) last = -1;
       for (int k = k0 + lane; k - lane < k0 + kRound && !end; k += 32) {
         int64_t src = -1, dst = -1;
         bool bad = false;
         if (k < count) {
-          const int node = __ldg(path + k), before = k > 0 ? __ldg(path + k - 1) : -1;
+          const int node = k == lane ? node0 : __ldg(path + k), before = k == lane ? last : __ldg(path + k - 1);
           const int64_t at = (int64_t)base + node;
           bad = node <= before || at >= cap;
           if (!bad && node != k) {
-            const int e = (int)(at / a.kv.page_size), f = (base + k) / a.kv.page_size;
+            const int e = (int)at / a.kv.page_size, f = (base + k) / a.kv.page_size;
             const int p = __ldg(table + e), q = __ldg(table + f);
             if (p >= 0 && p < a.kv.num_pages && q >= 0 && q < a.kv.num_pages) {
               src = p * a.kv.page_stride / 8 + (at - (int64_t)e * a.kv.page_size) * kColumns;
