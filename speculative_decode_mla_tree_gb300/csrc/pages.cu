@@ -116,14 +116,18 @@ __device__ __forceinline__ void all(int n) {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Sum over the block of v, and the part before this thread.
+// Numbers of pages are added up to one more than there can be, in 32 bits.
+__device__ __forceinline__ int plus(int x, int y) { return (int)min((unsigned)x + (unsigned)y, MT_MAX_FIT_PAGES + 1u); }
+
+// Sum over the block of v (at most MT_MAX_FIT_PAGES + 1), and the part before this
+// thread, which is right where the sum is not above MT_MAX_FIT_PAGES.
 __device__ __forceinline__ int block_scan(FitShared& sh, int v, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int inc = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int u = __shfl_up_sync(kFull, inc, o);
-    if (lane >= o) inc += u;
+    if (lane >= o) inc = plus(inc, u);
   }
   __syncthreads();
   if (lane == 31) sh.sums[warp] = inc;
@@ -132,7 +136,7 @@ __device__ __forceinline__ int block_scan(FitShared& sh, int v, int* total) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int u = __shfl_up_sync(kFull, at, o);
-    if (lane >= o) at += u;
+    if (lane >= o) at = plus(at, u);
   }
   const int before = __shfl_sync(kFull, at, warp > 0 ? warp - 1 : 0);
   *total = __shfl_sync(kFull, at, 31);
@@ -323,7 +327,7 @@ __global__ void __launch_bounds__(threads, 1) pages_fit_kernel(const FitArgs a) 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  int64_t asked = 0;
+  int asked = 0;
   // Requests tid, tid + threads, ... are this thread's, but for those that a
   // warp takes: of several columns to write or give back, or with a window that has
   // just come to bear. The first one's state stays in registers.
@@ -393,12 +397,12 @@ __global__ void __launch_bounds__(threads, 1) pages_fit_kernel(const FitArgs a) 
   if (me == 0) {
     for (int b = 0; b < a.batch && some; b += threads) {
       int sum;
-      const int v = b + tid < a.batch ? before[b + tid] : 0;
+      const int v = b + tid < a.batch ? plus(before[b + tid], 0) : 0;
       const int at = block_scan(sh, v, &sum);
-      if (b + tid < a.batch) before[b + tid] = (int)asked + at;
-      asked = min(asked + sum, (int64_t)INT32_MAX);  // more than there can be
+      if (b + tid < a.batch) before[b + tid] = plus(asked, at);
+      asked = plus(asked, sum);
     }
-    if (n > 1 && tid == 0) totals[0] = (int)asked;
+    if (n > 1 && tid == 0) totals[0] = asked;
   }
   if (n == 1 && asked <= kNear) frees = sh.frees;
   // Free pages: with several blocks each first counts those of its run of pages.

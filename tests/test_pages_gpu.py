@@ -224,6 +224,18 @@ def test_exactly_enough_and_one_too_few():
     assert status == 0 and held.tolist() == [1, 5] and table.tolist()[1][:5] == [3, 4, 5, 1, 2]
 
 
+@pytest.mark.parametrize("batch,columns", [(2, 1 << 30), (7, 300_000_000)])
+def test_needs_that_add_up_past_32_bits(batch, columns):
+    """Rows that all ask for more pages than there can be: a shortage like any other, and nothing is written."""
+    table = torch.empty(batch, columns, dtype=torch.int32, device="cuda")
+    refs, held, status = torch.zeros(64, dtype=torch.int32, device="cuda"), ints([0] * batch), ints([0])
+    copies = torch.full((batch, 3), 5, dtype=torch.int32, device="cuda")
+    ws = torch.empty(abi.mla_pages_fit_workspace_bytes(batch, 64), dtype=torch.uint8, device="cuda")
+    abi.mla_pages_fit(ints([0] * batch), ints([columns] * batch), held, table, refs, 1, copies, ws, 0, 0, status)
+    assert int(status) == abi.DEV_NO_PAGES
+    assert held.tolist() == [0] * batch and refs.tolist() == [0] * 64 and copies.tolist() == [[-1, -1, 0]] * batch
+
+
 def test_many_pages():
     """More pages than a block counts at a time, free ones far from the front."""
     m = Model(300000, 16, 5, 200)
