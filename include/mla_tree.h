@@ -523,6 +523,7 @@ int mla_paged_decode_window(const mt_bf16* q, int64_t q_token_stride, int64_t q_
 #define MT_LOGITS_FP32 2
 
 #define MT_MAX_TOP 32             /* alternatives a row (more: MT_EUNSUPPORTED) */
+#define MT_MAX_COLUMNS (1 << 30)  /* tokens a row, accepted nodes, pages of a row (more: MT_EUNSUPPORTED) */
 
 /*
  * Log probabilities of given tokens, entropy and most likely tokens of rows of
@@ -541,6 +542,7 @@ int mla_paged_decode_window(const mt_bf16* q, int64_t q_token_stride, int64_t q_
  *   logits: of logits_type, aligned to its elements; row_stride in elements,
  *            any (rows may overlap, or be the same row)
  *   tokens: int32; NULL with tokens_per_row 0, and logprobs then, too
+ *            (more than MT_MAX_COLUMNS a row: MT_EUNSUPPORTED)
  *   lse, entropy, top_logprobs: NULL leaves them out; top_ids: NULL with top_k 0
  *   top_k:  0 .. MT_MAX_TOP, not above vocab (MT_EINVAL)
  * Every result is the same in every run. No workspace.
@@ -569,8 +571,8 @@ int mla_token_logprobs(const void* logits, int logits_type, int64_t row_stride, 
  * than MT_MAX_TREE nodes set MT_DEV_TREE_TOO_BIG, a decreasing qo_indptr, one
  * that passes total_q, or more nodes than kv_lens[b] MT_DEV_BAD_INDPTR: such a
  * request takes nothing, with next_tokens -1 and new_lens kv_lens.
- * More than 65535 requests return MT_EUNSUPPORTED, here and in
- * mla_paged_compact.
+ * More than 65535 requests, or a max_accept above MT_MAX_COLUMNS, return
+ * MT_EUNSUPPORTED, here and in mla_paged_compact.
  */
 int mla_tree_accept(const int32_t* parents, const int32_t* tokens, const int32_t* targets,
                     int64_t target_stride, const int32_t* first, const int32_t* qo_indptr,
@@ -597,6 +599,8 @@ int mla_paged_compact(const int32_t* path, int64_t path_stride, int max_accept, 
                       int64_t num_pages, int page_size, int layers, int64_t layer_stride,
                       int32_t* dev_status, mt_stream_t stream);
 
+#define MT_MAX_FIT_PAGES (1 << 30)  /* pages of mla_pages_fit (more: MT_EUNSUPPORTED) */
+
 /*
  * Pages of a paged cache, held by reference: refs[p] (int32 [num_pages]) is
  * the number of table entries that hold page p, 0 where it is free. Request b
@@ -610,15 +614,13 @@ int mla_paged_compact(const int32_t* path, int64_t path_stride, int max_accept, 
  * A parent outside [-1, old_batch) sets MT_DEV_BAD_PARENT and counts as -1, a
  * held entry outside [0, max_pages] MT_DEV_BAD_INDPTR and counts as 0, a page
  * number that is neither -1 nor a page MT_DEV_BAD_SLOT and is copied as it is.
- * More than 65535 rows of a side return MT_EUNSUPPORTED.
+ * More than 65535 rows of a side or MT_MAX_COLUMNS pages of a row return MT_EUNSUPPORTED.
  */
 int mla_pages_fork(const int32_t* parents, const int32_t* kv_lens, const int32_t* held,
                    const int32_t* block_table, int64_t table_stride, int old_batch, int max_pages,
                    int32_t* refs, int64_t num_pages, int32_t* new_lens, int32_t* new_held,
                    int32_t* new_table, int64_t new_table_stride, int new_batch,
                    int32_t* dev_status, mt_stream_t stream);
-
-#define MT_MAX_FIT_PAGES (1 << 30)  /* pages of mla_pages_fit (more: MT_EUNSUPPORTED) */
 
 /*
  * Bytes of workspace mla_pages_fit needs (0 for arguments it would reject);
@@ -651,7 +653,8 @@ size_t mla_pages_fit_workspace_bytes(int batch, int64_t num_pages);
  * MT_DEV_BAD_INDPTR and leaves that request as it is; a page number that is
  * neither -1 nor a page sets MT_DEV_BAD_SLOT and counts as -1 (and may be -1
  * afterwards). A page that stands twice in a row is held twice.
- * More than 65535 requests return MT_EUNSUPPORTED.
+ * More than 65535 requests or MT_MAX_COLUMNS pages of a row return
+ * MT_EUNSUPPORTED.
  *   copies: int32 [batch, 3]; workspace: 16-byte aligned
  */
 int mla_pages_fit(const int32_t* kv_lens, const int32_t* want_lens, int32_t* held,

@@ -490,7 +490,7 @@ int mla_token_logprobs(const void* logits, int logits_type, int64_t row_stride, 
   if (rows < 0 || vocab < 1 || tokens_per_row < 0 || top_k < 0 || top_k > vocab) return MT_EINVAL;
   if (row_stride < 0 || (rows > 1 && row_stride > INT64_MAX / 8 / rows)) return MT_EINVAL;
   if (token_stride < 0 || (rows > 1 && token_stride > INT64_MAX / 8 / rows)) return MT_EINVAL;
-  if (top_k > MT_MAX_TOP) return MT_EUNSUPPORTED;
+  if (top_k > MT_MAX_TOP || tokens_per_row > MT_MAX_COLUMNS) return MT_EUNSUPPORTED;
   if (rows == 0) return MT_OK;
   if (tokens_per_row > 0 ? !tokens || !logprobs : tokens || logprobs) return MT_EINVAL;
   if (top_k > 0 ? !top_ids : top_ids || top_logprobs) return MT_EINVAL;
@@ -526,7 +526,7 @@ int mla_tree_accept(const int32_t* parents, const int32_t* tokens, const int32_t
   if (!qo_indptr || !kv_lens || !counts || !next_tokens || !new_lens) return MT_EINVAL;
   if (total_q > 0 && (!parents || !tokens || !targets)) return MT_EINVAL;
   if (max_accept > 0 && !path) return MT_EINVAL;
-  if (batch > 65535) return MT_EUNSUPPORTED;
+  if (batch > 65535 || max_accept > MT_MAX_COLUMNS) return MT_EUNSUPPORTED;
   const AcceptArgs a = {parents, tokens, targets, target_stride, first, qo_indptr, kv_lens, batch, total_q,
                         max_accept, path, counts, next_tokens, new_lens, dev_status};
   return cuda_status(launch_tree_accept(a, (cudaStream_t)stream));
@@ -543,7 +543,7 @@ int mla_paged_compact(const int32_t* path, int64_t path_stride, int max_accept, 
     return MT_EINVAL;
   if (batch == 0 || max_accept == 0 || layers == 0) return MT_OK;
   if (!path || !counts || !kv_lens || (max_pages > 0 && !block_table) || (num_pages > 0 && !cache)) return MT_EINVAL;
-  if (batch > 65535) return MT_EUNSUPPORTED;
+  if (batch > 65535 || max_accept > MT_MAX_COLUMNS) return MT_EUNSUPPORTED;
   CompactArgs a;
   a.path = path;
   a.path_stride = path_stride;
@@ -569,7 +569,7 @@ int mla_pages_fork(const int32_t* parents, const int32_t* kv_lens, const int32_t
   if (old_batch > 0 && (!kv_lens || !held || (max_pages > 0 && !block_table))) return MT_EINVAL;
   if (new_batch > 0 && (!parents || !new_lens || !new_held || (max_pages > 0 && !new_table))) return MT_EINVAL;
   if (num_pages > 0 && !refs) return MT_EINVAL;
-  if (old_batch > 65535 || new_batch > 65535) return MT_EUNSUPPORTED;
+  if (old_batch > 65535 || new_batch > 65535 || max_pages > MT_MAX_COLUMNS) return MT_EUNSUPPORTED;
   if (old_batch > 0 && new_batch > 0) {
     auto apart = [](const int32_t* x, int64_t n, const int32_t* y, int64_t m) {
       return n == 0 || m == 0 || (uintptr_t)(x + n) <= (uintptr_t)y || (uintptr_t)(y + m) <= (uintptr_t)x;
@@ -600,7 +600,7 @@ int mla_pages_fit(const int32_t* kv_lens, const int32_t* want_lens, int32_t* hel
   if (batch == 0) return MT_OK;
   if (!kv_lens || !want_lens || !held || !copies || (max_pages > 0 && !block_table) || (num_pages > 0 && !refs))
     return MT_EINVAL;
-  if (batch > 65535 || num_pages > MT_MAX_FIT_PAGES) return MT_EUNSUPPORTED;
+  if (batch > 65535 || num_pages > MT_MAX_FIT_PAGES || max_pages > MT_MAX_COLUMNS) return MT_EUNSUPPORTED;
   if (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < pages_fit_workspace(batch, num_pages))
     return MT_EWORKSPACE;
   const FitArgs a = {kv_lens, want_lens, held, block_table, table_stride, batch, max_pages, refs, num_pages,

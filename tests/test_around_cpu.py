@@ -113,6 +113,16 @@ def test_more_than_supported(lib):
     assert call(lib, "mla_paged_copy", layers=BIG) == abi.MT_EUNSUPPORTED
 
 
+def test_columns_that_a_step_of_a_warp_would_pass(lib):
+    """Rows of more than 2^30 columns: a lane's next column may be beyond 32 bits."""
+    wide = dict(max_pages=(1 << 30) + 1, table_stride=(1 << 30) + 1)
+    assert call(lib, "mla_pages_fork", new_stride=(1 << 30) + 1, **wide) == abi.MT_EUNSUPPORTED
+    assert call(lib, "mla_pages_fit", page_size=1, **wide) == abi.MT_EUNSUPPORTED
+    assert call(lib, "mla_token_logprobs", per_row=(1 << 30) + 1) == abi.MT_EUNSUPPORTED
+    assert call(lib, "mla_tree_accept", most=(1 << 30) + 1) == abi.MT_EUNSUPPORTED
+    assert call(lib, "mla_paged_compact", most=(1 << 30) + 1, path_stride=(1 << 30) + 1) == abi.MT_EUNSUPPORTED
+
+
 def test_empty_calls_launch_nothing(lib):
     for name, kw in [("mla_paged_decode_window", dict(batch=0)), ("mla_token_logprobs", dict(rows=0, logits=None, tokens=None,
                                                                                              logprobs=None)),
