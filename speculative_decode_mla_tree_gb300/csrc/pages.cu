@@ -84,7 +84,10 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const ForkArgs
 // with one of 1024 threads, 7.4 with one of 256; 512 requests that each replace a page
 // 10.2 us with 1024 threads, 8.6 with 512) and the registers to ask early for what the
 // search needs (32 beams forked, fitted and copied 10.8 -> 9.2 us, 256 19.6 -> 17.9).
-// The search reads refs up to the last page that it takes.
+// The search reads refs up to the last page that it takes, a warp 512 bytes at a time
+// (a thread's own 128 bytes keep the load unit busy for 2000 cycles; with the needs
+// and the free pages summed up together, 32 requests that each replace a page
+// 5.4 -> 4.4 us, 256 7.0 -> 5.7, 512 8.6 -> 6.6).
 constexpr int kFitThreads = 1024;     // or the fewest of 256 and 512 that are as many as the requests
 constexpr int kFitWarps = kFitThreads / 32;
 constexpr int kFitCtas = 8;
@@ -93,9 +96,10 @@ constexpr int kScan = 32;             // pages a thread looks at at a time (bits
 constexpr int kNear = 2048;           // numbers of each kind in shared memory
 
 struct FitShared {
-  int sums[kFitWarps];
+  int sums[2][kFitWarps];
   int before[kNear], frees[kNear];
   unsigned kept[kFitThreads];           // bits of the pages that a search looks at first
+  alignas(8) uint8_t free[kFitThreads * kScan / 4];  // four pages a byte, see free_word
   int longs;
 };
 
@@ -119,28 +123,51 @@ __device__ __forceinline__ void all(int n) {
 // Numbers of pages are added up to one more than there can be, in 32 bits.
 __device__ __forceinline__ int plus(int x, int y) { return (int)min((unsigned)x + (unsigned)y, MT_MAX_FIT_PAGES + 1u); }
 
-// Sum over the block of v (at most MT_MAX_FIT_PAGES + 1), and the part before this
-// thread, which is right where the sum is not above MT_MAX_FIT_PAGES.
-__device__ __forceinline__ int block_scan(FitShared& sh, int v, int* total) {
+// Sums over the block of N numbers a thread (at most MT_MAX_FIT_PAGES + 1), which
+// become the parts before this thread, right where the sum is not above
+// MT_MAX_FIT_PAGES.
+template <int N>
+__device__ __forceinline__ void block_scan(FitShared& sh, int (&v)[N], int (&total)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = v;
+  int inc[N], at[N];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(kFull, inc, o);
-    if (lane >= o) inc = plus(inc, u);
-  }
-  __syncthreads();
-  if (lane == 31) sh.sums[warp] = inc;
-  __syncthreads();
-  int at = lane < (int)blockDim.x / 32 ? sh.sums[lane] : 0;
+  for (int i = 0; i < N; ++i) inc[i] = v[i];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(kFull, at, o);
-    if (lane >= o) at = plus(at, u);
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int u = __shfl_up_sync(kFull, inc[i], o);
+      if (lane >= o) inc[i] = plus(inc[i], u);
+    }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (lane == 31) sh.sums[i][warp] = inc[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) at[i] = lane < (int)blockDim.x / 32 ? sh.sums[i][lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int u = __shfl_up_sync(kFull, at[i], o);
+      if (lane >= o) at[i] = plus(at[i], u);
+    }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int before = __shfl_sync(kFull, at[i], warp > 0 ? warp - 1 : 0);
+    total[i] = __shfl_sync(kFull, at[i], 31);
+    v[i] = inc[i] - v[i] + (warp > 0 ? before : 0);
   }
-  const int before = __shfl_sync(kFull, at, warp > 0 ? warp - 1 : 0);
-  *total = __shfl_sync(kFull, at, 31);
-  return inc - v + (warp > 0 ? before : 0);
+}
+
+// Which of four pages are free; and a word of them, of 32 pages, from eight bytes.
+__device__ __forceinline__ unsigned free_of(const int4& r) { return (r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3; }
+__device__ __forceinline__ unsigned free_word(const uint8_t* bytes) {
+  uint64_t x = *reinterpret_cast<const uint64_t*>(bytes);
+  x = (x | x >> 4) & 0x00ff00ff00ff00ffull;
+  x = (x | x >> 8) & 0x0000ffff0000ffffull;
+  return (unsigned)(x | x >> 16);
 }
 
 // What a call asks of one request.
@@ -374,17 +401,17 @@ __global__ void __launch_bounds__(threads, 1) pages_fit_kernel(const FitArgs a) 
   // One block asks for the first references of its search together with those
   // that decide what is kept, and strikes out what is kept afterwards.
   const bool early = kEarly && n == 1 && some && ((uintptr_t)a.refs & 15) == 0;
+  const int lane = tid & 31, q0 = (tid & ~31) * kScan + 4 * lane;  // of a warp's run of 32 words, 128 pages a load
   int4 refs[kScan / 4];
   int ends[3];                              // behind the last run of four
   const int end0 = (int)a.num_pages & -4;
+  const bool at_end = end0 / (32 * kScan) == tid / 32 && end0 % 128 / 4 == lane;
   if (early) {
 #pragma unroll
-    for (int i = 0; i < kScan / 4; ++i) {
-      const int q = tid * kScan + 4 * i;
-      refs[i] = q < end0 ? __ldcg(reinterpret_cast<const int4*>(a.refs + q)) : make_int4(1, 1, 1, 1);
-    }
+    for (int i = 0; i < kScan / 4; ++i)
+      refs[i] = q0 + 128 * i < end0 ? __ldcg(reinterpret_cast<const int4*>(a.refs + q0 + 128 * i)) : make_int4(1, 1, 1, 1);
 #pragma unroll
-    for (int i = 0; i < 3; ++i) ends[i] = tid == end0 / kScan && end0 + i < a.num_pages ? __ldcg(a.refs + end0 + i) : 1;
+    for (int i = 0; i < 3; ++i) ends[i] = at_end && end0 + i < a.num_pages ? __ldcg(a.refs + end0 + i) : 1;
   }
   if (any) {
     each([&](auto& j) {
@@ -394,13 +421,30 @@ __global__ void __launch_bounds__(threads, 1) pages_fit_kernel(const FitArgs a) 
     });
     __syncthreads();
   }
-  if (me == 0) {
+  // of the search's first step: this thread's word of free pages, how many there are before it, and in all
+  unsigned word0 = 0;
+  int at0 = 0, found0 = 0;
+  if (early) {
+#pragma unroll
+    for (int i = 0; i < kScan / 4; ++i) {
+      asm volatile("" : "+r"(refs[i].x), "+r"(refs[i].y), "+r"(refs[i].z), "+r"(refs[i].w));  // not looked at earlier
+      sh.free[q0 / 4 + 32 * i] = free_of(refs[i]);
+    }
+    if (at_end) sh.free[end0 / 4] = free_of(make_int4(ends[0], ends[1], ends[2], 1));
+    __syncwarp();                           // a warp's words are its own
+    word0 = free_word(sh.free + tid * (kScan / 4)) & ~sh.kept[tid];
+    int v[2] = {tid < a.batch ? plus(before[tid], 0) : 0, __popc(word0)}, sums[2];
+    block_scan(sh, v, sums);
+    if (tid < a.batch) before[tid] = v[0];
+    asked = sums[0];
+    at0 = v[1];
+    found0 = sums[1];
+  } else if (me == 0) {
     for (int b = 0; b < a.batch && some; b += threads) {
-      int sum;
-      const int v = b + tid < a.batch ? plus(before[b + tid], 0) : 0;
-      const int at = block_scan(sh, v, &sum);
-      if (b + tid < a.batch) before[b + tid] = plus(asked, at);
-      asked = plus(asked, sum);
+      int v[1] = {b + tid < a.batch ? plus(before[b + tid], 0) : 0}, sum[1];
+      block_scan(sh, v, sum);
+      if (b + tid < a.batch) before[b + tid] = plus(asked, v[0]);
+      asked = plus(asked, sum[0]);
     }
     if (n > 1 && tid == 0) totals[0] = asked;
   }
@@ -412,11 +456,11 @@ __global__ void __launch_bounds__(threads, 1) pages_fit_kernel(const FitArgs a) 
   int at = 0, there = 0;
   all(n);
   if (n > 1) {
-    int free = 0, sum;
+    int free[1] = {0}, sum[1];
 #pragma unroll 8
-    for (int p = p0 + tid; p < p1; p += threads) free += __ldcg(a.refs + p) == 0;
-    block_scan(sh, free, &sum);
-    if (tid == 0) totals[1 + me] = sum;
+    for (int p = p0 + tid; p < p1; p += threads) free[0] += __ldcg(a.refs + p) == 0;
+    block_scan(sh, free, sum);
+    if (tid == 0) totals[1 + me] = sum[0];
     asked = __ldcg(totals);
     all(n);
     for (int i = 0; i < n; ++i) {
@@ -427,29 +471,44 @@ __global__ void __launch_bounds__(threads, 1) pages_fit_kernel(const FitArgs a) 
   }
   if (n == 1 || asked <= there)
     for (int p = p0; p < p1 && at < asked; p += threads * kScan) {
-      unsigned is = 0;
-      int sum;
-      const int q0 = p + tid * kScan;
-      auto four = [&](int i, const int4& r) { is |= (unsigned)((r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3) << i; };
-      if (early && p == 0) {
+      unsigned is = word0;
+      int r = at0, sum = found0;
+      if (!early || p > 0) {
 #pragma unroll
         for (int i = 0; i < kScan / 4; ++i) {
-          asm volatile("" : "+r"(refs[i].x), "+r"(refs[i].y), "+r"(refs[i].z), "+r"(refs[i].w));  // not looked at earlier
-          four(4 * i, refs[i]);
+          const int q = p + q0 + 128 * i;
+          int4 x = make_int4(1, 1, 1, 1);
+          if (whole && q + 4 <= p1) {
+            x = __ldcg(reinterpret_cast<const int4*>(a.refs + q));
+          } else {
+            if (q < p1) x.x = __ldcg(a.refs + q);
+            if (q + 1 < p1) x.y = __ldcg(a.refs + q + 1);
+            if (q + 2 < p1) x.z = __ldcg(a.refs + q + 2);
+            if (q + 3 < p1) x.w = __ldcg(a.refs + q + 3);
+          }
+          sh.free[q0 / 4 + 32 * i] = free_of(x);
         }
-#pragma unroll
-        for (int i = 0; i < 3; ++i) is |= (unsigned)(ends[i] == 0) << (end0 % kScan + i);
-        is &= ~sh.kept[tid];
-      } else if (q0 + kScan <= p1 && whole) {
-#pragma unroll
-        for (int i = 0; i < kScan; i += 4) four(i, __ldcg(reinterpret_cast<const int4*>(a.refs + q0 + i)));
-      } else {
-#pragma unroll
-        for (int i = 0; i < kScan; ++i)
-          if (q0 + i < p1 && __ldcg(a.refs + q0 + i) == 0) is |= 1u << i;
+        __syncwarp();
+        is = free_word(sh.free + tid * (kScan / 4));
+        int v[1] = {__popc(is)}, sums[1];
+        block_scan(sh, v, sums);
+        r = at + v[0];
+        sum = sums[0];
       }
-      int r = at + block_scan(sh, __popc(is), &sum);
-      for (; is && r < asked; is &= is - 1, ++r) frees[r] = p + tid * kScan + __ffs(is) - 1;
+      // Those asked for are written down by thread, or a word at a time, whichever takes fewer steps.
+      const int take = max(0, min(asked - r, __popc(is)));
+      unsigned words = __ballot_sync(kFull, take > 0);
+      if (__reduce_max_sync(kFull, take) <= __popc(words)) {
+        for (int i = 0; i < take; ++i, is &= is - 1) frees[r + i] = p + tid * kScan + __ffs(is) - 1;
+      } else {
+        for (; words; words &= words - 1) {
+          const int from = __ffs(words) - 1;
+          const unsigned word = __shfl_sync(kFull, is, from);
+          const int first = __shfl_sync(kFull, r, from), n_of = __shfl_sync(kFull, take, from);
+          const int rank = __popc(word & ((1u << lane) - 1));
+          if ((word >> lane & 1) && rank < n_of) frees[first + rank] = p + ((tid & ~31) + from) * kScan + lane;
+        }
+      }
       at += sum;
     }
   const bool enough = n == 1 ? asked <= at : asked <= there;
