@@ -457,7 +457,7 @@ __device__ __forceinline__ uint32_t in_first(const void* p) {  // its place in t
 }
 
 template <typename T, int kThreads>
-__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobArgs a, const int parts) {
+__global__ void __launch_bounds__(kThreads, kThreads == 32 ? 32 : 0) token_logprobs_kernel(const LogprobArgs a, const int parts) {
   constexpr int E = Vec<T>::kN, kWarps = kThreads / 32;
   __shared__ Shared<kThreads> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -748,13 +748,16 @@ cudaError_t launch(const LogprobArgs& a, int num_sms, cudaStream_t stream) {
   // Blocks that all fit at once have 256 threads, for the time of one row; where
   // they follow one another the work of its end counts, which goes by the warp (2048 rows of
   // 131072 bf16 values: 256 threads 101 us, 128 98, 64 113; 8192 of 32000: 134, 108, 101;
-  // 8192 of 4000: 77, 43, 31; but 32 rows of 131072 in 4 parts: 9.1, 10.5, 15.8).
+  // 8192 of 4000: 77, 43, 30, and 32 threads 24; of 16000 57 and 54, of 32000 95 and 96; but 800
+  // rows of 4000: 64 threads 7.2, 32 7.6, and 32 rows of 131072 in 4 parts: 256 threads 9.1, 128
+  // 10.5, 64 15.8). For more alternatives few warps give a low bound: 8192 rows of 1000, 20 of
+  // them, 128 threads 47 us, 64 31, 32 29; of 8000 63, 53, 54; of 32000 115, 111, 144; 4096 of
+  // 65000 106, 109, 167; 2048 of 131072, 32 of them, 256 threads 116, 128 128.
   const int parts = parts_of(a.rows, a.vocab, sizeof(T), num_sms);
-  // For more than 8 alternatives few warps give a low bound (2048 rows, 32 of them: 256
-  // threads 116 us, 128 128).
-  const bool follow = (int64_t)a.rows * parts > 4LL * num_sms, small = a.vocab * sizeof(T) <= 65536, few = a.top_k <= 8;
-  if (follow && small && few) return launch<T, 64>(a, parts, stream);
-  if (follow && (small || few)) return launch<T, 128>(a, parts, stream);
+  const int64_t blocks = (int64_t)a.rows * parts, bytes = (int64_t)a.vocab * sizeof(T);
+  if (blocks > 8LL * num_sms && (a.top_k <= 8 ? bytes <= 16384 : bytes <= 8192 && a.top_k <= 20)) return launch<T, 32>(a, parts, stream);
+  if (blocks > 4LL * num_sms && bytes <= 65536) return launch<T, 64>(a, parts, stream);
+  if (blocks > 4LL * num_sms && a.top_k <= 8) return launch<T, 128>(a, parts, stream);
   return launch<T, 256>(a, parts, stream);
 }
 

@@ -120,6 +120,16 @@ def test_rows(t, v, dtype, k):
     check(x, tok, k)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("v", [1, 5, 8, 31, 127, 255, 256, 257, 264, 1000, 2047, 4001, 8192])
+def test_many_short_rows(dtype, v):
+    """More rows than blocks that run at once, of one warp each for the shortest."""
+    x, tok = rows(v, 1300, v, dtype, pad=v % 3, shift=v % 5)
+    for k in (0, 1, 8, 9, 20, 21, 32):
+        if k <= v:
+            check(x, tok, k)
+
+
 SPECIAL = {
     "all masked": lambda x: x.fill_(-INF),
     "one left": lambda x: x[:, 1:].fill_(-INF),
@@ -152,6 +162,21 @@ def test_special_rows(name, v, dtype):
         SPECIAL[name](x)
         for k in (1, 7, 13):
             check(x, tok, k)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("v", [13, 300, 2000])
+@pytest.mark.parametrize("name", SPECIAL)
+def test_special_rows_among_many(name, v, dtype):
+    """Every third row, so that others of the same launch see that nothing spills over."""
+    x, tok = rows(6, 1500, v, dtype, shift=1)
+    y = x[::3].clone()
+    SPECIAL[name](y)
+    x[::3] = y
+    x[4] = NAN
+    x[5, v // 2], x[7, 1] = INF, NAN
+    for k in (1, 8, 13):
+        check(x, tok, k)
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
