@@ -256,8 +256,9 @@ class Pages:
     ``fork``: branch r goes on from branch ``parents[r]`` (-1: from nothing).
     ``fit``: after ``want_lens`` has been set, positions kv_lens .. want_lens - 1
     may be written, pages that are not needed are free, and rows in pages that
-    were shared are copied. ``advance``: they have been written. DecodeStep reads
-    a side's table and lengths."""
+    were shared are copied; where the free pages do not suffice, ``status`` has
+    abi.DEV_NO_PAGES and nothing has changed. ``advance``: they have been
+    written. DecodeStep reads a side's table and lengths."""
 
     def __init__(self, layers, num_pages, page_size, batch, max_pages, window=0, sinks=0, device="cuda"):
         ints = lambda *n: torch.zeros(n, dtype=torch.int32, device=device)  # noqa: E731
@@ -294,5 +295,6 @@ class Pages:
                           self.workspace, self.window, self.sinks, self.status, stream)
         abi.mla_paged_copy(self.copies, self.cache, self.status, stream)
 
-    def advance(self):
-        self.kv_lens.copy_(self.want_lens)
+    def advance(self, stream=None):
+        with torch.cuda.stream(stream):
+            self.kv_lens.copy_(self.want_lens)

@@ -92,6 +92,39 @@ def test_scores_then_walk_then_moves_without_a_wait():
         assert torch.equal(cache.cpu(), want)
 
 
+def test_pages_on_a_stream_of_their_own():
+    """Every call of Pages goes to the stream that it is given: what that stream captures does not happen before the replay."""
+    pages = Pages(1, 8, 4, 2, 3)
+    pages.fit()
+    pages.want_lens.copy_(torch.tensor([3, 5]))
+    torch.cuda.synchronize()
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        graph.capture_begin(capture_error_mode="relaxed")
+    pages.fit(s)
+    pages.advance(s)
+    with torch.cuda.stream(s):
+        graph.capture_end()
+    assert pages.kv_lens.tolist() == [0, 0] and pages.held.tolist() == [0, 0]
+    graph.replay()
+    assert pages.kv_lens.tolist() == [3, 5] and pages.held.tolist() == [1, 2] and int(pages.status) == 0
+
+
+def test_walk_without_alternatives():
+    """Given targets and no alternatives: the step scores the rows alone."""
+    cache = torch.zeros(4, 8, 576, dtype=BF, device="cuda")
+    targets = torch.tensor([5, 6, 7], dtype=torch.int32, device="cuda")
+    step = AcceptStep(cache, [3, 0], 2, 50, top_k=0, targets=targets)
+    step.block_table.copy_(torch.tensor([[0, 1], [2, 3]]))
+    step.kv_lens.copy_(torch.tensor([7, 0]))
+    step.parents.copy_(torch.tensor([-1, 0, 1]))
+    step.tokens.copy_(torch.tensor([4, 5, 9]))
+    step.first.copy_(torch.tensor([4, 3]))
+    step.run()
+    assert step.counts.tolist() == [2, 0] and step.next_tokens.tolist() == [6, 3] and step.kv_lens.tolist() == [6, 0]
+    assert (step.entropy - math.log(50)).abs().max() < 1e-5 and int(step.status) == 0
+
+
 def test_walk_by_given_targets():
     """Tokens drawn elsewhere instead of the most likely ones."""
     cache = torch.zeros(4, 8, 576, dtype=BF, device="cuda")
