@@ -76,6 +76,9 @@ __global__ void __launch_bounds__(kWalkThreads) tree_accept_kernel(const AcceptA
 // its place as long as each 16-byte column is moved in order, which one thread
 // does: no two threads touch the same bytes. Loads go ahead of the stores by up
 // to kAhead rows: row path[j], j > k, is never row k.
+// Latency bound up to some MB: nodes, table, rows, one round to L2 or HBM each (64
+// trees in 32 layers 3.4 us, 5.3 with the walk). Four blocks an SM: with 72 registers a
+// thread instead of 56 the 512 blocks of that call do not all run at once, 5.7 us.
 constexpr int kColumns = kRowVec;           // 72
 constexpr int kLayersPerBlock = 4;
 constexpr int kMoveThreads = kColumns * kLayersPerBlock;
