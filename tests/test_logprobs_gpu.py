@@ -130,6 +130,14 @@ def test_many_short_rows(dtype, v):
             check(x, tok, k)
 
 
+@pytest.mark.parametrize("t", [300, 310, 450, 470, 600, 610])
+@pytest.mark.parametrize("v,dtype", [(999, torch.bfloat16), (32768, torch.bfloat16), (33001, torch.float16), (20001, torch.float32)])
+def test_two_to_four_blocks_a_multiprocessor(t, v, dtype):
+    x, tok = rows(t, t, v, dtype, pad=3)
+    for k in (0, 5, 20, 21):
+        check(x, tok, k)
+
+
 SPECIAL = {
     "all masked": lambda x: x.fill_(-INF),
     "one left": lambda x: x[:, 1:].fill_(-INF),
