@@ -92,6 +92,11 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
   return r;
 }
 
+// Rows whose maximum is as far from 0 as this are summed again, by exact differences.
+// The rounding of a reference (1/16 here) is in all exponents relative to it and comes
+// out again at the end; beside a maximum near 3e9 it may be -127, which leaves sums of 0.
+constexpr float kFar = 1e6f;
+
 // Values by 16 bytes. raised(): as fp32, -inf and the lowest of the type raised
 // to a floor, so that exp's argument is finite; largest(): ignores NaN. kLow is
 // above the floor.
@@ -630,8 +635,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 32 ? 32 : 0) token_logpr
     if (n > kFew && n <= sh.kCap) n = drop_below(sh, one_warps_bound(sh, own, k), n);
   }
   u = join(sh.sums, kWarps);
-  const bool odd = u.s != u.s || u.t != u.t;  // NaN, +inf, or a maximum that differences from are infinite
-  if (odd || (u.m < Vec<T>::kLow && u.m > -INFINITY)) u = careful_sums<T, kThreads>(sh, p);
+  const bool odd = u.s != u.s || u.t != u.t;  // NaN, +inf, or values far from 0
+  if (odd || (u.m > -INFINITY && (u.m <= Vec<T>::kLow || fabsf(u.m) >= kFar))) u = careful_sums<T, kThreads>(sh, p);
   if (k > 0 && (n > sh.kCap || odd)) {
     find_top<T, kThreads>(sh, p, k);
     n = k;
