@@ -534,7 +534,9 @@ int mla_paged_decode_window(const mt_bf16* q, int64_t q_token_stride, int64_t q_
  *     top_ids[r, i]  = the token of the i-th largest x_v, i < top_k, equal
  *                      values by the lower token (0 equals -0; NaN comes first)
  *     top_logprobs[r, i] = its x_v - lse[r]
- * Sums are fp32 (the reference of the exponent is the maximum so far). A row
+ * Sums are fp32 (the reference of the exponent is the maximum so far). A log
+ * probability is (x_tok - max x) - ln sum exp(x - max x), never above 0, and as
+ * exact for large logits as for small ones; lse is rounded to fp32. A row
  * whose values are all -inf has lse -inf, entropy 0 and log probabilities -inf;
  * one that holds NaN or +inf has NaN for all of them (its top_ids are as above).
  * Token -1 asks for nothing and gets -inf; one outside [-1, vocab) sets

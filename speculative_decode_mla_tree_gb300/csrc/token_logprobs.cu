@@ -2,7 +2,7 @@
 // logits, in one pass over them.
 //
 // With m = max x, e_v = exp(x_v - m), S = sum e_v and T = sum e_v (x_v - m):
-//     lse = m + ln S,   ln p_v = x_v - lse,   H = -sum p_v ln p_v = ln S - T / S.
+//     lse = m + ln S,   ln p_v = (x_v - m) - ln S,   H = -sum p_v ln p_v = ln S - T / S.
 // Each thread keeps an S and T of its own relative to a value m that follows its
 // maximum in steps (S' = f S, T' = f (T + (m - m') S), f = exp(m - m'), where a
 // value more than kSlack above m makes it m'), joined at the end, relative to
@@ -680,18 +680,23 @@ __global__ void __launch_bounds__(kThreads, kThreads == 32 ? 32 : 0) token_logpr
   }
 
   const bool none = u.m == -INFINITY && u.s == u.s;
-  const float log_s = __log2f(u.s);
-  const float lse = none ? -INFINITY : fmaf(log_s, kLn2, u.m);
+  const float ln_s = logf(u.s);
+  // m + ln S is rounded by up to half a unit of m, which is more than all of a likely
+  // token's log probability: x - m, often exact, and ln S stay apart.
+  auto log_p = [&](float x) {
+    const float v = x - u.m - ln_s;
+    return none ? -INFINITY : v > 0.f ? 0.f : v;
+  };
   if (tid == 0) {
-    if (a.lse) a.lse[r] = lse;
+    if (a.lse) a.lse[r] = none ? -INFINITY : u.m + ln_s;
     if (a.entropy) {
-      const float h = none ? 0.f : (log_s - u.t / u.s) * kLn2;
+      const float h = none ? 0.f : fmaf(-kLn2, u.t / u.s, ln_s);
       a.entropy[r] = h < 0.f ? 0.f : h;
     }
   }
   auto put = [&](int rank, Key key) {
     a.top_ids[r * k + rank] = place_of(key);
-    if (a.top_logprobs) a.top_logprobs[r * k + rank] = none ? -INFINITY : value_of(key) - lse;
+    if (a.top_logprobs) a.top_logprobs[r * k + rank] = log_p(value_of(key));
   };
   if (parts > 1) {
     // eight lanes a key, each of which counts in one part
@@ -714,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 32 ? 32 : 0) token_logpr
   }
   for (int g = tid; g < a.per_row; g += kThreads) {
     const T x = g == tid ? given : value_at(g, asked);
-    a.logprobs[r * a.per_row + g] = none || !asked ? -INFINITY : Vec<T>::one(x) - lse;
+    a.logprobs[r * a.per_row + g] = asked ? log_p(Vec<T>::one(x)) : -INFINITY;
   }
 }
 
