@@ -612,7 +612,8 @@ int mla_paged_compact(const int32_t* path, int64_t path_stride, int max_accept, 
  * Fork: row r < new_batch of the new table holds the pages of row parents[r] of
  * the old one (none for -1), with its held and kv_lens; rows of the old table
  * that are nobody's parent give their pages back. So one call forks, drops and
- * reorders. The tables, held and kv_lens of both sides may not overlap.
+ * reorders. The tables, held and kv_lens of both sides may not overlap (one
+ * table's rows may lie between the other's).
  * A parent outside [-1, old_batch) sets MT_DEV_BAD_PARENT and counts as -1, a
  * held entry outside [0, max_pages] MT_DEV_BAD_INDPTR and counts as 0, a page
  * number that is neither -1 nor a page MT_DEV_BAD_SLOT and is copied as it is.

@@ -456,6 +456,22 @@ static bool layers_ok(int layers, int64_t layer_stride, int64_t num_pages, int64
   return lo >= page && hi >= lo * ((inside ? layers : num_pages) - 1) + page;
 }
 
+// Whether n rows from x on and m from y on, `width` numbers each, share none. Where
+// one table does not lie behind the other, both lists of rows are walked in the order
+// of their addresses: one's rows may lie between the other's.
+static bool rows_apart(const int32_t* x, int64_t x_stride, int n, const int32_t* y, int64_t y_stride, int m, int64_t width) {
+  const uintptr_t size = (uintptr_t)width * 4;
+  auto x_at = [&](int i) { return (uintptr_t)(x + i * x_stride); };
+  auto y_at = [&](int j) { return (uintptr_t)(y + j * y_stride); };
+  if (width == 0 || x_at(n - 1) + size <= y_at(0) || y_at(m - 1) + size <= x_at(0)) return true;
+  for (int i = 0, j = 0; i < n && j < m;) {
+    if (x_at(i) + size <= y_at(j)) ++i;
+    else if (y_at(j) + size <= x_at(i)) ++j;
+    else return false;
+  }
+  return true;
+}
+
 extern "C" {
 
 int mla_paged_decode(const mt_bf16* q, int64_t q_token_stride, int64_t q_head_stride,
@@ -574,10 +590,8 @@ int mla_pages_fork(const int32_t* parents, const int32_t* kv_lens, const int32_t
     auto apart = [](const int32_t* x, int64_t n, const int32_t* y, int64_t m) {
       return n == 0 || m == 0 || (uintptr_t)(x + n) <= (uintptr_t)y || (uintptr_t)(y + m) <= (uintptr_t)x;
     };
-    const int64_t cells = max_pages ? (old_batch - 1) * table_stride + max_pages : 0;
-    const int64_t new_cells = max_pages ? (new_batch - 1) * new_table_stride + max_pages : 0;
     if (!apart(kv_lens, old_batch, new_lens, new_batch) || !apart(held, old_batch, new_held, new_batch) ||
-        !apart(block_table, cells, new_table, new_cells))
+        !rows_apart(block_table, table_stride, old_batch, new_table, new_table_stride, new_batch, max_pages))
       return MT_EINVAL;
   }
   const ForkArgs a = {parents, kv_lens, held, block_table, table_stride, old_batch, max_pages, refs, num_pages,
