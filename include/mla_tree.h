@@ -651,7 +651,8 @@ size_t mla_pages_fit_workspace_bytes(int batch, int64_t num_pages);
  * was replaced, (-1, -1, 0) where there is none: mla_paged_copy carries it out,
  * before the next append.
  * Where the free pages do not suffice for all requests, the call sets
- * MT_DEV_NO_PAGES and changes nothing (copies are all (-1, -1, 0)). A bad
+ * MT_DEV_NO_PAGES and changes nothing (copies are all (-1, -1, 0)): want_lens
+ * are no lengths to write to then (mla_pages_fit_lens). A bad
  * length (below 0, or want_lens beyond the table) or held entry sets
  * MT_DEV_BAD_INDPTR and leaves that request as it is; a page number that is
  * neither -1 nor a page sets MT_DEV_BAD_SLOT and counts as -1 (and may be -1
@@ -664,6 +665,23 @@ int mla_pages_fit(const int32_t* kv_lens, const int32_t* want_lens, int32_t* hel
                   int32_t* block_table, int64_t table_stride, int batch, int max_pages, int32_t* refs,
                   int64_t num_pages, int page_size, int window, int sinks, int32_t* copies,
                   void* workspace, size_t workspace_bytes, int32_t* dev_status, mt_stream_t stream);
+
+/*
+ * mla_pages_fit that also says what the calls behind it may go by, when nobody
+ * looks at the status between them (a captured step):
+ *     step_lens[b] = want_lens[b], or 0 where nothing may be written: for all
+ *                    requests after MT_DEV_NO_PAGES, for one with a bad length
+ * As the lengths of an append of one token a request and of the attention,
+ * step_lens leaves such a request out; want_lens would have it write over rows
+ * in pages that others hold. A request's new length is want_lens[b] where
+ * step_lens[b] equals it, else still kv_lens[b].
+ *   step_lens: int32 [batch], apart from kv_lens, want_lens and held; or NULL
+ */
+int mla_pages_fit_lens(const int32_t* kv_lens, const int32_t* want_lens, int32_t* held,
+                       int32_t* block_table, int64_t table_stride, int batch, int max_pages, int32_t* refs,
+                       int64_t num_pages, int page_size, int window, int sinks, int32_t* copies,
+                       int32_t* step_lens, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                       mt_stream_t stream);
 
 /*
  * Copies the first copies[i][2] rows of page copies[i][0] to page copies[i][1],

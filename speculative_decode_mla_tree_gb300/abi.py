@@ -27,7 +27,8 @@ EXPORTS = ["mla_tree_abi_version", "mla_tree_status_string", "mla_tree_draft_kv_
            "mla_tree_verify_validate", "mla_tree_verify_noalloc", "mla_tree_test_wait_limits",
            "mla_paged_append", "mla_paged_decode_workspace_bytes", "mla_paged_decode",
            "mla_paged_decode_window", "mla_token_logprobs", "mla_tree_accept", "mla_paged_compact",
-           "mla_pages_fork", "mla_pages_fit_workspace_bytes", "mla_pages_fit", "mla_paged_copy"]
+           "mla_pages_fork", "mla_pages_fit_workspace_bytes", "mla_pages_fit", "mla_pages_fit_lens",
+           "mla_paged_copy"]
 MT_ESCRATCH = -5
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -108,6 +109,8 @@ def load():
     lib.mla_pages_fit_workspace_bytes.argtypes = [I32, I64]
     lib.mla_pages_fit.restype = I32
     lib.mla_pages_fit.argtypes = [P, P, P, P, I64, I32, I32, P, I64, I32, I32, I32, P, P, SZ, P, P]
+    lib.mla_pages_fit_lens.restype = I32
+    lib.mla_pages_fit_lens.argtypes = [P, P, P, P, I64, I32, I32, P, I64, I32, I32, I32, P, P, P, SZ, P, P]
     lib.mla_paged_copy.restype = I32
     lib.mla_paged_copy.argtypes = [P, I64, P, I64, I64, I32, I32, I64, P, P]
     _lib = lib
@@ -362,7 +365,7 @@ def _load_paged_call():
     spec.loader.exec_module(mod)
     mod.bind(*(ctypes.cast(f, P).value for f in (
         lib.mla_paged_append, lib.mla_paged_decode, lib.mla_paged_decode_window, lib.mla_token_logprobs, lib.mla_tree_accept,
-        lib.mla_paged_compact, lib.mla_pages_fork, lib.mla_pages_fit, lib.mla_paged_copy)))
+        lib.mla_paged_compact, lib.mla_pages_fork, lib.mla_pages_fit_lens, lib.mla_paged_copy)))
     _paged_call = mod
     return mod
 
@@ -653,7 +656,7 @@ def mla_pages_fork(parents, kv_lens, held, block_table, refs, new_lens, new_held
         _check(rc, "mla_pages_fork")
 
 
-def _refuse_fit(kv_lens, want_lens, held, block_table, refs, page_size, copies, workspace, window, sinks, status):
+def _refuse_fit(kv_lens, want_lens, held, block_table, refs, page_size, copies, workspace, window, sinks, status, step_lens):
     i32, on = torch.int32, "refs"
     for name, v in (("page_size", page_size), ("window", window), ("sinks", sinks)):
         _refuse_int(name, v)
@@ -663,6 +666,8 @@ def _refuse_fit(kv_lens, want_lens, held, block_table, refs, page_size, copies, 
         _refuse(name, v, i32, 1, dev, (batch,), True, on)
     _refuse("copies", copies, i32, 2, dev, (batch, 3), True, on)
     _refuse("workspace", workspace, torch.uint8, 1, dev, None, True, on)
+    if step_lens is not None:
+        _refuse("step_lens", step_lens, i32, 1, dev, (batch,), True, on)
     _refuse_status(status, dev, on)
 
 
@@ -671,18 +676,20 @@ def mla_pages_fit_workspace_bytes(batch, num_pages):
 
 
 def mla_pages_fit(kv_lens, want_lens, held, block_table, refs, page_size, copies, workspace, window=0, sinks=0,
-                  status=None, stream=None):
+                  status=None, stream=None, step_lens=None):
     """Gives each request pages of its own for positions kv_lens .. want_lens -
     1 and takes back those behind want_lens and, with a window, those that lie
     wholly between the first sinks positions and the window of position kv_lens.
     copies [B, 3] gets (source page, destination page, rows) where a shared page
     was replaced, for mla_paged_copy. Without enough free pages DEV_NO_PAGES is
-    set and nothing changes. workspace: uint8, mla_pages_fit_workspace_bytes(B,
+    set and nothing changes: no position behind kv_lens may be written then.
+    step_lens [B] says so to the calls that follow: want_lens, or 0 for a request
+    that may not be written to. workspace: uint8, mla_pages_fit_workspace_bytes(B,
     num_pages)."""
     rc = (_paged_call or _load_paged_call()).fit(kv_lens, want_lens, held, block_table, refs, page_size, copies, workspace,
-                                                 window, sinks, status, None if stream is None else stream.cuda_stream)
+                                                 window, sinks, status, None if stream is None else stream.cuda_stream, step_lens)
     if rc is None:
-        _refuse_fit(kv_lens, want_lens, held, block_table, refs, page_size, copies, workspace, window, sinks, status)
+        _refuse_fit(kv_lens, want_lens, held, block_table, refs, page_size, copies, workspace, window, sinks, status, step_lens)
     if rc != MT_OK:
         _check(rc, "mla_pages_fit")
 

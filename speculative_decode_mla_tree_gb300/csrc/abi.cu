@@ -456,6 +456,11 @@ static bool layers_ok(int layers, int64_t layer_stride, int64_t num_pages, int64
   return lo >= page && hi >= lo * ((inside ? layers : num_pages) - 1) + page;
 }
 
+// Whether two arrays share no number.
+static bool apart(const int32_t* x, int64_t n, const int32_t* y, int64_t m) {
+  return n == 0 || m == 0 || (uintptr_t)(x + n) <= (uintptr_t)y || (uintptr_t)(y + m) <= (uintptr_t)x;
+}
+
 // Whether n rows from x on and m from y on, `width` numbers each, share none. Where
 // one table does not lie behind the other, both lists of rows are walked in the order
 // of their addresses: one's rows may lie between the other's.
@@ -587,9 +592,6 @@ int mla_pages_fork(const int32_t* parents, const int32_t* kv_lens, const int32_t
   if (num_pages > 0 && !refs) return MT_EINVAL;
   if (old_batch > 65535 || new_batch > 65535 || max_pages > MT_MAX_COLUMNS) return MT_EUNSUPPORTED;
   if (old_batch > 0 && new_batch > 0) {
-    auto apart = [](const int32_t* x, int64_t n, const int32_t* y, int64_t m) {
-      return n == 0 || m == 0 || (uintptr_t)(x + n) <= (uintptr_t)y || (uintptr_t)(y + m) <= (uintptr_t)x;
-    };
     if (!apart(kv_lens, old_batch, new_lens, new_batch) || !apart(held, old_batch, new_held, new_batch) ||
         !rows_apart(block_table, table_stride, old_batch, new_table, new_table_stride, new_batch, max_pages))
       return MT_EINVAL;
@@ -608,17 +610,29 @@ int mla_pages_fit(const int32_t* kv_lens, const int32_t* want_lens, int32_t* hel
                   int32_t* block_table, int64_t table_stride, int batch, int max_pages, int32_t* refs,
                   int64_t num_pages, int page_size, int window, int sinks, int32_t* copies,
                   void* workspace, size_t workspace_bytes, int32_t* dev_status, mt_stream_t stream) {
+  return mla_pages_fit_lens(kv_lens, want_lens, held, block_table, table_stride, batch, max_pages, refs, num_pages,
+                            page_size, window, sinks, copies, nullptr, workspace, workspace_bytes, dev_status, stream);
+}
+
+int mla_pages_fit_lens(const int32_t* kv_lens, const int32_t* want_lens, int32_t* held,
+                       int32_t* block_table, int64_t table_stride, int batch, int max_pages, int32_t* refs,
+                       int64_t num_pages, int page_size, int window, int sinks, int32_t* copies,
+                       int32_t* step_lens, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                       mt_stream_t stream) {
   if (batch < 0 || max_pages < 0 || table_stride < max_pages || num_pages < 0 || num_pages > INT32_MAX ||
       page_size < 1 || (int64_t)max_pages * page_size > INT32_MAX || window < 0 || sinks < 0)
     return MT_EINVAL;
   if (batch == 0) return MT_OK;
   if (!kv_lens || !want_lens || !held || !copies || (max_pages > 0 && !block_table) || (num_pages > 0 && !refs))
     return MT_EINVAL;
+  if (step_lens && (!apart(step_lens, batch, kv_lens, batch) || !apart(step_lens, batch, want_lens, batch) ||
+                    !apart(step_lens, batch, held, batch)))
+    return MT_EINVAL;
   if (batch > 65535 || num_pages > MT_MAX_FIT_PAGES || max_pages > MT_MAX_COLUMNS) return MT_EUNSUPPORTED;
   if (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < pages_fit_workspace(batch, num_pages))
     return MT_EWORKSPACE;
   const FitArgs a = {kv_lens, want_lens, held, block_table, table_stride, batch, max_pages, refs, num_pages,
-                     page_size, window, sinks, copies, (int32_t*)workspace, dev_status};
+                     page_size, window, sinks, copies, step_lens, (int32_t*)workspace, dev_status};
   return cuda_status(launch_pages_fit(a, (cudaStream_t)stream));
 }
 

@@ -131,6 +131,7 @@ struct FitArgs {
   int64_t num_pages;
   int page_size, window, sinks;
   int32_t* copies;              // [batch, 3] source page, destination page, rows
+  int32_t* step_lens;           // [batch] what may be written up to, or nullptr
   int32_t* ws;
   int32_t* status;
 };

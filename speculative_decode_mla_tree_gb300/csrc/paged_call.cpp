@@ -26,7 +26,7 @@ decltype(&mla_token_logprobs) g_logprobs = nullptr;
 decltype(&mla_tree_accept) g_accept = nullptr;
 decltype(&mla_paged_compact) g_compact = nullptr;
 decltype(&mla_pages_fork) g_fork = nullptr;
-decltype(&mla_pages_fit) g_fit = nullptr;
+decltype(&mla_pages_fit_lens) g_fit = nullptr;
 decltype(&mla_paged_copy) g_copy = nullptr;
 
 // One tensor argument; `none` where None may stand for it.
@@ -362,12 +362,13 @@ PyObject* fork_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
 }
 
-// fit(kv_lens, want_lens, held, block_table, refs, page_size, copies, workspace, window, sinks, status, stream)
+// fit(kv_lens, want_lens, held, block_table, refs, page_size, copies, workspace, window, sinks, status, stream, step_lens)
 PyObject* fit(PyObject*, PyObject* const* a, Py_ssize_t n) {
   try {
     int page, window, sinks;
-    if (n != 12 || !g_fit || !int_of(a[5], &page) || !int_of(a[8], &window) || !int_of(a[9], &sinks)) return does_not_fit();
-    Arg lens(a[0]), want(a[1]), held(a[2]), table(a[3]), refs(a[4]), copies(a[6]), ws(a[7]), status(a[10], true);
+    if (n != 13 || !g_fit || !int_of(a[5], &page) || !int_of(a[8], &window) || !int_of(a[9], &sinks)) return does_not_fit();
+    Arg lens(a[0]), want(a[1]), held(a[2]), table(a[3]), refs(a[4]), copies(a[6]), ws(a[7]), status(a[10], true),
+        step(a[12], true);
     if (!refs.here()) return does_not_fit();
     const int dev = refs.t->get_device();
     if (!refs.is(at::kInt, 1, dev) || !refs.t->is_contiguous() || !table.is(at::kInt, 2, dev) ||
@@ -376,14 +377,15 @@ PyObject* fit(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t batch = table.size(0), width = table.size(1), pages = refs.size(0);
     if (batch > INT_MAX || width > INT_MAX || !table.rows() || !ints(lens, batch, dev) || !ints(want, batch, dev) ||
         !ints(held, batch, dev) || !copies.sizes(batch, 3) || !copies.t->is_contiguous() || !ws.t->is_contiguous() ||
-        !status_ok(status, dev))
+        !step.ok || (step.t && !ints(step, batch, dev)) || !status_ok(status, dev))
       return does_not_fit();
     mt_stream_t stream;
     if (!stream_of(a[11], dev, &stream)) return does_not_fit();
     return guarded(dev, [&] {
       return g_fit(lens.data<int32_t>(), want.data<int32_t>(), held.data<int32_t>(), table.data<int32_t>(),
                    batch > 1 ? table.stride(0) : width, (int)batch, (int)width, refs.data<int32_t>(), pages, page, window,
-                   sinks, copies.data<int32_t>(), ws.data<void>(), (size_t)ws.t->numel(), status.data<int32_t>(), stream);
+                   sinks, copies.data<int32_t>(), step.data<int32_t>(), ws.data<void>(), (size_t)ws.t->numel(),
+                   status.data<int32_t>(), stream);
     });
   } catch (...) {
     return does_not_fit();
@@ -411,7 +413,7 @@ PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // bind(addresses of mla_paged_append, mla_paged_decode, mla_paged_decode_window, mla_token_logprobs,
-// mla_tree_accept, mla_paged_compact, mla_pages_fork, mla_pages_fit, mla_paged_copy)
+// mla_tree_accept, mla_paged_compact, mla_pages_fork, mla_pages_fit_lens, mla_paged_copy)
 PyObject* bind(PyObject*, PyObject* args) {
   PyObject* x[9];
   if (!PyArg_ParseTuple(args, "OOOOOOOOO", &x[0], &x[1], &x[2], &x[3], &x[4], &x[5], &x[6], &x[7], &x[8])) return nullptr;

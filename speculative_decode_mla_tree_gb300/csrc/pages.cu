@@ -304,7 +304,7 @@ struct Job {
       given_back([&](int, int p) {
         if (known(p)) atomicAdd(a.refs + p, 1);
       });
-    say(-1, -1, 0);
+    say(-1, -1, 0, false);
   }
   __device__ __forceinline__ void hand_out(const int32_t* pages) {
     int src = -1, dst = -1, rows = 0;
@@ -326,13 +326,14 @@ struct Job {
       }
       if (lane() == 0) a.held[b] = w.need;  // (the other lanes have long read it)
     }
-    say(src, dst, rows);
+    say(src, dst, rows, w.ok);
   }
-  __device__ __forceinline__ void say(int src, int dst, int rows) {
+  __device__ __forceinline__ void say(int src, int dst, int rows, bool granted) {
     if (lane() != 0) return;  // column w0 is lane 0's
     a.copies[3 * b] = src;
     a.copies[3 * b + 1] = dst;
     a.copies[3 * b + 2] = rows;
+    if (a.step_lens) a.step_lens[b] = granted ? __ldg(a.want + b) : 0;
   }
 };
 

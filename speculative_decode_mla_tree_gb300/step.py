@@ -257,8 +257,11 @@ class Pages:
     ``fit``: after ``want_lens`` has been set, positions kv_lens .. want_lens - 1
     may be written, pages that are not needed are free, and rows in pages that
     were shared are copied; where the free pages do not suffice, ``status`` has
-    abi.DEV_NO_PAGES and nothing has changed. ``advance``: they have been
-    written. DecodeStep reads a side's table and lengths."""
+    abi.DEV_NO_PAGES and nothing has changed. ``step_lens`` are the lengths to
+    append and attend by: want_lens, or 0 for a branch that has no page to write
+    to, which DecodeStep then leaves out (want_lens would have it write over rows
+    that others hold). ``advance``: what step_lens say has been written; other
+    branches keep their kv_lens. DecodeStep reads a side's table and step_lens."""
 
     def __init__(self, layers, num_pages, page_size, batch, max_pages, window=0, sinks=0, device="cuda"):
         ints = lambda *n: torch.zeros(n, dtype=torch.int32, device=device)  # noqa: E731
@@ -268,6 +271,7 @@ class Pages:
         self._tables = [ints(batch, max_pages) - 1, ints(batch, max_pages) - 1]
         self._held, self._lens = [ints(batch), ints(batch)], [ints(batch), ints(batch)]
         self.parents, self.want_lens, self.copies = ints(batch), ints(batch), ints(batch, 3)
+        self.step_lens, self._kept = ints(batch), torch.zeros(batch, dtype=torch.bool, device=device)
         n = abi.mla_pages_fit_workspace_bytes(batch, num_pages)
         self.workspace = torch.empty(n, dtype=torch.uint8, device=device)
         self.status = ints(1)
@@ -292,9 +296,10 @@ class Pages:
 
     def fit(self, stream=None):
         abi.mla_pages_fit(self.kv_lens, self.want_lens, self.held, self.block_table, self.refs, self.page_size, self.copies,
-                          self.workspace, self.window, self.sinks, self.status, stream)
+                          self.workspace, self.window, self.sinks, self.status, stream, self.step_lens)
         abi.mla_paged_copy(self.copies, self.cache, self.status, stream)
 
     def advance(self, stream=None):
         with torch.cuda.stream(stream):
-            self.kv_lens.copy_(self.want_lens)
+            torch.ne(self.step_lens, self.want_lens, out=self._kept)
+            torch.where(self._kept, self.kv_lens, self.want_lens, out=self.kv_lens)
