@@ -186,7 +186,7 @@ __device__ __forceinline__ Wish wish_of(const FitArgs& a, int b) {
   w.held = a.held[b];
   w.ok = w.len >= 0 && want >= 0 && want <= (int64_t)a.max_pages * a.page_size && w.held >= 0 && w.held <= a.max_pages;
   w.need = (int)(((unsigned)want + a.page_size - 1) / (unsigned)a.page_size);
-  w.w0 = w.len / a.page_size;
+  w.w0 = min(w.len / a.page_size, a.max_pages);  // beyond the table nothing is written, and w0 + lane stays in 32 bits
   w.w1 = want > w.len ? w.need : w.w0;
   w.gap0 = w.gap1 = 0;
   if (a.window > 0 && w.len >= a.window) {
