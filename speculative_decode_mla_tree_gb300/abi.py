@@ -370,7 +370,7 @@ def _load_paged_call():
     return mod
 
 
-def _refuse(name, t, dtype, dim, dev, shape=None, whole=False, other="cache"):
+def _refuse(name, t, dtype, dim, dev, shape=None, whole=False, other="cache", any_stride=False):
     """Raises what is wrong with one tensor, if anything is."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise MlaTreeError("%s must be a CUDA tensor" % name)
@@ -384,7 +384,7 @@ def _refuse(name, t, dtype, dim, dev, shape=None, whole=False, other="cache"):
                                               list(t.shape)))
     if whole and not t.is_contiguous():
         raise MlaTreeError("%s must be contiguous" % name)
-    if dim and t.shape[-1] > 1 and t.stride(-1) != 1:
+    if dim and t.shape[-1] > 1 and t.stride(-1) != 1 and not any_stride:
         raise MlaTreeError("%s must have unit stride in its last dimension" % name)
 
 
@@ -521,7 +521,7 @@ def _refuse_logprobs(logits, tokens, logprobs, lse, entropy, top_ids, top_logpro
         raise MlaTreeError("tokens and logprobs go together")
     if tokens is not None:
         dim = 2 if isinstance(tokens, torch.Tensor) and tokens.dim() == 2 else 1
-        _refuse("tokens", tokens, torch.int32, dim, dev, None, False, on)
+        _refuse("tokens", tokens, torch.int32, dim, dev, None, False, on, dim == 1)
         if tokens.shape[0] != rows:
             raise MlaTreeError("tokens must have the logits' %d rows, got %s" % (rows, list(tokens.shape)))
         _refuse("logprobs", logprobs, torch.float32, dim, dev, tokens.shape, True, on)
@@ -561,9 +561,7 @@ def _refuse_accept(parents, tokens, targets, qo_indptr, kv_lens, path, counts, n
     _refuse("path", path, i32, 2, dev, None, True, on)
     batch = path.shape[0]
     _refuse("tokens", tokens, i32, 1, dev, (t,), True, on)
-    if isinstance(targets, torch.Tensor) and targets.dim() == 1:
-        targets = targets.as_strided(targets.shape, (1,)) if targets.is_cuda else targets  # any stride
-    _refuse("targets", targets, i32, 1, dev, (t,), False, on)
+    _refuse("targets", targets, i32, 1, dev, (t,), False, on, True)
     _refuse("qo_indptr", qo_indptr, i32, 1, dev, (batch + 1,), True, on)
     for name, v in (("kv_lens", kv_lens), ("counts", counts), ("next_tokens", next_tokens), ("new_lens", new_lens)):
         _refuse(name, v, i32, 1, dev, (batch,), True, on)
