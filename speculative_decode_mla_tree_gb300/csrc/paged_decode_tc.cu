@@ -491,7 +491,10 @@ __device__ __forceinline__ void join_parts(const DecodeArgs& a, const float* par
 // ------------------------------------------------------------------- kernel
 
 // kGather: pages that are no whole groups of eight rows; two producer warps
-// bring single rows by gather, each every other quarter of a tile.
+// bring single rows by gather, each every other quarter of a tile. Their issue rate
+// bounds it: behind a window of 4096 + 64 the 64-request mix at 64 heads takes 70 us over pages of
+// 20, 7 or 1 rows, 47.5 over pages of 64; 48 requests of 128 heads behind 2047 + 5 82, and 51 over
+// pages of 16; 8 of 8 heads behind 512 + 4 11.8, and 9.1.
 // kJoin: the CTAs of a cluster share one request; each leaves its partial in shared
 // memory, and joins an equal part of the value dims of all of them. No workspace,
 // no second launch.
@@ -908,6 +911,10 @@ __global__ void __launch_bounds__(threads_of(kGather), 1)
             tc_fence_before();
           }
         }
+        // The weights become bf16, the values' type: a product has one type for both. Each is off by 2^-8 of
+        // itself at most; with their own sum as divisor outputs are 2.1e-3 off (2-norm), 1.7e-3 by the
+        // rounding of the output alone. A second product with what this rounding leaves would need 8 KB more
+        // of shared memory at 64 heads, which has 64 bytes left.
         uint32_t pk[NC / 4];  // key r0 at 2 i, key r0 + 8 at 2 i + 1; two heads each
 #pragma unroll
         for (int i = 0; i < NC / 8; ++i)

@@ -25,10 +25,11 @@
 // distributed shared memory: no workspace and no second launch.
 //
 // What bounds it: with many rows HBM, and beside it the issue slots (2.7 of 4
-// instructions a cycle): 2048 rows of 131072 bf16 values take 92 us, 5.8 TB/s, fp32
-// rows of half as many 81, 6.6 TB/s. The best tokens cost 5 us of them for k = 5, 20
-// for 32. 128 such rows take 13 us, 9.8 without tokens, where HBM needs 5: the start,
-// a ramp, and the joins. One row takes 5 to 6.4 us, nearly all of it latency.
+// instructions a cycle): 2048 rows of 131072 bf16 values take 93 us, 5.8 TB/s, fp16 ones,
+// with a conversion more for each pair, 96, fp32 rows of half as many 81, 6.6 TB/s. The best
+// tokens cost 5 us of them for k = 5, 20 for 32. 128 such rows take 13 us, 9.9 without tokens,
+// where HBM needs 5: the start, a ramp, and the joins. One row takes 5 to 6.4 us, nearly
+// all of it latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <float.h>
@@ -741,9 +742,10 @@ cudaError_t launch(const LogprobArgs& a, int parts, cudaStream_t stream, bool ea
 }
 
 // CTAs of a row: up to two an SM of at least 4096 values (128 rows of 131072 bf16
-// values: 2 parts 14.5 us, 1 15.6, 4 15.7, 8 22.2), or four of 160 KB (256 rows of
-// 100003 fp32 values: 2 parts 26.3, 1 29.1; 256 of 131072 bf16 values, 128 KB each
-// in 2 parts: 22.0, 1 20.5).
+// values: 2 parts of 256 threads 13.0 us, 4 14.1, 8 19.7, which do not all run at once; of 128
+// threads, which do, 2 16.6, 4 13.8, 8 15.8), or four of 160 KB (256 rows of 100003 fp32
+// values: 2 parts 25.6, 1 26.6; of 131072 and 150001 bf16 values, which make less: 20.0 and 21.9, 1
+// 18.6 and 21.0).
 int parts_of(int rows, int vocab, int size, int num_sms) {
   int parts = 1;
   while (parts < kMaxParts) {
@@ -771,8 +773,10 @@ cudaError_t launch(const LogprobArgs& a, int num_sms, cudaStream_t stream) {
   if (blocks > 4LL * num_sms && a.top_k <= 8) return launch<T, 128>(a, parts, stream);
   // Two to four blocks an SM: 128 threads for short rows, too (400 rows of 1000 6.1 -> 5.4 us, of
   // 32000 13.0 -> 11.7; 600 of 32000 13.4 -> 13.1, but 32 alternatives 15.7 -> 16.1). Others of at
-  // most three do not start early: blocks that a call before leaves room for on some SMs
-  // alone end up four on one (400 rows of 131072 30.0 -> 24.6).
+  // most three do not start early: blocks that a kernel before leaves room for on some SMs
+  // alone end up four on one. 400 rows of 131072, with the cuBLAS product that makes them from
+  // 256, 1024 or 4096 numbers each: 61.4 -> 55.0 us, 97.5 -> 92.5, 298 -> 295; 310 rows 53.0 -> 46.7,
+  // 86.8 -> 81.8, 262 -> 261; calls alone, one behind another, 30.2 -> 25.2.
   if (blocks > 2LL * num_sms && blocks <= 4LL * num_sms && bytes <= 65536 && a.top_k <= 20) return launch<T, 128>(a, parts, stream);
   return launch<T, 256>(a, parts, stream, blocks <= 2LL * num_sms || blocks > 3LL * num_sms);
 }
