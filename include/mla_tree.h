@@ -656,7 +656,8 @@ size_t mla_pages_fit_workspace_bytes(int batch, int64_t num_pages);
  * length (below 0, or want_lens beyond the table) or held entry sets
  * MT_DEV_BAD_INDPTR and leaves that request as it is; a page number that is
  * neither -1 nor a page sets MT_DEV_BAD_SLOT and counts as -1 (and may be -1
- * afterwards). A page that stands twice in a row is held twice.
+ * afterwards). A page that stands twice in a row is held twice. kv_lens
+ * beyond the table count as its end.
  * More than 65535 requests or MT_MAX_COLUMNS pages of a row return
  * MT_EUNSUPPORTED.
  *   copies: int32 [batch, 3]; workspace: 16-byte aligned
