@@ -657,7 +657,7 @@ size_t mla_pages_fit_workspace_bytes(int batch, int64_t num_pages);
  * MT_DEV_BAD_INDPTR and leaves that request as it is; a page number that is
  * neither -1 nor a page sets MT_DEV_BAD_SLOT and counts as -1 (and may be -1
  * afterwards). A page that stands twice in a row is held twice. kv_lens
- * beyond the table count as its end.
+ * may lie beyond the table: no position is to be written then.
  * More than 65535 requests or MT_MAX_COLUMNS pages of a row return
  * MT_EUNSUPPORTED.
  *   copies: int32 [batch, 3]; workspace: 16-byte aligned
